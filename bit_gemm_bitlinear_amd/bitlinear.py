@@ -1,4 +1,5 @@
-"""ctypes binding over libbitlinear.so (C ABI in include/bitlinear.h).
+"""ctypes binding over libbitlinear.so (C ABI in include/bitlinear.h and
+include/bitlinear_layer.h).
 
 Argument marshalling only: every step of the BitLinear forward pass runs in
 the library's HIP kernels.  PyTorch provides device memory and the current
@@ -11,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Sequence
+from typing import NamedTuple, Sequence
 
 import torch
 
@@ -25,6 +26,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 _i64, _i32, _sz, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
+_dbl = ctypes.c_double
 
 
 class Projection(ctypes.Structure):
@@ -73,6 +75,25 @@ _SIGS = {
     "bitlinear_forward_acc": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
     "bitlinear_forward_acc_tiled": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz,
                                                    _vp]),
+    # include/bitlinear_layer.h
+    "bitlinear_rms_norm_quant": (ctypes.c_int, [_i64, _i64, _vp, _vp, _vp, _i32, _dbl, _vp, _vp,
+                                                _vp, _vp, _vp, _vp]),
+    "bitlinear_rms_norm_quant_backward_workspace_bytes": (_sz, [_i64, _i64, _i32]),
+    "bitlinear_rms_norm_quant_backward": (ctypes.c_int, [_i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp,
+                                                         _vp, _vp, _i32, _vp, _sz, _vp]),
+    "bitlinear_restore_activations": (ctypes.c_int, [_i64, _i64, _vp, _vp, _vp, _vp]),
+    "bitlinear_backward_input_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "bitlinear_backward_input": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _vp,
+                                                _vp, _sz, _vp]),
+    "bitlinear_backward_weight_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "bitlinear_backward_weight": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32,
+                                                 _vp, _sz, _vp]),
+    "bitlinear_w4_codes_bytes": (_sz, [_i64, _i64]),
+    "bitlinear_w4_scales_bytes": (_sz, [_i64, _i64, _i64]),
+    "bitlinear_w4_pack": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "bitlinear_w4_unpack": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "bitlinear_w4_forward": (ctypes.c_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                            _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -436,3 +457,306 @@ class BitLinear:
         y = forward(x.reshape(-1, self.in_features).contiguous(), self.packed, self.w_scale,
                     bias=self.bias, residual=res)
         return y.reshape(*lead, self.out_features)
+
+
+# --------------------------------------------------------------------------
+# Operators around the product (include/bitlinear_layer.h)
+
+WEIGHT_NONE, WEIGHT_BF16, WEIGHT_F32 = 0, 1, 2  # BL_WEIGHT_*
+
+
+def _launch(fn, args, device: torch.device, stream=None) -> None:
+    """Calls an entry point on `device`'s current stream (or the given one),
+    with that device current: a kernel goes to the current device."""
+    if torch.cuda.current_device() == device.index:
+        s = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+        _check(fn(*args, s))
+        return
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+        _check(fn(*args, s))
+
+
+def _norm_weight(weight, k, device):
+    """BL_WEIGHT_* of a norm's weight (bf16 or fp32 [K], or None)."""
+    if weight is None:
+        return WEIGHT_NONE
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("weight must be a bfloat16 or float32 tensor, or None")
+    _require(weight, weight.dtype, 1, "weight", shape=(k,), device=device)
+    return WEIGHT_BF16 if weight.dtype == torch.bfloat16 else WEIGHT_F32
+
+
+def _opt(t: torch.Tensor | None):
+    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+
+
+def _rows_f32(m: int, device) -> torch.Tensor:
+    return torch.empty(max(m, 4), dtype=torch.float32, device=device)[:m]
+
+
+class Normed(NamedTuple):
+    """What a NormQuantCall writes: int8 codes [M, K] and scales [M] of the
+    norm's output, the residual stream h [M, K] (x itself without a residual),
+    1 / rms per row [M], and the norm's bf16 output n [M, K] (None unless
+    asked for)."""
+    q: torch.Tensor
+    x_scale: torch.Tensor
+    h: torch.Tensor
+    rstd: torch.Tensor
+    n: torch.Tensor | None
+
+
+class NormQuantCall:
+    """A prepared bitlinear_rms_norm_quant: h = bf16(x + residual), RMSNorm of
+    h with an optional bf16 or fp32 weight [K], and the int8 codes and scales
+    of its output.  Outputs are allocated once (or given as `out`, a Normed;
+    its h may be x or the residual, for an update in place); each call only
+    enqueues the kernel."""
+
+    def __init__(self, x, weight=None, residual=None, eps: float = 1e-6, want_norm: bool = False,
+                 out: Normed | None = None):
+        _require(x, torch.bfloat16, 2, "x")
+        (m, k), dev = x.shape, x.device
+        wtype = _norm_weight(weight, k, dev)
+        if residual is not None:
+            _require(residual, torch.bfloat16, 2, "residual", shape=(m, k), device=dev)
+        if out is None:
+            out = Normed(torch.empty((m, k), dtype=torch.int8, device=dev), _rows_f32(m, dev),
+                         x if residual is None else torch.empty_like(x), _rows_f32(m, dev),
+                         torch.empty_like(x) if want_norm else None)
+        _require(out.q, torch.int8, 2, "out.q", shape=(m, k), device=dev)
+        _require(out.x_scale, torch.float32, 1, "out.x_scale", shape=(m,), device=dev)
+        _require(out.h, torch.bfloat16, 2, "out.h", shape=(m, k), device=dev)
+        _require(out.rstd, torch.float32, 1, "out.rstd", shape=(m,), device=dev)
+        if out.n is not None:
+            _require(out.n, torch.bfloat16, 2, "out.n", shape=(m, k), device=dev)
+        self.out = out
+        self._dev, self._keep = dev, (x, weight, residual)
+        # without a residual h is x: nothing to write unless it goes elsewhere
+        h = None if residual is None and out.h.data_ptr() == x.data_ptr() else out.h
+        self._args = (m, k, _ptr(x), _opt(residual), _opt(weight), wtype, float(eps), _opt(h),
+                      _ptr(out.rstd), _opt(out.n), _ptr(out.q), _ptr(out.x_scale))
+
+    def __call__(self, stream=None) -> Normed:
+        _launch(_lib.bitlinear_rms_norm_quant, self._args, self._dev, stream)
+        return self.out
+
+
+def rms_norm_quant(x, weight=None, residual=None, eps: float = 1e-6, want_norm: bool = False) -> Normed:
+    """Residual add, RMSNorm and int8 codes of its output, one kernel (see
+    NormQuantCall)."""
+    return NormQuantCall(x, weight, residual, eps, want_norm)()
+
+
+class NormQuantBackwardCall:
+    """A prepared gradient of rms_norm_quant.  dn: bf16 gradient [M, K] of the
+    norm's output (the codes pass it straight through); h, rstd: what the
+    forward wrote; dh: bf16 gradient of h, or None.  A call returns (dx,
+    dweight): dx bf16 [M, K] is the gradient of x and of the residual, dweight
+    fp32 [K] that of the weight (None without a weight); with accumulate it is
+    added to the given `dweight`."""
+
+    def __init__(self, dn, h, rstd, weight=None, dh=None, dx=None, dweight=None,
+                 accumulate: bool = False, workspace=None):
+        _require(dn, torch.bfloat16, 2, "dn")
+        (m, k), dev = dn.shape, dn.device
+        _require(h, torch.bfloat16, 2, "h", shape=(m, k), device=dev)
+        _require(rstd, torch.float32, 1, "rstd", shape=(m,), device=dev)
+        wtype = _norm_weight(weight, k, dev)
+        if dh is not None:
+            _require(dh, torch.bfloat16, 2, "dh", shape=(m, k), device=dev)
+        if accumulate and dweight is None:
+            raise ValueError("accumulate needs the dweight to add to")
+        if dx is None:
+            dx = torch.empty_like(dn)
+        _require(dx, torch.bfloat16, 2, "dx", shape=(m, k), device=dev)
+        if dweight is None and weight is not None:
+            dweight = torch.empty(k, dtype=torch.float32, device=dev)
+        if dweight is not None:
+            _require(dweight, torch.float32, 1, "dweight", shape=(k,), device=dev)
+        need = int(_lib.bitlinear_rms_norm_quant_backward_workspace_bytes(m, k, dweight is not None))
+        self.workspace = _workspace(need, dev, workspace)
+        self.dx, self.dweight = dx, dweight
+        self._dev, self._keep = dev, (dn, h, rstd, weight, dh)
+        self._args = (m, k, _ptr(dn), _ptr(h), _ptr(rstd), _opt(weight), wtype, _opt(dh), _ptr(dx),
+                      _opt(dweight), int(accumulate), _ptr(self.workspace), _nbytes(self.workspace))
+
+    def __call__(self, stream=None):
+        _launch(_lib.bitlinear_rms_norm_quant_backward, self._args, self._dev, stream)
+        return self.dx, self.dweight
+
+
+def rms_norm_quant_backward(dn, h, rstd, weight=None, dh=None):
+    """(dx, dweight) of rms_norm_quant (see NormQuantBackwardCall)."""
+    return NormQuantBackwardCall(dn, h, rstd, weight, dh)()
+
+
+def restore_activations(q: torch.Tensor, x_scale: torch.Tensor,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
+    """The activations that int8 codes [M, K] and scales [M] stand for:
+    bf16(q / x_scale)."""
+    _require(q, torch.int8, 2, "q")
+    m, k = q.shape
+    _require(x_scale, torch.float32, 1, "x_scale", shape=(m,), device=q.device)
+    if out is None:
+        out = torch.empty((m, k), dtype=torch.bfloat16, device=q.device)
+    _require(out, torch.bfloat16, 2, "out", shape=(m, k), device=q.device)
+    _launch(_lib.bitlinear_restore_activations, (m, k, _ptr(q), _ptr(x_scale), _ptr(out)), q.device)
+    return out
+
+
+def backward_input(dy, packed, w_scale, k: int | None = None, residual=None, out=None,
+                   workspace=None) -> torch.Tensor:
+    """Gradient of BitLinear's input, bf16 [M, K], from dy bf16 [M, N] and the
+    packed weights in either layout (give K for the tiled one).  `residual`
+    (bf16 [M, K], may be `out`) is added: layers that share an input add their
+    gradients up."""
+    _require(dy, torch.bfloat16, 2, "dy")
+    _require(packed, torch.uint8, 2, "packed", device=dy.device)
+    _require_scale(w_scale, dy.device)
+    m, n = dy.shape
+    if k is None:
+        k = 4 * packed.shape[1]
+    rows, layout = weight_layout(packed, k)
+    if rows != n:
+        raise ValueError(f"packed weights have {rows} rows, dy {n} columns")
+    if residual is not None:
+        _require(residual, torch.bfloat16, 2, "residual", shape=(m, k), device=dy.device)
+    if out is None:
+        out = torch.empty((m, k), dtype=torch.bfloat16, device=dy.device)
+    _require(out, torch.bfloat16, 2, "out", shape=(m, k), device=dy.device)
+    ws = _workspace(int(_lib.bitlinear_backward_input_workspace_bytes(m, n, k)), dy.device, workspace)
+    _launch(_lib.bitlinear_backward_input,
+            (m, n, k, _ptr(dy), _ptr(packed), layout, _ptr(w_scale), _opt(residual), _ptr(out),
+             _ptr(ws), _nbytes(ws)), dy.device)
+    return out
+
+
+def backward_weight(dy, q, x_scale, bias: bool = False, out=None, dbias=None,
+                    accumulate: bool = False, workspace=None):
+    """Gradients of BitLinear's latent weights, fp32 [N, K], and of its bias,
+    fp32 [N] (None unless `bias`), from dy bf16 [M, N] and the int8 codes
+    [M, K] and scales [M] of the input.  With accumulate they are added to
+    `out` and `dbias`."""
+    _require(dy, torch.bfloat16, 2, "dy")
+    dev = dy.device
+    _require(q, torch.int8, 2, "q", device=dev)
+    (m, n), k = dy.shape, q.shape[1]
+    if q.shape[0] != m:
+        raise ValueError("dy and q must have one row per token")
+    _require(x_scale, torch.float32, 1, "x_scale", shape=(m,), device=dev)
+    bias = bias or dbias is not None
+    if accumulate and (out is None or (bias and dbias is None)):
+        raise ValueError("accumulate needs the tensors to add to")
+    if out is None:
+        out = torch.empty((n, k), dtype=torch.float32, device=dev)
+    _require(out, torch.float32, 2, "out", shape=(n, k), device=dev)
+    if bias and dbias is None:
+        dbias = _rows_f32(n, dev)
+    if dbias is not None:
+        _require(dbias, torch.float32, 1, "dbias", shape=(n,), device=dev)
+    ws = _workspace(int(_lib.bitlinear_backward_weight_workspace_bytes(m, n, k)), dev, workspace)
+    _launch(_lib.bitlinear_backward_weight,
+            (m, n, k, _ptr(dy), _ptr(q), _ptr(x_scale), _ptr(out), _opt(dbias), int(accumulate),
+             _ptr(ws), _nbytes(ws)), dev)
+    return out, dbias
+
+
+class BackwardCall:
+    """Prepared gradients of one BitLinear: dx (backward_input), then dw and
+    dbias (backward_weight), with buffers and one workspace allocated once.  A
+    call returns (dx, dw, dbias); dbias is None unless `bias`."""
+
+    def __init__(self, dy, q, x_scale, packed, w_scale, bias: bool = False):
+        _require(dy, torch.bfloat16, 2, "dy")
+        _require(q, torch.int8, 2, "q", device=dy.device)
+        (m, n), k, dev = dy.shape, q.shape[1], dy.device
+        self.dx = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
+        self.dw = torch.empty((n, k), dtype=torch.float32, device=dev)
+        self.dbias = _rows_f32(n, dev) if bias else None
+        need = max(int(_lib.bitlinear_backward_input_workspace_bytes(m, n, k)),
+                   int(_lib.bitlinear_backward_weight_workspace_bytes(m, n, k)))
+        self.workspace = _workspace(need, dev, None)
+        self._in = (dy, q, x_scale, packed, w_scale)
+
+    def __call__(self):
+        dy, q, x_scale, packed, w_scale = self._in
+        backward_input(dy, packed, w_scale, q.shape[1], out=self.dx, workspace=self.workspace)
+        backward_weight(dy, q, x_scale, out=self.dw, dbias=self.dbias, workspace=self.workspace)
+        return self.dx, self.dw, self.dbias
+
+
+class W4Weights(NamedTuple):
+    """4-bit weights of an [N, K] matrix with a bf16 scale per row and group of
+    `group` consecutive K (the storage of bitlinear_layer.h): codes uint8
+    [N/16, K/128, 4, 16, 16], scales bf16 [N/16, K/group, 16], both with N and
+    K rounded up to whole blocks."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    n: int
+    k: int
+    group: int
+
+
+def _require_w4(w: W4Weights, device=None):
+    nb, kt = (w.n + 15) // 16, (w.k + 127) // 128
+    _require(w.codes, torch.uint8, 5, "codes", shape=(nb, kt, 4, 16, 16), device=device)
+    _require(w.scales, torch.bfloat16, 3, "scales", shape=(nb, w.k // w.group, 16),
+             device=w.codes.device)
+
+
+def pack_weights_w4(w: torch.Tensor, group: int = 128) -> W4Weights:
+    """Latent fp32 weights [N, K] -> 4-bit codes and group scales.  group: a
+    power of two from 32 to 1024 that divides K."""
+    _require(w, torch.float32, 2, "w")
+    n, k = w.shape
+    if group < 32 or k % group:
+        raise ValueError("group must be a power of two from 32 to 1024 that divides K")
+    out = W4Weights(torch.empty(((n + 15) // 16, (k + 127) // 128, 4, 16, 16), dtype=torch.uint8,
+                                device=w.device),
+                    torch.empty(((n + 15) // 16, k // group, 16), dtype=torch.bfloat16,
+                                device=w.device), n, k, group)
+    _launch(_lib.bitlinear_w4_pack, (_ptr(w), n, k, group, _ptr(out.codes), _ptr(out.scales)),
+            w.device)
+    return out
+
+
+def unpack_weights_w4(w: W4Weights) -> torch.Tensor:
+    """The fp32 weights [N, K] that 4-bit codes and scales stand for."""
+    _require_w4(w)
+    out = torch.empty((w.n, w.k), dtype=torch.float32, device=w.codes.device)
+    _launch(_lib.bitlinear_w4_unpack,
+            (_ptr(w.codes), _ptr(w.scales), w.n, w.k, w.group, _ptr(out)), w.codes.device)
+    return out
+
+
+class W4Call:
+    """A prepared product of int8 activations (codes [M, K], scales [M]) with
+    4-bit weights: y bf16 [M, N], with an optional bf16 bias [N]."""
+
+    def __init__(self, q, x_scale, w: W4Weights, out=None, bias=None):
+        _require(q, torch.int8, 2, "q")
+        (m, k), dev = q.shape, q.device
+        _require(x_scale, torch.float32, 1, "x_scale", shape=(m,), device=dev)
+        _require_w4(w, dev)
+        if k != w.k:
+            raise ValueError(f"q has {k} columns, the weights {w.k}")
+        if bias is not None:
+            _require(bias, torch.bfloat16, 1, "bias", shape=(w.n,), device=dev)
+        if out is None:
+            out = torch.empty((m, w.n), dtype=torch.bfloat16, device=dev)
+        _require(out, torch.bfloat16, 2, "out", shape=(m, w.n), device=dev)
+        self.out = out
+        self._dev, self._keep = dev, (q, x_scale, w, bias)
+        self._args = (m, w.n, k, w.group, _ptr(q), _ptr(x_scale), _ptr(w.codes), _ptr(w.scales),
+                      _opt(bias), _ptr(out))
+
+    def __call__(self, stream=None) -> torch.Tensor:
+        _launch(_lib.bitlinear_w4_forward, self._args, self._dev, stream)
+        return self.out
+
+
+def forward_w4(q, x_scale, w: W4Weights, out=None, bias=None) -> torch.Tensor:
+    """y = (codes / x_scale) . weights^T as bf16 [M, N] (see W4Call)."""
+    return W4Call(q, x_scale, w, out, bias)()

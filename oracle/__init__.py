@@ -25,3 +25,4 @@ from .bitlinear_oracle import (  # noqa: F401
     weight_quant,
     weight_scale,
 )
+from . import layer_oracle as layer  # noqa: F401

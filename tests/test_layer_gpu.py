@@ -1,0 +1,395 @@
+"""The operators around the product (bitlinear_layer.h) on the GPU, against
+plain float64 forms (oracle/layer_oracle.py).
+
+What a definition rounds is compared bit for bit; sums are held to bounds by
+arithmetic: u = 2^-24 is half a step of fp32, a sum of t terms in any order is
+off by at most t steps of the sum of their magnitudes, and a result rounded to
+bf16 by 2^-8 of itself (half a step, relative).  The matrix cores' fp32 sums
+count a whole step (2^-23) per term, as their rounding mode is not ours to
+choose.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import layer as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+U = 2.0 ** -24
+BF = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def bl():
+    from bit_gemm_bitlinear_amd import bitlinear
+
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    return bitlinear
+
+
+def to_dev(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16).to(DEV)
+
+
+def bits_of(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def bf16_bits(a):
+    return oracle.f32_to_bf16(np.asarray(a, np.float32))
+
+
+def rows(rng, m, k, scale=1.0):
+    """Rows with a few large channels; every fifth row is zero, and every
+    seventh tiny (its codes' scale is clamped without a large weight)."""
+    x = rng.standard_normal((m, k)) * scale
+    x[:, rng.random(k) < 0.02] *= 20
+    x[3::5] = 0
+    x[6::7] *= 1e-9
+    return bf16_bits(x)
+
+
+def make_weight(rng, kind, k):
+    if kind == "none":
+        return None, None
+    w = 1 + 0.2 * rng.standard_normal(k)
+    if kind == "bf16":
+        b = bf16_bits(w)
+        return to_dev(b), oracle.bf16_to_f32(b)
+    w = w.astype(np.float32)
+    return torch.from_numpy(w).to(DEV), w
+
+
+# ------------------------------------------------------------------ norm
+
+NORM_SHAPES = [(1, 4), (1, 8), (3, 12), (9, 2048), (5, 2052), (8, 4096), (2, 6912), (7, 14332),
+               (4, 16384), (3, 16388), (2, 20000), (300, 260)]
+
+
+@pytest.mark.parametrize("weight", ["none", "bf16", "fp32"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("m,k", NORM_SHAPES)
+def test_norm_quant(bl, m, k, residual, weight):
+    rng = np.random.default_rng([1, m, k, residual])
+    x = rows(rng, m, k)
+    r = rows(rng, m, k, 3.0) if residual else None
+    wt, wf = make_weight(rng, weight, k)
+    eps = 1e-5
+    got = bl.rms_norm_quant(to_dev(x), wt, None if r is None else to_dev(r), eps=eps, want_norm=True)
+    rstd = got.rstd.cpu().numpy()
+    want = ref.rms_rstd(ref.residual_sum(x, r), eps)
+    # fp64 sums are off by less than 2^-30: rstd is the rounded value or, at a
+    # border, its neighbour
+    assert np.all(np.abs(rstd - want) <= (U + 2.0 ** -30) * want)
+    q, s, h, _, n = ref.rms_norm_quant(x, r, wf, eps, rstd=rstd)
+    assert np.array_equal(bits_of(got.h), h)
+    assert np.array_equal(bits_of(got.n), n)
+    assert np.array_equal(got.x_scale.cpu().numpy(), s)
+    assert np.array_equal(got.q.cpu().numpy(), q)
+    # the fused codes are those of the separate call on the norm's output
+    q2, s2 = bl.act_quant(got.n)
+    assert torch.equal(q2, got.q) and torch.equal(s2, got.x_scale)
+
+
+@pytest.mark.parametrize("k", [64, 2052, 16388])
+@pytest.mark.parametrize("which", ["x", "residual"])
+def test_norm_quant_in_place(bl, k, which):
+    rng = np.random.default_rng([2, k])
+    x, r = rows(rng, 6, k), rows(rng, 6, k, 3.0)
+    want = bl.rms_norm_quant(to_dev(x), None, to_dev(r))
+    xt, rt = to_dev(x), to_dev(r)
+    out = bl.Normed(torch.empty_like(want.q), torch.empty(6, device=DEV), xt if which == "x" else rt,
+                    torch.empty(6, device=DEV), None)
+    got = bl.NormQuantCall(xt, None, rt, out=out)()
+    for a, b in zip(got[:4], want[:4]):
+        assert torch.equal(a, b)
+
+
+def test_norm_quant_leaves_other_rows(bl):
+    """Rows behind the last token stay as they were."""
+    rng = np.random.default_rng(3)
+    x = to_dev(rows(rng, 5, 132))
+    q = torch.full((8, 132), 77, dtype=torch.int8, device=DEV)
+    s = torch.full((8,), 5.0, device=DEV)
+    h = torch.full((8, 132), 3.0, dtype=torch.bfloat16, device=DEV)
+    rstd = torch.full((8,), 6.0, device=DEV)
+    bl.NormQuantCall(x, None, x.clone(), out=bl.Normed(q[:5], s[:5], h[:5], rstd[:5], None))()
+    assert bool((q[5:] == 77).all()) and bool((s[5:] == 5).all())
+    assert bool((h[5:] == 3).all()) and bool((rstd[5:] == 6).all())
+
+
+def check_norm_backward(out, dxt, dwt, k, m, dh):
+    # dx: the mean's k terms, two products and a subtraction in fp32, one
+    # rounding to bf16
+    inner = np.abs(out["r"] * out["g"]) + np.abs(out["r"] * out["z"]) * out["c_abs"]
+    tol = BF * np.abs(out["dx"]) * (1 + BF) + (1 + BF) * U * (
+        (k + 8) * np.abs(out["r"] * out["z"]) * out["c_abs"] + 6 * inner +
+        (0 if dh is None else np.abs(dh)))
+    assert np.all(np.abs(f64(dxt) - out["dx"]) <= tol + 1e-40)
+    if dwt is not None:
+        assert np.all(np.abs(f64(dwt) - out["dweight"]) <= (m + 4) * U * out["dw_abs"] + 1e-40)
+
+
+@pytest.mark.parametrize("weight", ["none", "bf16", "fp32"])
+@pytest.mark.parametrize("with_dh", [False, True])
+@pytest.mark.parametrize("m,k", [(1, 4), (1, 2048), (3, 12), (40, 2052), (9, 4096), (2, 14332), (3, 16384),
+                                 (5, 16388), (1500, 64), (1100, 260), (1030, 16388)])
+def test_norm_backward(bl, m, k, with_dh, weight):
+    rng = np.random.default_rng([4, m, k])
+    h = rows(rng, m, k)
+    rstd = ref.rms_rstd(h, 1e-5).astype(np.float32)
+    dn = bf16_bits(rng.standard_normal((m, k)) * 1e-3)
+    dn[::4] = 0  # tokens that the loss masks out
+    dh = bf16_bits(rng.standard_normal((m, k)) * 1e-3) if with_dh else None
+    wt, wf = make_weight(rng, weight, k)
+    dx, dw = bl.rms_norm_quant_backward(to_dev(dn), to_dev(h), torch.from_numpy(rstd).to(DEV), wt,
+                                        None if dh is None else to_dev(dh))
+    f = oracle.bf16_to_f32
+    out = ref.rms_norm_quant_backward(f(dn), f(h), rstd, wf, None if dh is None else f(dh))
+    check_norm_backward(out, dx, dw, k, m, None if dh is None else f(dh).astype(np.float64))
+    assert (dw is None) == (weight == "none")
+
+
+def test_norm_backward_in_place_and_accumulate(bl):
+    rng = np.random.default_rng(5)
+    m, k = 37, 2056
+    h, dn, dh = rows(rng, m, k), bf16_bits(rng.standard_normal((m, k))), bf16_bits(rng.standard_normal((m, k)))
+    rstd = torch.from_numpy(ref.rms_rstd(h, 1e-5).astype(np.float32)).to(DEV)
+    wt, _ = make_weight(rng, "fp32", k)
+    dx, dw = bl.rms_norm_quant_backward(to_dev(dn), to_dev(h), rstd, wt, to_dev(dh))
+    for which in ("dn", "dh"):
+        a, b = to_dev(dn), to_dev(dh)
+        acc = torch.full((k,), 0.5, device=DEV)
+        dx2, dw2 = bl.NormQuantBackwardCall(a, to_dev(h), rstd, wt, b, dx=a if which == "dn" else b,
+                                            dweight=acc, accumulate=True)()
+        assert torch.equal(dx2, dx)
+        assert torch.equal(dw2, 0.5 + dw)
+
+
+@pytest.mark.parametrize("m,k", [(1, 4), (3, 16), (5, 132), (70, 2048), (2, 14332)])
+def test_restore_activations(bl, m, k):
+    rng = np.random.default_rng([6, m, k])
+    q = rng.integers(-128, 128, (m, k)).astype(np.int8)
+    s = (127 / np.exp(3 * rng.standard_normal(m))).astype(np.float32)
+    s[0] = np.float32(127) / np.float32(1e-5)
+    got = bl.restore_activations(torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV))
+    assert np.array_equal(bits_of(got), ref.restore_activations(q, s))
+
+
+# ------------------------------------------------------------------ gradients of BitLinear
+
+def layer_case(bl, seed, m, n, k):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16)
+    q, xs = bl.act_quant(x)
+    packed, ws = bl.pack_weights(0.02 * torch.randn(n, k, generator=g, device=DEV))
+    dy = torch.randn(m, n, generator=g, device=DEV) * torch.exp(torch.randn(m, 1, generator=g, device=DEV))
+    dy[2::5] = 0  # tokens that the loss masks out
+    return dy.to(torch.bfloat16), q, xs, packed, ws
+
+
+def input_gradient(bl, dy, packed, ws):
+    u = bl.unpack_weights(packed).double()
+    return dy.double() @ u / ws.double(), dy.double().abs() @ u.abs() / ws.double()
+
+
+def weight_gradient(bl, dy, q, xs):
+    xhat = bl.restore_activations(q, xs).double()
+    d = dy.double().t().contiguous()
+    return d @ xhat, d.abs() @ xhat.abs()
+
+
+def check_input(got, want, mag, n):
+    tol = BF * want.abs() + (1 + BF) * (n + 2) * 2 * U * mag
+    assert bool(((got.double() - want).abs() <= tol).all())
+
+
+def check_weight(got, want, mag, m):
+    assert bool(((got.double() - want).abs() <= (m + 2) * 2 * U * mag).all())
+
+
+BACKWARD_SHAPES = [(1, 1, 4), (1, 16, 64), (3, 5, 12), (64, 64, 64), (65, 130, 68), (17, 8, 2052),
+                   (130, 257, 516), (301, 1001, 1284), (2, 4096, 4096), (40, 2048, 2048),
+                   (700, 24, 24), (4096, 72, 4096), (72, 4096, 4100)]
+
+
+@pytest.mark.parametrize("m,n,k", BACKWARD_SHAPES)
+def test_backward(bl, m, n, k):
+    dy, q, xs, packed, ws = layer_case(bl, 10 + m, m, n, k)
+    call = bl.BackwardCall(dy, q, xs, packed, ws, bias=True)
+    dx, dw, db = call()
+    check_input(dx, *input_gradient(bl, dy, packed, ws), n)
+    check_weight(dw, *weight_gradient(bl, dy, q, xs), m)
+    d = dy.double()
+    assert bool(((db.double() - d.sum(0)).abs() <= (m + 2) * U * d.abs().sum(0)).all())
+    first = [t.clone() for t in (dx, dw, db)]
+    for a, b in zip(call(), first):  # the same bits every time
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 16, 256), (40, 48, 512), (130, 272, 2048), (1, 4096, 1024)])
+def test_backward_input_tiled_layout(bl, m, n, k):
+    dy, q, xs, packed, ws = layer_case(bl, 20 + m, m, n, k)
+    assert torch.equal(bl.backward_input(dy, bl.tile_weights(packed), ws, k=k),
+                       bl.backward_input(dy, packed, ws))
+
+
+def test_backward_shared_input_adds_up(bl):
+    """Layers that share an input: each adds to the gradient in place, rounded
+    to bf16 as a bf16 tensor add."""
+    dy, q, xs, packed, ws = layer_case(bl, 31, 33, 72, 260)
+    dx = bl.backward_input(dy, packed, ws)
+    prev = torch.randn(33, 260, device=DEV).to(torch.bfloat16)
+    want = dx + prev
+    out = prev.clone()
+    bl.backward_input(dy, packed, ws, residual=out, out=out)
+    assert torch.equal(out, want)
+    assert torch.equal(bl.backward_input(dy, packed, ws, residual=prev), want)
+
+
+def test_backward_weight_accumulates(bl):
+    dy, q, xs, packed, ws = layer_case(bl, 32, 100, 130, 132)
+    dw, db = bl.backward_weight(dy, q, xs, bias=True)
+    a, b = torch.full_like(dw, 0.25), torch.full_like(db, -2.0)
+    bl.backward_weight(dy, q, xs, out=a, dbias=b, accumulate=True)
+    assert torch.equal(a, dw + 0.25) and torch.equal(b, db - 2.0)
+
+
+def test_backward_not_finite_stays_in_its_row(bl):
+    """An infinity in one token's gradient reaches that token's dx alone."""
+    dy, q, xs, packed, ws = layer_case(bl, 33, 70, 136, 68)
+    clean = bl.backward_input(dy, packed, ws)
+    dy[4, 135] = float("inf")
+    got = bl.backward_input(dy, packed, ws)
+    keep = torch.arange(70, device=DEV) != 4
+    assert torch.equal(got[keep], clean[keep])
+
+
+# ------------------------------------------------------------------ 4-bit weights
+
+@pytest.mark.parametrize("n,k,group", [(1, 32, 32), (16, 128, 128), (17, 160, 32), (5, 192, 64),
+                                       (33, 256, 256), (20, 1024, 1024), (48, 2048, 512)])
+def test_w4_pack(bl, n, k, group):
+    rng = np.random.default_rng([7, n, k])
+    w = (rng.standard_normal((n, k)) * 0.02).astype(np.float32)
+    w[0, :group] = 0  # a group of zeros
+    w[-1, -group:] *= 1e-3
+    p = bl.pack_weights_w4(torch.from_numpy(w).to(DEV), group)
+    v, s = ref.w4_quant(w, group)
+    codes, scales = ref.w4_pack(v, s)
+    assert np.array_equal(p.codes.cpu().numpy().reshape(-1), codes)
+    assert np.array_equal(bits_of(p.scales).reshape(-1), scales)
+    full = v.astype(np.float32) * np.repeat(oracle.bf16_to_f32(s), group, axis=1)
+    assert np.array_equal(bl.unpack_weights_w4(p).cpu().numpy(), full)
+    # half a step of the group's scale, and the scale's own rounding at the
+    # largest value (7 s against max|w|: 2^-8 of it)
+    amax = np.repeat(np.abs(w.reshape(n, -1, group)).max(2), group, axis=1)
+    assert np.all(np.abs(full - w) <= amax / 14 * (1 + 2 * BF) + amax * BF)
+
+
+def w4_case(bl, seed, m, n, k, group):
+    rng = np.random.default_rng([8, seed])
+    q = rng.integers(-127, 128, (m, k)).astype(np.int8)
+    q[2::3] = 0
+    xs = (127 / np.exp(rng.standard_normal(m))).astype(np.float32)
+    w = torch.from_numpy((rng.standard_normal((n, k)) * 0.02).astype(np.float32)).to(DEV)
+    return torch.from_numpy(q).to(DEV), torch.from_numpy(xs).to(DEV), bl.pack_weights_w4(w, group)
+
+
+def w4_reference(bl, q, xs, p):
+    """y before rounding, and the sum of the group terms' magnitudes."""
+    m, g = q.shape[0], p.k // p.group
+    w = bl.unpack_weights_w4(p).double()
+    y, mag = torch.zeros(m, p.n, dtype=torch.float64, device=DEV), torch.zeros(m, p.n, dtype=torch.float64, device=DEV)
+    step = min(p.group, 128)  # a group over 128 is added up 128 at a time
+    for i in range(p.k // step):
+        t = q[:, i * step:(i + 1) * step].double() @ w[:, i * step:(i + 1) * step].t().contiguous()
+        y += t
+        mag += t.abs()
+    return y / xs.double()[:, None], mag / xs.double()[:, None]
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 256), (1, 16, 1024), (3, 35, 768), (16, 1003, 2304), (17, 64, 512),
+                                   (1, 4096, 4096), (5, 2048, 14336), (40, 128, 4352), (2, 8192, 256)])
+def test_w4_forward(bl, m, n, k, group):
+    q, xs, p = w4_case(bl, m + n, m, n, k, group)
+    bias = torch.randn(n, device=DEV).to(torch.bfloat16)
+    y = bl.forward_w4(q, xs, p)
+    want, mag = w4_reference(bl, q, xs, p)
+    # exact integers within a group; one fp32 product and sum per group, a
+    # division, the rounding to bf16
+    tol = BF * want.abs() + (1 + BF) * (2 * (k // min(group, 128)) + 8) * U * mag
+    assert bool(((y.double() - want).abs() <= tol).all())
+    assert torch.equal(bl.forward_w4(q, xs, p, bias=bias), y + bias)
+
+
+@pytest.mark.parametrize("k,group", [(32, 32), (96, 32), (64, 64), (2080, 32), (192, 64), (8256, 64)])
+def test_w4_forward_short_tiles(bl, k, group):
+    """K that ends inside a tile of 128."""
+    q, xs, p = w4_case(bl, k, 7, 50, k, group)
+    y = bl.forward_w4(q, xs, p)
+    want, mag = w4_reference(bl, q, xs, p)
+    tol = BF * want.abs() + (1 + BF) * (2 * (k // group) + 8) * U * mag
+    assert bool(((y.double() - want).abs() <= tol).all())
+
+
+def test_w4_forward_leaves_other_rows(bl):
+    q, xs, p = w4_case(bl, 3, 5, 37, 256, 64)
+    y = torch.full((9, 37), 7.0, dtype=torch.bfloat16, device=DEV)
+    bl.forward_w4(q, xs, p, out=y[:5])
+    assert bool((y[5:] == 7).all())
+
+
+# ------------------------------------------------------------------ streams and graphs
+
+def test_operators_on_a_side_stream_and_in_a_graph(bl):
+    """Norm, 4-bit product and the gradients, captured together and replayed on
+    new inputs: every replay against the eager result."""
+    m, n, k = 24, 96, 512
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16)
+    r = torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16)
+    w = (1 + 0.1 * torch.randn(k, generator=g, device=DEV))
+    w4 = bl.pack_weights_w4(torch.randn(n, k, generator=g, device=DEV), 64)
+    packed, ws = bl.pack_weights(torch.randn(n, k, generator=g, device=DEV))
+    norm = bl.NormQuantCall(x, w, r)
+    head = bl.W4Call(norm.out.q, norm.out.x_scale, w4)
+    back = bl.BackwardCall(head.out, norm.out.q, norm.out.x_scale, packed, ws, bias=True)
+    nback = bl.NormQuantBackwardCall(back.dx, norm.out.h, norm.out.rstd, w)
+
+    def step():
+        norm()
+        head()
+        back()
+        nback()
+        return [norm.out.q, norm.out.x_scale, norm.out.h, head.out, back.dx, back.dw, back.dbias,
+                nback.dx, nback.dweight]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        x.copy_(torch.randn(m, k, generator=g, device=DEV))
+        want = [t.clone() for t in step()]
+        for t in step():
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [norm.out.q, norm.out.x_scale, norm.out.h, head.out, back.dx, back.dw, back.dbias,
+               nback.dx, nback.dweight]
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
