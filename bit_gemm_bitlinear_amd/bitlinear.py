@@ -82,12 +82,9 @@ _SIGS = {
     "bitlinear_rms_norm_quant_backward": (ctypes.c_int, [_i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp,
                                                          _vp, _vp, _i32, _vp, _sz, _vp]),
     "bitlinear_restore_activations": (ctypes.c_int, [_i64, _i64, _vp, _vp, _vp, _vp]),
-    "bitlinear_backward_input_workspace_bytes": (_sz, [_i64, _i64, _i64]),
-    "bitlinear_backward_input": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _vp,
-                                                _vp, _sz, _vp]),
-    "bitlinear_backward_weight_workspace_bytes": (_sz, [_i64, _i64, _i64]),
-    "bitlinear_backward_weight": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32,
-                                                 _vp, _sz, _vp]),
+    "bitlinear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "bitlinear_backward": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                                          _vp, _vp, _i32, _vp, _sz, _vp]),
     "bitlinear_w4_codes_bytes": (_sz, [_i64, _i64]),
     "bitlinear_w4_scales_bytes": (_sz, [_i64, _i64, _i64]),
     "bitlinear_w4_pack": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
@@ -606,85 +603,86 @@ def restore_activations(q: torch.Tensor, x_scale: torch.Tensor,
     return out
 
 
+class BackwardCall:
+    """Prepared gradients of one BitLinear, from dy bf16 [M, N]: of its input
+    (packed weights in either layout and their scale), dx bf16 [M, K], and of
+    its latent weights (the input's int8 codes [M, K] and scales [M]: its 8-bit
+    checkpoint), dw fp32 [N, K] and with `bias` dbias fp32 [N].  Leave `packed`
+    out for no dx, or `q` for no dw.  `residual` (bf16 [M, K], may be dx) is
+    added to dx, so that layers that share an input add their gradients up;
+    with accumulate, dw and dbias are added to the given tensors.  Outputs and
+    workspace are allocated once unless given; a call returns (dx, dw, dbias),
+    None for what is left out."""
+
+    def __init__(self, dy, q=None, x_scale=None, packed=None, w_scale=None, bias: bool = False,
+                 k: int | None = None, residual=None, dx=None, dw=None, dbias=None,
+                 accumulate: bool = False, workspace=None):
+        _require(dy, torch.bfloat16, 2, "dy")
+        (m, n), dev = dy.shape, dy.device
+        if q is None and packed is None:
+            raise ValueError("nothing to do: give packed (for dx) or q (for dw)")
+        if q is not None:
+            _require(q, torch.int8, 2, "q", device=dev)
+            if k is not None and k != q.shape[1]:
+                raise ValueError(f"q has {q.shape[1]} columns, k is {k}")
+            k = q.shape[1]
+            _require(q, torch.int8, 2, "q", shape=(m, k))
+            _require(x_scale, torch.float32, 1, "x_scale", shape=(m,), device=dev)
+            bias = bias or dbias is not None
+            if accumulate and (dw is None or (bias and dbias is None)):
+                raise ValueError("accumulate needs the tensors to add to")
+            if dw is None:
+                dw = torch.empty((n, k), dtype=torch.float32, device=dev)
+            _require(dw, torch.float32, 2, "dw", shape=(n, k), device=dev)
+            if bias and dbias is None:
+                dbias = _rows_f32(n, dev)
+            if dbias is not None:
+                _require(dbias, torch.float32, 1, "dbias", shape=(n,), device=dev)
+        elif dw is not None or dbias is not None or bias:
+            raise ValueError("dw and dbias need q and x_scale")
+        layout = LAYOUT_ROWS
+        if packed is not None:
+            _require(packed, torch.uint8, 2, "packed", device=dev)
+            _require_scale(w_scale, dev)
+            if k is None:
+                k = 4 * packed.shape[1]
+            rows, layout = weight_layout(packed, k)
+            if rows != n:
+                raise ValueError(f"packed weights have {rows} rows, dy {n} columns")
+            if residual is not None:
+                _require(residual, torch.bfloat16, 2, "residual", shape=(m, k), device=dev)
+            if dx is None:
+                dx = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
+            _require(dx, torch.bfloat16, 2, "dx", shape=(m, k), device=dev)
+        elif dx is not None or residual is not None:
+            raise ValueError("dx needs packed and w_scale")
+        need = int(_lib.bitlinear_backward_workspace_bytes(m, n, k, dx is not None, dw is not None))
+        self.workspace = _workspace(need, dev, workspace)
+        self._out = (dx, dw, dbias)
+        self._dev, self._keep = dev, (dy, q, x_scale, packed, w_scale, residual)
+        self._args = (m, n, k, _ptr(dy), _opt(packed), layout, _opt(w_scale), _opt(residual),
+                      _opt(dx), _opt(q), _opt(x_scale), _opt(dw), _opt(dbias), int(accumulate),
+                      _ptr(self.workspace), _nbytes(self.workspace))
+
+    def __call__(self, stream=None):
+        _launch(_lib.bitlinear_backward, self._args, self._dev, stream)
+        return self._out
+
+
 def backward_input(dy, packed, w_scale, k: int | None = None, residual=None, out=None,
                    workspace=None) -> torch.Tensor:
-    """Gradient of BitLinear's input, bf16 [M, K], from dy bf16 [M, N] and the
-    packed weights in either layout (give K for the tiled one).  `residual`
-    (bf16 [M, K], may be `out`) is added: layers that share an input add their
-    gradients up."""
-    _require(dy, torch.bfloat16, 2, "dy")
-    _require(packed, torch.uint8, 2, "packed", device=dy.device)
-    _require_scale(w_scale, dy.device)
-    m, n = dy.shape
-    if k is None:
-        k = 4 * packed.shape[1]
-    rows, layout = weight_layout(packed, k)
-    if rows != n:
-        raise ValueError(f"packed weights have {rows} rows, dy {n} columns")
-    if residual is not None:
-        _require(residual, torch.bfloat16, 2, "residual", shape=(m, k), device=dy.device)
-    if out is None:
-        out = torch.empty((m, k), dtype=torch.bfloat16, device=dy.device)
-    _require(out, torch.bfloat16, 2, "out", shape=(m, k), device=dy.device)
-    ws = _workspace(int(_lib.bitlinear_backward_input_workspace_bytes(m, n, k)), dy.device, workspace)
-    _launch(_lib.bitlinear_backward_input,
-            (m, n, k, _ptr(dy), _ptr(packed), layout, _ptr(w_scale), _opt(residual), _ptr(out),
-             _ptr(ws), _nbytes(ws)), dy.device)
-    return out
+    """Gradient of BitLinear's input, bf16 [M, K] (see BackwardCall; give K for
+    tiled weights)."""
+    return BackwardCall(dy, None, None, packed, w_scale, k=k, residual=residual, dx=out,
+                        workspace=workspace)()[0]
 
 
 def backward_weight(dy, q, x_scale, bias: bool = False, out=None, dbias=None,
                     accumulate: bool = False, workspace=None):
     """Gradients of BitLinear's latent weights, fp32 [N, K], and of its bias,
-    fp32 [N] (None unless `bias`), from dy bf16 [M, N] and the int8 codes
-    [M, K] and scales [M] of the input.  With accumulate they are added to
-    `out` and `dbias`."""
-    _require(dy, torch.bfloat16, 2, "dy")
-    dev = dy.device
-    _require(q, torch.int8, 2, "q", device=dev)
-    (m, n), k = dy.shape, q.shape[1]
-    if q.shape[0] != m:
-        raise ValueError("dy and q must have one row per token")
-    _require(x_scale, torch.float32, 1, "x_scale", shape=(m,), device=dev)
-    bias = bias or dbias is not None
-    if accumulate and (out is None or (bias and dbias is None)):
-        raise ValueError("accumulate needs the tensors to add to")
-    if out is None:
-        out = torch.empty((n, k), dtype=torch.float32, device=dev)
-    _require(out, torch.float32, 2, "out", shape=(n, k), device=dev)
-    if bias and dbias is None:
-        dbias = _rows_f32(n, dev)
-    if dbias is not None:
-        _require(dbias, torch.float32, 1, "dbias", shape=(n,), device=dev)
-    ws = _workspace(int(_lib.bitlinear_backward_weight_workspace_bytes(m, n, k)), dev, workspace)
-    _launch(_lib.bitlinear_backward_weight,
-            (m, n, k, _ptr(dy), _ptr(q), _ptr(x_scale), _ptr(out), _opt(dbias), int(accumulate),
-             _ptr(ws), _nbytes(ws)), dev)
-    return out, dbias
-
-
-class BackwardCall:
-    """Prepared gradients of one BitLinear: dx (backward_input), then dw and
-    dbias (backward_weight), with buffers and one workspace allocated once.  A
-    call returns (dx, dw, dbias); dbias is None unless `bias`."""
-
-    def __init__(self, dy, q, x_scale, packed, w_scale, bias: bool = False):
-        _require(dy, torch.bfloat16, 2, "dy")
-        _require(q, torch.int8, 2, "q", device=dy.device)
-        (m, n), k, dev = dy.shape, q.shape[1], dy.device
-        self.dx = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
-        self.dw = torch.empty((n, k), dtype=torch.float32, device=dev)
-        self.dbias = _rows_f32(n, dev) if bias else None
-        need = max(int(_lib.bitlinear_backward_input_workspace_bytes(m, n, k)),
-                   int(_lib.bitlinear_backward_weight_workspace_bytes(m, n, k)))
-        self.workspace = _workspace(need, dev, None)
-        self._in = (dy, q, x_scale, packed, w_scale)
-
-    def __call__(self):
-        dy, q, x_scale, packed, w_scale = self._in
-        backward_input(dy, packed, w_scale, q.shape[1], out=self.dx, workspace=self.workspace)
-        backward_weight(dy, q, x_scale, out=self.dw, dbias=self.dbias, workspace=self.workspace)
-        return self.dx, self.dw, self.dbias
+    fp32 [N] (None unless `bias`; see BackwardCall)."""
+    return BackwardCall(dy, q, x_scale, bias=bias, dw=out, dbias=dbias, accumulate=accumulate,
+                        workspace=workspace)()[1:]
 
 
 class W4Weights(NamedTuple):

@@ -4,26 +4,41 @@
 //   dw[n][k] = sum_m dy[m][n] * xhat[m][k],  xhat = bf16(q / x_scale)
 //   db[n]    = sum_m dy[m][n]
 //
-// u in {-1, 0, 1} and xhat are bf16 values, so every product is exact in the
-// bf16 matrix cores' fp32 sums.  Both are matrix products C[i][j] = sum_c
-// A[i][c] B[j][c] of operands whose summed index c is contiguous; what is
-// stored the other way round is transposed into the workspace first (dy and
-// the restored activations for dw, the expanded weights for dx), with c padded
-// by zeros to whole slabs.
+// Both are matrix products C[i][j] = sum_c A[i][c] B[j][c].  u in {-1, 0, 1}
+// and xhat are bf16 values, so every product is exact on the bf16 matrix cores
+// and the sums are fp32.  A call is two launches (three where a product's c is
+// split): one prepares the operands, one multiplies, dx and dw in one grid.
+//
+// Operands (prepare_kernel, in the workspace).  A matrix-core operand wants
+// its c contiguous, which for dw is the token index and for the weights of dx
+// the output index: both stored the other way round.  Each operand is kept as
+// slabs of 64 c, [slab][row][64], zero-padded: a tile's slab is then one
+// contiguous piece of memory whatever the row count (rows at a power-of-two
+// stride would all fall on the same cache channels), 128 bytes a row:
+//   dy  as A of dx: rows m, c = n;    dy^T as A of dw: rows n, c = m
+//   xhat^T as B of dw: rows k, c = m (bf16)
+//   u^T as B of dx: rows k, c = n, two bits a weight (16 bytes a row and slab)
 #include "../../include/bitlinear_layer.h"
 #include "common.hpp"
 #include "internal.hpp"
 #include "layer_internal.hpp"
+#include "restore.hpp"
 
+#include <algorithm>
 #include <atomic>
 
 namespace bl {
 
 namespace {
 
-constexpr int kSlab = 64;  // c per slab: 128 bytes of a bf16 row
+constexpr int kSlab = 64;       // c per slab
+constexpr int kRow = 2 * kSlab;  // bytes of a bf16 row of a slab
+constexpr int kCodes = kSlab / 4;  // bytes of a two-bit row of a slab
 
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef int32_t v2i __attribute__((ext_vector_type(2)));
+typedef v4i v4i_any __attribute__((aligned(2)));  // 16 bytes at any even address
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ v16f mfma_32x32x16(v4i a, v4i b, v16f c) {
@@ -31,93 +46,209 @@ __device__ __forceinline__ v16f mfma_32x32x16(v4i a, v4i b, v16f c) {
                                                  __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// ---- operands laid out with the summed index contiguous ----
+// ---------------------------------------------------------------------------
+// Operands
 
-// 64 x 64 tiles of src [rows][cols] (bf16) to dst [cols][ldd], dst columns
-// past `rows` zeroed.
-// KIND 0: bf16 as it is.  1: int8 codes q restored to bf16(q / x_scale[row]).
-// 2: packed ternary weights [rows][cols / 4] as bf16 u; `tiled`: their layout.
-template <int KIND>
-__global__ __launch_bounds__(256) void transpose_kernel(const void* __restrict__ src,
-                                                        const float* __restrict__ x_scale,
-                                                        int64_t rows, int64_t cols, int tiled,
-                                                        uint16_t* __restrict__ dst, int64_t ldd) {
-  __shared__ uint16_t t[64][66];
-  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-#pragma unroll 4
-  for (int i = ty; i < 64; i += 4) {
-    const int64_t r = r0 + i, c = c0 + tx;
-    uint16_t v = 0;
-    if (r < rows && c < cols) {
-      if constexpr (KIND == 0) {
-        v = *G(static_cast<const uint16_t*>(src) + r * cols + c);
-      } else if constexpr (KIND == 1) {
-        v = f32_to_bf16((float)*G(static_cast<const int8_t*>(src) + r * cols + c) / *G(x_scale + r));
-      } else {
-        const int64_t rb = cols / 4, o = c >> 2;
-        const int64_t off = tiled ? tiled_chunk_offset(r, o & ~(int64_t)15, rb) + (o & 15) : r * rb + o;
-        const uint32_t code = (*G(static_cast<const uint8_t*>(src) + off) >> (2 * (c & 3))) & 3u;
-        v = f32_to_bf16((float)((int)code - 1));
-      }
+struct PrepArgs {
+  int32_t begin[3];  // first workgroup of: dy, xhat, weights
+  int64_t m, n, k;
+  const uint16_t* dy;
+  uint16_t* dys;  // [ceil(n/64)][m][64], or nullptr (no dx)
+  uint16_t* dyt;  // [ceil(m/64)][n][64], or nullptr (no dw)
+  float* dbp;     // [ceil(m/64)][n] sums over the slab's tokens, or nullptr
+  const int8_t* q;
+  const float* x_scale;
+  uint16_t* xt;  // [ceil(m/64)][k][64]
+  const uint8_t* packed;
+  int32_t tiled;
+  uint8_t* ut;  // [ceil(n/64)][k][16]
+};
+
+// Column j of eight rows of eight bf16 values: a byte select per pair of rows.
+__device__ __forceinline__ v4i column8(const v4i (&r)[8], int j) {
+  v4i o;
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    o[p] = (int32_t)__builtin_amdgcn_perm((uint32_t)r[2 * p + 1][j >> 1], (uint32_t)r[2 * p][j >> 1],
+                                          (j & 1) ? 0x07060302u : 0x05040100u);
+  return o;
+}
+
+// A thread's 8 tokens x 8 columns; a workgroup's 64 tokens x 256 columns.
+// Eight lanes side by side hold one row's 64 columns on the way in and one
+// column's 64 tokens on the way out: 128-byte pieces both ways.
+__device__ __forceinline__ void prepare_dy(const PrepArgs& A, int wg) {
+  const int cols = (int)((A.n + 255) >> 8);
+  const int64_t ms = wg / cols, n0 = (int64_t)(wg - (int)ms * cols) * 256;
+  const int mi = threadIdx.x & 7, ni = threadIdx.x >> 3;
+  const int64_t m0 = ms * 64 + 8 * mi, n = n0 + 8 * ni;
+  const int mv = (int)min((int64_t)8, A.m - m0);  // rows of the eight that exist (may be <= 0)
+  const int nv = (int)min((int64_t)8, A.n - n);   // columns
+  v4i r[8];
+  if (nv >= 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // rows start at any even address; missing ones read the last
+      const v4i v = *G(reinterpret_cast<const v4i_any*>(A.dy + min(m0 + i, A.m - 1) * A.n + n));
+      r[i] = i < mv ? v : v4i{0, 0, 0, 0};
     }
-    t[i][tx] = v;
-  }
-  __syncthreads();
-#pragma unroll 4
-  for (int i = ty; i < 64; i += 4) {
-    const int64_t c = c0 + i;
-    if (c < cols) *G(dst + c * ldd + r0 + tx) = t[tx][i];
-  }
-}
-
-// Rows of dy [m][n] copied to [m][ldd], zero-padded: only where n % 8 != 0
-// (the matrix product reads 16-byte aligned rows).
-__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t m,
-                                                       int64_t n, uint16_t* __restrict__ dst,
-                                                       int64_t ldd) {
-  for (int64_t r = blockIdx.y; r < m; r += gridDim.y) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c < ldd) *G(dst + r * ldd + c) = c < n ? *G(src + r * n + c) : (uint16_t)0;
-  }
-}
-
-// db: one wave per row of the transposed dy.
-__global__ __launch_bounds__(256) void row_sum_kernel(const uint16_t* __restrict__ a, int64_t rows,
-                                                      int64_t ld, float* __restrict__ out,
-                                                      int accumulate) {
-  const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= rows) return;
-  float s = 0.0f;
-  for (int64_t c = 8 * lane; c < ld; c += 512) {
-    const v4i v = *G(reinterpret_cast<const v4i*>(a + r * ld + c));
+  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      s += __uint_as_float((uint32_t)v[i] << 16) + __uint_as_float((uint32_t)v[i] & 0xFFFF0000u);
+    for (int i = 0; i < 8; ++i) {
+      const uint16_t* p = A.dy + min(m0 + i, A.m - 1) * A.n + n;
+      uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+      for (int e = 0; e < nv && i < mv; ++e) {
+        const uint64_t v = (uint64_t)*G(p + e) << (16 * (e & 3));
+        lo |= e < 4 ? v : 0;
+        hi |= e < 4 ? 0 : v;
+      }
+      r[i] = v4i{(int32_t)lo, (int32_t)(lo >> 32), (int32_t)hi, (int32_t)(hi >> 32)};
+    }
   }
+  if (A.dys && n < ((A.n + 63) & ~(int64_t)63)) {
+    uint16_t* d = A.dys + ((n >> 6) * A.m + m0) * 64 + (n & 63);
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
-  if (lane == 0) out[r] = accumulate ? out[r] + s : s;
+    for (int i = 0; i < 8; ++i)
+      if (i < mv) *G(reinterpret_cast<v4i*>(d + 64 * i)) = r[i];
+  }
+  if (A.dbp) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w = (uint32_t)r[i][e >> 1];
+        s += __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
+      }
+      s += __shfl_xor(s, 1);
+      s += __shfl_xor(s, 2);
+      s += __shfl_xor(s, 4);
+      if (mi == e && n + e < A.n) *G(A.dbp + ms * A.n + n + e) = s;
+    }
+  }
+  if (A.dyt) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j < A.n) *G(reinterpret_cast<v4i*>(A.dyt + (ms * A.n + n + j) * 64 + 8 * mi)) = column8(r, j);
+  }
 }
 
-// ---- the matrix product ----
+__device__ __forceinline__ void prepare_xhat(const PrepArgs& A, int wg) {
+  const int cols = (int)((A.k + 255) >> 8);
+  const int64_t ms = wg / cols, k0 = (int64_t)(wg - (int)ms * cols) * 256;
+  const int mi = threadIdx.x & 7, ki = threadIdx.x >> 3;
+  const int64_t m0 = ms * 64 + 8 * mi, k = k0 + 8 * ki;
+  if (k >= A.k) return;
+  const bool second = k + 4 < A.k;  // K % 4 == 0: the last piece may be four codes
+  v2i c[8];
+  float xs[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i] = v2i{0, 0};
+    xs[i] = 1.0f;
+    if (m0 + i >= A.m) continue;
+    const int8_t* p = A.q + (m0 + i) * A.k + k;
+    c[i].x = *G(reinterpret_cast<const int32_t*>(p));
+    if (second) c[i].y = *G(reinterpret_cast<const int32_t*>(p + 4));
+    xs[i] = *G(A.x_scale + m0 + i);
+  }
+  v4i r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const RestoreRow d = restore_row(xs[i]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[i][e] = (int32_t)restore2((uint32_t)c[i][e >> 1], 2 * (e & 1), d);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (k + j < A.k) *G(reinterpret_cast<v4i*>(A.xt + (ms * A.k + k + j) * 64 + 8 * mi)) = column8(r, j);
+}
 
-struct GemmArgs {
-  const uint16_t* a;  // [ra][lda]
-  const uint16_t* b;  // [rb][ldb]
-  int64_t lda, ldb;
-  int32_t ra, rb;      // rows of A and B: C is [ra][rb]
-  int32_t ca;          // columns of A that hold data (a multiple of 8; chunks past them
-                       // are read from the row's last one and meet zeros in B)
-  int32_t slabs;       // of kSlab
+// Two-bit transpose: a thread takes 16 weights k of 16 rows n (a dword each)
+// to 16 dwords of 16 n, one per k, by four rounds of exchanges of ever
+// smaller blocks.  In the result the codes of n = 2a and n = 2a + 1 sit at bits
+// 2a and 16 + 2a (the rows are loaded in that order), where the product's
+// expansion takes them as pairs.  Rows past N are code 1 (u = 0).
+__device__ __forceinline__ void prepare_weights(const PrepArgs& A, int wg) {
+  const int cols = (int)((A.k + 1023) >> 10);
+  const int64_t slab = wg / cols;
+  const int d = threadIdx.x & 3;
+  const int64_t k = (int64_t)(wg - (int)slab * cols) * 1024 + 16 * (threadIdx.x >> 2);
+  if (k >= A.k) return;
+  const int64_t n0 = slab * 64 + 16 * d, rb = A.k >> 2, o = k >> 2;
+  uint32_t w[16];
+#pragma unroll
+  for (int p = 0; p < 16; ++p) {
+    const int64_t n = n0 + (p < 8 ? 2 * p : 2 * (p - 8) + 1);
+    w[p] = 0x55555555u;
+    if (n >= A.n) continue;
+    if (A.tiled) {
+      w[p] = *G(reinterpret_cast<const uint32_t*>(
+          A.packed + tiled_chunk_offset(n, o & ~(int64_t)15, rb) + (o & 15)));
+    } else if ((rb & 3) == 0) {
+      w[p] = *G(reinterpret_cast<const uint32_t*>(A.packed + n * rb + o));
+    } else {
+      w[p] = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (o + b < rb) w[p] |= (uint32_t)*G(A.packed + n * rb + o + b) << (8 * b);
+    }
+  }
+#pragma unroll
+  for (int h = 8; h >= 1; h >>= 1) {
+    // exchange the upper half of each 2h-block of row p with the lower of row p + h
+    const uint32_t mask = h == 8 ? 0x0000FFFFu : (h == 4 ? 0x00FF00FFu : (h == 2 ? 0x0F0F0F0Fu : 0x33333333u));
+#pragma unroll
+    for (int p = 0; p < 16; ++p) {
+      if (p & h) continue;
+      const uint32_t t = ((w[p] >> (2 * h)) ^ w[p + h]) & mask;
+      w[p + h] ^= t;
+      w[p] ^= t << (2 * h);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (k + j < A.k)
+      *G(reinterpret_cast<uint32_t*>(A.ut + (slab * A.k + k + j) * kCodes + 4 * d)) = w[j];
+}
+
+__global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs A) {
+  const int wg = blockIdx.x;
+  if (wg >= A.begin[2])
+    prepare_weights(A, wg - A.begin[2]);
+  else if (wg >= A.begin[1])
+    prepare_xhat(A, wg - A.begin[1]);
+  else
+    prepare_dy(A, wg);
+}
+
+// ---------------------------------------------------------------------------
+// The matrix products
+
+struct GemmJob {
+  const uint8_t* a;  // [slabs][ra] rows of 128 bytes
+  const uint8_t* b;  // [slabs][rb] rows of 128 bytes, or 16 (two-bit weights)
+  int32_t ra, rb;    // C is [ra][rb]; rb % 4 == 0
+  int32_t slabs;
   int32_t tiles_i, tiles_j;
-  // output
-  float* cf;           // fp32 [ra][rb], or nullptr
-  int32_t accumulate;  // cf: add to what is there
-  uint16_t* cb;        // bf16 [ra][rb] of c / *scale (+ res), or nullptr
+  int32_t ksplit, kspw;  // parts of c and slabs per part
+  int32_t codes;         // 1: b holds two-bit weights, c is half of the product's sum
+  float* part;           // ksplit > 1: fp32 sums [ksplit][ra][rb]
+  float* cf;             // fp32 output [ra][rb] (+ what is there), or nullptr
+  int32_t accumulate;
+  uint16_t* cb;          // bf16 output [ra][rb] = c / *scale (+ res)
   const float* scale;
   const uint16_t* res;
+};
+
+struct GemmArgs {
+  GemmJob j[2];
+  int32_t begin[3];  // first workgroup of each job (multiples of 8), of the bias sums
+  // bias sums
+  const float* dbp;
+  int32_t dbp_rows, n;
+  float* db;
+  int32_t accumulate;
 };
 
 template <int N>
@@ -126,50 +257,106 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// Waits until at most `ahead` slabs of D loads each are still in flight.
+template <int D, int C>
+__device__ __forceinline__ void wait_slabs(int ahead) {
+  if constexpr (C == 0) {
+    wait_vm<0>();
+  } else {
+    if (ahead >= C)
+      wait_vm<C * D>();
+    else
+      wait_slabs<D, C - 1>(ahead);
+  }
+}
+
 __device__ __forceinline__ void dma16(const void* src, int8_t* lds_dst) {
   __builtin_amdgcn_global_load_lds((const BL_GLOBAL void*)src,
                                    (__attribute__((address_space(3))) void*)lds_dst, 16, 0, 0);
 }
 
-// Tile TI x TJ with WI x WJ waves.  Slabs of both operands go from global
-// memory straight into LDS, two buffers: slab s + 1 is in flight while slab s
-// is multiplied.  Chunk c (16 bytes) of row r of a slab sits at chunk
-// c ^ ((r / 2) & 7) of its 128-byte row, so that the 16 rows that LDS serves
-// together lie in distinct banks.
-template <int TI, int TJ, int WI, int WJ>
-__global__ __launch_bounds__(64 * WI * WJ) void gemm_kernel(const GemmArgs A) {
-  constexpr int NT = 64 * WI * WJ;
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");  // no LDS access moves across
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Eight weights (four dwords of two bf16 each) from two-bit codes: q holds
+// pair a at bits 8 + 2a and 24 + 2a.  A byte select looks the high bytes of
+// u / 2 up (-0.5, 0, 0.5: their low bytes are zero); shift, mask-or, select.
+__device__ __forceinline__ v4i expand8(uint32_t q) {
+  v4i r;
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+    r[a] = (int32_t)__builtin_amdgcn_perm(0u, 0x003F00BFu, ((q >> (2 * a)) & 0x03000300u) | 0x000C000Cu);
+  return r;
+}
+
+// Output of four columns of one row.
+__device__ __forceinline__ void put4(const GemmJob& J, int64_t o, v4f v, float scale) {
+  if (J.cf) {
+    if (J.accumulate) v += *G(reinterpret_cast<const v4f*>(J.cf + o));
+    *G(reinterpret_cast<v4f*>(J.cf + o)) = v;
+    return;
+  }
+  v2i w;
+  // c is half of the sum (expand8): doubling is exact
+  w.x = (int32_t)pack_bf16x2(2.0f * v[0] / scale, 2.0f * v[1] / scale);
+  w.y = (int32_t)pack_bf16x2(2.0f * v[2] / scale, 2.0f * v[3] / scale);
+  if (J.res) {
+    const v2i r = *G(reinterpret_cast<const v2i*>(J.res + o));
+    w.x = (int32_t)add_bf16x2((uint32_t)w.x, (uint32_t)r.x);
+    w.y = (int32_t)add_bf16x2((uint32_t)w.y, (uint32_t)r.y);
+  }
+  *G(reinterpret_cast<v2i*>(J.cb + o)) = w;
+}
+
+// One tile of TI x TJ by WI x WJ waves.  Slabs of both operands go from
+// global memory straight into a ring of NST buffers in LDS.  Chunk c (16
+// bytes) of row r of a slab sits at chunk c ^ ((r / 2) & 7) of its 128-byte
+// row, so that the 16 rows that LDS serves together lie in distinct banks.
+template <int TI, int TJ, int WI, int WJ, int NST, bool CODES>
+__device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int kp, int8_t* smem) {
+  constexpr int NW = WI * WJ;
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;
-  constexpr int kStage = (TI + TJ) * 128;
-  constexpr int DA = TI * 8 / NT, DB = TJ * 8 / NT;
-  extern __shared__ __align__(16) int8_t smem[];
+  constexpr int kStage = (TI + TJ) * kRow;
+  constexpr int DA = TI / 8 / NW, DB = CODES ? 1 : TJ / 8 / NW;
+  constexpr int CW = TJ / 64;  // CODES: DMA instructions that hold a slab's codes
+  static_assert(DA * 8 * NW == TI && (CODES || DB * 8 * NW == TJ) && NW % CW == 0, "whole loads");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 31, lg = lane >> 5;
-  const int ti = (int)(blockIdx.x % (unsigned)A.tiles_i), tj = (int)(blockIdx.x / (unsigned)A.tiles_i);
   const int i0 = ti * TI, j0 = tj * TJ;
   const int wi0 = (wave % WI) * (TI / WI), wj0 = (wave / WI) * (TJ / WJ);
+  const int s0 = kp * J.kspw, nsl = min(J.slabs - s0, J.kspw);
 
-  const uint16_t* pa[DA];
-  int ca[DA];
-  const uint16_t* pb[DB];
+  const uint8_t* pa[DA];
+  const uint8_t* pb[DB];
+  const int64_t step_a = (int64_t)J.ra * kRow, step_b = (int64_t)J.rb * (CODES ? kCodes : kRow);
 #pragma unroll
   for (int i = 0; i < DA; ++i) {
     const int pos = (wave * DA + i) * 64 + lane, r = pos >> 3;
-    ca[i] = 8 * ((pos & 7) ^ ((r >> 1) & 7));
-    pa[i] = A.a + (int64_t)min(i0 + r, A.ra - 1) * A.lda;
+    pa[i] = J.a + s0 * step_a + (int64_t)min(i0 + r, J.ra - 1) * kRow + 16 * ((pos & 7) ^ ((r >> 1) & 7));
   }
 #pragma unroll
   for (int i = 0; i < DB; ++i) {
-    const int pos = (wave * DB + i) * 64 + lane, r = pos >> 3;
-    pb[i] = A.b + (int64_t)min(j0 + r, A.rb - 1) * A.ldb + 8 * ((pos & 7) ^ ((r >> 1) & 7));
+    if constexpr (CODES) {  // waves past CW load the same codes again, so that all wait alike
+      pb[i] = J.b + s0 * step_b + (int64_t)min(j0 + (wave % CW) * 64 + lane, J.rb - 1) * kCodes;
+    } else {
+      const int pos = (wave * DB + i) * 64 + lane, r = pos >> 3;
+      pb[i] = J.b + s0 * step_b + (int64_t)min(j0 + r, J.rb - 1) * kRow + 16 * ((pos & 7) ^ ((r >> 1) & 7));
+    }
   }
-  auto issue = [&](int s, int8_t* st) {
+  auto issue = [&](int8_t* st) {
 #pragma unroll
-    for (int i = 0; i < DA; ++i)
-      dma16(pa[i] + min(s * kSlab + ca[i], A.ca - 8), st + (wave * DA + i) * 1024);
+    for (int i = 0; i < DA; ++i) {
+      dma16(pa[i], st + (wave * DA + i) * 1024);
+      pa[i] += step_a;
+    }
 #pragma unroll
-    for (int i = 0; i < DB; ++i)
-      dma16(pb[i] + s * kSlab, st + TI * 128 + (wave * DB + i) * 1024);
+    for (int i = 0; i < DB; ++i) {
+      dma16(pb[i], st + TI * kRow + (CODES ? wave % CW : wave * DB + i) * 1024);
+      pb[i] += step_b;
+    }
   };
 
   v16f acc[FI][FJ];
@@ -180,153 +367,308 @@ __global__ __launch_bounds__(64 * WI * WJ) void gemm_kernel(const GemmArgs A) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  issue(0, smem);
-  for (int s = 0; s < A.slabs; ++s) {
-    wait_vm<0>();
-    __builtin_amdgcn_s_barrier();
-    if (s + 1 < A.slabs) issue(s + 1, smem + ((s + 1) & 1) * kStage);
-    const int8_t* sa = smem + (s & 1) * kStage;
-    const int8_t* sb = sa + TI * 128;
+  // Fragments of step ks of a slab: 16 c, eight a lane half.
+  v4i fa[2][FI], fb[2][FJ], cj[FJ];
+  const int8_t* sa = smem;  // the current slab's buffer
+  auto load = [&](int ks, v4i (&a)[FI], v4i (&b)[FJ]) {
 #pragma unroll
-    for (int ks = 0; ks < kSlab / 16; ++ks) {
-      v4i fa[FI], fb[FJ];
-#pragma unroll
-      for (int i = 0; i < FI; ++i) {
-        const int r = wi0 + 32 * i + lr;
-        fa[i] = *reinterpret_cast<const v4i*>(sa + 128 * r + 16 * ((2 * ks + lg) ^ ((r >> 1) & 7)));
-      }
-#pragma unroll
-      for (int j = 0; j < FJ; ++j) {
-        const int r = wj0 + 32 * j + lr;
-        fb[j] = *reinterpret_cast<const v4i*>(sb + 128 * r + 16 * ((2 * ks + lg) ^ ((r >> 1) & 7)));
-      }
-#pragma unroll
-      for (int i = 0; i < FI; ++i)
-#pragma unroll
-        for (int j = 0; j < FJ; ++j) acc[i][j] = mfma_32x32x16(fa[i], fb[j], acc[i][j]);
+    for (int i = 0; i < FI; ++i) {
+      const int r = wi0 + 32 * i + lr;
+      a[i] = *reinterpret_cast<const v4i*>(sa + kRow * r + 16 * ((2 * ks + lg) ^ ((r >> 1) & 7)));
     }
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) {
+      const int r = wj0 + 32 * j + lr;
+      if constexpr (!CODES)
+        b[j] = *reinterpret_cast<const v4i*>(sa + TI * kRow + kRow * r + 16 * ((2 * ks + lg) ^ ((r >> 1) & 7)));
+      else if (ks == 0)
+        b[j] = *reinterpret_cast<const v4i*>(sa + TI * kRow + kCodes * r);
+    }
+  };
+  auto multiply = [&](int ks, const v4i (&a)[FI], const v4i (&b)[FJ]) {
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) {
+      v4i w;
+      if constexpr (CODES)
+        w = expand8((uint32_t)cj[j][ks] << (8 - 8 * lg));  // the lane half's eight c
+      else
+        w = b[j];
+#pragma unroll
+      for (int i = 0; i < FI; ++i) acc[i][j] = mfma_32x32x16(w, a[i], acc[i][j]);
+    }
+  };
+
+  constexpr int KS = kSlab / 16;
+#pragma unroll
+  for (int p = 0; p < NST; ++p)
+    if (p < nsl) issue(smem + p * kStage);
+  wait_slabs<DA + DB, NST - 1>(min(nsl - 1, NST - 1));
+  barrier();
+  load(0, fa[0], fb[0]);
+  int buf = 0;
+  for (int s = 0; s < nsl; ++s) {
+    if constexpr (CODES) {
+#pragma unroll
+      for (int j = 0; j < FJ; ++j) cj[j] = fb[0][j];
+    }
+#pragma unroll
+    for (int ks = 0; ks < KS - 1; ++ks) {
+      load(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);  // the reads go out ahead of this step's products
+      multiply(ks, fa[ks & 1], fb[ks & 1]);
+    }
+    // The slab's last fragments are in registers: its buffer is free once
+    // every wave is here.  The next slab's first fragments are read, and the
+    // buffer refilled, ahead of the last products.
+    if (s + 1 < nsl) {
+      __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // LDS reads done (lgkmcnt 0)
+      wait_slabs<DA + DB, NST - 2>(min(nsl - 2 - s, NST - 2));
+      barrier();
+      if (s + NST < nsl) issue(smem + buf * kStage);
+      buf = buf + 1 == NST ? 0 : buf + 1;
+      sa = smem + buf * kStage;
+      load(0, fa[0], fb[0]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(KS - 1, fa[(KS - 1) & 1], fb[(KS - 1) & 1]);
   }
 
-  // lane (lr, lg) holds rows 8 (e / 4) + 4 lg + e % 4 of column lr of each subtile
-  const float sc = A.cb ? load_f32_vmem(A.scale) : 1.0f;
+  // B is the matrix core's first operand: lane (lr, lg) holds, of each
+  // subtile, row lr at columns 8 e + 4 lg .. + 3 in elements 4 e .. 4 e + 3
+  // (rb % 4 == 0: such a run is whole or outside)
+  const float sc = !J.cf ? load_f32_vmem(J.scale) : 1.0f;
 #pragma unroll
-  for (int i = 0; i < FI; ++i)
+  for (int i = 0; i < FI; ++i) {
+    const int r = i0 + wi0 + 32 * i + lr;
+    if (r >= J.ra) continue;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int r = i0 + wi0 + 32 * i + 8 * (e >> 2) + 4 * lg + (e & 3);
-      if (r >= A.ra) continue;
+    for (int j = 0; j < FJ; ++j)
 #pragma unroll
-      for (int j = 0; j < FJ; ++j) {
-        const int c = j0 + wj0 + 32 * j + lr;
-        if (c >= A.rb) continue;
-        const int64_t o = (int64_t)r * A.rb + c;
-        if (A.cf) {
-          *G(A.cf + o) = A.accumulate ? *G(A.cf + o) + acc[i][j][e] : acc[i][j][e];
-        } else {
-          uint16_t v = f32_to_bf16(acc[i][j][e] / sc);
-          if (A.res) v = add_bf16(v, *G(A.res + o));
-          *G(A.cb + o) = v;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int c = j0 + wj0 + 32 * j + 8 * e + 4 * lg;
+        if (c >= J.rb) continue;
+        const v4f v = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+        const int64_t o = (int64_t)r * J.rb + c;
+        if (J.ksplit > 1)
+          *G(reinterpret_cast<v4f*>(J.part + (int64_t)kp * J.ra * J.rb + o)) = v;
+        else
+          put4(J, o, v, sc);
       }
-    }
+  }
 }
 
-template <int TI, int TJ, int WI, int WJ>
-hipError_t launch_gemm(GemmArgs a, hipStream_t s) {
-  constexpr size_t lds = 2 * (TI + TJ) * 128;
+// Workgroups go to the 8 XCDs round-robin and each has its own L2, so each XCD
+// takes one contiguous share of a job's tiles, walked in groups of up to four
+// tile rows so that neighbours in time share operands both ways.
+__device__ __forceinline__ bool tile_of(int l, const GemmJob& J, int* ti, int* tj, int* kp) {
+  const int T = J.tiles_i * J.tiles_j * J.ksplit, chunk = (T + 7) >> 3;
+  const int w = l >> 3;
+  int t = (l & 7) * chunk + w;
+  if (w >= chunk || t >= T) return false;
+  const int per = J.tiles_i * J.tiles_j;
+  *kp = t / per;
+  t -= *kp * per;
+  const int g = t / (4 * J.tiles_j), rows = min(4, J.tiles_i - 4 * g);
+  t -= g * 4 * J.tiles_j;
+  *ti = 4 * g + t % rows;
+  *tj = t / rows;
+  return true;
+}
+
+template <int TI, int TJ, int WI, int WJ, int NST>
+__global__ __launch_bounds__(64 * WI * WJ) void gemm_kernel(const GemmArgs A) {
+  extern __shared__ __align__(16) int8_t smem[];
+  const int wg = blockIdx.x;
+  if (wg >= A.begin[2]) {  // bias sums: one column a thread, the slabs' sums in order
+    const int c = (wg - A.begin[2]) * 64 * WI * WJ + (int)threadIdx.x;
+    if (c >= A.n) return;
+    float s = 0.0f;
+    for (int r = 0; r < A.dbp_rows; ++r) s += *G(A.dbp + (int64_t)r * A.n + c);
+    *G(A.db + c) = A.accumulate ? *G(A.db + c) + s : s;
+    return;
+  }
+  const int ji = wg >= A.begin[1] ? 1 : 0;
+  const GemmJob& J = A.j[ji];
+  int ti, tj, kp;
+  if (!tile_of(wg - A.begin[ji], J, &ti, &tj, &kp)) return;
+  if (J.codes)
+    gemm_tile<TI, TJ, WI, WJ, NST, true>(J, ti, tj, kp, smem);
+  else
+    gemm_tile<TI, TJ, WI, WJ, NST, false>(J, ti, tj, kp, smem);
+}
+
+// Adds the parts of the split products, in order: four columns a thread.
+__global__ __launch_bounds__(256) void gemm_finish_kernel(const GemmArgs A, int64_t first1, int64_t total) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= total) return;
+  const GemmJob& J = A.j[id >= first1 ? 1 : 0];
+  const int64_t o = 4 * (id - (id >= first1 ? first1 : 0)), slice = (int64_t)J.ra * J.rb;
+  v4f v = *G(reinterpret_cast<const v4f*>(J.part + o));
+  for (int p = 1; p < J.ksplit; ++p) v += *G(reinterpret_cast<const v4f*>(J.part + p * slice + o));
+  put4(J, o, v, !J.cf ? load_f32_vmem(J.scale) : 1.0f);
+}
+
+// ---------------------------------------------------------------------------
+// Plans (from the shapes alone, so that the workspace queries agree)
+
+struct Config {
+  int ti, tj;
+};
+constexpr Config kConfigs[3] = {{64, 64}, {128, 128}, {256, 256}};
+constexpr int kPlanCus = 256;   // MI355X
+constexpr int kMinPart = 4;     // slabs of a part
+
+struct Plan {
+  int cfg;
+  int ksplit[2], kspw[2];  // dx, dw
+};
+
+int64_t slabs_of(int64_t c) { return (c + kSlab - 1) / kSlab; }
+
+Plan plan_backward(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
+  Plan p;
+  const int64_t rows[2] = {m, n}, slabs[2] = {slabs_of(n), slabs_of(m)};
+  const bool want[2] = {dx, dw};
+  auto tiles = [&](int c, int j) {
+    return ((rows[j] + kConfigs[c].ti - 1) / kConfigs[c].ti) * ((k + kConfigs[c].tj - 1) / kConfigs[c].tj);
+  };
+  for (p.cfg = 2; p.cfg > 0; --p.cfg) {
+    int64_t t = 0;
+    for (int j = 0; j < 2; ++j) t += want[j] ? tiles(p.cfg, j) : 0;
+    if (t >= kPlanCus) break;
+  }
+  int64_t total = 0;
+  for (int j = 0; j < 2; ++j) total += want[j] ? tiles(p.cfg, j) * slabs[j] : 0;
+  // a part is at most about the load per CU, and worth a few slabs
+  const int64_t load = std::max<int64_t>(kMinPart, (total + kPlanCus - 1) / kPlanCus);
+  for (int j = 0; j < 2; ++j) {
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(16, (slabs[j] + load / 2) / load));
+    p.kspw[j] = (int)((slabs[j] + parts - 1) / parts);
+    p.ksplit[j] = (int)((slabs[j] + p.kspw[j] - 1) / p.kspw[j]);
+  }
+  return p;
+}
+
+struct WsLayout {
+  size_t dys, dyt, dbp, xt, ut, part[2], total;
+};
+
+WsLayout layout(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
+  WsLayout L = {};
+  const Plan p = plan_backward(m, n, k, dx, dw);
+  auto take = [&](size_t& off, bool want, int64_t bytes) {
+    off = L.total;
+    if (want) L.total = align256(L.total + (size_t)bytes);
+  };
+  take(L.dys, dx, slabs_of(n) * m * kRow);
+  take(L.ut, dx, slabs_of(n) * k * kCodes);
+  take(L.dyt, dw, slabs_of(m) * n * kRow);
+  take(L.xt, dw, slabs_of(m) * k * kRow);
+  take(L.dbp, dw, slabs_of(m) * n * 4);
+  take(L.part[0], dx && p.ksplit[0] > 1, 4 * p.ksplit[0] * m * k);
+  take(L.part[1], dw && p.ksplit[1] > 1, 4 * p.ksplit[1] * n * k);
+  return L;
+}
+
+template <int TI, int TJ, int WI, int WJ, int NST>
+hipError_t launch_gemm(const GemmArgs& a, int64_t wgs, hipStream_t s) {
+  constexpr size_t lds = (size_t)NST * (TI + TJ) * kRow;
   if (lds > 64 * 1024) {  // the attribute is needed above 64 KB; once per device
     static std::atomic<bool> done[kMaxDevices];
     const int dev = current_device_index();
     if (!done[dev].load(std::memory_order_acquire)) {
       const hipError_t e = hipFuncSetAttribute(
-          reinterpret_cast<const void*>(&gemm_kernel<TI, TJ, WI, WJ>),
+          reinterpret_cast<const void*>(&gemm_kernel<TI, TJ, WI, WJ, NST>),
           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return e;
       done[dev].store(true, std::memory_order_release);
     }
   }
-  a.tiles_i = (a.ra + TI - 1) / TI;
-  a.tiles_j = (a.rb + TJ - 1) / TJ;
-  const int64_t tiles = (int64_t)a.tiles_i * a.tiles_j;
-  gemm_kernel<TI, TJ, WI, WJ><<<(unsigned)tiles, 64 * WI * WJ, lds, s>>>(a);
+  gemm_kernel<TI, TJ, WI, WJ, NST><<<(unsigned)wgs, 64 * WI * WJ, lds, s>>>(a);
   return hipGetLastError();
-}
-
-hipError_t gemm(const GemmArgs& a, hipStream_t s) {
-  const int64_t big = (int64_t)((a.ra + 255) / 256) * ((a.rb + 255) / 256);
-  if (big >= 256) return launch_gemm<256, 256, 2, 4>(a, s);
-  return launch_gemm<128, 128, 2, 2>(a, s);
-}
-
-size_t bf16_bytes(int64_t rows, int64_t ld) { return align256((size_t)rows * (size_t)ld * 2); }
-
-dim3 tiles64(int64_t rows, int64_t cols) {
-  return dim3((unsigned)((cols + 63) / 64), (unsigned)((rows + 63) / 64));
 }
 
 }  // namespace
 
-size_t backward_input_bytes(int64_t m, int64_t n, int64_t k) {
-  const int64_t np = round_up(n, kSlab);
-  return bf16_bytes(k, np) + (n % 8 ? bf16_bytes(m, np) : 0);
+size_t backward_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
+  return layout(m, n, k, dx, dw).total;
 }
 
-hipError_t launch_backward_input(int64_t m, int64_t n, int64_t k, const uint16_t* dy,
-                                 const uint8_t* packed, bool tiled, const float* w_scale,
-                                 const uint16_t* residual, uint16_t* dx, char* ws, hipStream_t s) {
-  const int64_t np = round_up(n, kSlab);
-  uint16_t* ut = reinterpret_cast<uint16_t*>(ws);
-  transpose_kernel<2><<<tiles64(n, k), 256, 0, s>>>(packed, nullptr, n, k, tiled ? 1 : 0, ut, np);
+hipError_t launch_backward(const BackwardArgs& b, char* ws, hipStream_t s) {
+  const bool dx = b.dx != nullptr, dw = b.dw != nullptr;
+  const Plan p = plan_backward(b.m, b.n, b.k, dx, dw);
+  const WsLayout L = layout(b.m, b.n, b.k, dx, dw);
+  const int64_t ms = slabs_of(b.m), ns = slabs_of(b.n);
+
+  PrepArgs pa = {};
+  pa.m = b.m;
+  pa.n = b.n;
+  pa.k = b.k;
+  pa.dy = b.dy;
+  pa.dys = dx ? reinterpret_cast<uint16_t*>(ws + L.dys) : nullptr;
+  pa.dyt = dw ? reinterpret_cast<uint16_t*>(ws + L.dyt) : nullptr;
+  pa.dbp = b.dbias ? reinterpret_cast<float*>(ws + L.dbp) : nullptr;
+  pa.q = b.q;
+  pa.x_scale = b.x_scale;
+  pa.xt = reinterpret_cast<uint16_t*>(ws + L.xt);
+  pa.packed = b.packed;
+  pa.tiled = b.tiled ? 1 : 0;
+  pa.ut = reinterpret_cast<uint8_t*>(ws + L.ut);
+  int64_t wgs = ms * ((b.n + 255) / 256);
+  pa.begin[0] = 0;
+  pa.begin[1] = (int32_t)wgs;
+  if (dw) wgs += ms * ((b.k + 255) / 256);
+  pa.begin[2] = (int32_t)wgs;
+  if (dx) wgs += ns * ((b.k + 1023) / 1024);
+  prepare_kernel<<<(unsigned)wgs, 256, 0, s>>>(pa);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+
   GemmArgs g = {};
-  g.a = dy;
-  g.lda = n;
-  g.ca = (int32_t)n;
-  if (n % 8) {
-    uint16_t* p = reinterpret_cast<uint16_t*>(ws + bf16_bytes(k, np));
-    pad_rows_kernel<<<dim3((unsigned)((np + 255) / 256), (unsigned)(m < 65535 ? m : 65535)), 256, 0, s>>>(
-        dy, m, n, p, np);
-    g.a = p;
-    g.lda = np;
-    g.ca = (int32_t)np;
+  const int64_t rows[2] = {b.m, b.n}, slabs[2] = {ns, ms};
+  const bool want[2] = {dx, dw};
+  int64_t grid = 0, finish[2] = {0, 0};
+  for (int j = 0; j < 2; ++j) {
+    GemmJob& J = g.j[j];
+    g.begin[j] = (int32_t)grid;
+    if (!want[j]) continue;
+    J.a = reinterpret_cast<const uint8_t*>(ws + (j ? L.dyt : L.dys));
+    J.b = reinterpret_cast<const uint8_t*>(ws + (j ? L.xt : L.ut));
+    J.ra = (int32_t)rows[j];
+    J.rb = (int32_t)b.k;
+    J.slabs = (int32_t)slabs[j];
+    J.tiles_i = (int32_t)((rows[j] + kConfigs[p.cfg].ti - 1) / kConfigs[p.cfg].ti);
+    J.tiles_j = (int32_t)((b.k + kConfigs[p.cfg].tj - 1) / kConfigs[p.cfg].tj);
+    J.ksplit = p.ksplit[j];
+    J.kspw = p.kspw[j];
+    J.codes = j == 0;
+    J.part = reinterpret_cast<float*>(ws + L.part[j]);
+    J.cf = j ? b.dw : nullptr;
+    J.accumulate = b.accumulate ? 1 : 0;
+    J.cb = j ? nullptr : b.dx;
+    J.scale = b.w_scale;
+    J.res = j ? nullptr : b.residual;
+    if (J.ksplit > 1) finish[j] = rows[j] * (b.k / 4);
+    grid += round_up((int64_t)J.tiles_i * J.tiles_j * J.ksplit, 8);
   }
-  g.b = ut;
-  g.ldb = np;
-  g.ra = (int32_t)m;
-  g.rb = (int32_t)k;
-  g.slabs = (int32_t)(np / kSlab);
-  g.cb = dx;
-  g.scale = w_scale;
-  g.res = residual;
-  return gemm(g, s);
-}
-
-size_t backward_weight_bytes(int64_t m, int64_t n, int64_t k) {
-  const int64_t mp = round_up(m, kSlab);
-  return bf16_bytes(n, mp) + bf16_bytes(k, mp);
-}
-
-hipError_t launch_backward_weight(int64_t m, int64_t n, int64_t k, const uint16_t* dy,
-                                  const int8_t* q, const float* x_scale, float* dw, float* dbias,
-                                  bool accumulate, char* ws, hipStream_t s) {
-  const int64_t mp = round_up(m, kSlab);
-  uint16_t* dyt = reinterpret_cast<uint16_t*>(ws);
-  uint16_t* xt = reinterpret_cast<uint16_t*>(ws + bf16_bytes(n, mp));
-  transpose_kernel<0><<<tiles64(m, n), 256, 0, s>>>(dy, nullptr, m, n, 0, dyt, mp);
-  transpose_kernel<1><<<tiles64(m, k), 256, 0, s>>>(q, x_scale, m, k, 0, xt, mp);
-  if (dbias)
-    row_sum_kernel<<<(unsigned)((n + 3) / 4), 256, 0, s>>>(dyt, n, mp, dbias, accumulate ? 1 : 0);
-  GemmArgs g = {};
-  g.a = dyt;
-  g.lda = mp;
-  g.ca = (int32_t)mp;
-  g.b = xt;
-  g.ldb = mp;
-  g.ra = (int32_t)n;
-  g.rb = (int32_t)k;
-  g.slabs = (int32_t)(mp / kSlab);
-  g.cf = dw;
-  g.accumulate = accumulate ? 1 : 0;
-  return gemm(g, s);
+  if (!dw) g.begin[1] = (int32_t)grid;
+  g.begin[2] = (int32_t)grid;
+  if (b.dbias) {
+    g.dbp = pa.dbp;
+    g.dbp_rows = (int32_t)ms;
+    g.n = (int32_t)b.n;
+    g.db = b.dbias;
+    g.accumulate = b.accumulate ? 1 : 0;
+    const int threads = p.cfg == 2 ? 512 : 256;
+    grid += (b.n + threads - 1) / threads;
+  }
+  if (p.cfg == 2) e = launch_gemm<256, 256, 2, 4, 2>(g, grid, s);
+  else if (p.cfg == 1) e = launch_gemm<128, 128, 2, 2, 2>(g, grid, s);
+  else e = launch_gemm<64, 64, 2, 2, 4>(g, grid, s);
+  const int64_t total = finish[0] + finish[1];
+  if (e != hipSuccess || total == 0) return e;
+  gemm_finish_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(g, finish[0], total);
+  return hipGetLastError();
 }
 
 }  // namespace bl

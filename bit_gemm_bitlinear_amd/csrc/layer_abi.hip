@@ -19,10 +19,11 @@ constexpr int64_t kMaxK = int64_t(1) << 22;
 constexpr int64_t kMaxN = int64_t(1) << 30;
 constexpr int64_t kMaxM = int64_t(1) << 24;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
-// Grids of the gradients' and the 4-bit kernels: their second dimension
-// counts blocks of 64 (16) rows and holds 65535, the first one 2^32 threads.
+// Grids of the gradients' and the 4-bit kernels: a grid dimension holds 2^32
+// threads, the second one 65535 workgroups.
 constexpr int64_t kMaxBwdRows = int64_t(1) << 21;
 constexpr int64_t kMaxBwdTiles = int64_t(1) << 22;  // 128 x 128 tiles of dx or dw
+constexpr int64_t kMaxBwdElems = int64_t(1) << 37;  // of dy or q
 constexpr int64_t kMaxW4N = int64_t(1) << 24;
 constexpr int64_t kMaxW4M = int64_t(1) << 19;
 
@@ -102,6 +103,7 @@ bl_status check_backward_shape(int64_t m, int64_t n, int64_t k) {
   const bl_status st = check_shape(m, n, k);
   if (st != BL_OK) return st;
   if (m > kMaxBwdRows || n > kMaxBwdRows) return BL_ESHAPE;
+  if (m * n > kMaxBwdElems || m * k > kMaxBwdElems) return BL_ESHAPE;
   const int64_t ti = (m + 127) / 128, tn = (n + 127) / 128, tk = (k + 127) / 128;
   return ti * tk > kMaxBwdTiles || tn * tk > kMaxBwdTiles ? BL_ESHAPE : BL_OK;
 }
@@ -208,53 +210,55 @@ bl_status bitlinear_restore_activations(int64_t m, int64_t k, const int8_t* q,
              : BL_EHIP;
 }
 
-size_t bitlinear_backward_input_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  return check_backward_shape(m, n, k) == BL_OK ? backward_input_bytes(m, n, k) : 0;
+size_t bitlinear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t want_dx,
+                                          int32_t want_dw) {
+  if (check_backward_shape(m, n, k) != BL_OK || (!want_dx && !want_dw)) return 0;
+  return backward_bytes(m, n, k, want_dx != 0, want_dw != 0);
 }
 
-bl_status bitlinear_backward_input(int64_t m, int64_t n, int64_t k, const uint16_t* dy,
-                                   const uint8_t* packed, int32_t layout, const float* w_scale,
-                                   const uint16_t* residual, uint16_t* dx, void* workspace,
-                                   size_t workspace_bytes, void* stream) {
+bl_status bitlinear_backward(int64_t m, int64_t n, int64_t k, const uint16_t* dy,
+                             const uint8_t* packed, int32_t layout, const float* w_scale,
+                             const uint16_t* residual, uint16_t* dx, const int8_t* q,
+                             const float* x_scale, float* dw, float* dbias, int32_t accumulate,
+                             void* workspace, size_t workspace_bytes, void* stream) {
   bl_status st;
   if ((st = check_backward_shape(m, n, k)) != BL_OK) return st;
   if (layout != BL_LAYOUT_ROWS && layout != BL_LAYOUT_TILED) return BL_EINVAL;
-  if (layout == BL_LAYOUT_TILED && (n % 16 != 0 || k % 256 != 0)) return BL_ESHAPE;
-  if ((st = check_ptrs({dy, packed, w_scale, dx})) != BL_OK) return st;
-  if ((st = check_optional({residual})) != BL_OK) return st;
-  const size_t need = backward_input_bytes(m, n, k);
+  if (accumulate != 0 && accumulate != 1) return BL_EINVAL;
+  if ((!dx && !dw) || (!dx && residual) || (!dw && dbias)) return BL_EINVAL;
+  if ((st = check_ptr(dy)) != BL_OK) return st;
+  if (dx) {
+    if (layout == BL_LAYOUT_TILED && (n % 16 != 0 || k % 256 != 0)) return BL_ESHAPE;
+    if ((st = check_ptrs({packed, w_scale, dx})) != BL_OK) return st;
+  }
+  if (dw && (st = check_ptrs({q, x_scale, dw})) != BL_OK) return st;
+  if ((st = check_optional({residual, dbias})) != BL_OK) return st;
+  const size_t need = backward_bytes(m, n, k, dx != nullptr, dw != nullptr);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != BL_OK) return st;
   const Range rdx = {dx, 2 * m * k}, rres = {residual, 2 * m * k}, rws = {workspace, (int64_t)need};
-  if (!disjoint({rdx, rws}, {{dy, 2 * m * n}, {packed, n * (k / 4)}, {w_scale, 4}})) return BL_EINVAL;
-  if (overlap(rws, rres) || (residual != dx && overlap(rdx, rres))) return BL_EINVAL;
-  return launch_backward_input(m, n, k, dy, packed, layout == BL_LAYOUT_TILED, w_scale, residual, dx,
-                               static_cast<char*>(workspace),
-                               static_cast<hipStream_t>(stream)) == hipSuccess
-             ? BL_OK
-             : BL_EHIP;
-}
-
-size_t bitlinear_backward_weight_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  return check_backward_shape(m, n, k) == BL_OK ? backward_weight_bytes(m, n, k) : 0;
-}
-
-bl_status bitlinear_backward_weight(int64_t m, int64_t n, int64_t k, const uint16_t* dy,
-                                    const int8_t* q, const float* x_scale, float* dw, float* dbias,
-                                    int32_t accumulate, void* workspace, size_t workspace_bytes,
-                                    void* stream) {
-  bl_status st;
-  if ((st = check_backward_shape(m, n, k)) != BL_OK) return st;
-  if ((st = check_ptrs({dy, q, x_scale, dw})) != BL_OK) return st;
-  if (accumulate != 0 && accumulate != 1) return BL_EINVAL;
-  if ((st = check_optional({dbias})) != BL_OK) return st;
-  const size_t need = backward_weight_bytes(m, n, k);
-  if ((st = check_workspace(workspace, workspace_bytes, need)) != BL_OK) return st;
-  if (!disjoint({{dw, 4 * n * k}, {dbias, 4 * n}, {workspace, (int64_t)need}},
-                {{dy, 2 * m * n}, {q, m * k}, {x_scale, 4 * m}}))
-    return BL_EINVAL;
-  return launch_backward_weight(m, n, k, dy, q, x_scale, dw, dbias, accumulate != 0,
-                                static_cast<char*>(workspace),
-                                static_cast<hipStream_t>(stream)) == hipSuccess
+  const Range rdw = {dw, 4 * n * k}, rdb = {dbias, 4 * n}, rdy = {dy, 2 * m * n};
+  const Range rp = {dx ? packed : nullptr, n * (k / 4)}, rs = {dx ? w_scale : nullptr, 4};
+  const Range rq = {dw ? q : nullptr, m * k}, rx = {dw ? x_scale : nullptr, 4 * m};
+  if (!disjoint({rdx, rdw, rdb, rws}, {rdy, rp, rs, rq, rx})) return BL_EINVAL;
+  if (overlap(rws, rres) || overlap(rdw, rres) || overlap(rdb, rres)) return BL_EINVAL;
+  if (residual != dx && overlap(rdx, rres)) return BL_EINVAL;
+  BackwardArgs a = {};
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  a.dy = dy;
+  a.packed = packed;
+  a.tiled = layout == BL_LAYOUT_TILED;
+  a.w_scale = w_scale;
+  a.residual = residual;
+  a.dx = dx;
+  a.q = q;
+  a.x_scale = x_scale;
+  a.dw = dw;
+  a.dbias = dbias;
+  a.accumulate = accumulate != 0;
+  return launch_backward(a, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)) ==
+                 hipSuccess
              ? BL_OK
              : BL_EHIP;
 }

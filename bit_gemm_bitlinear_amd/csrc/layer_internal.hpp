@@ -46,14 +46,24 @@ hipError_t launch_restore(const int8_t* q, const float* x_scale, int64_t m, int6
                           uint16_t* out, hipStream_t s);
 
 // ---- gradients of BitLinear (backward.hip) ----
-size_t backward_input_bytes(int64_t m, int64_t n, int64_t k);
-hipError_t launch_backward_input(int64_t m, int64_t n, int64_t k, const uint16_t* dy,
-                                 const uint8_t* packed, bool tiled, const float* w_scale,
-                                 const uint16_t* residual, uint16_t* dx, char* ws, hipStream_t s);
-size_t backward_weight_bytes(int64_t m, int64_t n, int64_t k);
-hipError_t launch_backward_weight(int64_t m, int64_t n, int64_t k, const uint16_t* dy,
-                                  const int8_t* q, const float* x_scale, float* dw, float* dbias,
-                                  bool accumulate, char* ws, hipStream_t s);
+struct BackwardArgs {
+  int64_t m, n, k;
+  const uint16_t* dy;
+  // dx (nullptr: not wanted)
+  const uint8_t* packed;
+  bool tiled;
+  const float* w_scale;
+  const uint16_t* residual;
+  uint16_t* dx;
+  // dw (nullptr: not wanted) and dbias (only with dw)
+  const int8_t* q;
+  const float* x_scale;
+  float* dw;
+  float* dbias;
+  bool accumulate;
+};
+size_t backward_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw);
+hipError_t launch_backward(const BackwardArgs& a, char* ws, hipStream_t s);
 
 // ---- 4-bit weights (w4.hip) ----
 hipError_t launch_w4_pack(const float* w, int64_t n, int64_t k, int group, uint8_t* codes,

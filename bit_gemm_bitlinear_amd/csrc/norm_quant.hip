@@ -17,6 +17,7 @@
 #include "common.hpp"
 #include "internal.hpp"
 #include "layer_internal.hpp"
+#include "restore.hpp"
 
 namespace bl {
 
@@ -410,23 +411,26 @@ __global__ __launch_bounds__(kT) void norm_backward_long_kernel(const NormBwdArg
 }
 
 // dweight[k] = sum over the workgroups' partial rows: 32 columns a workgroup,
-// 8 slices of the rows, joined in a fixed order.
-__global__ __launch_bounds__(256) void column_join_kernel(const float* __restrict__ part, int rows,
-                                                          int k, float* __restrict__ out,
-                                                          int accumulate) {
-  __shared__ float red[8][32];
+// 32 slices of the rows, joined in a fixed order.
+__global__ __launch_bounds__(1024) void column_join_kernel(const float* __restrict__ part, int rows,
+                                                           int k, float* __restrict__ out,
+                                                           int accumulate) {
+  __shared__ float red[32][33];
   const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
   const int col = 32 * blockIdx.x + c;
   float v = 0.0f;
-  if (col < k)
-    for (int r = s; r < rows; r += 8) v += *G(part + (int64_t)r * k + col);
+  if (col < k) {
+#pragma unroll 8
+    for (int r = s; r < rows; r += 32) v += *G(part + (int64_t)r * k + col);
+  }
   red[s][c] = v;
   __syncthreads();
-  if (s == 0 && col < k) {
+  // transposed: wave w adds columns 2w and 2w + 1, 32 lanes each
+  float t = red[threadIdx.x & 31][threadIdx.x >> 5];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += red[i][c];
-    out[col] = accumulate ? out[col] + v : v;
-  }
+  for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor(t, o);
+  const int oc = 32 * blockIdx.x + (threadIdx.x >> 5);
+  if ((threadIdx.x & 31) == 0 && oc < k) out[oc] = accumulate ? out[oc] + t : t;
 }
 
 // ---- restored activations ----
@@ -440,7 +444,7 @@ __global__ __launch_bounds__(256) void restore_kernel(const int8_t* __restrict__
   const int e = W * ((int)blockIdx.x * 256 + (int)threadIdx.x);
   if (e >= k) return;
   for (int64_t r = blockIdx.y; r < m; r += gridDim.y) {
-    const RowDiv d = row_div_setup(*G(x_scale + r));
+    const RestoreRow d = restore_row(*G(x_scale + r));
     uint32_t v[W / 4];
     if constexpr (WIDE) {
       const v4i t = *G(reinterpret_cast<const v4i*>(q + r * k + e));
@@ -451,10 +455,7 @@ __global__ __launch_bounds__(256) void restore_kernel(const int8_t* __restrict__
     }
     uint32_t o[W / 2];
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      const uint32_t p = v[i >> 1] >> (16 * (i & 1));
-      o[i] = pack_bf16x2(row_div((float)(int8_t)(p & 0xFFu), d), row_div((float)(int8_t)((p >> 8) & 0xFFu), d));
-    }
+    for (int i = 0; i < W / 2; ++i) o[i] = restore2(v[i >> 1], 2 * (i & 1), d);
     uint16_t* dst = out + r * k + e;
     if constexpr (WIDE) {
       *G(reinterpret_cast<v4i*>(dst)) = v4i{(int32_t)o[0], (int32_t)o[1], (int32_t)o[2], (int32_t)o[3]};
@@ -489,7 +490,7 @@ hipError_t launch_norm_quant(const NormArgs& a, hipStream_t s) {
 
 int norm_backward_blocks(int64_t m, int64_t k) {
   (void)k;
-  return (int)(m < 1024 ? m : 1024);
+  return (int)(m <= 512 ? (m + 1) / 2 : 512);
 }
 
 hipError_t launch_norm_backward(const NormBwdArgs& a, float* dweight, bool accumulate,
@@ -511,7 +512,7 @@ hipError_t launch_norm_backward(const NormBwdArgs& a, float* dweight, bool accum
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
-  column_join_kernel<<<(unsigned)((a.k + 31) / 32), 256, 0, s>>>(a.part, g, a.k, dweight,
+  column_join_kernel<<<(unsigned)((a.k + 31) / 32), 1024, 0, s>>>(a.part, g, a.k, dweight,
                                                                 accumulate ? 1 : 0);
   return hipGetLastError();
 }

@@ -79,7 +79,7 @@ bl_status bitlinear_rms_norm_quant_backward(
     void *stream);
 
 /* The activations that 8-bit codes stand for: out[m][k] = bf16(q / x_scale),
- * one correctly rounded fp32 division rounded to bf16 (x_scale: finite, > 0).
+ * one correctly rounded fp32 division rounded to bf16 (0 < x_scale <= 2^100).
  * One kernel. */
 bl_status bitlinear_restore_activations(int64_t m, int64_t k, const int8_t *q,
                                         const float *x_scale, uint16_t *out,
@@ -87,33 +87,35 @@ bl_status bitlinear_restore_activations(int64_t m, int64_t k, const int8_t *q,
 
 /* --- gradients of BitLinear -------------------------------------------- */
 
-/* Bytes of workspace bitlinear_backward_input needs. */
-size_t bitlinear_backward_input_workspace_bytes(int64_t m, int64_t n, int64_t k);
+/* Bytes of workspace bitlinear_backward needs for dx and/or dw.  Shapes: M and
+ * N up to 2^21, M*N and M*K up to 2^37, M*K and N*K up to 2^36. */
+size_t bitlinear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k,
+                                          int32_t want_dx, int32_t want_dw);
 
-/* Gradient of the layer's input: dx = bf16(sum_n dy[m][n] * u[n][k] / w_scale)
- * [M][K], fp32 sums, one division.  dy: [M][N] bf16; packed: the layer's
- * weights in `layout` (codes 0..2 only: what bitlinear_pack_weights writes).
- * residual: [M][K] bf16 added to the rounded dx (rounded again), or NULL; may
- * be dx itself, so that layers that share an input add their gradients up. */
-bl_status bitlinear_backward_input(int64_t m, int64_t n, int64_t k, const uint16_t *dy,
-                                   const uint8_t *packed, int32_t layout,
-                                   const float *w_scale, const uint16_t *residual,
-                                   uint16_t *dx, void *workspace, size_t workspace_bytes,
-                                   void *stream);
-
-/* Bytes of workspace bitlinear_backward_weight needs. */
-size_t bitlinear_backward_weight_workspace_bytes(int64_t m, int64_t n, int64_t k);
-
-/* Gradients of the latent weights and of the bias, from the activation
- * checkpoint: with xhat = bf16(q / x_scale) as bitlinear_restore_activations,
- *   dw[n][k]  = sum_m dy[m][n] * xhat[m][k]   (fp32 [N][K])
- *   dbias[n]  = sum_m dy[m][n]                (fp32 [N]; NULL: not wanted)
- * with fp32 sums; with accumulate != 0 both are added to what dw and dbias
- * hold. */
-bl_status bitlinear_backward_weight(int64_t m, int64_t n, int64_t k, const uint16_t *dy,
-                                    const int8_t *q, const float *x_scale, float *dw,
-                                    float *dbias, int32_t accumulate, void *workspace,
-                                    size_t workspace_bytes, void *stream);
+/* Gradients of one BitLinear y = x . u^T / w_scale (+ bias), from dy [M][N]
+ * bf16, the gradient of y.  Either part is left out where its output is NULL
+ * (its inputs are then not read and may be NULL):
+ *
+ * of the input, dx = bf16(sum_n dy[m][n] * u[n][k] / w_scale) [M][K] bf16
+ *   packed: the layer's weights in `layout` (codes 0..2 only, what
+ *   bitlinear_pack_weights writes); w_scale: 1 float.  residual: [M][K] bf16
+ *   added to the rounded dx (rounded again), or NULL; may be dx itself, so
+ *   that layers that share an input add their gradients up.
+ *
+ * of the latent weights, dw = sum_m dy[m][n] * xhat[m][k] [N][K] fp32, and of
+ * the bias, dbias = sum_m dy[m][n] [N] fp32 (NULL: not wanted; only with dw)
+ *   xhat = bf16(q / x_scale), what bitlinear_restore_activations gives, from
+ *   the codes q [M][K] and scales x_scale [M] of the layer's input: its 8-bit
+ *   checkpoint.  accumulate: 0, or 1 to add to what dw and dbias hold.
+ *
+ * Products are exact and sums fp32.  Two kernels, three where a product's sum
+ * is split across workgroups. */
+bl_status bitlinear_backward(int64_t m, int64_t n, int64_t k, const uint16_t *dy,
+                             const uint8_t *packed, int32_t layout,
+                             const float *w_scale, const uint16_t *residual,
+                             uint16_t *dx, const int8_t *q, const float *x_scale,
+                             float *dw, float *dbias, int32_t accumulate,
+                             void *workspace, size_t workspace_bytes, void *stream);
 
 /* --- 4-bit weights with group scales ------------------------------------ */
 
