@@ -26,6 +26,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace bl {
 
@@ -39,6 +40,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int32_t v2i __attribute__((ext_vector_type(2)));
 typedef v4i v4i_any __attribute__((aligned(2)));  // 16 bytes at any even address
+typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ v16f mfma_32x32x16(v4i a, v4i b, v16f c) {
@@ -93,16 +95,18 @@ __device__ __forceinline__ void prepare_dy(const PrepArgs& A, int wg) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint16_t* p = A.dy + min(m0 + i, A.m - 1) * A.n + n;
-      uint64_t lo = 0, hi = 0;
+    for (int i = 0; i < 8; ++i) r[i] = v4i{0, 0, 0, 0};
+    // the row's last columns, fewer than eight: one column of the eight rows a turn
 #pragma unroll 1
-      for (int e = 0; e < nv && i < mv; ++e) {
-        const uint64_t v = (uint64_t)*G(p + e) << (16 * (e & 3));
-        lo |= e < 4 ? v : 0;
-        hi |= e < 4 ? 0 : v;
-      }
-      r[i] = v4i{(int32_t)lo, (int32_t)(lo >> 32), (int32_t)hi, (int32_t)(hi >> 32)};
+    for (int e = 0; e < nv; ++e) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = *G(A.dy + min(m0 + i, A.m - 1) * A.n + n + e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          r[i][h] |= (int32_t)((e >> 1) == h && i < mv ? v[i] << (16 * (e & 1)) : 0u);
     }
   }
   if (A.dys && n < ((A.n + 63) & ~(int64_t)63)) {
@@ -177,23 +181,31 @@ __device__ __forceinline__ void prepare_weights(const PrepArgs& A, int wg) {
   if (k >= A.k) return;
   const int64_t n0 = slab * 64 + 16 * d, rb = A.k >> 2, o = k >> 2;
   uint32_t w[16];
+  // Every load unconditional: rows past N read the last one (and become code
+  // 1), a row's last dword is read up to its end and shifted into place.
+  if (rb >= 4) {
+    const int64_t oc = min(o, rb - 4);
+    const int sh = 8 * (int)(o - oc);
 #pragma unroll
-  for (int p = 0; p < 16; ++p) {
-    const int64_t n = n0 + (p < 8 ? 2 * p : 2 * (p - 8) + 1);
-    w[p] = 0x55555555u;
-    if (n >= A.n) continue;
-    if (A.tiled) {
-      w[p] = *G(reinterpret_cast<const uint32_t*>(
-          A.packed + tiled_chunk_offset(n, o & ~(int64_t)15, rb) + (o & 15)));
-    } else if ((rb & 3) == 0) {
-      w[p] = *G(reinterpret_cast<const uint32_t*>(A.packed + n * rb + o));
-    } else {
+    for (int p = 0; p < 16; ++p) {
+      const int64_t n = min(n0 + (p < 8 ? 2 * p : 2 * (p - 8) + 1), A.n - 1);
+      const int64_t at = A.tiled ? tiled_chunk_offset(n, o & ~(int64_t)15, rb) + (o & 15) : n * rb + oc;
+      w[p] = *G(reinterpret_cast<const u32_any*>(A.packed + at));
+    }
+#pragma unroll
+    for (int p = 0; p < 16; ++p) w[p] >>= sh;
+  } else {
+#pragma unroll
+    for (int p = 0; p < 16; ++p) {
+      const int64_t n = min(n0 + (p < 8 ? 2 * p : 2 * (p - 8) + 1), A.n - 1);
       w[p] = 0;
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (o + b < rb) w[p] |= (uint32_t)*G(A.packed + n * rb + o + b) << (8 * b);
+      for (int b = 0; b < 3; ++b) w[p] |= (uint32_t)*G(A.packed + n * rb + min((int64_t)b, rb - 1)) << (8 * b);
     }
   }
+#pragma unroll
+  for (int p = 0; p < 16; ++p)
+    if (n0 + (p < 8 ? 2 * p : 2 * (p - 8) + 1) >= A.n) w[p] = 0x55555555u;
 #pragma unroll
   for (int h = 8; h >= 1; h >>= 1) {
     // exchange the upper half of each 2h-block of row p with the lower of row p + h
@@ -206,10 +218,27 @@ __device__ __forceinline__ void prepare_weights(const PrepArgs& A, int wg) {
       w[p] ^= t << (2 * h);
     }
   }
+  // The four lanes of a quad hold the four dwords of a row's slab: exchange
+  // them (4 x 4), so that a lane stores whole rows, 16 bytes each.
+  const bool odd = d & 1, upper = d & 2;
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (k + j < A.k)
-      *G(reinterpret_cast<uint32_t*>(A.ut + (slab * A.k + k + j) * kCodes + 4 * d)) = w[j];
+  for (int j = 0; j < 16; j += 2) {
+    const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(odd ? w[j] : w[j + 1]), 0xB1, 0xF, 0xF, false);
+    w[j] = odd ? y : w[j];
+    w[j + 1] = odd ? w[j + 1] : y;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (j & 2) continue;
+    const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(upper ? w[j] : w[j + 2]), 0x4E, 0xF, 0xF, false);
+    w[j] = upper ? y : w[j];
+    w[j + 2] = upper ? w[j + 2] : y;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; j += 4)
+    if (k + j < A.k)  // K % 4 == 0
+      *G(reinterpret_cast<v4i*>(A.ut + (slab * A.k + k + j + d) * kCodes)) =
+          v4i{(int32_t)w[j], (int32_t)w[j + 1], (int32_t)w[j + 2], (int32_t)w[j + 3]};
 }
 
 __global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs A) {
@@ -311,6 +340,9 @@ __device__ __forceinline__ void put4(const GemmJob& J, int64_t o, v4f v, float s
   *G(reinterpret_cast<v2i*>(J.cb + o)) = w;
 }
 
+// Bytes of one slab of both operands.
+constexpr int stage_bytes(int ti, int tj, bool codes) { return ti * kRow + tj * (codes ? kCodes : kRow); }
+
 // One tile of TI x TJ by WI x WJ waves.  Slabs of both operands go from
 // global memory straight into a ring of NST buffers in LDS.  Chunk c (16
 // bytes) of row r of a slab sits at chunk c ^ ((r / 2) & 7) of its 128-byte
@@ -319,43 +351,44 @@ template <int TI, int TJ, int WI, int WJ, int NST, bool CODES>
 __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int kp, int8_t* smem) {
   constexpr int NW = WI * WJ;
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;
-  constexpr int kStage = (TI + TJ) * kRow;
+  constexpr int kStage = stage_bytes(TI, TJ, CODES);
   constexpr int DA = TI / 8 / NW, DB = CODES ? 1 : TJ / 8 / NW;
   constexpr int CW = TJ / 64;  // CODES: DMA instructions that hold a slab's codes
   static_assert(DA * 8 * NW == TI && (CODES || DB * 8 * NW == TJ) && NW % CW == 0, "whole loads");
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int lr = lane & 31, lg = lane >> 5;
   const int i0 = ti * TI, j0 = tj * TJ;
   const int wi0 = (wave % WI) * (TI / WI), wj0 = (wave / WI) * (TJ / WJ);
   const int s0 = kp * J.kspw, nsl = min(J.slabs - s0, J.kspw);
 
-  const uint8_t* pa[DA];
-  const uint8_t* pb[DB];
+  // Per lane the offsets within a slab, per wave the slab's address.
+  uint32_t oa[DA], ob[DB];
   const int64_t step_a = (int64_t)J.ra * kRow, step_b = (int64_t)J.rb * (CODES ? kCodes : kRow);
+  const uint8_t *pa = J.a + s0 * step_a, *pb = J.b + s0 * step_b;
 #pragma unroll
   for (int i = 0; i < DA; ++i) {
     const int pos = (wave * DA + i) * 64 + lane, r = pos >> 3;
-    pa[i] = J.a + s0 * step_a + (int64_t)min(i0 + r, J.ra - 1) * kRow + 16 * ((pos & 7) ^ ((r >> 1) & 7));
+    oa[i] = (uint32_t)min(i0 + r, J.ra - 1) * kRow + 16 * ((pos & 7) ^ ((r >> 1) & 7));
   }
 #pragma unroll
   for (int i = 0; i < DB; ++i) {
     if constexpr (CODES) {  // waves past CW load the same codes again, so that all wait alike
-      pb[i] = J.b + s0 * step_b + (int64_t)min(j0 + (wave % CW) * 64 + lane, J.rb - 1) * kCodes;
+      ob[i] = (uint32_t)min(j0 + (wave % CW) * 64 + lane, J.rb - 1) * kCodes;
     } else {
       const int pos = (wave * DB + i) * 64 + lane, r = pos >> 3;
-      pb[i] = J.b + s0 * step_b + (int64_t)min(j0 + r, J.rb - 1) * kRow + 16 * ((pos & 7) ^ ((r >> 1) & 7));
+      ob[i] = (uint32_t)min(j0 + r, J.rb - 1) * kRow + 16 * ((pos & 7) ^ ((r >> 1) & 7));
     }
   }
-  auto issue = [&](int8_t* st) {
-#pragma unroll
-    for (int i = 0; i < DA; ++i) {
-      dma16(pa[i], st + (wave * DA + i) * 1024);
-      pa[i] += step_a;
-    }
-#pragma unroll
-    for (int i = 0; i < DB; ++i) {
-      dma16(pb[i], st + TI * kRow + (CODES ? wave % CW : wave * DB + i) * 1024);
-      pb[i] += step_b;
+  // Load d (of DA + DB) of the next slab into the buffer st.
+  constexpr int D = DA + DB;
+  auto issue_one = [&](int d, int8_t* st) {
+    if (d < DA)
+      dma16(pa + oa[d], st + (wave * DA + d) * 1024);
+    else
+      dma16(pb + ob[d - DA], st + TI * kRow + (CODES ? wave % CW : wave * DB + d - DA) * 1024);
+    if (d == D - 1) {
+      pa += step_a;
+      pb += step_b;
     }
   };
 
@@ -385,7 +418,12 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
         b[j] = *reinterpret_cast<const v4i*>(sa + TI * kRow + kCodes * r);
     }
   };
-  auto multiply = [&](int ks, const v4i (&a)[FI], const v4i (&b)[FJ]) {
+  // Products of step ks; with ISSUE, a load of the slab that goes to `st`
+  // between any two of them (all at once would hold up the products behind
+  // them).
+  auto multiply = [&](auto issue, int ks, const v4i (&a)[FI], const v4i (&b)[FJ], int8_t* st) {
+    constexpr bool ISSUE = decltype(issue)::value;
+    constexpr int P = FI * FJ;
 #pragma unroll
     for (int j = 0; j < FJ; ++j) {
       v4i w;
@@ -394,19 +432,38 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
       else
         w = b[j];
 #pragma unroll
-      for (int i = 0; i < FI; ++i) acc[i][j] = mfma_32x32x16(w, a[i], acc[i][j]);
+      for (int i = 0; i < FI; ++i) {
+        acc[i][j] = mfma_32x32x16(w, a[i], acc[i][j]);
+        if constexpr (ISSUE) {
+#pragma unroll
+          for (int d = 0; d < D; ++d)
+            if (d * P / D == j * FI + i) {
+              __builtin_amdgcn_sched_barrier(0);
+              issue_one(d, st);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+      }
     }
   };
 
   constexpr int KS = kSlab / 16;
 #pragma unroll
   for (int p = 0; p < NST; ++p)
-    if (p < nsl) issue(smem + p * kStage);
-  wait_slabs<DA + DB, NST - 1>(min(nsl - 1, NST - 1));
+    if (p < nsl) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) issue_one(d, smem + p * kStage);
+    }
+  wait_slabs<D, NST - 1>(min(nsl - 1, NST - 1));
   barrier();
   load(0, fa[0], fb[0]);
   int buf = 0;
-  for (int s = 0; s < nsl; ++s) {
+  // A slab: its first steps, then, when its last fragments are in registers
+  // and every wave is there, its buffer is free.  The next slab's first
+  // fragments are read ahead of the last products, and the buffer refilled
+  // between them.
+  auto slab = [&](auto issue, int s) {
+    constexpr bool ISSUE = decltype(issue)::value;
     if constexpr (CODES) {
 #pragma unroll
       for (int j = 0; j < FJ; ++j) cj[j] = fb[0][j];
@@ -415,23 +472,23 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
     for (int ks = 0; ks < KS - 1; ++ks) {
       load(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
       __builtin_amdgcn_sched_barrier(0);  // the reads go out ahead of this step's products
-      multiply(ks, fa[ks & 1], fb[ks & 1]);
+      multiply(std::false_type{}, ks, fa[ks & 1], fb[ks & 1], nullptr);
     }
-    // The slab's last fragments are in registers: its buffer is free once
-    // every wave is here.  The next slab's first fragments are read, and the
-    // buffer refilled, ahead of the last products.
-    if (s + 1 < nsl) {
-      __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // LDS reads done (lgkmcnt 0)
-      wait_slabs<DA + DB, NST - 2>(min(nsl - 2 - s, NST - 2));
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // LDS reads done (lgkmcnt 0)
+    int8_t* st = smem + buf * kStage;
+    if (ISSUE || s + 1 < nsl) {
+      wait_vm<ISSUE ? (NST - 2) * D : 0>();
       barrier();
-      if (s + NST < nsl) issue(smem + buf * kStage);
       buf = buf + 1 == NST ? 0 : buf + 1;
       sa = smem + buf * kStage;
       load(0, fa[0], fb[0]);
     }
     __builtin_amdgcn_sched_barrier(0);
-    multiply(KS - 1, fa[(KS - 1) & 1], fb[(KS - 1) & 1]);
-  }
+    multiply(issue, KS - 1, fa[(KS - 1) & 1], fb[(KS - 1) & 1], st);
+  };
+  int s = 0;
+  for (; s + NST < nsl; ++s) slab(std::true_type{}, s);
+  for (; s < nsl; ++s) slab(std::false_type{}, s);
 
   // B is the matrix core's first operand: lane (lr, lg) holds, of each
   // subtile, row lr at columns 8 e + 4 lg .. + 3 in elements 4 e .. 4 e + 3
@@ -475,7 +532,7 @@ __device__ __forceinline__ bool tile_of(int l, const GemmJob& J, int* ti, int* t
   return true;
 }
 
-template <int TI, int TJ, int WI, int WJ, int NST>
+template <int TI, int TJ, int WI, int WJ, int NST, int NSTC>
 __global__ __launch_bounds__(64 * WI * WJ) void gemm_kernel(const GemmArgs A) {
   extern __shared__ __align__(16) int8_t smem[];
   const int wg = blockIdx.x;
@@ -492,7 +549,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void gemm_kernel(const GemmArgs A) {
   int ti, tj, kp;
   if (!tile_of(wg - A.begin[ji], J, &ti, &tj, &kp)) return;
   if (J.codes)
-    gemm_tile<TI, TJ, WI, WJ, NST, true>(J, ti, tj, kp, smem);
+    gemm_tile<TI, TJ, WI, WJ, NSTC, true>(J, ti, tj, kp, smem);
   else
     gemm_tile<TI, TJ, WI, WJ, NST, false>(J, ti, tj, kp, smem);
 }
@@ -570,21 +627,21 @@ WsLayout layout(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
   return L;
 }
 
-template <int TI, int TJ, int WI, int WJ, int NST>
+template <int TI, int TJ, int WI, int WJ, int NST, int NSTC>
 hipError_t launch_gemm(const GemmArgs& a, int64_t wgs, hipStream_t s) {
-  constexpr size_t lds = (size_t)NST * (TI + TJ) * kRow;
+  constexpr size_t lds = std::max(NST * stage_bytes(TI, TJ, false), NSTC * stage_bytes(TI, TJ, true));
   if (lds > 64 * 1024) {  // the attribute is needed above 64 KB; once per device
     static std::atomic<bool> done[kMaxDevices];
     const int dev = current_device_index();
     if (!done[dev].load(std::memory_order_acquire)) {
       const hipError_t e = hipFuncSetAttribute(
-          reinterpret_cast<const void*>(&gemm_kernel<TI, TJ, WI, WJ, NST>),
+          reinterpret_cast<const void*>(&gemm_kernel<TI, TJ, WI, WJ, NST, NSTC>),
           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return e;
       done[dev].store(true, std::memory_order_release);
     }
   }
-  gemm_kernel<TI, TJ, WI, WJ, NST><<<(unsigned)wgs, 64 * WI * WJ, lds, s>>>(a);
+  gemm_kernel<TI, TJ, WI, WJ, NST, NSTC><<<(unsigned)wgs, 64 * WI * WJ, lds, s>>>(a);
   return hipGetLastError();
 }
 
@@ -662,9 +719,9 @@ hipError_t launch_backward(const BackwardArgs& b, char* ws, hipStream_t s) {
     const int threads = p.cfg == 2 ? 512 : 256;
     grid += (b.n + threads - 1) / threads;
   }
-  if (p.cfg == 2) e = launch_gemm<256, 256, 2, 4, 2>(g, grid, s);
-  else if (p.cfg == 1) e = launch_gemm<128, 128, 2, 2, 2>(g, grid, s);
-  else e = launch_gemm<64, 64, 2, 2, 4>(g, grid, s);
+  if (p.cfg == 2) e = launch_gemm<256, 256, 2, 4, 2, 4>(g, grid, s);
+  else if (p.cfg == 1) e = launch_gemm<128, 128, 2, 2, 2, 4>(g, grid, s);
+  else e = launch_gemm<64, 64, 2, 2, 4, 7>(g, grid, s);
   const int64_t total = finish[0] + finish[1];
   if (e != hipSuccess || total == 0) return e;
   gemm_finish_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(g, finish[0], total);
