@@ -261,6 +261,7 @@ struct GemmJob {
   int32_t slabs;
   int32_t tiles_i, tiles_j;
   int32_t ksplit, kspw;  // parts of c and slabs per part
+  int32_t cfg;           // tile size (kConfigs)
   int32_t codes;         // 1: b holds two-bit weights, c is half of the product's sum
   float* part;           // ksplit > 1: fp32 sums [ksplit][ra][rb]
   float* cf;             // fp32 output [ra][rb] (+ what is there), or nullptr
@@ -532,12 +533,23 @@ __device__ __forceinline__ bool tile_of(int l, const GemmJob& J, int* ti, int* t
   return true;
 }
 
-template <int TI, int TJ, int WI, int WJ, int NST, int NSTC>
-__global__ __launch_bounds__(64 * WI * WJ) void gemm_kernel(const GemmArgs A) {
+// The kernels: tiles of 64 x 64 and 128 x 128, whichever the plan takes for
+// each product, by four waves (two workgroups a CU), and tiles of 256 x 256 by
+// eight.  Slab rings are as deep as the LDS allows (two-bit slabs are smaller).
+constexpr int kDeep64 = 4, kDeep64c = 8, kDeep128 = 2, kDeep128c = 4, kDeep256 = 2, kDeep256c = 4;
+constexpr int ring_bytes(int t, int deep, int deepc) {
+  return std::max(deep * stage_bytes(t, t, false), deepc * stage_bytes(t, t, true));
+}
+constexpr size_t kLdsSmall = std::max(ring_bytes(64, kDeep64, kDeep64c), ring_bytes(128, kDeep128, kDeep128c));
+constexpr size_t kLdsBig = ring_bytes(256, kDeep256, kDeep256c);
+static_assert(2 * kLdsSmall <= 160 * 1024 && kLdsBig <= 160 * 1024, "LDS of a CU");
+
+template <bool BIG>
+__global__ __launch_bounds__(BIG ? 512 : 256, 2) void gemm_kernel(const GemmArgs A) {
   extern __shared__ __align__(16) int8_t smem[];
   const int wg = blockIdx.x;
   if (wg >= A.begin[2]) {  // bias sums: one column a thread, the slabs' sums in order
-    const int c = (wg - A.begin[2]) * 64 * WI * WJ + (int)threadIdx.x;
+    const int c = (wg - A.begin[2]) * (BIG ? 512 : 256) + (int)threadIdx.x;
     if (c >= A.n) return;
     float s = 0.0f;
     for (int r = 0; r < A.dbp_rows; ++r) s += *G(A.dbp + (int64_t)r * A.n + c);
@@ -548,10 +560,22 @@ __global__ __launch_bounds__(64 * WI * WJ) void gemm_kernel(const GemmArgs A) {
   const GemmJob& J = A.j[ji];
   int ti, tj, kp;
   if (!tile_of(wg - A.begin[ji], J, &ti, &tj, &kp)) return;
-  if (J.codes)
-    gemm_tile<TI, TJ, WI, WJ, NSTC, true>(J, ti, tj, kp, smem);
-  else
-    gemm_tile<TI, TJ, WI, WJ, NST, false>(J, ti, tj, kp, smem);
+  if constexpr (BIG) {
+    if (J.codes)
+      gemm_tile<256, 256, 2, 4, kDeep256c, true>(J, ti, tj, kp, smem);
+    else
+      gemm_tile<256, 256, 2, 4, kDeep256, false>(J, ti, tj, kp, smem);
+  } else if (J.cfg == 1) {
+    if (J.codes)
+      gemm_tile<128, 128, 2, 2, kDeep128c, true>(J, ti, tj, kp, smem);
+    else
+      gemm_tile<128, 128, 2, 2, kDeep128, false>(J, ti, tj, kp, smem);
+  } else {
+    if (J.codes)
+      gemm_tile<64, 64, 2, 2, kDeep64c, true>(J, ti, tj, kp, smem);
+    else
+      gemm_tile<64, 64, 2, 2, kDeep64, false>(J, ti, tj, kp, smem);
+  }
 }
 
 // Adds the parts of the split products, in order: four columns a thread.
@@ -568,51 +592,115 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const GemmArgs A, int6
 // ---------------------------------------------------------------------------
 // Plans (from the shapes alone, so that the workspace queries agree)
 
+struct Plan {
+  int cfg[2], ksplit[2], kspw[2];  // dx, dw
+  int order;                       // which of them goes first
+};
+
+// Tile sizes, with what the plan needs to know of each, measured on an
+// MI355X: the time of a slab when the CU's other tiles keep the matrix cores
+// busy, that of a slab of a tile by itself (the latency of a step), and the
+// time to start a tile and write its outputs, bf16 or fp32 (us).
 struct Config {
   int ti, tj;
+  float slab, alone, put16, put32;
 };
-constexpr Config kConfigs[3] = {{64, 64}, {128, 128}, {256, 256}};
-constexpr int kPlanCus = 256;   // MI355X
-constexpr int kMinPart = 4;     // slabs of a part
-
-struct Plan {
-  int cfg;
-  int ksplit[2], kspw[2];  // dx, dw
-};
+constexpr Config kConfigs[3] = {{64, 64, 0.22f, 0.36f, 0.4f, 1.2f},
+                                {128, 128, 0.49f, 0.60f, 1.5f, 3.8f},
+                                {256, 256, 1.55f, 1.55f, 5.0f, 9.0f}};
+constexpr int kPlanCus = 256;      // MI355X
+constexpr int kMinPart = 4;        // slabs of a part
+constexpr float kFinishUs = 3.0f;  // one more launch
+constexpr float kBytesPerUs = 6e6f;
 
 int64_t slabs_of(int64_t c) { return (c + kSlab - 1) / kSlab; }
 
+// When kPlanCus CUs are done with na tiles of time a, dealt out first, and nb
+// of time b, each to the CU that is free first.
+float makespan(int64_t na, float a, int64_t nb, float b) {
+  const int64_t q = na / kPlanCus, more = na % kPlanCus;
+  const float l1 = q * a, l2 = more ? l1 + a : l1;  // kPlanCus - more CUs, `more` CUs
+  if (nb == 0) return l2;
+  const float mean = ((kPlanCus - more) * l1 + more * l2 + nb * b) / kPlanCus;
+  // tiles of the second kind that the two groups of CUs have room for by `mean`
+  // (no schedule ends before it), then one more a CU, whichever group ends it first
+  int64_t c1 = (int64_t)std::max(0.0f, (mean - l1) / b), c2 = (int64_t)std::max(0.0f, (mean - l2) / b);
+  float t = mean;
+  while ((kPlanCus - more) * c1 + more * c2 < nb) {
+    const float t1 = l1 + (c1 + 1) * b, t2 = l2 + (c2 + 1) * b;
+    t = more && t2 < t1 ? t2 : t1;
+    ++(more && t2 < t1 ? c2 : c1);
+  }
+  return std::max(t, l2);
+}
+
+// Per product the tile size and the parts of its sum, with the smallest
+// estimated time of all together.  256 x 256 tiles are a kernel of their own.
 Plan plan_backward(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
-  Plan p;
   const int64_t rows[2] = {m, n}, slabs[2] = {slabs_of(n), slabs_of(m)};
   const bool want[2] = {dx, dw};
-  auto tiles = [&](int c, int j) {
-    return ((rows[j] + kConfigs[c].ti - 1) / kConfigs[c].ti) * ((k + kConfigs[c].tj - 1) / kConfigs[c].tj);
+  struct Option {
+    int cfg, ksplit, kspw;
+    int64_t count;
+    float us, alone, finish;
   };
-  for (p.cfg = 2; p.cfg > 0; --p.cfg) {
-    int64_t t = 0;
-    for (int j = 0; j < 2; ++j) t += want[j] ? tiles(p.cfg, j) : 0;
-    if (t >= kPlanCus) break;
-  }
-  int64_t total = 0;
-  for (int j = 0; j < 2; ++j) total += want[j] ? tiles(p.cfg, j) * slabs[j] : 0;
-  // a part is at most about the load per CU, and worth a few slabs
-  const int64_t load = std::max<int64_t>(kMinPart, (total + kPlanCus - 1) / kPlanCus);
+  Option opt[2][24];
+  int num[2] = {0, 0};
+  static const int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16};
   for (int j = 0; j < 2; ++j) {
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(16, (slabs[j] + load / 2) / load));
-    p.kspw[j] = (int)((slabs[j] + parts - 1) / parts);
-    p.ksplit[j] = (int)((slabs[j] + p.kspw[j] - 1) / p.kspw[j]);
+    if (!want[j]) {  // one option, for each kernel, of no tiles
+      opt[j][num[j]++] = Option{0, 1, 1, 0, 0.0f, 0.0f, 0.0f};
+      opt[j][num[j]++] = Option{2, 1, 1, 0, 0.0f, 0.0f, 0.0f};
+      continue;
+    }
+    for (int c = 0; c < 3; ++c) {
+      const Config& C = kConfigs[c];
+      const int64_t tiles = ((rows[j] + C.ti - 1) / C.ti) * ((k + C.tj - 1) / C.tj);
+      if ((c == 0 && tiles > 16 * kPlanCus) || (c == 2 && tiles < kPlanCus / 16)) continue;
+      for (const int p : kParts) {
+        if (p > 1 && (slabs[j] < p * kMinPart || tiles * p > 8 * kPlanCus)) break;
+        Option o;
+        o.cfg = c;
+        o.kspw = (int)((slabs[j] + p - 1) / p);
+        o.ksplit = (int)((slabs[j] + o.kspw - 1) / o.kspw);
+        o.count = tiles * o.ksplit;
+        const float put = j == 1 || o.ksplit > 1 ? C.put32 : C.put16;
+        o.us = o.kspw * C.slab + put;
+        o.alone = o.kspw * C.alone + put;
+        o.finish = o.ksplit > 1 ? 4.0f * rows[j] * k * (o.ksplit + 1) / kBytesPerUs : 0.0f;
+        opt[j][num[j]++] = o;
+      }
+    }
   }
-  return p;
+  const Option *best0 = nullptr, *best1 = nullptr;
+  float best = 0.0f;
+  for (int x = 0; x < num[0]; ++x)
+    for (int y = 0; y < num[1]; ++y) {
+      const Option &a = opt[0][x], &b = opt[1][y];
+      if ((a.cfg == 2) != (b.cfg == 2)) continue;
+      const float finish = a.finish + b.finish > 0.0f ? kFinishUs + a.finish + b.finish : 0.0f;
+      // what no order of the tiles can beat
+      const float least = std::max(std::max(a.alone, b.alone), (a.count * a.us + b.count * b.us) / kPlanCus);
+      if (best0 && least + finish >= best) continue;
+      const float us = finish + std::max(least, a.us >= b.us ? makespan(a.count, a.us, b.count, b.us)
+                                                             : makespan(b.count, b.us, a.count, a.us));
+      if (best0 && us >= best) continue;
+      best = us;
+      best0 = &a;
+      best1 = &b;
+    }
+  return Plan{{best0->cfg, best1->cfg}, {best0->ksplit, best1->ksplit}, {best0->kspw, best1->kspw},
+              best0->us >= best1->us ? 0 : 1};  // the longer tiles first
 }
 
 struct WsLayout {
+  Plan plan;
   size_t dys, dyt, dbp, xt, ut, part[2], total;
 };
 
 WsLayout layout(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
   WsLayout L = {};
-  const Plan p = plan_backward(m, n, k, dx, dw);
+  const Plan p = L.plan = plan_backward(m, n, k, dx, dw);
   auto take = [&](size_t& off, bool want, int64_t bytes) {
     off = L.total;
     if (want) L.total = align256(L.total + (size_t)bytes);
@@ -627,21 +715,19 @@ WsLayout layout(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
   return L;
 }
 
-template <int TI, int TJ, int WI, int WJ, int NST, int NSTC>
+template <bool BIG>
 hipError_t launch_gemm(const GemmArgs& a, int64_t wgs, hipStream_t s) {
-  constexpr size_t lds = std::max(NST * stage_bytes(TI, TJ, false), NSTC * stage_bytes(TI, TJ, true));
-  if (lds > 64 * 1024) {  // the attribute is needed above 64 KB; once per device
-    static std::atomic<bool> done[kMaxDevices];
-    const int dev = current_device_index();
-    if (!done[dev].load(std::memory_order_acquire)) {
-      const hipError_t e = hipFuncSetAttribute(
-          reinterpret_cast<const void*>(&gemm_kernel<TI, TJ, WI, WJ, NST, NSTC>),
-          hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-      if (e != hipSuccess) return e;
-      done[dev].store(true, std::memory_order_release);
-    }
+  constexpr size_t lds = BIG ? kLdsBig : kLdsSmall;
+  static_assert(lds > 64 * 1024, "the attribute is needed above 64 KB");
+  static std::atomic<bool> done[kMaxDevices];  // once per device
+  const int dev = current_device_index();
+  if (!done[dev].load(std::memory_order_acquire)) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gemm_kernel<BIG>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    done[dev].store(true, std::memory_order_release);
   }
-  gemm_kernel<TI, TJ, WI, WJ, NST, NSTC><<<(unsigned)wgs, 64 * WI * WJ, lds, s>>>(a);
+  gemm_kernel<BIG><<<(unsigned)wgs, BIG ? 512 : 256, lds, s>>>(a);
   return hipGetLastError();
 }
 
@@ -651,10 +737,11 @@ size_t backward_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
   return layout(m, n, k, dx, dw).total;
 }
 
-hipError_t launch_backward(const BackwardArgs& b, char* ws, hipStream_t s) {
+hipError_t launch_backward(const BackwardArgs& b, char* ws, size_t ws_bytes, hipStream_t s) {
   const bool dx = b.dx != nullptr, dw = b.dw != nullptr;
-  const Plan p = plan_backward(b.m, b.n, b.k, dx, dw);
   const WsLayout L = layout(b.m, b.n, b.k, dx, dw);
+  const Plan& p = L.plan;
+  if (ws_bytes < L.total) return hipErrorInvalidValue;
   const int64_t ms = slabs_of(b.m), ns = slabs_of(b.n);
 
   PrepArgs pa = {};
@@ -684,20 +771,23 @@ hipError_t launch_backward(const BackwardArgs& b, char* ws, hipStream_t s) {
   GemmArgs g = {};
   const int64_t rows[2] = {b.m, b.n}, slabs[2] = {ns, ms};
   const bool want[2] = {dx, dw};
+  const bool big = p.cfg[0] == 2;
   int64_t grid = 0, finish[2] = {0, 0};
-  for (int j = 0; j < 2; ++j) {
-    GemmJob& J = g.j[j];
-    g.begin[j] = (int32_t)grid;
+  for (int o = 0; o < 2; ++o) {
+    const int j = o == 0 ? p.order : 1 - p.order;  // 0: dx, 1: dw
+    GemmJob& J = g.j[o];
+    g.begin[o] = (int32_t)grid;
     if (!want[j]) continue;
     J.a = reinterpret_cast<const uint8_t*>(ws + (j ? L.dyt : L.dys));
     J.b = reinterpret_cast<const uint8_t*>(ws + (j ? L.xt : L.ut));
     J.ra = (int32_t)rows[j];
     J.rb = (int32_t)b.k;
     J.slabs = (int32_t)slabs[j];
-    J.tiles_i = (int32_t)((rows[j] + kConfigs[p.cfg].ti - 1) / kConfigs[p.cfg].ti);
-    J.tiles_j = (int32_t)((b.k + kConfigs[p.cfg].tj - 1) / kConfigs[p.cfg].tj);
+    J.tiles_i = (int32_t)((rows[j] + kConfigs[p.cfg[j]].ti - 1) / kConfigs[p.cfg[j]].ti);
+    J.tiles_j = (int32_t)((b.k + kConfigs[p.cfg[j]].tj - 1) / kConfigs[p.cfg[j]].tj);
     J.ksplit = p.ksplit[j];
     J.kspw = p.kspw[j];
+    J.cfg = p.cfg[j];
     J.codes = j == 0;
     J.part = reinterpret_cast<float*>(ws + L.part[j]);
     J.cf = j ? b.dw : nullptr;
@@ -705,10 +795,9 @@ hipError_t launch_backward(const BackwardArgs& b, char* ws, hipStream_t s) {
     J.cb = j ? nullptr : b.dx;
     J.scale = b.w_scale;
     J.res = j ? nullptr : b.residual;
-    if (J.ksplit > 1) finish[j] = rows[j] * (b.k / 4);
+    if (J.ksplit > 1) finish[o] = rows[j] * (b.k / 4);
     grid += round_up((int64_t)J.tiles_i * J.tiles_j * J.ksplit, 8);
   }
-  if (!dw) g.begin[1] = (int32_t)grid;
   g.begin[2] = (int32_t)grid;
   if (b.dbias) {
     g.dbp = pa.dbp;
@@ -716,12 +805,10 @@ hipError_t launch_backward(const BackwardArgs& b, char* ws, hipStream_t s) {
     g.n = (int32_t)b.n;
     g.db = b.dbias;
     g.accumulate = b.accumulate ? 1 : 0;
-    const int threads = p.cfg == 2 ? 512 : 256;
+    const int threads = big ? 512 : 256;
     grid += (b.n + threads - 1) / threads;
   }
-  if (p.cfg == 2) e = launch_gemm<256, 256, 2, 4, 2, 4>(g, grid, s);
-  else if (p.cfg == 1) e = launch_gemm<128, 128, 2, 2, 2, 4>(g, grid, s);
-  else e = launch_gemm<64, 64, 2, 2, 4, 7>(g, grid, s);
+  e = big ? launch_gemm<true>(g, grid, s) : launch_gemm<false>(g, grid, s);
   const int64_t total = finish[0] + finish[1];
   if (e != hipSuccess || total == 0) return e;
   gemm_finish_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(g, finish[0], total);

@@ -257,7 +257,7 @@ bl_status bitlinear_backward(int64_t m, int64_t n, int64_t k, const uint16_t* dy
   a.dw = dw;
   a.dbias = dbias;
   a.accumulate = accumulate != 0;
-  return launch_backward(a, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)) ==
+  return launch_backward(a, static_cast<char*>(workspace), need, static_cast<hipStream_t>(stream)) ==
                  hipSuccess
              ? BL_OK
              : BL_EHIP;

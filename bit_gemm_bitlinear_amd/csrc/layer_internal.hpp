@@ -63,7 +63,7 @@ struct BackwardArgs {
   bool accumulate;
 };
 size_t backward_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw);
-hipError_t launch_backward(const BackwardArgs& a, char* ws, hipStream_t s);
+hipError_t launch_backward(const BackwardArgs& a, char* ws, size_t ws_bytes, hipStream_t s);
 
 // ---- 4-bit weights (w4.hip) ----
 hipError_t launch_w4_pack(const float* w, int64_t n, int64_t k, int group, uint8_t* codes,
