@@ -462,16 +462,30 @@ class BitLinear:
 WEIGHT_NONE, WEIGHT_BF16, WEIGHT_F32 = 0, 1, 2  # BL_WEIGHT_*
 
 
+# The current stream's handle of a device index, and the current device: what
+# torch.cuda.current_stream and current_device look up, without the objects
+# around it (1.9 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(fn, args, device: torch.device, stream=None) -> None:
     """Calls an entry point on `device`'s current stream (or the given one),
     with that device current: a kernel goes to the current device."""
     if torch.cuda.current_device() == device.index:
-        s = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
-        _check(fn(*args, s))
-        return
-    with torch.cuda.device(device):
-        s = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
-        _check(fn(*args, s))
+        status = fn(*args, _raw_stream(device.index) if stream is None else stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device.index) if stream is None else stream)
+    if status:
+        raise BitLinearError(status)
+
+
+def _need(t, dtype, name, shape, device):
+    """_require of a tensor of a known shape and device, quickly when it fits."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.device == device and t.is_contiguous()):
+        _require(t, dtype, len(shape), name, shape, device)
 
 
 def _norm_weight(weight, k, device):
@@ -594,12 +608,14 @@ def restore_activations(q: torch.Tensor, x_scale: torch.Tensor,
     """The activations that int8 codes [M, K] and scales [M] stand for:
     bf16(q / x_scale)."""
     _require(q, torch.int8, 2, "q")
-    m, k = q.shape
-    _require(x_scale, torch.float32, 1, "x_scale", shape=(m,), device=q.device)
+    shape, dev = q.shape, q.device
+    _need(x_scale, torch.float32, "x_scale", shape[:1], dev)
     if out is None:
-        out = torch.empty((m, k), dtype=torch.bfloat16, device=q.device)
-    _require(out, torch.bfloat16, 2, "out", shape=(m, k), device=q.device)
-    _launch(_lib.bitlinear_restore_activations, (m, k, _ptr(q), _ptr(x_scale), _ptr(out)), q.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, torch.bfloat16, "out", shape, dev)
+    _launch(_lib.bitlinear_restore_activations,
+            (*shape, q.data_ptr(), x_scale.data_ptr(), out.data_ptr()), dev)
     return out
 
 

@@ -147,6 +147,7 @@ bl_status bitlinear_rms_norm_quant(int64_t m, int64_t k, const uint16_t* x,
   a.k = (int32_t)k;
   a.m = m;
   a.eps = eps;
+  a.inv_k = 1.0 / (double)k;
   a.h = h;
   a.rstd = rstd;
   a.n = n;

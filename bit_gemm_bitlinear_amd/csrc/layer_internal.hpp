@@ -16,7 +16,7 @@ struct NormArgs {
   int32_t wtype;        // BL_WEIGHT_*
   int32_t k;
   int64_t m;
-  double eps;
+  double eps, inv_k;  // inv_k: 1 / k
   uint16_t* h;    // [m][k] bf16, or nullptr
   float* rstd;    // [m], or nullptr
   uint16_t* n;    // [m][k] bf16, or nullptr

@@ -23,108 +23,123 @@ namespace bl {
 
 namespace {
 
-constexpr int kT = 256;  // threads of a row's workgroup
-constexpr int kWaves = kT / 64;
-
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// VEC (4 or 8) consecutive bf16 values as VEC / 2 dwords.
-template <int VEC>
+typedef int32_t v2i __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+// K % 4 == 0: rows start at any multiple of 8 bytes (4 for int8 codes).
+typedef v4i v4i_8 __attribute__((aligned(8)));
+typedef v2i v2i_4 __attribute__((aligned(4)));
+typedef v4i v4i_4 __attribute__((aligned(4)));
+
+// Eight consecutive bf16 values as four dwords.  A row's last piece may hold
+// four (`n` values; the others are zeros and are not stored).
 struct Piece {
-  uint32_t w[VEC / 2];
+  uint32_t w[4];
 };
 
-template <int VEC>
-__device__ __forceinline__ Piece<VEC> load_bf16(const uint16_t* p) {
-  Piece<VEC> r;
-  if constexpr (VEC == 8) {
-    const v4i v = *G(reinterpret_cast<const v4i*>(p));
+__device__ __forceinline__ Piece load_bf16(const uint16_t* p, int n) {
+  Piece r;
+  if (n >= 8) {
+    const v4i v = *G(reinterpret_cast<const v4i_8*>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i) r.w[i] = (uint32_t)v[i];
   } else {
-    typedef int32_t v2i __attribute__((ext_vector_type(2)));
-    const v2i v = *G(reinterpret_cast<const v2i*>(p));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) r.w[i] = (uint32_t)v[i];
+    const v2i v = n > 0 ? *G(reinterpret_cast<const v2i*>(p)) : v2i{0, 0};
+    r.w[0] = (uint32_t)v.x;
+    r.w[1] = (uint32_t)v.y;
+    r.w[2] = r.w[3] = 0u;
   }
   return r;
 }
 
-template <int VEC>
-__device__ __forceinline__ void store_bf16(uint16_t* p, const Piece<VEC>& r) {
-  if constexpr (VEC == 8) {
-    *G(reinterpret_cast<v4i*>(p)) =
-        v4i{(int32_t)r.w[0], (int32_t)r.w[1], (int32_t)r.w[2], (int32_t)r.w[3]};
-  } else {
-    typedef int32_t v2i __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void store_bf16(uint16_t* p, int n, const Piece& r) {
+  if (n >= 8)
+    *G(reinterpret_cast<v4i_8*>(p)) = v4i{(int32_t)r.w[0], (int32_t)r.w[1], (int32_t)r.w[2], (int32_t)r.w[3]};
+  else if (n > 0)
     *G(reinterpret_cast<v2i*>(p)) = v2i{(int32_t)r.w[0], (int32_t)r.w[1]};
-  }
 }
 
-// VEC weights at column e as fp32 (ones without a weight).
-template <int VEC>
-__device__ __forceinline__ void load_weight(const void* w, int wtype, int e, float (&o)[VEC]) {
+// Eight weights at column e as fp32 (ones without a weight).
+__device__ __forceinline__ void load_weight(const void* w, int wtype, int e, int n, float (&o)[8]) {
   if (wtype == BL_WEIGHT_BF16) {
-    const Piece<VEC> p = load_bf16<VEC>(static_cast<const uint16_t*>(w) + e);
+    const Piece p = load_bf16(static_cast<const uint16_t*>(w) + e, n);
 #pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       o[2 * i] = lo_f(p.w[i]);
       o[2 * i + 1] = hi_f(p.w[i]);
     }
   } else if (wtype == BL_WEIGHT_F32) {
-    typedef float v4f __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-      const v4f v = *G(reinterpret_cast<const v4f*>(static_cast<const float*>(w) + e + i));
+    for (int i = 0; i < 8; i += 4) {
+      const v4f v = i < n ? *G(reinterpret_cast<const v4f*>(static_cast<const float*>(w) + e + i)) : v4f{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i + j] = v[j];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) o[i] = 1.0f;
+    for (int i = 0; i < 8; ++i) o[i] = 1.0f;
   }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* red) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+// Reductions over a wave: exchanges within 16 lanes (quad swaps, rotations of
+// a row), then the four rows' values by lane reads.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)b) | ((uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+__device__ __forceinline__ uint32_t read_lane(uint32_t v, int l) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, l);
+}
+__device__ __forceinline__ float read_lane(float v, int l) { return __uint_as_float(read_lane(__float_as_uint(v), l)); }
+__device__ __forceinline__ double read_lane(double v, int l) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)read_lane((uint32_t)b, l) | ((uint64_t)read_lane((uint32_t)(b >> 32), l) << 32));
+}
+
+template <typename V, typename Op>
+__device__ __forceinline__ V wave_reduce(V v, Op op) {
+  v = op(v, dpp<0xB1>(v));   // quad: lanes 1 0 3 2
+  v = op(v, dpp<0x4E>(v));   // 2 3 0 1
+  v = op(v, dpp<0x124>(v));  // row rotated by 4
+  v = op(v, dpp<0x128>(v));  // by 8
+  return op(op(read_lane(v, 0), read_lane(v, 16)), op(read_lane(v, 32), read_lane(v, 48)));
+}
+
+// The same over a workgroup of up to 16 waves.
+template <typename V, typename Op>
+__device__ __forceinline__ V row_reduce(V v, V* red, Op op) {
+  v = wave_reduce(v, op);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  double t = red[0];
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i) t += red[i];
-  return t;
+  v = red[0];
+  for (int i = 1; i < waves; ++i) v = op(v, red[i]);
+  return v;
+}
+template <typename V>
+__device__ __forceinline__ V row_sum(V v, V* red) {
+  return row_reduce(v, red, [](V a, V b) { return a + b; });
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+  return row_reduce(v, red, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  uint32_t t = red[0];
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i) t = max(t, red[i]);
-  return t;
-}
-
-// h of one piece: x, or the bf16 sum of x and the residual.
-template <int VEC>
-__device__ __forceinline__ Piece<VEC> load_h(const uint16_t* x, const uint16_t* r, int e) {
-  Piece<VEC> p = load_bf16<VEC>(x + e);
-  if (r) {
-    const Piece<VEC> b = load_bf16<VEC>(r + e);
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) p.w[i] = add_bf16x2(p.w[i], b.w[i]);
-  }
-  return p;
-}
-
-template <int VEC>
-__device__ __forceinline__ double square_sum(const Piece<VEC>& p) {
+__device__ __forceinline__ double square_sum(const Piece& p) {
   double s = 0.0;
 #pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const double a = (double)lo_f(p.w[i]), b = (double)hi_f(p.w[i]);
     s = __builtin_fma(a, a, s);
     s = __builtin_fma(b, b, s);
@@ -134,240 +149,285 @@ __device__ __forceinline__ double square_sum(const Piece<VEC>& p) {
 
 // n = bf16((h * rstd) * w), two fp32 products each rounded (one without a
 // weight: multiplying by 1 changes nothing).
-template <int VEC>
-__device__ __forceinline__ Piece<VEC> normed(const Piece<VEC>& h, float rstd, const float (&w)[VEC]) {
-  Piece<VEC> o;
+__device__ __forceinline__ Piece normed(const Piece& h, float rstd, const float (&w)[8]) {
+  Piece o;
 #pragma unroll
-  for (int i = 0; i < VEC / 2; ++i)
+  for (int i = 0; i < 4; ++i)
     o.w[i] = pack_bf16x2((lo_f(h.w[i]) * rstd) * w[2 * i], (hi_f(h.w[i]) * rstd) * w[2 * i + 1]);
   return o;
 }
 
-template <int VEC>
-__device__ __forceinline__ uint32_t absmax_bits(const Piece<VEC>& p) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int i = 0; i < VEC / 2; i += 2) a = max(a, absmax_bits4(p.w[i], p.w[i + 1]));
-  return a;
+__device__ __forceinline__ uint32_t absmax_bits(const Piece& p) {
+  return max(absmax_bits4(p.w[0], p.w[1]), absmax_bits4(p.w[2], p.w[3]));
 }
 
-template <int VEC>
-__device__ __forceinline__ void store_codes(int8_t* q, const Piece<VEC>& n, float s) {
-  uint32_t d[VEC / 4];
+__device__ __forceinline__ void store_codes(int8_t* q, int n, const Piece& v, float s) {
+  uint32_t d[2];
 #pragma unroll
-  for (int i = 0; i < VEC / 4; ++i)
-    d[i] = ((uint32_t)quant_i8(lo_f(n.w[2 * i]), s) & 0xFFu) |
-           (((uint32_t)quant_i8(hi_f(n.w[2 * i]), s) & 0xFFu) << 8) |
-           (((uint32_t)quant_i8(lo_f(n.w[2 * i + 1]), s) & 0xFFu) << 16) |
-           (((uint32_t)quant_i8(hi_f(n.w[2 * i + 1]), s) & 0xFFu) << 24);
-  if constexpr (VEC == 8) {
-    typedef int32_t v2i __attribute__((ext_vector_type(2)));
-    *G(reinterpret_cast<v2i*>(q)) = v2i{(int32_t)d[0], (int32_t)d[1]};
-  } else {
+  for (int i = 0; i < 2; ++i)
+    d[i] = ((uint32_t)quant_i8(lo_f(v.w[2 * i]), s) & 0xFFu) |
+           (((uint32_t)quant_i8(hi_f(v.w[2 * i]), s) & 0xFFu) << 8) |
+           (((uint32_t)quant_i8(lo_f(v.w[2 * i + 1]), s) & 0xFFu) << 16) |
+           (((uint32_t)quant_i8(hi_f(v.w[2 * i + 1]), s) & 0xFFu) << 24);
+  if (n >= 8)
+    *G(reinterpret_cast<v2i_4*>(q)) = v2i{(int32_t)d[0], (int32_t)d[1]};
+  else if (n > 0)
     *G(reinterpret_cast<uint32_t*>(q)) = d[0];
-  }
 }
 
-__device__ __forceinline__ float rstd_of(double sum, int k, double eps) {
-  return (float)(1.0 / sqrt(sum / (double)k + eps));
+// fp32(1 / sqrt(sum / k + eps)) from the hardware's fp64 estimate y and one
+// third-order step: with r = 1 - x y^2, 1 / sqrt(x) = y (1 + r / 2 + 3 r^2 / 8 + O(r^3)),
+// exact to fp64 rounding.  (Square root and divisions proper are some 80 fp64
+// instructions in every wave: 2.7 us of the 12 us of 2048 rows of 2560.)
+__device__ __forceinline__ float rstd_of(double sum, double inv_k, double eps) {
+  const double x = __builtin_fma(sum, inv_k, eps);
+  const double y = __builtin_amdgcn_rsq(x);
+  const double r = __builtin_fma(-x * y, y, 1.0);
+  return (float)__builtin_fma(y * r, __builtin_fma(r, 0.375, 0.5), y);
 }
 
 // Rows go over two grid dimensions: one alone holds 2^32 threads.
 constexpr int64_t kGridX = 1 << 20;
 __device__ __forceinline__ int64_t row_index() { return (int64_t)blockIdx.y * kGridX + blockIdx.x; }
 
-// One workgroup per row; the row stays in registers (NCH pieces a thread)
-// between the sum, the maximum and the codes: x and the residual are read
-// once, everything else written once.
-template <int VEC, int NCH>
-__global__ __launch_bounds__(kT) void norm_quant_kernel(const NormArgs A) {
-  __shared__ double red[kWaves];
-  __shared__ uint32_t redu[kWaves];
-  const int tid = threadIdx.x, k = A.k;
+// A workgroup a row, of as many threads as it has pieces, NCH a thread.  The
+// row stays in registers between the sum, the maximum and the codes: x and
+// the residual are read once, everything else written once.  The weights are
+// loaded with them where the registers allow: the norm then does not wait for
+// memory again after the sum.
+constexpr int kMaxT = 1024;
+template <int NCH>
+__global__ __launch_bounds__(kMaxT) void norm_quant_kernel(const NormArgs A) {
+  __shared__ double red[kMaxT / 64];
+  __shared__ uint32_t redu[kMaxT / 64];
+  const int tid = threadIdx.x, T = blockDim.x, k = A.k;
   const int64_t m = row_index();
   if (m >= A.m) return;
   const int64_t row = m * k;
-  const uint16_t* x = A.x + row;
-  const uint16_t* r = A.res ? A.res + row : nullptr;
-  Piece<VEC> h[NCH];
+  constexpr bool HOLD = NCH <= 2;
+  Piece h[NCH];
+  float w[HOLD ? NCH : 1][8];
+#pragma unroll
+  for (int b = 0; b < NCH; ++b) {
+    const int e = 8 * (tid + T * b);
+    h[b] = load_bf16(A.x + row + e, k - e);
+  }
+  Piece r[NCH];
+  if (A.res) {
+#pragma unroll
+    for (int b = 0; b < NCH; ++b) {
+      const int e = 8 * (tid + T * b);
+      r[b] = load_bf16(A.res + row + e, k - e);
+    }
+  }
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int b = 0; b < NCH; ++b) {
+      const int e = 8 * (tid + T * b);
+      load_weight(A.weight, A.wtype, e, k - e, w[b]);
+    }
+  }
+  if (A.res) {
+#pragma unroll
+    for (int b = 0; b < NCH; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[b].w[i] = add_bf16x2(h[b].w[i], r[b].w[i]);
+  }
   double ss = 0.0;
 #pragma unroll
   for (int b = 0; b < NCH; ++b) {
-    const int e = VEC * (tid + kT * b);
-    if (e < k) {
-      h[b] = load_h<VEC>(x, r, e);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC / 2; ++i) h[b].w[i] = 0u;
-    }
-  }
-#pragma unroll
-  for (int b = 0; b < NCH; ++b) {
-    const int e = VEC * (tid + kT * b);
+    const int e = 8 * (tid + T * b);
     ss += square_sum(h[b]);
-    if (A.h && e < k) store_bf16<VEC>(A.h + row + e, h[b]);
+    if (A.h) store_bf16(A.h + row + e, k - e, h[b]);
   }
-  const float rstd = rstd_of(block_sum(ss, red), k, A.eps);
+  const float rstd = rstd_of(row_sum(ss, red), A.inv_k, A.eps);
   if (A.rstd && tid == 0) A.rstd[m] = rstd;
   uint32_t amax = 0;
 #pragma unroll
   for (int b = 0; b < NCH; ++b) {
-    const int e = VEC * (tid + kT * b);
-    if (e < k) {
-      float w[VEC];
-      load_weight<VEC>(A.weight, A.wtype, e, w);
-      h[b] = normed<VEC>(h[b], rstd, w);
-      if (A.n) store_bf16<VEC>(A.n + row + e, h[b]);
-      amax = max(amax, absmax_bits<VEC>(h[b]));
+    const int e = 8 * (tid + T * b);
+    if constexpr (HOLD) {
+      h[b] = normed(h[b], rstd, w[b]);
+    } else {
+      load_weight(A.weight, A.wtype, e, k - e, w[0]);
+      h[b] = normed(h[b], rstd, w[0]);
     }
+    if (A.n) store_bf16(A.n + row + e, k - e, h[b]);
+    amax = max(amax, absmax_bits(h[b]));
   }
   if (!A.q) return;
-  const float s = act_scale(bf16_to_f32(block_max(amax, redu)));
+  const float s = act_scale(bf16_to_f32(row_max(amax, redu)));
   if (tid == 0) A.x_scale[m] = s;
 #pragma unroll
   for (int b = 0; b < NCH; ++b) {
-    const int e = VEC * (tid + kT * b);
-    if (e < k) store_codes<VEC>(A.q + row + e, h[b], s);
+    const int e = 8 * (tid + T * b);
+    store_codes(A.q + row + e, k - e, h[b], s);
   }
 }
 
 // Rows longer than the registers hold: three passes over the row (the later
 // ones read h where it was written, else add again).
-__global__ __launch_bounds__(kT) void norm_quant_long_kernel(const NormArgs A) {
-  __shared__ double red[kWaves];
-  __shared__ uint32_t redu[kWaves];
+constexpr int kLongT = 1024;
+__global__ __launch_bounds__(kLongT) void norm_quant_long_kernel(const NormArgs A) {
+  __shared__ double red[kLongT / 64];
+  __shared__ uint32_t redu[kLongT / 64];
   const int tid = threadIdx.x, k = A.k;
   const int64_t m = row_index();
   if (m >= A.m) return;
   const int64_t row = m * k;
   const uint16_t* x = A.x + row;
   const uint16_t* r = A.res ? A.res + row : nullptr;
+  auto load_h = [&](int e) {
+    Piece p = load_bf16(x + e, k - e);
+    if (r) {
+      const Piece b = load_bf16(r + e, k - e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p.w[i] = add_bf16x2(p.w[i], b.w[i]);
+    }
+    return p;
+  };
   double ss = 0.0;
-  for (int e = 4 * tid; e < k; e += 4 * kT) {
-    const Piece<4> h = load_h<4>(x, r, e);
+  for (int e = 8 * tid; e < k; e += 8 * kLongT) {
+    const Piece h = load_h(e);
     ss += square_sum(h);
-    if (A.h) store_bf16<4>(A.h + row + e, h);
+    if (A.h) store_bf16(A.h + row + e, k - e, h);
   }
   if (A.h) {  // each thread reads back what it wrote itself
     x = A.h + row;
     r = nullptr;
   }
-  const float rstd = rstd_of(block_sum(ss, red), k, A.eps);
+  const float rstd = rstd_of(row_sum(ss, red), A.inv_k, A.eps);
   if (A.rstd && tid == 0) A.rstd[m] = rstd;
   uint32_t amax = 0;
-  for (int e = 4 * tid; e < k; e += 4 * kT) {
-    float w[4];
-    load_weight<4>(A.weight, A.wtype, e, w);
-    const Piece<4> n = normed<4>(load_h<4>(x, r, e), rstd, w);
-    if (A.n) store_bf16<4>(A.n + row + e, n);
-    amax = max(amax, absmax_bits<4>(n));
+  for (int e = 8 * tid; e < k; e += 8 * kLongT) {
+    float w[8];
+    load_weight(A.weight, A.wtype, e, k - e, w);
+    const Piece n = normed(load_h(e), rstd, w);
+    if (A.n) store_bf16(A.n + row + e, k - e, n);
+    amax = max(amax, absmax_bits(n));
   }
   if (!A.q) return;
-  const float s = act_scale(bf16_to_f32(block_max(amax, redu)));
+  const float s = act_scale(bf16_to_f32(row_max(amax, redu)));
   if (tid == 0) A.x_scale[m] = s;
-  for (int e = 4 * tid; e < k; e += 4 * kT) {
-    float w[4];
-    load_weight<4>(A.weight, A.wtype, e, w);
-    store_codes<4>(A.q + row + e, normed<4>(load_h<4>(x, r, e), rstd, w), s);
+  for (int e = 8 * tid; e < k; e += 8 * kLongT) {
+    float w[8];
+    load_weight(A.weight, A.wtype, e, k - e, w);
+    store_codes(A.q + row + e, k - e, normed(load_h(e), rstd, w), s);
   }
 }
 
 // ---- gradient ----
+//
+//   g = dn * w, z = h * rstd, dx = bf16(rstd * (g - z * mean(g * z)) + dh),
+//   dw = sum over the rows of dn * z
 
-__device__ __forceinline__ float block_sum_f(float v, float* red) {
+__device__ __forceinline__ Piece dx_piece(const Piece& dn, const Piece& h, const Piece& dh,
+                                          const float (&w)[8], float rstd, float c) {
+  Piece o;
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float t = red[0];
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i) t += red[i];
-  return t;
+  for (int i = 0; i < 4; ++i) {
+    const float z0 = lo_f(h.w[i]) * rstd, z1 = hi_f(h.w[i]) * rstd;
+    const float g0 = lo_f(dn.w[i]) * w[2 * i], g1 = hi_f(dn.w[i]) * w[2 * i + 1];
+    o.w[i] = pack_bf16x2(__builtin_fmaf(rstd, g0 - z0 * c, lo_f(dh.w[i])),
+                         __builtin_fmaf(rstd, g1 - z1 * c, hi_f(dh.w[i])));
+  }
+  return o;
 }
 
-// Each workgroup takes every gridDim.x-th row and each thread fixed columns,
-// so the thread keeps its columns' sums for dweight in registers over the
-// rows; the partial rows of all workgroups are added by a second kernel, in a
-// fixed order.
-template <int VEC, int NCH>
-__global__ __launch_bounds__(kT) void norm_backward_kernel(const NormBwdArgs A) {
-  __shared__ float red[2][kWaves];
-  const int tid = threadIdx.x, k = A.k;
+// A row as the kernel holds it.
+template <int NCH>
+struct BwdRow {
+  Piece dn[NCH], h[NCH], dh[NCH];
+  float rstd;
+};
+
+// Threads and pieces as in the forward kernel; a workgroup takes rows a whole
+// grid apart, the next one loading while it works on the current, and each
+// thread fixed columns, so that it keeps its columns' sums for dweight in
+// registers over the rows.  The partial rows of the workgroups are added by a
+// second kernel, in a fixed order.
+constexpr int kBwdT = 512;
+template <int NCH>
+__global__ __launch_bounds__(kBwdT) void norm_backward_kernel(const NormBwdArgs A) {
+  __shared__ float red[2][kBwdT / 64];
+  const int tid = threadIdx.x, T = blockDim.x, k = A.k;
   const float inv_k = 1.0f / (float)k;
-  float dw[NCH][VEC], w[NCH][VEC];
+  float dw[NCH][8], w[NCH][8];
 #pragma unroll
   for (int b = 0; b < NCH; ++b) {
-    const int e = VEC * (tid + kT * b);
+    const int e = 8 * (tid + T * b);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) dw[b][i] = w[b][i] = 0.0f;
-    if (e < k) load_weight<VEC>(A.weight, A.wtype, e, w[b]);
+    for (int i = 0; i < 8; ++i) dw[b][i] = 0.0f;
+    load_weight(A.weight, A.wtype, e, k - e, w[b]);
   }
-  int it = 0;
-  for (int64_t m = blockIdx.x; m < A.m; m += gridDim.x, it ^= 1) {
+  auto load = [&](BwdRow<NCH>& r, int64_t m) {
     const int64_t row = m * k;
-    Piece<VEC> dn[NCH], h[NCH], dh[NCH];
 #pragma unroll
     for (int b = 0; b < NCH; ++b) {
-      const int e = VEC * (tid + kT * b);
-      if (e < k) {
-        dn[b] = load_bf16<VEC>(A.dn + row + e);
-        h[b] = load_bf16<VEC>(A.h + row + e);
-      } else {
+      const int e = 8 * (tid + T * b);
+      r.dn[b] = load_bf16(A.dn + row + e, k - e);
+      r.h[b] = load_bf16(A.h + row + e, k - e);
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) dn[b].w[i] = h[b].w[i] = 0u;
-      }
+      for (int i = 0; i < 4; ++i) r.dh[b].w[i] = 0u;
+      if (A.dh) r.dh[b] = load_bf16(A.dh + row + e, k - e);
     }
-#pragma unroll
-    for (int b = 0; b < NCH; ++b) {
-      const int e = VEC * (tid + kT * b);
-#pragma unroll
-      for (int i = 0; i < VEC / 2; ++i) dh[b].w[i] = 0u;
-      if (A.dh && e < k) dh[b] = load_bf16<VEC>(A.dh + row + e);
-    }
-    const float rstd = A.rstd[m];
+    r.rstd = *G(A.rstd + m);
+  };
+  int it = 0;
+  auto work = [&](const BwdRow<NCH>& r, int64_t m) {
     float dot = 0.0f;
 #pragma unroll
     for (int b = 0; b < NCH; ++b)
 #pragma unroll
-      for (int i = 0; i < VEC / 2; ++i) {
-        const float z0 = lo_f(h[b].w[i]) * rstd, z1 = hi_f(h[b].w[i]) * rstd;
-        const float d0 = lo_f(dn[b].w[i]), d1 = hi_f(dn[b].w[i]);
-        const float t0 = d0 * z0, t1 = d1 * z1;
+      for (int i = 0; i < 4; ++i) {
+        const float t0 = lo_f(r.dn[b].w[i]) * (lo_f(r.h[b].w[i]) * r.rstd);
+        const float t1 = hi_f(r.dn[b].w[i]) * (hi_f(r.h[b].w[i]) * r.rstd);
         dw[b][2 * i] += t0;
         dw[b][2 * i + 1] += t1;
         dot = __builtin_fmaf(t0, w[b][2 * i], dot);
         dot = __builtin_fmaf(t1, w[b][2 * i + 1], dot);
       }
-    const float c = block_sum_f(dot, red[it]) * inv_k;
+    const float c = row_sum(dot, red[it]) * inv_k;
+    it ^= 1;
 #pragma unroll
     for (int b = 0; b < NCH; ++b) {
-      const int e = VEC * (tid + kT * b);
-      if (e >= k) continue;
-      Piece<VEC> o;
-#pragma unroll
-      for (int i = 0; i < VEC / 2; ++i) {
-        const float z0 = lo_f(h[b].w[i]) * rstd, z1 = hi_f(h[b].w[i]) * rstd;
-        const float g0 = lo_f(dn[b].w[i]) * w[b][2 * i], g1 = hi_f(dn[b].w[i]) * w[b][2 * i + 1];
-        o.w[i] = pack_bf16x2(__builtin_fmaf(rstd, g0 - z0 * c, lo_f(dh[b].w[i])),
-                             __builtin_fmaf(rstd, g1 - z1 * c, hi_f(dh[b].w[i])));
-      }
-      store_bf16<VEC>(A.dx + row + e, o);
+      const int e = 8 * (tid + T * b);
+      store_bf16(A.dx + m * k + e, k - e, dx_piece(r.dn[b], r.h[b], r.dh[b], w[b], r.rstd, c));
+    }
+  };
+  const int64_t step = gridDim.x;
+  if constexpr (NCH <= 2) {
+    BwdRow<NCH> p, q;
+    load(p, blockIdx.x);
+    for (int64_t m = blockIdx.x; m < A.m; m += 2 * step) {
+      if (m + step < A.m) load(q, m + step);
+      work(p, m);
+      if (m + step >= A.m) break;
+      if (m + 2 * step < A.m) load(p, m + 2 * step);
+      work(q, m + step);
+    }
+  } else {
+    BwdRow<NCH> p;
+    for (int64_t m = blockIdx.x; m < A.m; m += step) {
+      load(p, m);
+      work(p, m);
     }
   }
   if (!A.part) return;
+  float* part = A.part + (int64_t)blockIdx.x * k;
 #pragma unroll
   for (int b = 0; b < NCH; ++b) {
-    const int e = VEC * (tid + kT * b);
-    if (e >= k) continue;
+    const int e = 8 * (tid + T * b);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) *G(A.part + (int64_t)blockIdx.x * k + e + i) = dw[b][i];
+    for (int i = 0; i < 8; i += 4)
+      if (e + i < k) *G(reinterpret_cast<v4f*>(part + e + i)) = v4f{dw[b][i], dw[b][i + 1], dw[b][i + 2], dw[b][i + 3]};
   }
 }
 
 // Rows longer than the registers hold: two passes over the row, the sums for
 // dweight kept in the workgroup's partial row (each thread its own columns).
-__global__ __launch_bounds__(kT) void norm_backward_long_kernel(const NormBwdArgs A) {
-  __shared__ float red[2][kWaves];
+__global__ __launch_bounds__(kLongT) void norm_backward_long_kernel(const NormBwdArgs A) {
+  __shared__ float red[2][kLongT / 64];
   const int tid = threadIdx.x, k = A.k;
   const float inv_k = 1.0f / (float)k;
   float* part = A.part ? A.part + (int64_t)blockIdx.x * k : nullptr;
@@ -375,157 +435,129 @@ __global__ __launch_bounds__(kT) void norm_backward_long_kernel(const NormBwdArg
   for (int64_t m = blockIdx.x; m < A.m; m += gridDim.x, it ^= 1) {
     const int64_t row = m * k;
     const bool first = m < (int64_t)gridDim.x;
-    const float rstd = A.rstd[m];
+    const float rstd = *G(A.rstd + m);
     float dot = 0.0f;
-    for (int e = 4 * tid; e < k; e += 4 * kT) {
-      const Piece<4> dn = load_bf16<4>(A.dn + row + e), h = load_bf16<4>(A.h + row + e);
-      float w[4];
-      load_weight<4>(A.weight, A.wtype, e, w);
+    for (int e = 8 * tid; e < k; e += 8 * kLongT) {
+      const Piece dn = load_bf16(A.dn + row + e, k - e), h = load_bf16(A.h + row + e, k - e);
+      float w[8];
+      load_weight(A.weight, A.wtype, e, k - e, w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const float z = (i & 1 ? hi_f(h.w[i >> 1]) : lo_f(h.w[i >> 1])) * rstd;
         const float t = (i & 1 ? hi_f(dn.w[i >> 1]) : lo_f(dn.w[i >> 1])) * z;
-        if (part) *G(part + e + i) = first ? t : *G(part + e + i) + t;
+        if (part && e + i < k) *G(part + e + i) = first ? t : *G(part + e + i) + t;
         dot = __builtin_fmaf(t, w[i], dot);
       }
     }
-    const float c = block_sum_f(dot, red[it]) * inv_k;
-    for (int e = 4 * tid; e < k; e += 4 * kT) {
-      const Piece<4> dn = load_bf16<4>(A.dn + row + e), h = load_bf16<4>(A.h + row + e);
-      Piece<4> dh;
-      dh.w[0] = dh.w[1] = 0u;
-      if (A.dh) dh = load_bf16<4>(A.dh + row + e);
-      float w[4];
-      load_weight<4>(A.weight, A.wtype, e, w);
-      Piece<4> o;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float z0 = lo_f(h.w[i]) * rstd, z1 = hi_f(h.w[i]) * rstd;
-        const float g0 = lo_f(dn.w[i]) * w[2 * i], g1 = hi_f(dn.w[i]) * w[2 * i + 1];
-        o.w[i] = pack_bf16x2(__builtin_fmaf(rstd, g0 - z0 * c, lo_f(dh.w[i])),
-                             __builtin_fmaf(rstd, g1 - z1 * c, hi_f(dh.w[i])));
-      }
-      store_bf16<4>(A.dx + row + e, o);
+    const float c = row_sum(dot, red[it]) * inv_k;
+    for (int e = 8 * tid; e < k; e += 8 * kLongT) {
+      const Piece dn = load_bf16(A.dn + row + e, k - e), h = load_bf16(A.h + row + e, k - e);
+      Piece dh = {{0u, 0u, 0u, 0u}};
+      if (A.dh) dh = load_bf16(A.dh + row + e, k - e);
+      float w[8];
+      load_weight(A.weight, A.wtype, e, k - e, w);
+      store_bf16(A.dx + row + e, k - e, dx_piece(dn, h, dh, w, rstd, c));
     }
   }
 }
 
-// dweight[k] = sum over the workgroups' partial rows: 32 columns a workgroup,
-// 32 slices of the rows, joined in a fixed order.
+// dweight[k] = sum over the workgroups' partial rows: 16 columns a workgroup,
+// 64 slices of the rows, joined in a fixed order.
 __global__ __launch_bounds__(1024) void column_join_kernel(const float* __restrict__ part, int rows,
                                                            int k, float* __restrict__ out,
                                                            int accumulate) {
-  __shared__ float red[32][33];
-  const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
-  const int col = 32 * blockIdx.x + c;
+  __shared__ float red[64][17];
+  const int c = threadIdx.x & 15, s = threadIdx.x >> 4;
+  const int col = 16 * blockIdx.x + c;
   float v = 0.0f;
   if (col < k) {
 #pragma unroll 8
-    for (int r = s; r < rows; r += 32) v += *G(part + (int64_t)r * k + col);
+    for (int r = s; r < rows; r += 64) v += *G(part + (int64_t)r * k + col);
   }
   red[s][c] = v;
   __syncthreads();
-  // transposed: wave w adds columns 2w and 2w + 1, 32 lanes each
-  float t = red[threadIdx.x & 31][threadIdx.x >> 5];
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor(t, o);
-  const int oc = 32 * blockIdx.x + (threadIdx.x >> 5);
-  if ((threadIdx.x & 31) == 0 && oc < k) out[oc] = accumulate ? out[oc] + t : t;
+  // transposed: wave w adds column w, a slice a lane
+  const float t = wave_reduce(red[threadIdx.x & 63][threadIdx.x >> 6], [](float a, float b) { return a + b; });
+  const int oc = 16 * blockIdx.x + (threadIdx.x >> 6);
+  if ((threadIdx.x & 63) == 0 && oc < k) out[oc] = accumulate ? out[oc] + t : t;
 }
 
 // ---- restored activations ----
 
-// bf16(q / s) for 16 (WIDE) or 4 codes a thread; blockIdx.y walks the rows.
-template <bool WIDE>
+// bf16(q / s), 16 codes a thread; blockIdx.y walks the rows.
 __global__ __launch_bounds__(256) void restore_kernel(const int8_t* __restrict__ q,
                                                       const float* __restrict__ x_scale, int64_t m,
                                                       int k, uint16_t* __restrict__ out) {
-  constexpr int W = WIDE ? 16 : 4;
-  const int e = W * ((int)blockIdx.x * 256 + (int)threadIdx.x);
+  const int e = 16 * ((int)blockIdx.x * 256 + (int)threadIdx.x);
   if (e >= k) return;
   for (int64_t r = blockIdx.y; r < m; r += gridDim.y) {
     const RestoreRow d = restore_row(*G(x_scale + r));
-    uint32_t v[W / 4];
-    if constexpr (WIDE) {
-      const v4i t = *G(reinterpret_cast<const v4i*>(q + r * k + e));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (uint32_t)t[i];
-    } else {
-      v[0] = *G(reinterpret_cast<const uint32_t*>(q + r * k + e));
-    }
-    uint32_t o[W / 2];
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) o[i] = restore2(v[i >> 1], 2 * (i & 1), d);
+    const int8_t* src = q + r * k + e;
     uint16_t* dst = out + r * k + e;
-    if constexpr (WIDE) {
-      *G(reinterpret_cast<v4i*>(dst)) = v4i{(int32_t)o[0], (int32_t)o[1], (int32_t)o[2], (int32_t)o[3]};
-      *G(reinterpret_cast<v4i*>(dst + 8)) = v4i{(int32_t)o[4], (int32_t)o[5], (int32_t)o[6], (int32_t)o[7]};
+    if (e + 16 <= k) {
+      const v4i v = *G(reinterpret_cast<const v4i_4*>(src));
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        store_bf16(dst + 8 * i, 8, Piece{{restore2((uint32_t)v[2 * i], 0, d), restore2((uint32_t)v[2 * i], 2, d),
+                                          restore2((uint32_t)v[2 * i + 1], 0, d), restore2((uint32_t)v[2 * i + 1], 2, d)}});
     } else {
-      typedef int32_t v2i __attribute__((ext_vector_type(2)));
-      *G(reinterpret_cast<v2i*>(dst)) = v2i{(int32_t)o[0], (int32_t)o[1]};
+      for (int i = 0; e + i < k; i += 4) {
+        const uint32_t v = *G(reinterpret_cast<const uint32_t*>(src + i));
+        *G(reinterpret_cast<v2i*>(dst + i)) = v2i{(int32_t)restore2(v, 0, d), (int32_t)restore2(v, 2, d)};
+      }
     }
   }
 }
 
 }  // namespace
 
+// Threads for `pieces` at n a thread: whole waves.
+static int threads_for(int pieces, int n) { return ((pieces + n - 1) / n + 63) / 64 * 64; }
+
 hipError_t launch_norm_quant(const NormArgs& a, hipStream_t s) {
+  const int pieces = (a.k + 7) / 8;
   const dim3 g((unsigned)(a.m < kGridX ? a.m : kGridX), (unsigned)((a.m + kGridX - 1) / kGridX));
-  if (a.k % 8 == 0 && a.k <= 8 * 8 * kT) {
-    const int n = (a.k + 8 * kT - 1) / (8 * kT);
-    if (n <= 1) norm_quant_kernel<8, 1><<<g, kT, 0, s>>>(a);
-    else if (n <= 2) norm_quant_kernel<8, 2><<<g, kT, 0, s>>>(a);
-    else if (n <= 4) norm_quant_kernel<8, 4><<<g, kT, 0, s>>>(a);
-    else norm_quant_kernel<8, 8><<<g, kT, 0, s>>>(a);
-  } else if (a.k <= 16 * 4 * kT) {
-    const int n = (a.k + 4 * kT - 1) / (4 * kT);
-    if (n <= 2) norm_quant_kernel<4, 2><<<g, kT, 0, s>>>(a);
-    else if (n <= 8) norm_quant_kernel<4, 8><<<g, kT, 0, s>>>(a);
-    else norm_quant_kernel<4, 16><<<g, kT, 0, s>>>(a);
-  } else {
-    norm_quant_long_kernel<<<g, kT, 0, s>>>(a);
-  }
+  // One piece a thread up to 8192 columns where rows are few (their latency
+  // counts), else up to 4096.
+  if (pieces <= (a.m <= 256 ? 1024 : 512))
+    norm_quant_kernel<1><<<g, threads_for(pieces, 1), 0, s>>>(a);
+  else if (pieces <= 2 * 512 || (a.m <= 256 && pieces <= 2 * 1024))
+    norm_quant_kernel<2><<<g, threads_for(pieces, 2), 0, s>>>(a);
+  else if (pieces <= 4 * 1024)
+    norm_quant_kernel<4><<<g, threads_for(pieces, 4), 0, s>>>(a);
+  else
+    norm_quant_long_kernel<<<g, kLongT, 0, s>>>(a);
   return hipGetLastError();
 }
 
 int norm_backward_blocks(int64_t m, int64_t k) {
   (void)k;
-  return (int)(m <= 512 ? (m + 1) / 2 : 512);
+  return (int)(m <= 1024 ? (m + 1) / 2 : 512);
 }
 
 hipError_t launch_norm_backward(const NormBwdArgs& a, float* dweight, bool accumulate,
                                 hipStream_t s) {
   const int g = norm_backward_blocks(a.m, a.k);
-  if (a.k % 8 == 0 && a.k <= 8 * 8 * kT) {
-    const int n = (a.k + 8 * kT - 1) / (8 * kT);
-    if (n <= 1) norm_backward_kernel<8, 1><<<g, kT, 0, s>>>(a);
-    else if (n <= 2) norm_backward_kernel<8, 2><<<g, kT, 0, s>>>(a);
-    else if (n <= 4) norm_backward_kernel<8, 4><<<g, kT, 0, s>>>(a);
-    else norm_backward_kernel<8, 8><<<g, kT, 0, s>>>(a);
-  } else if (a.k <= 16 * 4 * kT) {
-    const int n = (a.k + 4 * kT - 1) / (4 * kT);
-    if (n <= 2) norm_backward_kernel<4, 2><<<g, kT, 0, s>>>(a);
-    else if (n <= 8) norm_backward_kernel<4, 8><<<g, kT, 0, s>>>(a);
-    else norm_backward_kernel<4, 16><<<g, kT, 0, s>>>(a);
-  } else {
-    norm_backward_long_kernel<<<g, kT, 0, s>>>(a);
-  }
+  const int pieces = (a.k + 7) / 8;
+  if (pieces <= kBwdT)
+    norm_backward_kernel<1><<<g, threads_for(pieces, 1), 0, s>>>(a);
+  else if (pieces <= 2 * kBwdT)
+    norm_backward_kernel<2><<<g, threads_for(pieces, 2), 0, s>>>(a);
+  else if (pieces <= 4 * kBwdT)
+    norm_backward_kernel<4><<<g, threads_for(pieces, 4), 0, s>>>(a);
+  else
+    norm_backward_long_kernel<<<g, kLongT, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
-  column_join_kernel<<<(unsigned)((a.k + 31) / 32), 1024, 0, s>>>(a.part, g, a.k, dweight,
-                                                                accumulate ? 1 : 0);
+  column_join_kernel<<<(unsigned)((a.k + 15) / 16), 1024, 0, s>>>(a.part, g, a.k, dweight,
+                                                                 accumulate ? 1 : 0);
   return hipGetLastError();
 }
 
 hipError_t launch_restore(const int8_t* q, const float* x_scale, int64_t m, int64_t k,
                           uint16_t* out, hipStream_t s) {
-  const int64_t w = k % 16 == 0 ? 16 : 4;
-  const unsigned gx = (unsigned)((k / w + 255) / 256);
-  const unsigned gy = (unsigned)(m < 65535 ? m : 65535);
-  if (w == 16)
-    restore_kernel<true><<<dim3(gx, gy), 256, 0, s>>>(q, x_scale, m, (int)k, out);
-  else
-    restore_kernel<false><<<dim3(gx, gy), 256, 0, s>>>(q, x_scale, m, (int)k, out);
+  const dim3 g((unsigned)((k + 4095) / 4096), (unsigned)(m < 65535 ? m : 65535));
+  restore_kernel<<<g, 256, 0, s>>>(q, x_scale, m, (int)k, out);
   return hipGetLastError();
 }
 

@@ -18,6 +18,8 @@
 #include "internal.hpp"
 #include "layer_internal.hpp"
 
+#include <algorithm>
+
 namespace bl {
 
 namespace {
@@ -89,104 +91,158 @@ struct W4Args {
   int32_t ktiles, groups;
   int32_t gshift;  // log2(group / 128) where a group spans tiles, else 0
   int32_t blocks;  // blocks of 16 rows
+  int32_t wk;      // waves sharing a block along K
+  int32_t seg;     // K tiles whose activations are in LDS at a time
 };
 
-// One workgroup: R blocks of 16 weight rows times 16 token rows, the K tiles
-// dealt out to its W waves and the waves' sums joined in LDS, in wave order.
-// GP: groups per tile (1, 2 or 4; 1 also where a group spans tiles).
-template <int W, int R, int GP>
+// What a wave holds of U tiles.
+template <int GP, int U>
+struct W4Chunk {
+  v4i c[U];
+  v2i s[U][GP];
+};
+
+// One workgroup: W / wk blocks of 16 weight rows times up to 16 token rows;
+// wk waves share a block along K (contiguous shares of its tiles) and their
+// sums are joined in LDS, in wave order.  The token rows' codes are staged in
+// LDS first, a segment of K that fits at a time (32 bytes between rows: the 16
+// rows of an operand then lie in distinct banks), so a wave's memory loads are
+// the weights' alone.  It goes through its tiles U at a time, the next ones
+// loading while the current ones multiply.  GP: groups per tile (1, 2 or 4; 1
+// also where a group spans tiles).
+template <int W, int GP, int U>
 __global__ __launch_bounds__(64 * W) void w4_kernel(const W4Args A) {
-  __shared__ float red[W][R * 4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  extern __shared__ __align__(16) int8_t xs_lds[];
+  __shared__ float red[W][4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int lr = lane & 15, lg = lane >> 4;
-  const int blk0 = (int)blockIdx.x * R;
-  const int m0 = (int)blockIdx.y * 16;
-  const bool live = m0 + lr < A.m;
-  const int8_t* qrow = A.q + (int64_t)min(m0 + lr, A.m - 1) * A.k + 8 * lg;
-  const uint8_t* cp[R];
-  const uint16_t* sp[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int b = min(blk0 + r, A.blocks - 1);
-    cp[r] = A.codes + (int64_t)b * A.ktiles * 1024 + 256 * lg + 16 * lr;
-    sp[r] = A.scales + (int64_t)b * A.groups * 16 + 4 * lg;
-  }
-  float sum[R][4];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[r][e] = 0.0f;
+  const int blk = (int)blockIdx.x * (W / A.wk) + wave / A.wk;
+  const int part = wave % A.wk;
+  const int m0 = (int)blockIdx.y * 16, rows = min(16, A.m - m0);
+  const int ldx = A.seg * 128 + 32;
+  // blocks and token rows past the end read the last one: their sums are not stored
+  const int b = min(blk, A.blocks - 1);
+  const uint8_t* cp = A.codes + (int64_t)b * A.ktiles * 1024 + 256 * lg + 16 * lr;
+  const uint16_t* sp = A.scales + (int64_t)b * A.groups * 16 + 4 * lg;
+  const int8_t* xl = xs_lds + min(lr, rows - 1) * ldx + 8 * lg;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int t = wave; t < A.ktiles; t += W) {
-    v4i c[R];
+  auto load = [&](W4Chunk<GP, U>& h, int tb) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) c[r] = *G(reinterpret_cast<const v4i*>(cp[r] + (int64_t)t * 1024));
-    v2i x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = v2i{0, 0};
-      if (live && 128 * t + 32 * i < A.k)
-        x[i] = *G(reinterpret_cast<const v2i*>(qrow + 128 * t + 32 * i));
-    }
-    v2i s[R][GP];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int u = 0; u < U; ++u) {
+      const int t = min(tb + u, A.ktiles - 1);
+      h.c[u] = *G(reinterpret_cast<const v4i*>(cp + (int64_t)t * 1024));
 #pragma unroll
       for (int g = 0; g < GP; ++g) {
-        // a group past K (the padding of the last tile) meets zero codes
         const int gi = GP == 1 ? t >> A.gshift : min(GP * t + g, A.groups - 1);
-        s[r][g] = *G(reinterpret_cast<const v2i*>(sp[r] + (int64_t)gi * 16));
+        h.s[u][g] = *G(reinterpret_cast<const v2i*>(sp + (int64_t)gi * 16));
       }
+    }
+  };
+
+  for (int seg0 = 0; seg0 < A.ktiles; seg0 += A.seg) {
+    const int tiles = min(A.seg, A.ktiles - seg0);
+    const int per = (tiles + A.wk - 1) / A.wk;
+    const int t0 = seg0 + min(part * per, tiles), t1 = min(t0 + per, seg0 + tiles);
+    W4Chunk<GP, U> ca, cb;
+    if (t0 < t1) load(ca, t0);
+    // codes past K are zeros in LDS (they meet the last tile's padding, zeros too)
+    if (seg0) __syncthreads();
+    const int cpr = tiles * 8;  // 16-byte pieces of a row
+    for (int i = threadIdx.x; i < rows * cpr; i += 64 * W) {
+      const int r = i / cpr, c = i - r * cpr, k = 128 * seg0 + 16 * c;
+      const v4i v = k < A.k ? *G(reinterpret_cast<const v4i*>(A.q + (int64_t)(m0 + r) * A.k + k)) : v4i{0, 0, 0, 0};
+      *reinterpret_cast<v4i*>(xs_lds + r * ldx + 16 * c) = v;
+    }
+    __syncthreads();
+    auto multiply = [&](const W4Chunk<GP, U>& h, int tb) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+      for (int u = 0; u < U; ++u) {
+        if (tb + u >= t1) break;
+        v2i x[4];
 #pragma unroll
-      for (int g = 0; g < GP; ++g) {
-        v4i acc = {0, 0, 0, 0};
+        for (int i = 0; i < 4; ++i)
+          x[i] = *reinterpret_cast<const v2i*>(xl + 128 * (tb + u - seg0) + 32 * i);
 #pragma unroll
-        for (int j = 0; j < 4 / GP; ++j) {
-          const int i = g * (4 / GP) + j;
-          const uint32_t d = (uint32_t)c[r][i];
-          const v2i w = {(int32_t)(d & 0xF0F0F0F0u), (int32_t)((d << 4) & 0xF0F0F0F0u)};
-          acc = __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, w),
-                                                      __builtin_bit_cast(long, x[i]), acc, 0, 0, 0);
-        }
+        for (int g = 0; g < GP; ++g) {
+          v4i acc = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t sw = (uint32_t)s[r][g][e >> 1];
-          const float sf = __uint_as_float((e & 1) ? (sw & 0xFFFF0000u) : (sw << 16));
-          sum[r][e] = __builtin_fmaf(sf, (float)acc[e], sum[r][e]);
+          for (int j = 0; j < 4 / GP; ++j) {
+            const int i = g * (4 / GP) + j;
+            const uint32_t d = (uint32_t)h.c[u][i];
+            const v2i w = {(int32_t)(d & 0xF0F0F0F0u), (int32_t)((d << 4) & 0xF0F0F0F0u)};
+            acc = __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, w),
+                                                        __builtin_bit_cast(long, x[i]), acc, 0, 0, 0);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t sw = (uint32_t)h.s[u][g][e >> 1];
+            const float sf = __uint_as_float((e & 1) ? (sw & 0xFFFF0000u) : (sw << 16));
+            sum[e] = __builtin_fmaf(sf, (float)acc[e], sum[e]);
+          }
         }
       }
+    };
+    for (int t = t0; t < t1; t += 2 * U) {
+      if (t + U < t1) load(cb, t + U);
+      multiply(ca, t);
+      if (t + U >= t1) break;
+      if (t + 2 * U < t1) load(ca, t + 2 * U);
+      multiply(cb, t + U);
+    }
   }
 
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[wave][4 * r + e][lane] = sum[r][e];
+  for (int e = 0; e < 4; ++e) red[wave][e][lane] = sum[e];
   __syncthreads();
-  // wave w finishes blocks w, w + W, ...: lane = token lr, rows 4 lg .. 4 lg + 3
+  // the first wave of a block finishes it: lane = token lr, rows 4 lg .. 4 lg + 3
+  const int n = 16 * blk + 4 * lg;
+  if (part != 0 || lr >= rows || n >= A.n) return;
+  float v[4];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (r % W != wave) continue;
-    const int n = 16 * (blk0 + r) + 4 * lg;
-    if (!live || n >= A.n) continue;
-    float v[4];
+  for (int e = 0; e < 4; ++e) v[e] = sum[e];
+  for (int w = 1; w < A.wk; ++w)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = red[0][4 * r + e][lane];
+    for (int e = 0; e < 4; ++e) v[e] += red[wave + w][e][lane];
+  const float xs = *G(A.x_scale + m0 + lr);
+  uint16_t* yr = A.y + (int64_t)(m0 + lr) * A.n + n;
 #pragma unroll
-      for (int w = 1; w < W; ++w) v[e] += red[w][4 * r + e][lane];
-    }
-    const float xs = *G(A.x_scale + m0 + lr);
-    uint16_t* yr = A.y + (int64_t)(m0 + lr) * A.n + n;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (n + e >= A.n) continue;
-      uint16_t o = f32_to_bf16((v[e] * 0.0625f) / xs);
-      if (A.bias) o = add_bf16(o, *G(A.bias + n + e));
-      *G(yr + e) = o;
-    }
+  for (int e = 0; e < 4; ++e) {
+    if (n + e >= A.n) continue;
+    uint16_t o = f32_to_bf16((v[e] * 0.0625f) / xs);
+    if (A.bias) o = add_bf16(o, *G(A.bias + n + e));
+    *G(yr + e) = o;
   }
+}
+
+// LDS for activations, with the 1 KB a wave of the join within 64 KB: two
+// workgroups a CU.
+constexpr int kXBytes8 = 57000, kXBytes16 = 49000;
+
+// Waves per block.  Eight, one block a workgroup, unless
+//  * there are few blocks of many tiles (up to one block a CU): sixteen, the
+//    memory latency of a wave's share being what counts (4096 x 14336 at one
+//    token 8.3 -> 7.8 us, 2048 x 8192 at 16 tokens 13.7 -> 10.6; of few tiles,
+//    512 x 1024 at 3 tokens, eight are better: 4.0 -> 3.6); or
+//  * there are many blocks and many tokens: as few as leave 16 waves a CU, so
+//    that a workgroup stages its activations for several blocks (32768 x 4096
+//    at 16 tokens, eight waves a block 29.5 us, two 17.0; at one token, where
+//    the activations are small, 12.7 against 13.4).
+template <int GP>
+void launch_w4(W4Args a, hipStream_t s) {
+  const int rows = a.m < 16 ? a.m : 16;
+  a.wk = 8;
+  while (rows > 4 && a.wk > 1 && (int64_t)a.blocks * (a.wk / 2) >= 4096) a.wk /= 2;
+  const bool wide = (int64_t)a.blocks <= 256 && a.ktiles >= 64;
+  if (wide) a.wk = 16;
+  a.seg = std::min(a.ktiles, ((wide ? kXBytes16 : kXBytes8) / rows - 32) / 128);
+  const size_t lds = (size_t)rows * (a.seg * 128 + 32);
+  const int per = wide ? 1 : 8 / a.wk;
+  const dim3 grid((unsigned)((a.blocks + per - 1) / per), (unsigned)((a.m + 15) / 16));
+  if (wide)
+    w4_kernel<16, GP, 1><<<grid, 1024, lds, s>>>(a);
+  else
+    w4_kernel<8, GP, 2><<<grid, 512, lds, s>>>(a);
 }
 
 }  // namespace
@@ -226,10 +282,12 @@ hipError_t launch_w4_forward(int64_t m, int64_t n, int64_t k, int group, const i
   a.groups = (int32_t)(k / group);
   a.blocks = (int32_t)((n + 15) / 16);
   while ((128 << a.gshift) < group) ++a.gshift;
-  const dim3 grid((unsigned)a.blocks, (unsigned)((m + 15) / 16));
-  if (group == 32) w4_kernel<4, 1, 4><<<grid, 256, 0, s>>>(a);
-  else if (group == 64) w4_kernel<4, 1, 2><<<grid, 256, 0, s>>>(a);
-  else w4_kernel<4, 1, 1><<<grid, 256, 0, s>>>(a);
+  if (group == 32)
+    launch_w4<4>(a, s);
+  else if (group == 64)
+    launch_w4<2>(a, s);
+  else
+    launch_w4<1>(a, s);
   return hipGetLastError();
 }
 
