@@ -157,22 +157,31 @@ __device__ __forceinline__ Piece normed(const Piece& h, float rstd, const float 
   return o;
 }
 
-__device__ __forceinline__ uint32_t absmax_bits(const Piece& p) {
-  return max(absmax_bits4(p.w[0], p.w[1]), absmax_bits4(p.w[2], p.w[3]));
-}
-
-__device__ __forceinline__ void store_codes(int8_t* q, int n, const Piece& v, float s) {
-  uint32_t d[2];
+// Largest magnitude pattern of a piece's values and `a`, for each half of a
+// dword: the patterns of |bf16| order like the values.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 absmax2(u16x2 a, const Piece& p) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    d[i] = ((uint32_t)quant_i8(lo_f(v.w[2 * i]), s) & 0xFFu) |
-           (((uint32_t)quant_i8(hi_f(v.w[2 * i]), s) & 0xFFu) << 8) |
-           (((uint32_t)quant_i8(lo_f(v.w[2 * i + 1]), s) & 0xFFu) << 16) |
-           (((uint32_t)quant_i8(hi_f(v.w[2 * i + 1]), s) & 0xFFu) << 24);
+  for (int i = 0; i < 4; ++i)
+    a = __builtin_elementwise_max(a, __builtin_bit_cast(u16x2, p.w[i] & 0x7FFF7FFFu));
+  return a;
+}
+__device__ __forceinline__ uint32_t absmax_bits(u16x2 a) { return max((uint32_t)a.x, (uint32_t)a.y); }
+
+// Codes of a piece: round(n * s) is at most 127 in magnitude, so that plus 128
+// converts to an unsigned byte exactly, into its place, and one xor a dword
+// turns the bytes into int8.
+__device__ __forceinline__ void store_codes(int8_t* q, int n, const Piece& v, float s) {
+  uint32_t d[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = i & 1 ? hi_f(v.w[i >> 1]) : lo_f(v.w[i >> 1]);
+    d[i >> 2] = __builtin_amdgcn_cvt_pk_u8_f32(rintf(x * s) + 128.0f, i & 3, d[i >> 2]);
+  }
   if (n >= 8)
-    *G(reinterpret_cast<v2i_4*>(q)) = v2i{(int32_t)d[0], (int32_t)d[1]};
+    *G(reinterpret_cast<v2i_4*>(q)) = v2i{(int32_t)(d[0] ^ 0x80808080u), (int32_t)(d[1] ^ 0x80808080u)};
   else if (n > 0)
-    *G(reinterpret_cast<uint32_t*>(q)) = d[0];
+    *G(reinterpret_cast<uint32_t*>(q)) = d[0] ^ 0x80808080u;
 }
 
 // fp32(1 / sqrt(sum / k + eps)) from the hardware's fp64 estimate y and one
@@ -242,7 +251,7 @@ __global__ __launch_bounds__(kMaxT) void norm_quant_kernel(const NormArgs A) {
   }
   const float rstd = rstd_of(row_sum(ss, red), A.inv_k, A.eps);
   if (A.rstd && tid == 0) A.rstd[m] = rstd;
-  uint32_t amax = 0;
+  u16x2 amax = {0, 0};
 #pragma unroll
   for (int b = 0; b < NCH; ++b) {
     const int e = 8 * (tid + T * b);
@@ -253,10 +262,10 @@ __global__ __launch_bounds__(kMaxT) void norm_quant_kernel(const NormArgs A) {
       h[b] = normed(h[b], rstd, w[0]);
     }
     if (A.n) store_bf16(A.n + row + e, k - e, h[b]);
-    amax = max(amax, absmax_bits(h[b]));
+    amax = absmax2(amax, h[b]);
   }
   if (!A.q) return;
-  const float s = act_scale(bf16_to_f32(row_max(amax, redu)));
+  const float s = act_scale(bf16_to_f32(row_max(absmax_bits(amax), redu)));
   if (tid == 0) A.x_scale[m] = s;
 #pragma unroll
   for (int b = 0; b < NCH; ++b) {
@@ -298,16 +307,16 @@ __global__ __launch_bounds__(kLongT) void norm_quant_long_kernel(const NormArgs 
   }
   const float rstd = rstd_of(row_sum(ss, red), A.inv_k, A.eps);
   if (A.rstd && tid == 0) A.rstd[m] = rstd;
-  uint32_t amax = 0;
+  u16x2 amax = {0, 0};
   for (int e = 8 * tid; e < k; e += 8 * kLongT) {
     float w[8];
     load_weight(A.weight, A.wtype, e, k - e, w);
     const Piece n = normed(load_h(e), rstd, w);
     if (A.n) store_bf16(A.n + row + e, k - e, n);
-    amax = max(amax, absmax_bits(n));
+    amax = absmax2(amax, n);
   }
   if (!A.q) return;
-  const float s = act_scale(bf16_to_f32(row_max(amax, redu)));
+  const float s = act_scale(bf16_to_f32(row_max(absmax_bits(amax), redu)));
   if (tid == 0) A.x_scale[m] = s;
   for (int e = 8 * tid; e < k; e += 8 * kLongT) {
     float w[8];
