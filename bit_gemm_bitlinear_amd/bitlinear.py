@@ -42,6 +42,11 @@ class Inspect(ctypes.Structure):
     _fields_ = [("q", _vp), ("x_scale", _vp), ("qsum", _vp), ("acc", _vp)]
 
 
+class Codes(ctypes.Structure):
+    """bl_codes: int8 activations of a projection (codes and scales)."""
+    _fields_ = [("q", _vp), ("x_scale", _vp)]
+
+
 LAYOUT_ROWS = 0   # BL_LAYOUT_ROWS: packed uint8 [N, K/4]
 LAYOUT_TILED = 1  # BL_LAYOUT_TILED: uint8 [N/16, 4*K], one row per block of 16 weight rows
 
@@ -82,6 +87,9 @@ _SIGS = {
     "bitlinear_rms_norm_quant_backward": (ctypes.c_int, [_i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp,
                                                          _vp, _vp, _i32, _vp, _sz, _vp]),
     "bitlinear_restore_activations": (ctypes.c_int, [_i64, _i64, _vp, _vp, _vp, _vp]),
+    "bitlinear_forward_grouped_quantized": (ctypes.c_int, [_i32, ctypes.POINTER(Projection),
+                                                           ctypes.POINTER(Codes), _i64, _vp, _sz,
+                                                           _vp]),
     "bitlinear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
     "bitlinear_backward": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
                                           _vp, _vp, _i32, _vp, _sz, _vp]),
@@ -617,6 +625,64 @@ def restore_activations(q: torch.Tensor, x_scale: torch.Tensor,
     _launch(_lib.bitlinear_restore_activations,
             (*shape, q.data_ptr(), x_scale.data_ptr(), out.data_ptr()), dev)
     return out
+
+
+class GroupedQuantizedCall:
+    """A prepared grouped forward on int8 activations: per projection the codes
+    [M, K] and scales [M] (of rms_norm_quant or act_quant; projections may share
+    them), the packed weights in either layout and their scale, and optionally a
+    bf16 bias [N] and residual [M, N] (may be the output).  Results are those of
+    GroupedCall on the bf16 activations behind the codes."""
+
+    def __init__(self, qs, x_scales, packeds, w_scales, outs=None, workspace=None, biases=None,
+                 residuals=None):
+        count = len(qs)
+        if not (count == len(x_scales) == len(packeds) == len(w_scales)) or not count:
+            raise ValueError("qs, x_scales, packeds and w_scales must be non-empty lists of one length")
+        for lst, what in ((outs, "outs"), (biases, "biases"), (residuals, "residuals")):
+            if lst is not None and len(lst) != count:
+                raise ValueError(f"{what}: one entry per projection")
+        _require(qs[0], torch.int8, 2, "q")
+        m, dev = qs[0].shape[0], qs[0].device
+        self._arr, self._codes = (Projection * count)(), (Codes * count)()
+        self.outs = []
+        for i, (q, xs, p, s) in enumerate(zip(qs, x_scales, packeds, w_scales)):
+            _require(q, torch.int8, 2, "q", device=dev)
+            k = q.shape[1]
+            _need(q, torch.int8, "q", (m, k), dev)
+            _need(xs, torch.float32, "x_scale", (m,), dev)
+            _require(p, torch.uint8, 2, "packed", device=dev)
+            _require_scale(s, dev)
+            n, layout = weight_layout(p, k)
+            y = outs[i] if outs is not None else torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+            _need(y, torch.bfloat16, "out", (m, n), dev)
+            b = biases[i] if biases is not None else None
+            r = residuals[i] if residuals is not None else None
+            if b is not None:
+                _need(b, torch.bfloat16, "bias", (n,), dev)
+            if r is not None:
+                _need(r, torch.bfloat16, "residual", (m, n), dev)
+            self.outs.append(y)
+            self._codes[i] = Codes(q.data_ptr(), xs.data_ptr())
+            self._arr[i] = Projection(0, p.data_ptr(), s.data_ptr(), y.data_ptr(), n, k, layout, 0,
+                                      0 if b is None else b.data_ptr(), 0 if r is None else r.data_ptr())
+        need = int(_lib.bitlinear_forward_grouped_workspace_bytes(count, self._arr, m))
+        self.workspace = _workspace(need, dev, workspace)
+        self._dev = dev
+        self._keep = (list(qs), list(x_scales), list(packeds), list(w_scales), biases, residuals)
+        self._args = (count, self._arr, self._codes, m, _ptr(self.workspace), _nbytes(self.workspace))
+
+    def __call__(self, stream=None):
+        _launch(_lib.bitlinear_forward_grouped_quantized, self._args, self._dev, stream)
+        return self.outs
+
+
+def forward_quantized(q, x_scale, packed, w_scale, out=None, workspace=None, bias=None,
+                      residual=None) -> torch.Tensor:
+    """forward() on int8 activations: codes [M, K] and scales [M] (see
+    GroupedQuantizedCall)."""
+    return GroupedQuantizedCall([q], [x_scale], [packed], [w_scale], None if out is None else [out],
+                                workspace, [bias], [residual])()[0]
 
 
 class BackwardCall:

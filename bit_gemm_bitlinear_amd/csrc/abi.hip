@@ -3,6 +3,7 @@
 // entry point allocates, frees or synchronizes; every argument is checked
 // before anything is enqueued.
 #include "../../include/bitlinear.h"
+#include "../../include/bitlinear_layer.h"
 
 #include <hip/hip_runtime.h>
 
@@ -181,6 +182,7 @@ struct ProjIO {
   int32_t* ins_qs;
   const uint16_t* bias;  // [n] bf16, or nullptr
   const uint16_t* res;   // [m][n] bf16, or nullptr
+  const float* xs_in;    // scales of caller-supplied codes q_in, or nullptr
 };
 
 // Diagnostics of a call: the decode kernel's wait bound and status word.
@@ -218,7 +220,9 @@ bl_status run_forward(int32_t count, const ProjIO* io, int64_t m, void* workspac
   int rows = 0, jobs = 0;
   for (int i = 0; i < count; ++i) {
     qptr[i] = reinterpret_cast<int8_t*>(ws + L.q_off[i]);
-    xsptr[i] = reinterpret_cast<float*>(ws + L.xs_off[i]);
+    // scales that come with the codes are read where they are
+    xsptr[i] = io[i].xs_in ? const_cast<float*>(io[i].xs_in)
+                           : reinterpret_cast<float*>(ws + L.xs_off[i]);
     qsptr[i] = reinterpret_cast<int32_t*>(ws + L.qs_off[i]);
     if (L.decode && L.plan[i].fused) continue;
     ActQuantJob& J = qa.j[jobs++];
@@ -542,7 +546,7 @@ static bl_status forward_one(int64_t m, int64_t n, int64_t k, const uint16_t* x,
       (st = check_ptr(w_scale)) != BL_OK || (st = check_ptr(y)) != BL_OK)
     return st;
   ProjIO io = {x, nullptr, packed, w_scale, y, nullptr, n, k, tiled,
-               nullptr, nullptr, nullptr, nullptr, nullptr};
+               nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   return run_forward(1, &io, m, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
@@ -572,7 +576,9 @@ size_t bitlinear_forward_grouped_workspace_bytes(int32_t count, const bl_project
   return L.total;
 }
 
-static bl_status grouped_io(int32_t count, const bl_projection* projs, int64_t m, ProjIO* io) {
+// `codes`: the activations are these and every projection's x is NULL.
+static bl_status grouped_io(int32_t count, const bl_projection* projs, int64_t m, ProjIO* io,
+                            const bl_codes* codes = nullptr) {
   if (count < 1 || count > kMaxProj || !projs) return BL_EINVAL;
   for (int i = 0; i < count; ++i) {
     const bl_projection& p = projs[i];
@@ -581,7 +587,10 @@ static bl_status grouped_io(int32_t count, const bl_projection* projs, int64_t m
     if ((p.layout != BL_LAYOUT_ROWS && p.layout != BL_LAYOUT_TILED) || p.reserved != 0)
       return BL_EINVAL;
     if (p.layout == BL_LAYOUT_TILED && (st = check_tiled_shape(p.n, p.k)) != BL_OK) return st;
-    if ((st = check_ptr(p.x)) != BL_OK || (st = check_ptr(p.packed)) != BL_OK ||
+    if (codes && p.x) return BL_EINVAL;
+    if (codes && ((st = check_ptr(codes[i].q)) != BL_OK || (st = check_ptr(codes[i].x_scale)) != BL_OK))
+      return st;
+    if ((!codes && (st = check_ptr(p.x)) != BL_OK) || (st = check_ptr(p.packed)) != BL_OK ||
         (st = check_ptr(p.w_scale)) != BL_OK || (st = check_ptr(p.y)) != BL_OK)
       return st;
     if ((p.bias && !aligned16(p.bias)) || (p.residual && !aligned16(p.residual))) return BL_EALIGN;
@@ -591,9 +600,9 @@ static bl_status grouped_io(int32_t count, const bl_projection* projs, int64_t m
       const uintptr_t bytes = (uintptr_t)(m * p.n) * 2;
       if (a < b + bytes && b < a + bytes) return BL_EINVAL;
     }
-    io[i] = ProjIO{p.x,     nullptr, p.packed, p.w_scale, p.y,    nullptr,
+    io[i] = ProjIO{p.x,     codes ? codes[i].q : nullptr, p.packed, p.w_scale, p.y,    nullptr,
                    p.n,     p.k,     p.layout == BL_LAYOUT_TILED ? 1 : 0,   nullptr, nullptr,
-                   nullptr, p.bias,  p.residual};
+                   nullptr, p.bias,  p.residual, codes ? codes[i].x_scale : nullptr};
   }
   return BL_OK;
 }
@@ -625,6 +634,16 @@ bl_status bitlinear_forward_grouped(int32_t count, const bl_projection* projs, i
                                     void* workspace, size_t workspace_bytes, void* stream) {
   ProjIO io[kMaxProj];
   const bl_status st = grouped_io(count, projs, m, io);
+  if (st != BL_OK) return st;
+  return run_forward(count, io, m, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+bl_status bitlinear_forward_grouped_quantized(int32_t count, const bl_projection* projs,
+                                              const bl_codes* codes, int64_t m, void* workspace,
+                                              size_t workspace_bytes, void* stream) {
+  if (!codes) return BL_EINVAL;
+  ProjIO io[kMaxProj];
+  const bl_status st = grouped_io(count, projs, m, io, codes);
   if (st != BL_OK) return st;
   return run_forward(count, io, m, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
@@ -719,7 +738,7 @@ bl_status bitlinear_forward_latent(int64_t m, int64_t n, int64_t k, const uint16
       hipSuccess)
     return BL_EHIP;
   ProjIO io = {x, nullptr, packed, scale, y, nullptr, n, k, 0,
-               nullptr, nullptr, nullptr, nullptr, nullptr};
+               nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   return run_forward(1, &io, m, ws + L.fwd, workspace_bytes - L.fwd, s);
 }
 
@@ -733,7 +752,7 @@ static bl_status forward_acc_one(int64_t m, int64_t n, int64_t k, const int8_t* 
       (st = check_ptr(acc)) != BL_OK)
     return st;
   ProjIO io = {nullptr, q, packed, nullptr, nullptr, acc, n, k, tiled,
-               nullptr, nullptr, nullptr, nullptr, nullptr};
+               nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   return run_forward(1, &io, m, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 

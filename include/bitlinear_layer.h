@@ -85,6 +85,26 @@ bl_status bitlinear_restore_activations(int64_t m, int64_t k, const int8_t *q,
                                         const float *x_scale, uint16_t *out,
                                         void *stream);
 
+/* --- forward on int8 codes ---------------------------------------------- */
+
+/* Activations of a projection as bitlinear_rms_norm_quant or
+ * bitlinear_act_quant write them (device pointers). */
+typedef struct {
+  const int8_t *q;      /* [M][K] int8 codes, -127..127 */
+  const float *x_scale; /* [M] fp32 scales */
+} bl_codes;
+
+/* bitlinear_forward_grouped on activations that are int8 codes already:
+ * codes: HOST array of `count`; every projs[i].x must be NULL (BL_EINVAL).
+ * Results are those of bitlinear_forward_grouped on the bf16 activations
+ * that the codes were made of, bit for bit.  Workspace:
+ * bitlinear_forward_grouped_workspace_bytes.  The first kernel brings the
+ * codes into the contraction's order; then as bitlinear_forward. */
+bl_status bitlinear_forward_grouped_quantized(int32_t count, const bl_projection *projs,
+                                              const bl_codes *codes, int64_t m,
+                                              void *workspace, size_t workspace_bytes,
+                                              void *stream);
+
 /* --- gradients of BitLinear -------------------------------------------- */
 
 /* Bytes of workspace bitlinear_backward needs for dx and/or dw.  Shapes: M and

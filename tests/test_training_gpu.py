@@ -1,0 +1,256 @@
+"""The training form (training.py) on the GPU: values against the inference
+path, gradients against the formulas in float64 and against differences of the
+straight-through function, and the operators run together as a block uses them.
+
+Bounds count roundings: u = 2^-24 a half step of fp32 (a whole one, 2u, per term
+of a matrix-core sum), 2^-8 one of bf16, relative.
+"""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+U, BF = 2.0 ** -24, 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def bl():
+    from bit_gemm_bitlinear_amd import bitlinear
+
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    return bitlinear
+
+
+@pytest.fixture(scope="module")
+def tr(bl):
+    from bit_gemm_bitlinear_amd import training
+
+    return training
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def leaf(shape, g, dtype=torch.bfloat16, scale=1.0):
+    return (scale * torch.randn(shape, generator=g, device=DEV)).to(dtype).requires_grad_()
+
+
+@pytest.mark.parametrize("shape,n,bias", [((1, 64), 16, False), ((5, 7, 132), 33, True), ((40, 1024), 96, True)])
+def test_linear(bl, tr, shape, n, bias):
+    g = gen(1)
+    k = shape[-1]
+    x, w = leaf(shape, g), leaf((n, k), g, torch.float32, 0.02)
+    b = leaf((n,), g) if bias else None
+    y = tr.linear(x, w, b)
+    rows = x.detach().reshape(-1, k)
+    packed, ws = bl.pack_weights(w.detach())
+    assert torch.equal(y.detach().reshape(-1, n), bl.forward(rows, packed, ws, bias=None if b is None else b.detach()))
+    dy = torch.randn(y.shape, generator=g, device=DEV).to(torch.bfloat16)
+    y.backward(dy)
+    d = dy.reshape(-1, n).double()
+    q, xs = bl.act_quant(rows)
+    u, xhat = bl.unpack_weights(packed).double(), bl.restore_activations(q, xs).double()
+    want = d @ u / ws.double()
+    mag = d.abs() @ u.abs() / ws.double()
+    assert x.grad.shape == x.shape
+    assert bool(((x.grad.reshape(-1, k).double() - want).abs() <= BF * want.abs() + (1 + BF) * (n + 2) * 2 * U * mag).all())
+    dt = d.t().contiguous()
+    assert bool(((w.grad.double() - dt @ xhat).abs() <= (len(rows) + 2) * 2 * U * (dt.abs() @ xhat.abs())).all())
+    if bias:
+        s = d.sum(0)
+        assert bool(((b.grad.double() - s).abs() <= BF * s.abs() + (1 + BF) * (len(rows) + 2) * U * d.abs().sum(0)).all())
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("weight", ["none", "bf16", "fp32"])
+def test_norm_linear(bl, tr, weight, residual):
+    """Three projections of one norm's output; the middle one's output unused."""
+    g = gen(2)
+    m, k, ns = 50, 516, (64, 8, 130)
+    x = leaf((2, 25, k), g)
+    r = leaf((2, 25, k), g, scale=2.0) if residual else None
+    nw = None if weight == "none" else leaf((k,), g, torch.bfloat16 if weight == "bf16" else torch.float32)
+    ws = [leaf((n, k), g, torch.float32, 0.02) for n in ns]
+    b = leaf((ns[2],), g)
+    h, ys = tr.norm_linear(x, ws, nw, r, biases=[None, None, b], eps=1e-5)
+    x2 = x.detach().reshape(m, k)
+    normed = bl.rms_norm_quant(x2, None if nw is None else nw.detach(), None if r is None else r.detach().reshape(m, k),
+                               eps=1e-5, want_norm=True)
+    packs = [bl.pack_weights(w.detach()) for w in ws]
+    assert torch.equal(h.detach().reshape(m, k), normed.h)
+    for i in range(3):  # the codes' product is the product of the norm's bf16 output
+        want = bl.forward(normed.n, *packs[i], bias=b.detach() if i == 2 else None)
+        assert torch.equal(ys[i].detach().reshape(m, ns[i]), want)
+    dys = [torch.randn(y.shape, generator=g, device=DEV).to(torch.bfloat16) for y in ys]
+    dh = torch.randn(h.shape, generator=g, device=DEV).to(torch.bfloat16)
+    torch.autograd.backward([h, ys[0], ys[2]], [dh, dys[0], dys[2]])
+    assert ws[1].grad is None
+    dx0 = bl.backward_input(dys[0].reshape(m, -1), *packs[0])
+    dn = bl.backward_input(dys[2].reshape(m, -1), *packs[2], residual=dx0)
+    dx, dweight = bl.rms_norm_quant_backward(dn, normed.h, normed.rstd, None if nw is None else nw.detach(),
+                                             dh.reshape(m, k) if residual else None)
+    if not residual:  # h is x itself
+        dx = dx + dh.reshape(m, k)
+    assert torch.equal(x.grad.reshape(m, k), dx)
+    if residual:
+        assert torch.equal(r.grad.reshape(m, k), dx)
+    if nw is not None:
+        assert torch.equal(nw.grad, dweight.to(nw.dtype))
+    for i in (0, 2):
+        dw, db = bl.backward_weight(dys[i].reshape(m, -1), normed.q, normed.x_scale, bias=i == 2)
+        assert torch.equal(ws[i].grad, dw)
+        if i == 2:
+            assert torch.equal(b.grad, db.to(torch.bfloat16))
+
+
+def test_gradient_against_differences(bl, tr):
+    """Directional differences of the straight-through function in float64 (the
+    weights' and activations' rounded values held where the forward put them,
+    so that it is y = (norm(h) + c) . (w + d)^T with constants c, d)."""
+    g = gen(3)
+    m, n, k, eps = 12, 40, 256, 1e-5
+    x, w, nw = leaf((m, k), g), leaf((n, k), g, torch.float32, 0.02), leaf((k,), g, torch.float32)
+    r = leaf((m, k), g)
+    h, (y,) = tr.norm_linear(x, [w], nw, r, eps=eps)
+    dy = torch.randn(m, n, generator=g, device=DEV).to(torch.bfloat16)
+    y.backward(dy)
+    normed = bl.rms_norm_quant(x.detach(), nw.detach(), r.detach(), eps=eps)
+    xhat = bl.restore_activations(normed.q, normed.x_scale).double()
+    packed, ws = bl.pack_weights(w.detach())
+    what = bl.unpack_weights(packed).double() / ws.double()
+
+    def value(hh, nn, ww):
+        z = hh / torch.sqrt((hh * hh).mean(1, keepdim=True) + eps) * nn
+        z = z + (xhat - z0)
+        return ((z @ (ww + (what - w.detach().double())).t().contiguous()) * dy.double()).sum()
+
+    h0, n0, w0 = normed.h.double(), nw.detach().double(), w.detach().double()
+    z0 = h0 / torch.sqrt((h0 * h0).mean(1, keepdim=True) + eps) * n0
+    for got, at in ((x.grad, 0), (nw.grad, 1), (w.grad, 2)):
+        d = torch.randn(got.shape, generator=g, device=DEV, dtype=torch.float64)
+        t = 1e-5
+        args = [[h0, n0, w0], [h0, n0, w0]]
+        args[0][at], args[1][at] = args[0][at] + t * d, args[1][at] - t * d
+        diff = (value(*args[0]) - value(*args[1])) / (2 * t)
+        slope = (got.double() * d).sum()
+        # dx passes two roundings to bf16 (of the product's gradient and its
+        # own), each off by 2^-8 of a value at most; differences are good to
+        # 1e-6 of the terms
+        tol = 2 * BF * (got.double().abs() * d.abs()).sum() + 1e-6 * abs(float(diff))
+        if at != 2:  # the first rounding, before the norm's gradient takes the mean off
+            dn = dy.double() @ what
+            back = (dn.abs() * (n0.abs() if at == 0 else 1.0) * normed.rstd.double()[:, None] *
+                    (1.0 if at == 0 else h0.abs()))
+            tol = tol + 2 * BF * ((back * d.abs()).sum() if at == 0 else (back.sum(0) * d.abs()).sum())
+            if at == 0:
+                z = h0 * normed.rstd.double()[:, None]
+                c = (dn.abs() * n0.abs() * z.abs()).mean(1, keepdim=True)
+                tol = tol + 2 * BF * (normed.rstd.double()[:, None] * z.abs() * c * d.abs()).sum()
+        assert abs(float(slope - diff)) <= float(tol), at
+
+
+def test_frozen_inputs(bl, tr):
+    g = gen(4)
+    x, w = leaf((9, 64), g), leaf((24, 64), g, torch.float32, 0.02)
+    tr.linear(x.detach(), w).sum().backward()
+    assert w.grad is not None
+    wg = w.grad.clone()
+    tr.linear(x, w.detach()).sum().backward()
+    assert x.grad is not None and torch.equal(w.grad, wg)
+    h, (y,) = tr.norm_linear(x.detach(), [w.detach()], None, x.detach())
+    assert not h.requires_grad and not y.requires_grad
+    r = x.detach().clone().requires_grad_()
+    h, _ = tr.norm_linear(x.detach(), [w.detach()], None, r)
+    h.sum().backward()  # only the residual stream is used
+    assert torch.equal(r.grad, torch.ones_like(r))
+
+
+def test_second_gradient_is_refused(tr):
+    g = gen(5)
+    x, w = leaf((4, 64), g), leaf((8, 64), g, torch.float32, 0.02)
+    gx, = torch.autograd.grad(tr.linear(x, w).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        gx.sum().backward()
+
+
+def test_module_and_checkpoint_size(bl, tr):
+    """The module's forward is the inference layer's; what it keeps for the
+    backward pass is 8 bits an activation and 2 a weight."""
+    m, k, n = 256, 1024, 512
+    layer = tr.BitLinear(k, n, bias=True, device=DEV)
+    x = torch.randn(m, k, device=DEV).to(torch.bfloat16).requires_grad_()
+    kept = {}
+
+    def pack(t):
+        kept[t.data_ptr()] = t.numel() * t.element_size()
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        y = layer(x)
+    assert sum(kept.values()) <= m * k + 4 * m + n * k // 4 + 4
+    frozen = bl.BitLinear(layer.weight.detach(), layer.bias.detach())
+    assert torch.equal(frozen(x.detach()), y.detach())
+    y.float().square().mean().backward()
+    assert layer.weight.grad.shape == layer.weight.shape and layer.bias.grad.dtype == torch.bfloat16
+
+
+def test_serving_block_together(bl):
+    """The decode side together: residual add + norm, the projections on its
+    codes, the output head in 4 bits on the same kind of codes."""
+    g = gen(6)
+    m, d, f, v = 3, 512, 768, 1000
+    x = torch.randn(m, d, generator=g, device=DEV).to(torch.bfloat16)
+    r = torch.randn(m, d, generator=g, device=DEV).to(torch.bfloat16)
+    nw = (1 + 0.1 * torch.randn(d, generator=g, device=DEV)).to(torch.bfloat16)
+    up, us = bl.pack_weights(0.02 * torch.randn(f, d, generator=g, device=DEV))
+    down, ds = bl.pack_weights(0.02 * torch.randn(d, f, generator=g, device=DEV))
+    head = bl.pack_weights_w4(0.02 * torch.randn(v, d, generator=g, device=DEV), 128)
+    a = bl.rms_norm_quant(x, nw, r, want_norm=True)
+    up_t = bl.tile_weights(up)
+    y = bl.forward_quantized(a.q, a.x_scale, up_t, us)
+    assert torch.equal(y, bl.forward(a.n, up, us))
+    z = bl.forward(y, down, ds, residual=a.h)
+    b = bl.rms_norm_quant(z, nw)
+    logits = bl.forward_w4(b.q, b.x_scale, head)
+    want = bl.restore_activations(b.q, b.x_scale).double()
+    xd = b.q.double() / b.x_scale.double()[:, None]
+    w = bl.unpack_weights_w4(head).double().t().contiguous()
+    exact = xd @ w
+    assert bool(((logits.double() - exact).abs() <= BF * exact.abs() + 20 * U * (xd.abs() @ w.abs())).all())
+    # the restored activations are the codes' values to a rounding of bf16
+    assert bool(((want - xd).abs() <= BF * xd.abs()).all())
+
+
+@pytest.mark.parametrize("m", [1, 4, 5, 16, 17, 40, 130, 300])
+@pytest.mark.parametrize("n,k", [(64, 256), (33, 260), (17, 516), (1024, 2048)])
+def test_forward_quantized_is_the_forward(bl, m, n, k):
+    g = gen(m)
+    x = torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16)
+    if m > 2:
+        x[1] = 0
+    q, xs = bl.act_quant(x)
+    packed, ws = bl.pack_weights(0.02 * torch.randn(n, k, generator=g, device=DEV))
+    bias = torch.randn(n, generator=g, device=DEV).to(torch.bfloat16)
+    res = torch.randn(m, n, generator=g, device=DEV).to(torch.bfloat16)
+    for layout in ([packed, bl.tile_weights(packed)] if n % 16 == 0 and k % 256 == 0 else [packed]):
+        assert torch.equal(bl.forward_quantized(q, xs, layout, ws), bl.forward(x, packed, ws))
+        assert torch.equal(bl.forward_quantized(q, xs, layout, ws, bias=bias, residual=res),
+                           bl.forward(x, packed, ws, bias=bias, residual=res))
+
+
+def test_grouped_quantized_shares_codes(bl):
+    """Projections that share codes, and one on codes of its own, in one call."""
+    g = gen(9)
+    m = 7
+    xa = torch.randn(m, 512, generator=g, device=DEV).to(torch.bfloat16)
+    xb = torch.randn(m, 768, generator=g, device=DEV).to(torch.bfloat16)
+    ws = [bl.pack_weights(0.02 * torch.randn(n, k, generator=g, device=DEV)) for n, k in ((64, 512), (96, 512), (512, 768))]
+    qa, sa = bl.act_quant(xa)
+    qb, sb = bl.act_quant(xb)
+    got = bl.GroupedQuantizedCall([qa, qa, qb], [sa, sa, sb], [p for p, _ in ws], [s for _, s in ws])()
+    want = bl.GroupedCall([xa, xa, xb], [p for p, _ in ws], [s for _, s in ws])()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
