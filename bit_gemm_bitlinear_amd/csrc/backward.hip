@@ -40,6 +40,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int32_t v2i __attribute__((ext_vector_type(2)));
 typedef v4i v4i_any __attribute__((aligned(2)));  // 16 bytes at any even address
+typedef v2i v2i_any __attribute__((aligned(2)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
@@ -76,21 +77,16 @@ __device__ __forceinline__ v4i column8(const v4i (&r)[8], int j) {
   return o;
 }
 
-// A thread's 8 tokens x 8 columns; a workgroup's 64 tokens x 256 columns.
-// Eight lanes side by side hold one row's 64 columns on the way in and one
-// column's 64 tokens on the way out: 128-byte pieces both ways.
-__device__ __forceinline__ void prepare_dy(const PrepArgs& A, int wg) {
-  const int cols = (int)((A.n + 255) >> 8);
-  const int64_t ms = wg / cols, n0 = (int64_t)(wg - (int)ms * cols) * 256;
-  const int mi = threadIdx.x & 7, ni = threadIdx.x >> 3;
-  const int64_t m0 = ms * 64 + 8 * mi, n = n0 + 8 * ni;
-  const int mv = (int)min((int64_t)8, A.m - m0);  // rows of the eight that exist (may be <= 0)
-  const int nv = (int)min((int64_t)8, A.n - n);   // columns
-  v4i r[8];
+// Eight rows of eight columns of dy [m][n] from (m0, n) on; what lies outside
+// is zeros.
+__device__ __forceinline__ void load_dy8(const uint16_t* __restrict__ dy, int64_t m, int64_t cols, int64_t m0,
+                                         int64_t n, v4i (&r)[8]) {
+  const int mv = (int)min((int64_t)8, m - m0);   // rows of the eight that exist (may be <= 0)
+  const int nv = (int)min((int64_t)8, cols - n);  // columns
   if (nv >= 8) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // rows start at any even address; missing ones read the last
-      const v4i v = *G(reinterpret_cast<const v4i_any*>(A.dy + min(m0 + i, A.m - 1) * A.n + n));
+      const v4i v = *G(reinterpret_cast<const v4i_any*>(dy + min(m0 + i, m - 1) * cols + n));
       r[i] = i < mv ? v : v4i{0, 0, 0, 0};
     }
   } else {
@@ -101,7 +97,7 @@ __device__ __forceinline__ void prepare_dy(const PrepArgs& A, int wg) {
     for (int e = 0; e < nv; ++e) {
       uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = *G(A.dy + min(m0 + i, A.m - 1) * A.n + n + e);
+      for (int i = 0; i < 8; ++i) v[i] = *G(dy + min(m0 + i, m - 1) * cols + n + e);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -109,6 +105,59 @@ __device__ __forceinline__ void prepare_dy(const PrepArgs& A, int wg) {
           r[i][h] |= (int32_t)((e >> 1) == h && i < mv ? v[i] << (16 * (e & 1)) : 0u);
     }
   }
+}
+
+// Eight rows of eight codes of q [m][k] from (m0, k0) on, restored to bf16, in
+// rows; what lies outside is zeros (K % 4 == 0: four columns or eight).
+struct Codes8 {
+  v2i c[8];
+  float xs[8];
+};
+__device__ __forceinline__ void load_codes8(const int8_t* __restrict__ q, const float* __restrict__ x_scale,
+                                            int64_t m, int64_t cols, int64_t m0, int64_t k, Codes8& o) {
+  const bool second = k + 4 < cols;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    o.c[i] = v2i{0, 0};
+    o.xs[i] = 1.0f;
+    if (m0 + i >= m || k >= cols) continue;
+    const int8_t* p = q + (m0 + i) * cols + k;
+    o.c[i].x = *G(reinterpret_cast<const int32_t*>(p));
+    if (second) o.c[i].y = *G(reinterpret_cast<const int32_t*>(p + 4));
+    o.xs[i] = *G(x_scale + m0 + i);
+  }
+}
+__device__ __forceinline__ void restore8(const Codes8& o, v4i (&r)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const RestoreRow d = restore_row(o.xs[i]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[i][e] = (int32_t)restore2((uint32_t)o.c[i][e >> 1], 2 * (e & 1), d);
+  }
+}
+
+// Sums over eight rows of each of the eight columns.
+__device__ __forceinline__ float column_sum8(const v4i (&r)[8], int e) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = (uint32_t)r[i][e >> 1];
+    s += __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
+  }
+  return s;
+}
+
+// A thread's 8 tokens x 8 columns; a workgroup's 64 tokens x 256 columns.
+// Eight lanes side by side hold one row's 64 columns on the way in and one
+// column's 64 tokens on the way out: 128-byte pieces both ways.
+__device__ __forceinline__ void prepare_dy(const PrepArgs& A, int wg) {
+  const int cols = (int)((A.n + 255) >> 8);
+  const int64_t ms = wg / cols, n0 = (int64_t)(wg - (int)ms * cols) * 256;
+  const int mi = threadIdx.x & 7, ni = threadIdx.x >> 3;
+  const int64_t m0 = ms * 64 + 8 * mi, n = n0 + 8 * ni;
+  const int mv = (int)min((int64_t)8, A.m - m0);  // rows of the eight that exist (may be <= 0)
+  v4i r[8];
+  load_dy8(A.dy, A.m, A.n, m0, n, r);
   if (A.dys && n < ((A.n + 63) & ~(int64_t)63)) {
     uint16_t* d = A.dys + ((n >> 6) * A.m + m0) * 64 + (n & 63);
 #pragma unroll
@@ -118,12 +167,7 @@ __device__ __forceinline__ void prepare_dy(const PrepArgs& A, int wg) {
   if (A.dbp) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w = (uint32_t)r[i][e >> 1];
-        s += __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
-      }
+      float s = column_sum8(r, e);
       s += __shfl_xor(s, 1);
       s += __shfl_xor(s, 2);
       s += __shfl_xor(s, 4);
@@ -143,26 +187,10 @@ __device__ __forceinline__ void prepare_xhat(const PrepArgs& A, int wg) {
   const int mi = threadIdx.x & 7, ki = threadIdx.x >> 3;
   const int64_t m0 = ms * 64 + 8 * mi, k = k0 + 8 * ki;
   if (k >= A.k) return;
-  const bool second = k + 4 < A.k;  // K % 4 == 0: the last piece may be four codes
-  v2i c[8];
-  float xs[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = v2i{0, 0};
-    xs[i] = 1.0f;
-    if (m0 + i >= A.m) continue;
-    const int8_t* p = A.q + (m0 + i) * A.k + k;
-    c[i].x = *G(reinterpret_cast<const int32_t*>(p));
-    if (second) c[i].y = *G(reinterpret_cast<const int32_t*>(p + 4));
-    xs[i] = *G(A.x_scale + m0 + i);
-  }
+  Codes8 c;
+  load_codes8(A.q, A.x_scale, A.m, A.k, m0, k, c);
   v4i r[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const RestoreRow d = restore_row(xs[i]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[i][e] = (int32_t)restore2((uint32_t)c[i][e >> 1], 2 * (e & 1), d);
-  }
+  restore8(c, r);
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (k + j < A.k) *G(reinterpret_cast<v4i*>(A.xt + (ms * A.k + k + j) * 64 + 8 * mi)) = column8(r, j);
@@ -255,8 +283,9 @@ __global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs A) {
 // The matrix products
 
 struct GemmJob {
-  const uint8_t* a;  // [slabs][ra] rows of 128 bytes
+  const uint8_t* a;  // [slabs][ra] rows of 128 bytes, a_row and a_slab bytes apart
   const uint8_t* b;  // [slabs][rb] rows of 128 bytes, or 16 (two-bit weights)
+  int64_t a_row, a_slab;
   int32_t ra, rb;    // C is [ra][rb]; rb % 4 == 0
   int32_t slabs;
   int32_t tiles_i, tiles_j;
@@ -314,13 +343,22 @@ __device__ __forceinline__ void barrier() {
 // Eight weights (four dwords of two bf16 each) from two-bit codes: q holds
 // pair a at bits 8 + 2a and 24 + 2a.  A byte select looks the high bytes of
 // u / 2 up (-0.5, 0, 0.5: their low bytes are zero); shift, mask-or, select.
-__device__ __forceinline__ v4i expand8(uint32_t q) {
-  v4i r;
+// The mask and the constant bytes are kept in registers (one scalar, one
+// vector), where the mask-or is a single instruction.
+struct Expand {
+  uint32_t mask, zero;
+  __device__ __forceinline__ Expand() : mask(0x03000300u), zero(0x000C000Cu) {
+    asm("" : "+s"(mask));
+    asm("" : "+v"(zero));
+  }
+  __device__ __forceinline__ v4i operator()(uint32_t q) const {
+    v4i r;
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
-    r[a] = (int32_t)__builtin_amdgcn_perm(0u, 0x003F00BFu, ((q >> (2 * a)) & 0x03000300u) | 0x000C000Cu);
-  return r;
-}
+    for (int a = 0; a < 4; ++a)
+      r[a] = (int32_t)__builtin_amdgcn_perm(0u, 0x003F00BFu, ((q >> (2 * a)) & mask) | zero);
+    return r;
+  }
+};
 
 // Output of four columns of one row.
 __device__ __forceinline__ void put4(const GemmJob& J, int64_t o, v4f v, float scale) {
@@ -330,7 +368,7 @@ __device__ __forceinline__ void put4(const GemmJob& J, int64_t o, v4f v, float s
     return;
   }
   v2i w;
-  // c is half of the sum (expand8): doubling is exact
+  // c is half of the sum (Expand): doubling is exact
   w.x = (int32_t)pack_bf16x2(2.0f * v[0] / scale, 2.0f * v[1] / scale);
   w.y = (int32_t)pack_bf16x2(2.0f * v[2] / scale, 2.0f * v[3] / scale);
   if (J.res) {
@@ -364,12 +402,12 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
 
   // Per lane the offsets within a slab, per wave the slab's address.
   uint32_t oa[DA], ob[DB];
-  const int64_t step_a = (int64_t)J.ra * kRow, step_b = (int64_t)J.rb * (CODES ? kCodes : kRow);
-  const uint8_t *pa = J.a + s0 * step_a, *pb = J.b + s0 * step_b;
+  const int64_t step_a = J.a_slab, step_b = (int64_t)J.rb * (CODES ? kCodes : kRow);
+  const uint8_t *pa = J.a + s0 * step_a + i0 * J.a_row, *pb = J.b + s0 * step_b;
 #pragma unroll
   for (int i = 0; i < DA; ++i) {
     const int pos = (wave * DA + i) * 64 + lane, r = pos >> 3;
-    oa[i] = (uint32_t)min(i0 + r, J.ra - 1) * kRow + 16 * ((pos & 7) ^ ((r >> 1) & 7));
+    oa[i] = (uint32_t)min(r, J.ra - 1 - i0) * (uint32_t)J.a_row + 16 * ((pos & 7) ^ ((r >> 1) & 7));
   }
 #pragma unroll
   for (int i = 0; i < DB; ++i) {
@@ -401,6 +439,7 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
+  const Expand expand;
   // Fragments of step ks of a slab: 16 c, eight a lane half.
   v4i fa[2][FI], fb[2][FJ], cj[FJ];
   const int8_t* sa = smem;  // the current slab's buffer
@@ -429,7 +468,7 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
     for (int j = 0; j < FJ; ++j) {
       v4i w;
       if constexpr (CODES)
-        w = expand8((uint32_t)cj[j][ks] << (8 - 8 * lg));  // the lane half's eight c
+        w = expand((uint32_t)cj[j][ks] << (8 - 8 * lg));  // the lane half's eight c
       else
         w = b[j];
 #pragma unroll
@@ -590,11 +629,297 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const GemmArgs A, int6
 }
 
 // ---------------------------------------------------------------------------
+// Small products, in one launch: a workgroup lays its operands out itself.
+//
+// Tiles of 64 x 64 by four waves of 32 x 32, c in steps of 128 (two slabs) from
+// registers to one of two LDS buffers while the other multiplies.  Operands
+// that several tiles share are laid out again by each, and a step waits for
+// its loads: worth it while there are few steps next to a second launch and the
+// trip of the operands through memory (both gradients of 16 x 480 x 960: 8.6
+// us against 12.4; of 301 x 1001 x 1284, 8 steps: 17.6 against 16.9).
+
+struct DirectArgs {
+  int64_t m, n, k;
+  const uint16_t* dy;
+  const uint8_t* packed;
+  int32_t tiled;
+  const int8_t* q;
+  const float* x_scale;
+  float* db;
+  int32_t tiles_k;    // tiles along K
+  int32_t dw_begin;   // first workgroup of dw
+  GemmJob dx, dw;     // their outputs
+};
+
+constexpr int kStep = 2 * kSlab;
+constexpr int kDirectA = 64 * kRow, kDirectB = 64 * kRow;  // bytes of a slab
+constexpr int kDirectBuf = 2 * (kDirectA + kDirectB);
+
+// Place of chunk c (16 bytes) of row r in a slab's image.
+__device__ __forceinline__ int image(int r, int c) { return kRow * r + 16 * (c ^ ((r >> 1) & 7)); }
+
+// Operand steps of dw: a lane takes 8 tokens x 4 columns of dy and of xhat;
+// lanes 0-7 side by side a column's 64 tokens, waves 0 and 1 (2 and 3) the two
+// slabs of the first (last) 32 columns.
+struct DirectDw {
+  const DirectArgs& A;
+  int64_t i0, j0;
+  bool sums;  // this tile also sums dy's columns
+  v2i d[8];
+  uint32_t c[8];
+  float xs[8], sum[4];
+  __device__ __forceinline__ DirectDw(const DirectArgs& a, int64_t i, int64_t j) : A(a), i0(i), j0(j) {
+    sums = A.db && j0 == 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = 0.0f;
+  }
+  __device__ __forceinline__ int column() const {
+    return 4 * (8 * ((int)threadIdx.x >> 7) + (((int)threadIdx.x >> 3) & 7));
+  }
+  __device__ __forceinline__ int slab() const { return ((int)threadIdx.x >> 6) & 1; }
+  __device__ __forceinline__ void load(int64_t c0) {
+    const int64_t m0 = c0 + 64 * slab() + 8 * (threadIdx.x & 7), n = i0 + column(), k = j0 + column();
+    const int mv = (int)min((int64_t)8, A.m - m0);  // tokens that exist (may be <= 0)
+    const int nv = (int)min((int64_t)4, A.n - n);
+    const bool kv = k < A.k;  // K % 4 == 0
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // tokens that do not exist read the last one
+      const int64_t m = min(m0 + i, A.m - 1);
+      c[i] = *G(reinterpret_cast<const uint32_t*>(A.q + m * A.k + (kv ? k : 0)));
+      xs[i] = *G(A.x_scale + m);
+    }
+    if (nv >= 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        d[i] = *G(reinterpret_cast<const v2i_any*>(A.dy + min(m0 + i, A.m - 1) * A.n + n));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = v2i{0, 0};
+#pragma unroll 1
+      for (int e = 0; e < nv; ++e) {
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = *G(A.dy + min(m0 + i, A.m - 1) * A.n + n + e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          d[i].x |= (int32_t)(e < 2 ? v[i] << (16 * (e & 1)) : 0u);
+          d[i].y |= (int32_t)(e < 2 ? 0u : v[i] << (16 * (e & 1)));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= mv) d[i] = v2i{0, 0};
+      if (i >= mv || !kv) c[i] = 0u;
+    }
+  }
+  // Column j of the eight tokens' four bf16 values, as a 16-byte chunk.
+  static __device__ __forceinline__ v4i column4(const v2i (&r)[8], int j) {
+    v4i o;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      o[p] = (int32_t)__builtin_amdgcn_perm((uint32_t)r[2 * p + 1][j >> 1], (uint32_t)r[2 * p][j >> 1],
+                                            (j & 1) ? 0x07060302u : 0x05040100u);
+    return o;
+  }
+  __device__ __forceinline__ void store(int8_t* buf) {
+    v2i x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const RestoreRow r = restore_row(xs[i]);
+      x[i] = v2i{(int32_t)restore2(c[i], 0, r), (int32_t)restore2(c[i], 2, r)};
+    }
+    const int mi = threadIdx.x & 7, col = column();
+    int8_t* at = buf + kDirectA * slab();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<v4i*>(at + image(col + j, mi)) = column4(d, j);
+    at = buf + 2 * kDirectA + kDirectB * slab();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<v4i*>(at + image(col + j, mi)) = column4(x, j);
+    if (sums) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = (uint32_t)d[i][e >> 1];
+          sum[e] += __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
+        }
+    }
+  }
+  __device__ __forceinline__ void finish(int8_t* smem) {
+    if (!sums) return;
+    float* red = reinterpret_cast<float*>(smem);  // the buffers are done with
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float s = sum[e];
+      s += __shfl_xor(s, 1);
+      s += __shfl_xor(s, 2);
+      s += __shfl_xor(s, 4);
+      if ((threadIdx.x & 7) == e) red[64 * slab() + column() + e] = s;
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < 64 && i0 + t < A.n) {
+      const float s = red[t] + red[64 + t];
+      *G(A.db + i0 + t) = A.dw.accumulate ? *G(A.db + i0 + t) + s : s;
+    }
+  }
+};
+
+// Operand steps of dx: dy's rows as they are, four 16-byte chunks a thread;
+// waves 2 and 3 transpose the weights, 16 rows n of one byte (four k) a lane.
+struct DirectDx {
+  const DirectArgs& A;
+  int64_t i0, j0;
+  v4i a[4];
+  uint32_t w[4];
+  __device__ __forceinline__ DirectDx(const DirectArgs& x, int64_t i, int64_t j) : A(x), i0(i), j0(j) {}
+  __device__ __forceinline__ void load(int64_t c0) {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t row = min(i0 + (tid >> 4) + 16 * q, A.m - 1), n = c0 + 8 * (tid & 15);
+      const int nv = (int)min((int64_t)8, A.n - n);
+      const uint16_t* p = A.dy + row * A.n + n;
+      a[q] = v4i{0, 0, 0, 0};
+      if (nv >= 8) {
+        a[q] = *G(reinterpret_cast<const v4i_any*>(p));
+      } else {
+        uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+        for (int e = 0; e < nv; ++e) {
+          const uint64_t v = (uint64_t)*G(p + e) << (16 * (e & 3));
+          lo |= e < 4 ? v : 0;
+          hi |= e < 4 ? 0 : v;
+        }
+        a[q] = v4i{(int32_t)lo, (int32_t)(lo >> 32), (int32_t)hi, (int32_t)(hi >> 32)};
+      }
+    }
+    if (tid < 128) return;
+    // byte b of w[r] is row n0 + order(4 b + r): in the result the codes of
+    // n = 2a and 2a + 1 then sit at bits 2a and 16 + 2a, as Expand takes them.
+    // The 16 rows are a fixed stride apart in either layout (n0 % 16 == 0).
+    const int64_t rb = A.k >> 2, n0 = c0 + 16 * ((tid - 128) >> 4);
+    const int64_t o = min((j0 >> 2) + (tid & 15), rb - 1);
+    const int last = (int)min((int64_t)15, A.n - 1 - n0);  // its rows that exist (may be < 0)
+    const uint8_t* base = A.packed + (last < 0 ? 0 : A.tiled ? tiled_chunk_offset(n0, o & ~(int64_t)15, rb) + (o & 15) : n0 * rb + o);
+    const uint32_t stride = A.tiled ? 16u : (uint32_t)rb;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      uint32_t v[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int p = 4 * b + r, row = p < 8 ? 2 * p : 2 * (p - 8) + 1;
+        v[b] = *G(base + (uint32_t)max(0, min(row, last)) * stride);
+        if (row > last) v[b] = 0x55u;  // rows past N: code 1, u = 0
+      }
+      w[r] = v[0] | (v[1] << 8) | (v[2] << 16) | (v[3] << 24);
+    }
+  }
+  __device__ __forceinline__ void store(int8_t* buf) {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = (tid >> 4) + 16 * q, c = tid & 15;
+      *reinterpret_cast<v4i*>(buf + kDirectA * (c >> 3) + image(r, c & 7)) = a[q];
+    }
+    if (tid < 128) return;
+    // 4 x 4 exchange of the two-bit fields of every byte
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t t = ((w[r] >> 4) ^ w[r + 2]) & 0x0F0F0F0Fu;
+      w[r + 2] ^= t;
+      w[r] ^= t << 4;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; r += 2) {
+      const uint32_t t = ((w[r] >> 2) ^ w[r + 1]) & 0x33333333u;
+      w[r + 1] ^= t;
+      w[r] ^= t << 2;
+    }
+    const int d = (tid - 128) >> 4, k = 4 * (tid & 15);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint32_t*>(buf + 2 * kDirectA + kDirectB * (d >> 2) + kCodes * (k + j) + 4 * (d & 3)) = w[j];
+  }
+  __device__ __forceinline__ void finish(int8_t*) {}
+};
+
+template <bool CODES, typename Operands>
+__device__ __forceinline__ void direct_tile(const DirectArgs& A, const GemmJob& J, Operands& op, int64_t c_len,
+                                            int8_t* smem) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lr = lane & 31, lg = lane >> 5;
+  const int wi0 = (wave & 1) * 32, wj0 = (wave >> 1) * 32;
+  const Expand expand;
+  v16f acc;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+  op.load(0);
+  op.store(smem);
+  __syncthreads();
+  int at = 0;
+  for (int64_t c0 = 0; c0 < c_len; c0 += kStep, at ^= 1) {
+    const bool more = c0 + kStep < c_len;
+    if (more) op.load(c0 + kStep);
+    const int8_t* buf = smem + at * kDirectBuf;
+    v4i fa[8], fb[8], cj[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int8_t* sa = buf + kDirectA * s;
+      const int8_t* sb = buf + 2 * kDirectA + kDirectB * s;
+      if constexpr (CODES) cj[s] = *reinterpret_cast<const v4i*>(sb + kCodes * (wj0 + lr));
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        fa[4 * s + ks] = *reinterpret_cast<const v4i*>(sa + image(wi0 + lr, 2 * ks + lg));
+        if constexpr (!CODES) fb[4 * s + ks] = *reinterpret_cast<const v4i*>(sb + image(wj0 + lr, 2 * ks + lg));
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      v4i w;
+      if constexpr (CODES)
+        w = expand((uint32_t)cj[t >> 2][t & 3] << (8 - 8 * lg));
+      else
+        w = fb[t];
+      acc = mfma_32x32x16(w, fa[t], acc);
+    }
+    if (more) op.store(smem + (at ^ 1) * kDirectBuf);
+    __syncthreads();
+  }
+  op.finish(smem);
+  const float sc = !J.cf ? load_f32_vmem(J.scale) : 1.0f;
+  const int64_t r = op.i0 + wi0 + lr;
+  if (r >= J.ra) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t c = op.j0 + wj0 + 8 * e + 4 * lg;
+    if (c >= J.rb) continue;
+    put4(J, r * J.rb + c, v4f{acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]}, sc);
+  }
+}
+
+__global__ __launch_bounds__(256, 2) void direct_kernel(const DirectArgs A) {
+  __shared__ __align__(16) int8_t smem[2 * kDirectBuf];
+  const bool dw = (int)blockIdx.x >= A.dw_begin;
+  const int t = dw ? (int)blockIdx.x - A.dw_begin : (int)blockIdx.x;
+  const int64_t i0 = (int64_t)(t / A.tiles_k) * 64, j0 = (int64_t)(t % A.tiles_k) * 64;
+  if (dw) {
+    DirectDw op(A, i0, j0);
+    direct_tile<false>(A, A.dw, op, A.m, smem);
+  } else {
+    DirectDx op(A, i0, j0);
+    direct_tile<true>(A, A.dx, op, A.n, smem);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Plans (from the shapes alone, so that the workspace queries agree)
 
 struct Plan {
   int cfg[2], ksplit[2], kspw[2];  // dx, dw
   int order;                       // which of them goes first
+  bool direct;                     // the one-launch kernel instead
 };
 
 // Tile sizes, with what the plan needs to know of each, measured on an
@@ -605,13 +930,16 @@ struct Config {
   int ti, tj;
   float slab, alone, put16, put32;
 };
-constexpr Config kConfigs[3] = {{64, 64, 0.22f, 0.36f, 0.4f, 1.2f},
-                                {128, 128, 0.49f, 0.60f, 1.5f, 3.8f},
-                                {256, 256, 1.55f, 1.55f, 5.0f, 9.0f}};
+constexpr Config kConfigs[3] = {{64, 64, 0.22f, 0.36f, 0.4f, 1.0f},
+                                {128, 128, 0.49f, 0.60f, 1.5f, 3.2f},
+                                {256, 256, 1.55f, 1.55f, 4.5f, 11.0f}};
 constexpr int kPlanCus = 256;      // MI355X
 constexpr int kMinPart = 4;        // slabs of a part
 constexpr float kFinishUs = 3.0f;  // one more launch
 constexpr float kBytesPerUs = 6e6f;
+constexpr float kPrepareUs = 5.0f;  // the operands' launch, empty
+// A step of the one-launch kernel as above, alone for dx and dw, and its start.
+constexpr float kDirectUs = 1.1f, kDirectAloneUs[2] = {1.3f, 2.8f}, kDirectStartUs = 1.5f;
 
 int64_t slabs_of(int64_t c) { return (c + kSlab - 1) / kSlab; }
 
@@ -672,6 +1000,17 @@ Plan plan_backward(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
       }
     }
   }
+  // The one-launch kernel: its longest sum's steps one after the other, or all
+  // its steps where they fill the chip; no other launch, no operands to write.
+  const int64_t step[2] = {(n + kStep - 1) / kStep, (m + kStep - 1) / kStep};
+  float direct = 0.0f, steps = 0.0f;
+  for (int j = 0; j < 2; ++j) {
+    if (!want[j]) continue;
+    const float tiles = (float)((rows[j] + 63) / 64) * (float)((k + 63) / 64);
+    direct = std::max(direct, step[j] * kDirectAloneUs[j]);
+    steps += tiles * (step[j] * kDirectUs + (j ? kConfigs[0].put32 : kConfigs[0].put16));
+  }
+  direct = kDirectStartUs + std::max(direct, steps / kPlanCus);
   const Option *best0 = nullptr, *best1 = nullptr;
   float best = 0.0f;
   for (int x = 0; x < num[0]; ++x)
@@ -689,9 +1028,14 @@ Plan plan_backward(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
       best0 = &a;
       best1 = &b;
     }
+  const float operands = (dx ? 2.0f * m * n + 0.25f * n * k : 0.0f) + (dw ? 2.0f * m * n + 2.0f * m * k : 0.0f);
+  if (direct <= best + kPrepareUs + 2.0f * operands / kBytesPerUs) return Plan{{0, 0}, {1, 1}, {1, 1}, 0, true};
   return Plan{{best0->cfg, best1->cfg}, {best0->ksplit, best1->ksplit}, {best0->kspw, best1->kspw},
-              best0->us >= best1->us ? 0 : 1};  // the longer tiles first
+              best0->us >= best1->us ? 0 : 1, false};  // the longer tiles first
 }
+
+// dy's own rows are slabs already: whole ones, 16-byte aligned.
+bool dy_as_is(int64_t n) { return n % kSlab == 0; }
 
 struct WsLayout {
   Plan plan;
@@ -701,11 +1045,12 @@ struct WsLayout {
 WsLayout layout(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
   WsLayout L = {};
   const Plan p = L.plan = plan_backward(m, n, k, dx, dw);
+  if (p.direct) return L;  // no workspace
   auto take = [&](size_t& off, bool want, int64_t bytes) {
     off = L.total;
     if (want) L.total = align256(L.total + (size_t)bytes);
   };
-  take(L.dys, dx, slabs_of(n) * m * kRow);
+  take(L.dys, dx && !dy_as_is(n), slabs_of(n) * m * kRow);
   take(L.ut, dx, slabs_of(n) * k * kCodes);
   take(L.dyt, dw, slabs_of(m) * n * kRow);
   take(L.xt, dw, slabs_of(m) * k * kRow);
@@ -742,6 +1087,31 @@ hipError_t launch_backward(const BackwardArgs& b, char* ws, size_t ws_bytes, hip
   const WsLayout L = layout(b.m, b.n, b.k, dx, dw);
   const Plan& p = L.plan;
   if (ws_bytes < L.total) return hipErrorInvalidValue;
+  if (p.direct) {
+    DirectArgs d = {};
+    d.m = b.m;
+    d.n = b.n;
+    d.k = b.k;
+    d.dy = b.dy;
+    d.packed = b.packed;
+    d.tiled = b.tiled ? 1 : 0;
+    d.q = b.q;
+    d.x_scale = b.x_scale;
+    d.db = b.dbias;
+    d.tiles_k = (int32_t)((b.k + 63) / 64);
+    d.dx.ra = (int32_t)b.m;
+    d.dw.ra = (int32_t)b.n;
+    d.dx.rb = d.dw.rb = (int32_t)b.k;
+    d.dx.cb = b.dx;
+    d.dx.scale = b.w_scale;
+    d.dx.res = b.residual;
+    d.dw.cf = b.dw;
+    d.dw.accumulate = b.accumulate ? 1 : 0;
+    d.dw_begin = dx ? (int32_t)((b.m + 63) / 64) * d.tiles_k : 0;
+    const int64_t wgs = d.dw_begin + (dw ? (b.n + 63) / 64 * d.tiles_k : 0);
+    direct_kernel<<<(unsigned)wgs, 256, 0, s>>>(d);
+    return hipGetLastError();
+  }
   const int64_t ms = slabs_of(b.m), ns = slabs_of(b.n);
 
   PrepArgs pa = {};
@@ -749,7 +1119,7 @@ hipError_t launch_backward(const BackwardArgs& b, char* ws, size_t ws_bytes, hip
   pa.n = b.n;
   pa.k = b.k;
   pa.dy = b.dy;
-  pa.dys = dx ? reinterpret_cast<uint16_t*>(ws + L.dys) : nullptr;
+  pa.dys = dx && !dy_as_is(b.n) ? reinterpret_cast<uint16_t*>(ws + L.dys) : nullptr;
   pa.dyt = dw ? reinterpret_cast<uint16_t*>(ws + L.dyt) : nullptr;
   pa.dbp = b.dbias ? reinterpret_cast<float*>(ws + L.dbp) : nullptr;
   pa.q = b.q;
@@ -758,7 +1128,7 @@ hipError_t launch_backward(const BackwardArgs& b, char* ws, size_t ws_bytes, hip
   pa.packed = b.packed;
   pa.tiled = b.tiled ? 1 : 0;
   pa.ut = reinterpret_cast<uint8_t*>(ws + L.ut);
-  int64_t wgs = ms * ((b.n + 255) / 256);
+  int64_t wgs = pa.dys || dw ? ms * ((b.n + 255) / 256) : 0;
   pa.begin[0] = 0;
   pa.begin[1] = (int32_t)wgs;
   if (dw) wgs += ms * ((b.k + 255) / 256);
@@ -779,6 +1149,13 @@ hipError_t launch_backward(const BackwardArgs& b, char* ws, size_t ws_bytes, hip
     g.begin[o] = (int32_t)grid;
     if (!want[j]) continue;
     J.a = reinterpret_cast<const uint8_t*>(ws + (j ? L.dyt : L.dys));
+    J.a_row = kRow;
+    J.a_slab = rows[j] * kRow;
+    if (j == 0 && dy_as_is(b.n)) {
+      J.a = reinterpret_cast<const uint8_t*>(b.dy);
+      J.a_row = 2 * b.n;
+      J.a_slab = kRow;
+    }
     J.b = reinterpret_cast<const uint8_t*>(ws + (j ? L.xt : L.ut));
     J.ra = (int32_t)rows[j];
     J.rb = (int32_t)b.k;

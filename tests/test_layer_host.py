@@ -110,8 +110,8 @@ def test_restore_refusals(lib):
     assert f(2, 64, A[0], A[1], A[0], None) == EINVAL
 
 
-def back(lib, m=4, n=32, k=256, dy=A[0], packed=A[1], layout=0, s=A[2], res=None, dx=A[3], q=A[4], xs=A[5], dw=A[6],
-         db=A[7], acc=0, ws=A[8], size=BIG):
+def back(lib, m=512, n=2048, k=2048, dy=A[0], packed=A[1], layout=0, s=A[2], res=None, dx=A[3], q=A[4], xs=A[5],
+         dw=A[6], db=A[7], acc=0, ws=A[8], size=BIG):
     return lib.bitlinear_backward(m, n, k, dy, packed, layout, s, res, dx, q, xs, dw, db, acc, ws, size, None)
 
 
@@ -121,15 +121,15 @@ def test_backward_refusals(lib):
                     (4, 4, 2 ** 22 + 4), (2 ** 21, 2 ** 21, 4), (2 ** 21, 4, 2 ** 20), (4, 2 ** 21, 2 ** 20)]:
         assert back(lib, m, n, k) == ESHAPE, (m, n, k)
         assert need(m, n, k, 1, 1) == 0
-    assert need(4, 32, 256, 0, 0) == 0
-    assert need(4, 32, 256, 1, 1) > max(need(4, 32, 256, 1, 0), need(4, 32, 256, 0, 1)) > 0
+    assert need(512, 2048, 2048, 0, 0) == 0
+    assert need(512, 2048, 2048, 1, 1) > max(need(512, 2048, 2048, 1, 0), need(512, 2048, 2048, 0, 1)) > 0
     for bad in (dict(dy=None), dict(packed=None), dict(s=None), dict(q=None), dict(xs=None), dict(layout=2),
                 dict(layout=-1), dict(acc=2), dict(dx=None, dw=None, db=None), dict(dw=None), dict(dx=None, res=A[9])):
         assert back(lib, **bad) == EINVAL, bad
     assert back(lib, n=33, layout=1) == ESHAPE and back(lib, k=260, layout=1) == ESHAPE
     for name in ("dy", "packed", "s", "res", "dx", "q", "xs", "dw", "db", "ws"):
         assert back(lib, **{name: ODD}) == EALIGN, name
-    size = need(4, 32, 256, 1, 1)
+    size = need(512, 2048, 2048, 1, 1)
     assert back(lib, ws=None) == EWORKSPACE and back(lib, size=ctypes.c_size_t(size - 1)) == EWORKSPACE
     for bad in (dict(dx=A[0]), dict(dw=A[4]), dict(db=A[6]), dict(ws=A[3]), dict(ws=A[0]), dict(res=P(A[3].value + 64)),
                 dict(res=A[6]), dict(res=A[8])):
@@ -137,17 +137,20 @@ def test_backward_refusals(lib):
 
 
 def test_backward_workspace_holds_every_plan(lib):
-    """Sizes over the range: the operands' slabs at least, and no more than
-    them and sixteen parts of the outputs."""
+    """Sizes over the range: none (the one-launch kernel), or the operands'
+    slabs and no more than sixteen parts of the outputs besides."""
     need = lib.bitlinear_backward_workspace_bytes
     rng = np.random.default_rng(1)
+    sizes = set()
     for _ in range(2000):
         m, n, k = (int(2 ** rng.uniform(0, 14)) for _ in range(3))
         k = 4 * max(1, k // 4)
         mp, np_ = -(-m // 64) * 64, -(-n // 64) * 64
-        least = 2 * np_ * m + np_ * k // 4 + 2 * mp * (n + k)
+        least = (2 * np_ * m if n % 64 else 0) + np_ * k // 4 + 2 * mp * (n + k)
         size = need(m, n, k, 1, 1)
-        assert least <= size <= least + 4 * mp // 64 * n + 64 * k * (m + n) + 8 * 256
+        assert size == 0 or least <= size <= least + 4 * mp // 64 * n + 64 * k * (m + n) + 8 * 256
+        sizes.add(size > 0)
+    assert sizes == {False, True}
 
 
 def w4(lib, m=3, n=20, k=256, group=64, q=A[0], xs=A[1], codes=A[2], scales=A[3], bias=None, y=A[4]):
