@@ -394,3 +394,112 @@ def test_operators_on_a_side_stream_and_in_a_graph(bl):
                nback.dx, nback.dweight]
         for a, b in zip(got, want):
             assert torch.equal(a, b), i
+
+
+def test_a_side_stream_waits_for_nothing_else(bl):
+    """Calls go to the current stream: results on a side stream, read there."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randn(64, 1024, generator=g, device=DEV).to(torch.bfloat16)
+    want = bl.rms_norm_quant(x)
+    dy, q, xs, packed, ws = layer_case(bl, 40, 64, 512, 1024)
+    first = bl.BackwardCall(dy, q, xs, packed, ws)()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = bl.rms_norm_quant(x)
+        again = bl.BackwardCall(dy, q, xs, packed, ws)()
+        same = [torch.equal(a, b) for a, b in zip(got[:4], want[:4])]
+        same += [torch.equal(a, b) for a, b in zip(again[:2], first[:2])]
+    side.synchronize()
+    assert all(same)
+
+
+def test_concurrent_calls_from_threads(bl):
+    """Several host threads, each on its own stream and workspaces."""
+    import threading
+
+    cases = [layer_case(bl, 50 + i, 40 + 100 * i, 256, 1024) for i in range(4)]
+    want = [[t.clone() for t in bl.BackwardCall(*c, bias=True)()] for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                call = bl.BackwardCall(*cases[i], bias=True)
+                for _ in range(10):
+                    got = call()
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    bad.append(i)
+        except Exception as e:  # reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+
+
+# ------------------------------------------------------------------ offsets past 2^31 and 2^32
+
+def test_norm_far_rows(bl):
+    """Rows past 2^31 elements (2^32 bytes) are those of a call on them alone."""
+    k = 4100
+    m = 2 ** 31 // k + 5
+    x = torch.empty(m, k, dtype=torch.bfloat16, device=DEV)
+    x[:-8] = 1.0
+    x[-8:] = torch.randn(8, k, device=DEV).to(torch.bfloat16)
+    w = torch.randn(k, device=DEV)
+    got = bl.rms_norm_quant(x, w)
+    few = bl.rms_norm_quant(x[-8:].clone(), w)
+    for a, b in zip((got.q, got.x_scale, got.rstd), (few.q, few.x_scale, few.rstd)):
+        assert torch.equal(a[-8:], b)
+    xhat = bl.restore_activations(got.q, got.x_scale)
+    assert torch.equal(xhat[-8:], bl.restore_activations(few.q, few.x_scale))
+    del xhat
+    dn = torch.zeros_like(x)
+    dn[-8:] = torch.randn(8, k, device=DEV).to(torch.bfloat16)
+    dx, dw = bl.rms_norm_quant_backward(dn, x, got.rstd, w)
+    dx2, dw2 = bl.rms_norm_quant_backward(dn[-8:].clone(), x[-8:].clone(), few.rstd, w)
+    assert torch.equal(dx[-8:], dx2)
+    assert bool(((dw - dw2).abs() <= 16 * U * (dn[-8:].double() * x[-8:].double() * few.rstd.double()[:, None]).abs().sum(0)).all())
+
+
+def test_backward_far_weights(bl):
+    """Weights past 2^31 elements: the last rows' gradient, and an input
+    gradient that sums over all of them."""
+    m, k = 3, 36864
+    n = 2 ** 31 // k + 64
+    n += -n % 16
+    g = torch.Generator(device=DEV).manual_seed(3)
+    packed = torch.full((n, k // 4), 0x55, dtype=torch.uint8, device=DEV)  # zeros
+    w = 0.02 * torch.randn(32, k, generator=g, device=DEV)
+    tail, ws = bl.pack_weights(w)
+    packed[-32:] = tail
+    dy = torch.randn(m, n, generator=g, device=DEV).to(torch.bfloat16)
+    q, xs = bl.act_quant(torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16))
+    dx, dw, _ = bl.BackwardCall(dy, q, xs, packed, ws)()
+    last = dy[:, -32:].contiguous()
+    check_input(dx, *input_gradient(bl, last, tail, ws), n)
+    check_weight(dw[-32:], *weight_gradient(bl, last, q, xs), m)
+    check_weight(dw[:32], *weight_gradient(bl, dy[:, :32].contiguous(), q, xs), m)
+
+
+def test_w4_far_weights(bl):
+    """4-bit codes past 2^31 bytes: the last rows' outputs."""
+    k, group = 8192, 128
+    n = 2 ** 31 // (k // 2) + 48
+    g = torch.Generator(device=DEV).manual_seed(4)
+    tail = bl.pack_weights_w4(torch.randn(32, k, generator=g, device=DEV), group)
+    codes = torch.zeros(n // 16, k // 128, 4, 16, 16, dtype=torch.uint8, device=DEV)
+    scales = torch.ones(n // 16, k // group, 16, dtype=torch.bfloat16, device=DEV)
+    codes[-2:], scales[-2:] = tail.codes, tail.scales
+    q = torch.randint(-127, 128, (2, k), generator=g, device=DEV).to(torch.int8)
+    xs = torch.ones(2, device=DEV)
+    y = bl.forward_w4(q, xs, bl.W4Weights(codes, scales, n, k, group))
+    want, mag = w4_reference(bl, q, xs, tail)
+    assert bool(((y[:, -32:].double() - want).abs() <= BF * want.abs() + (1 + BF) * (2 * (k // group) + 8) * U * mag).all())
+    assert bool((y[:, :-32] == 0).all())

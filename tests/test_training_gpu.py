@@ -254,3 +254,62 @@ def test_grouped_quantized_shares_codes(bl):
     want = bl.GroupedCall([xa, xa, xb], [p for p, _ in ws], [s for _, s in ws])()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_training_step_in_a_graph(bl, tr):
+    """Forward and backward captured once and replayed on new inputs, each
+    replay against the eager step."""
+    g = gen(11)
+    m, k, n = 96, 512, 160
+    x = torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16).requires_grad_()
+    r = torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16)
+    nw = leaf((k,), g, torch.float32)
+    w = [leaf((n, k), g, torch.float32, 0.02) for _ in range(2)]
+    target = torch.randn(m, n, generator=g, device=DEV).to(torch.bfloat16)
+
+    def step():
+        h, (a, b) = tr.norm_linear(x, w, nw, r)
+        return torch.autograd.grad((a, b, h), (x, nw, *w), (target, target, r))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        with torch.no_grad():
+            x.copy_(torch.randn(m, k, generator=g, device=DEV))
+            target.copy_(torch.randn(m, n, generator=g, device=DEV))
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b), i
+
+
+def test_same_weight_twice_and_broadcast_input(bl, tr):
+    """A weight shared by two projections gets both gradients; a broadcast
+    input the sum over its copies."""
+    g = gen(12)
+    x, w = leaf((1, 256), g), leaf((32, 256), g, torch.float32, 0.02)
+    big = x.expand(24, 256)
+    h, (a, b) = tr.norm_linear(big, [w, w])
+    assert torch.equal(a, b)
+    da = torch.randn(24, 32, generator=g, device=DEV).to(torch.bfloat16)
+    db = torch.randn(24, 32, generator=g, device=DEV).to(torch.bfloat16)
+    torch.autograd.backward([a, b], [da, db])
+    normed = bl.rms_norm_quant(big.detach().contiguous())
+    each = [bl.backward_weight(d, normed.q, normed.x_scale)[0] for d in (da, db)]
+    assert torch.equal(w.grad, each[0] + each[1])
+    packed, ws = bl.pack_weights(w.detach())
+    dn = bl.backward_input(db, packed, ws, residual=bl.backward_input(da, packed, ws))
+    dx, _ = bl.rms_norm_quant_backward(dn, normed.h, normed.rstd)
+    s = dx.double().sum(0)
+    assert x.grad.shape == x.shape
+    # torch adds the 24 rows in bf16 or wider: at most a bf16 rounding a term
+    assert bool(((x.grad[0].double() - s).abs() <= 24 * BF * dx.double().abs().sum(0)).all())
