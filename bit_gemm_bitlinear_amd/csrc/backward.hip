@@ -532,25 +532,38 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
 
   // B is the matrix core's first operand: lane (lr, lg) holds, of each
   // subtile, row lr at columns 8 e + 4 lg .. + 3 in elements 4 e .. 4 e + 3
-  // (rb % 4 == 0: such a run is whole or outside)
+  // (rb % 4 == 0: such a run is whole or outside).  Stored like that, an
+  // instruction would touch 32 rows; a pass through LDS, 32 rows of the wave's
+  // columns at a time in a part of its own, makes it whole rows (the ring is
+  // done with: its last loads have landed, and every wave is here).
+  barrier();
   const float sc = !J.cf ? load_f32_vmem(J.scale) : 1.0f;
+  constexpr int kPitch = 32 * FJ * 4 + 16;  // 16 bytes off: rows start at distinct banks
+  static_assert(NW * 32 * kPitch <= NST * kStage, "the parts fit the ring");
+  constexpr int LPR = 8 * FJ, RPI = 64 / LPR;  // lanes a row, rows an instruction
+  int8_t* mine = smem + wave * 32 * kPitch;
 #pragma unroll
   for (int i = 0; i < FI; ++i) {
-    const int r = i0 + wi0 + 32 * i + lr;
-    if (r >= J.ra) continue;
 #pragma unroll
     for (int j = 0; j < FJ; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = j0 + wj0 + 32 * j + 8 * e + 4 * lg;
-        if (c >= J.rb) continue;
-        const v4f v = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
-        const int64_t o = (int64_t)r * J.rb + c;
-        if (J.ksplit > 1)
-          *G(reinterpret_cast<v4f*>(J.part + (int64_t)kp * J.ra * J.rb + o)) = v;
-        else
-          put4(J, o, v, sc);
-      }
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<v4f*>(mine + lr * kPitch + 4 * (32 * j + 8 * e + 4 * lg)) =
+            v4f{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < 32 / RPI; ++q) {
+      const int row = q * RPI + lane / LPR;
+      const v4f v = *reinterpret_cast<const v4f*>(mine + row * kPitch + 16 * (lane % LPR));
+      const int r = i0 + wi0 + 32 * i + row, c = j0 + wj0 + 4 * (lane % LPR);
+      if (r >= J.ra || c >= J.rb) continue;
+      const int64_t o = (int64_t)r * J.rb + c;
+      if (J.ksplit > 1)
+        *G(reinterpret_cast<v4f*>(J.part + (int64_t)kp * J.ra * J.rb + o)) = v;
+      else
+        put4(J, o, v, sc);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
