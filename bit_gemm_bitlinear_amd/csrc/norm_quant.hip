@@ -203,7 +203,9 @@ __device__ __forceinline__ int64_t row_index() { return (int64_t)blockIdx.y * kG
 // row stays in registers between the sum, the maximum and the codes: x and
 // the residual are read once, everything else written once.  The weights are
 // loaded with them where the registers allow: the norm then does not wait for
-// memory again after the sum.
+// memory again after the sum.  2048 rows of 2560 with a residual (36.7 MB): 10.0-10.9 us, one round of
+// workgroups, so a chain of load, sum, maximum and store; one row of 4096:
+// 3.1 us.  A wave a row instead took 11.8 us.
 constexpr int kMaxT = 1024;
 template <int NCH>
 __global__ __launch_bounds__(kMaxT) void norm_quant_kernel(const NormArgs A) {
@@ -354,7 +356,8 @@ struct BwdRow {
 // grid apart, the next one loading while it works on the current, and each
 // thread fixed columns, so that it keeps its columns' sums for dweight in
 // registers over the rows.  The partial rows of the workgroups are added by a
-// second kernel, in a fixed order.
+// second kernel, in a fixed order.  8191 rows of 2560: 33-35 us, 4.9 TB/s of the
+// 5.1 that a large copy reaches; 512 rows of 4096: 7.2 us, its two rows' latency.
 constexpr int kBwdT = 512;
 template <int NCH>
 __global__ __launch_bounds__(kBwdT) void norm_backward_kernel(const NormBwdArgs A) {
@@ -471,7 +474,7 @@ __global__ __launch_bounds__(kLongT) void norm_backward_long_kernel(const NormBw
 }
 
 // dweight[k] = sum over the workgroups' partial rows: 16 columns a workgroup,
-// 64 slices of the rows, joined in a fixed order.
+// 64 slices of the rows, joined in a fixed order (512 rows of 2560: 4.7 us).
 __global__ __launch_bounds__(1024) void column_join_kernel(const float* __restrict__ part, int rows,
                                                            int k, float* __restrict__ out,
                                                            int accumulate) {
@@ -493,7 +496,7 @@ __global__ __launch_bounds__(1024) void column_join_kernel(const float* __restri
 
 // ---- restored activations ----
 
-// bf16(q / s), 16 codes a thread; blockIdx.y walks the rows.
+// bf16(q / s), 16 codes a thread; blockIdx.y walks the rows.  2048 x 2560: 5.4 us.
 __global__ __launch_bounds__(256) void restore_kernel(const int8_t* __restrict__ q,
                                                       const float* __restrict__ x_scale, int64_t m,
                                                       int k, uint16_t* __restrict__ out) {

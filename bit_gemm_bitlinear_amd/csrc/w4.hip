@@ -109,7 +109,9 @@ struct W4Chunk {
 // rows of an operand then lie in distinct banks), so a wave's memory loads are
 // the weights' alone.  It goes through its tiles U at a time, the next ones
 // loading while the current ones multiply.  GP: groups per tile (1, 2 or 4; 1
-// also where a group spans tiles).
+// also where a group spans tiles).  14336 x 4096 at one token: 6.8-7.9 us for 30
+// MB; 32768 x 4096 at 16 tokens: 17 us for 72 MB, 4.3 TB/s (36 us when every wave
+// loaded its own activations from memory).
 template <int W, int GP, int U>
 __global__ __launch_bounds__(64 * W) void w4_kernel(const W4Args A) {
   extern __shared__ __align__(16) int8_t xs_lds[];

@@ -128,8 +128,9 @@ size_t bitlinear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k,
  *   the codes q [M][K] and scales x_scale [M] of the layer's input: its 8-bit
  *   checkpoint.  accumulate: 0, or 1 to add to what dw and dbias hold.
  *
- * Products are exact and sums fp32.  Two kernels, three where a product's sum
- * is split across workgroups. */
+ * Products are exact and sums fp32.  One kernel for small shapes (no workspace:
+ * the size is 0 and `workspace` may be NULL), else two, or three where a
+ * product's sum is split across workgroups. */
 bl_status bitlinear_backward(int64_t m, int64_t n, int64_t k, const uint16_t *dy,
                              const uint8_t *packed, int32_t layout,
                              const float *w_scale, const uint16_t *residual,
@@ -165,7 +166,8 @@ bl_status bitlinear_w4_unpack(const uint8_t *codes, const uint16_t *scales, int6
                               int64_t k, int64_t group, float *out, void *stream);
 
 /* y = bf16(sum_g scale[n][g] * (sum_{k in g} q[m][k] * v[n][k]) / x_scale[m])
- * [M][N] bf16: exact int32 sums within a group, fp32 over the groups.  q,
+ * [M][N] bf16: exact int32 sums within a group (128 of it at a time), fp32
+ * over the groups.  q,
  * x_scale: int8 codes [M][K] and scales [M] of the activations.  bias: [N]
  * bf16, added to the rounded output (rounded again), or NULL.  One kernel;
  * the weights are read once for every 16 token rows. */
