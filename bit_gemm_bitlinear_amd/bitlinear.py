@@ -780,6 +780,8 @@ class W4Weights(NamedTuple):
 
 
 def _require_w4(w: W4Weights, device=None):
+    if w.n < 1 or w.k < 1 or w.group < 1 or w.k % w.group:
+        raise ValueError("W4Weights: n, k and group must be positive and group divide k")
     nb, kt = (w.n + 15) // 16, (w.k + 127) // 128
     _require(w.codes, torch.uint8, 5, "codes", shape=(nb, kt, 4, 16, 16), device=device)
     _require(w.scales, torch.bfloat16, 3, "scales", shape=(nb, w.k // w.group, 16),
@@ -791,7 +793,7 @@ def pack_weights_w4(w: torch.Tensor, group: int = 128) -> W4Weights:
     power of two from 32 to 1024 that divides K."""
     _require(w, torch.float32, 2, "w")
     n, k = w.shape
-    if group < 32 or k % group:
+    if group < 32 or group > 1024 or group & (group - 1) or k % group:
         raise ValueError("group must be a power of two from 32 to 1024 that divides K")
     out = W4Weights(torch.empty(((n + 15) // 16, (k + 127) // 128, 4, 16, 16), dtype=torch.uint8,
                                 device=w.device),

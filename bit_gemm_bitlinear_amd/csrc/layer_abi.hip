@@ -129,7 +129,7 @@ bl_status bitlinear_rms_norm_quant(int64_t m, int64_t k, const uint16_t* x,
   bl_status st;
   if ((st = check_shape(m, 1, k)) != BL_OK) return st;
   if ((st = check_ptr(x)) != BL_OK || (st = check_weight(weight, weight_type)) != BL_OK) return st;
-  if (!(eps > 0.0 && eps <= 1e300)) return BL_EINVAL;
+  if (!(eps >= 1e-60 && eps <= 1e60)) return BL_EINVAL;  // rstd of a zero row fits fp32
   if (!q != !x_scale || (!h && !rstd && !n && !q)) return BL_EINVAL;
   if ((st = check_optional({residual, h, rstd, n, q, x_scale})) != BL_OK) return st;
   const int64_t e = m * k;

@@ -48,7 +48,7 @@ extern "C" {
  *   x_scale = 127 / max(max_k |n|, 1e-5);  q = clamp(round(n * x_scale), -128, 127)
  * that is, q and x_scale are bitlinear_act_quant of n, bit for bit.
  * x, residual: [M][K] bf16.  weight: [K] of weight_type, NULL for
- * BL_WEIGHT_NONE.  eps: finite and > 0.  Written, each NULL where it is not
+ * BL_WEIGHT_NONE.  eps: 1e-60 to 1e60.  Written, each NULL where it is not
  * wanted: h [M][K] bf16, rstd [M] fp32, n [M][K] bf16; q [M][K] int8 and
  * x_scale [M] fp32 go together (both or neither).  h may be x or residual
  * themselves (the residual stream updated in place); no other output may

@@ -273,6 +273,44 @@ def test_backward_not_finite_stays_in_its_row(bl):
     assert torch.equal(got[keep], clean[keep])
 
 
+# Shapes by the kernels they take: one launch; operand pass and 64 or 128 tiles;
+# dx in parts; dw in parts; 256 tiles; 256 tiles with dx in parts.
+PLANS = [(33, 72, 260), (512, 1024, 1024), (45, 4000, 480), (2048, 512, 512), (300, 4096, 4096), (2048, 6912, 2560)]
+
+
+@pytest.mark.parametrize("m,n,k", PLANS)
+def test_backward_options_on_every_plan(bl, m, n, k):
+    """Residual in place, accumulation, the tiled layout and a value that is not
+    finite, against the plain call of the same shape."""
+    dy, q, xs, packed, ws = layer_case(bl, 60 + m, m, n, k)
+    dx, dw, db = bl.BackwardCall(dy, q, xs, packed, ws, bias=True)()
+    check_input(dx, *input_gradient(bl, dy, packed, ws), n)
+    check_weight(dw, *weight_gradient(bl, dy, q, xs), m)
+    prev = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+    rx, rw, rb = prev.clone(), torch.full_like(dw, 0.5), torch.full_like(db, -1.0)
+    bl.BackwardCall(dy, q, xs, packed, ws, residual=rx, dx=rx, dw=rw, dbias=rb, accumulate=True)()
+    assert torch.equal(rx, dx + prev) and torch.equal(rw, dw + 0.5) and torch.equal(rb, db - 1.0)
+    if n % 16 == 0 and k % 256 == 0:
+        tx, tw, _ = bl.BackwardCall(dy, q, xs, bl.tile_weights(packed), ws)()
+        assert torch.equal(tx, dx) and torch.equal(tw, dw)
+    bad = dy.clone()
+    bad[m // 2, n - 1] = float("nan")
+    bx, bw, _ = bl.BackwardCall(bad, q, xs, packed, ws)()
+    rows, cols = torch.arange(m, device=DEV) != m // 2, torch.arange(n, device=DEV) != n - 1
+    assert torch.equal(bx[rows], dx[rows]) and torch.equal(bw[cols], dw[cols])
+
+
+@pytest.mark.parametrize("m,n,k", PLANS)
+def test_backward_leaves_what_is_behind(bl, m, n, k):
+    """Rows behind the outputs' last stay as they were."""
+    dy, q, xs, packed, ws = layer_case(bl, 70 + m, m, n, k)
+    dx = torch.full((m + 2, k), 7.0, dtype=torch.bfloat16, device=DEV)
+    dw = torch.full((n + 2, k), 7.0, device=DEV)
+    db = torch.full((n + 8,), 7.0, device=DEV)
+    bl.BackwardCall(dy, q, xs, packed, ws, dx=dx[:m], dw=dw[:n], dbias=db[:n])()
+    assert bool((dx[m:] == 7).all()) and bool((dw[n:] == 7).all()) and bool((db[n:] == 7).all())
+
+
 # ------------------------------------------------------------------ 4-bit weights
 
 @pytest.mark.parametrize("n,k,group", [(1, 32, 32), (16, 128, 128), (17, 160, 32), (5, 192, 64),

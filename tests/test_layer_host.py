@@ -61,7 +61,7 @@ def test_norm_refusals(lib):
     assert norm(lib, x=None) == EINVAL
     for bad in (dict(w=None), dict(wt=0), dict(wt=3), dict(wt=-1)):
         assert norm(lib, **bad) == EINVAL
-    for eps in (0.0, -1e-5, float("nan"), float("inf")):
+    for eps in (0.0, -1e-5, 1e-61, 1e61, float("nan"), float("inf")):
         assert norm(lib, eps=eps) == EINVAL
     assert norm(lib, q=None) == EINVAL and norm(lib, xs=None) == EINVAL
     assert norm(lib, h=None, rstd=None, q=None, xs=None) == EINVAL  # nothing to write
@@ -206,6 +206,10 @@ def test_binding_refuses_host_tensors(bl):
                  lambda: bl.forward_w4(q, s, bl.W4Weights(q, x, 4, 64, 32))):
         with pytest.raises(TypeError):
             call()
+    with pytest.raises(ValueError):
+        bl.unpack_weights_w4(bl.W4Weights(q, x, 4, 64, 0))
+    with pytest.raises(ValueError):
+        bl.unpack_weights_w4(bl.W4Weights(q, x, 0, 64, 32))
 
 
 # ------------------------------------------------------------------ formulas
