@@ -96,7 +96,8 @@ bl_status check_workspace(const void* ws, size_t have, size_t need) {
 }
 
 size_t norm_backward_bytes(int64_t m, int64_t k, bool dweight) {
-  return dweight ? align256(sizeof(float) * (size_t)norm_backward_blocks(m, k) * (size_t)k) : 0;
+  const int blocks = norm_backward_blocks(m, k);
+  return dweight && blocks > 1 ? align256(sizeof(float) * (size_t)blocks * (size_t)k) : 0;
 }
 
 bl_status check_backward_shape(int64_t m, int64_t n, int64_t k) {
@@ -194,6 +195,7 @@ bl_status bitlinear_rms_norm_quant_backward(int64_t m, int64_t k, const uint16_t
   a.dh = dh;
   a.dx = dx;
   a.part = dweight ? static_cast<float*>(workspace) : nullptr;
+  a.add = 0;
   return launch_norm_backward(a, dweight, accumulate != 0, static_cast<hipStream_t>(stream)) ==
                  hipSuccess
              ? BL_OK

@@ -35,12 +35,12 @@ struct NormBwdArgs {
   int64_t m;
   const uint16_t* dh;  // or nullptr
   uint16_t* dx;
-  float* part;         // [blocks][k] fp32 partial sums of dweight, or nullptr
+  float* part;         // [blocks][k] fp32 partial sums of dweight (one block: dweight), or nullptr
+  int32_t add;         // one block: dweight is added to
 };
 // Workgroups of the backward kernel, each with a partial row of dweight.
 int norm_backward_blocks(int64_t m, int64_t k);
-hipError_t launch_norm_backward(const NormBwdArgs& a, float* dweight, bool accumulate,
-                                hipStream_t s);
+hipError_t launch_norm_backward(NormBwdArgs a, float* dweight, bool accumulate, hipStream_t s);
 
 hipError_t launch_restore(const int8_t* q, const float* x_scale, int64_t m, int64_t k,
                           uint16_t* out, hipStream_t s);

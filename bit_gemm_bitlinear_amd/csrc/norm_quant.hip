@@ -432,7 +432,11 @@ __global__ __launch_bounds__(kBwdT) void norm_backward_kernel(const NormBwdArgs 
     const int e = 8 * (tid + T * b);
 #pragma unroll
     for (int i = 0; i < 8; i += 4)
-      if (e + i < k) *G(reinterpret_cast<v4f*>(part + e + i)) = v4f{dw[b][i], dw[b][i + 1], dw[b][i + 2], dw[b][i + 3]};
+      if (e + i < k) {
+        v4f v = {dw[b][i], dw[b][i + 1], dw[b][i + 2], dw[b][i + 3]};
+        if (A.add) v += *G(reinterpret_cast<const v4f*>(part + e + i));
+        *G(reinterpret_cast<v4f*>(part + e + i)) = v;
+      }
   }
 }
 
@@ -446,7 +450,7 @@ __global__ __launch_bounds__(kLongT) void norm_backward_long_kernel(const NormBw
   int it = 0;
   for (int64_t m = blockIdx.x; m < A.m; m += gridDim.x, it ^= 1) {
     const int64_t row = m * k;
-    const bool first = m < (int64_t)gridDim.x;
+    const bool first = m < (int64_t)gridDim.x && !A.add;
     const float rstd = *G(A.rstd + m);
     float dot = 0.0f;
     for (int e = 8 * tid; e < k; e += 8 * kLongT) {
@@ -542,14 +546,23 @@ hipError_t launch_norm_quant(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Two rows a workgroup, or more where that would be over 512 partial rows to
+// join (8191 x 2560: 512 and 768 alike, 1024 slower).  A few short rows are one
+// workgroup's, which writes dweight itself, where the rows one after the other
+// cost less than a second launch (8 rows of 512: 5.4 us against 7.8; 6 of 4096:
+// 7.2 against 7.9, but 8 of them 8.9; 2 of 14336: 7.1 against 10.5, 4 of them 11.1).
+// (Rows over 16384 columns: one a workgroup, their sums go through memory.)
 int norm_backward_blocks(int64_t m, int64_t k) {
-  (void)k;
-  return (int)(m <= 1024 ? (m + 1) / 2 : 512);
+  if (k > 8 * 4 * kBwdT) return (int)(m <= 512 ? m : 512);
+  return (int)(m <= 8 && m * k <= 28672 ? 1 : (m <= 1024 ? (m + 1) / 2 : 512));
 }
 
-hipError_t launch_norm_backward(const NormBwdArgs& a, float* dweight, bool accumulate,
-                                hipStream_t s) {
+hipError_t launch_norm_backward(NormBwdArgs a, float* dweight, bool accumulate, hipStream_t s) {
   const int g = norm_backward_blocks(a.m, a.k);
+  if (g == 1) {
+    a.part = dweight;
+    a.add = accumulate ? 1 : 0;
+  }
   const int pieces = (a.k + 7) / 8;
   if (pieces <= kBwdT)
     norm_backward_kernel<1><<<g, threads_for(pieces, 1), 0, s>>>(a);
@@ -560,7 +573,7 @@ hipError_t launch_norm_backward(const NormBwdArgs& a, float* dweight, bool accum
   else
     norm_backward_long_kernel<<<g, kLongT, 0, s>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.part) return e;
+  if (e != hipSuccess || !dweight || g == 1) return e;
   column_join_kernel<<<(unsigned)((a.k + 15) / 16), 1024, 0, s>>>(a.part, g, a.k, dweight,
                                                                  accumulate ? 1 : 0);
   return hipGetLastError();

@@ -71,7 +71,7 @@ size_t bitlinear_rms_norm_quant_backward_workspace_bytes(int64_t m, int64_t k,
  *   dweight = sum_m dn * z                                 (fp32 [K])
  * Sums are fp32.  dweight may be NULL; with accumulate != 0 the sum is added
  * to what dweight holds.  dx may be dn or dh themselves, and must not overlap
- * an input otherwise.  One kernel, two with dweight. */
+ * an input otherwise.  One kernel; two with dweight, but for a few short rows. */
 bl_status bitlinear_rms_norm_quant_backward(
     int64_t m, int64_t k, const uint16_t *dn, const uint16_t *h, const float *rstd,
     const void *weight, int32_t weight_type, const uint16_t *dh, uint16_t *dx,

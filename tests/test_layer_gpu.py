@@ -140,7 +140,7 @@ def check_norm_backward(out, dxt, dwt, k, m, dh):
 
 @pytest.mark.parametrize("weight", ["none", "bf16", "fp32"])
 @pytest.mark.parametrize("with_dh", [False, True])
-@pytest.mark.parametrize("m,k", [(1, 4), (1, 2048), (3, 12), (40, 2052), (9, 4096), (2, 14332), (3, 16384),
+@pytest.mark.parametrize("m,k", [(1, 4), (1, 2048), (3, 12), (8, 1032), (9, 1032), (8, 16388), (40, 2052), (9, 4096), (2, 14332), (3, 16384),
                                  (5, 16388), (1500, 64), (1100, 260), (1030, 16388)])
 def test_norm_backward(bl, m, k, with_dh, weight):
     rng = np.random.default_rng([4, m, k])
@@ -158,9 +158,9 @@ def test_norm_backward(bl, m, k, with_dh, weight):
     assert (dw is None) == (weight == "none")
 
 
-def test_norm_backward_in_place_and_accumulate(bl):
+@pytest.mark.parametrize("m,k", [(37, 2056), (5, 2056), (8, 2056), (8, 8192), (7, 33000), (1, 33000)])
+def test_norm_backward_in_place_and_accumulate(bl, m, k):
     rng = np.random.default_rng(5)
-    m, k = 37, 2056
     h, dn, dh = rows(rng, m, k), bf16_bits(rng.standard_normal((m, k))), bf16_bits(rng.standard_normal((m, k)))
     rstd = torch.from_numpy(ref.rms_rstd(h, 1e-5).astype(np.float32)).to(DEV)
     wt, _ = make_weight(rng, "fp32", k)

@@ -74,7 +74,7 @@ def test_norm_refusals(lib):
         assert norm(lib, **bad) == EINVAL, bad
 
 
-def nback(lib, m=2, k=64, dn=A[0], h=A[1], rstd=A[2], w=A[3], wt=2, dh=A[4], dx=A[5], dw=A[6], acc=0, ws=A[7], n=BIG):
+def nback(lib, m=20, k=64, dn=A[0], h=A[1], rstd=A[2], w=A[3], wt=2, dh=A[4], dx=A[5], dw=A[6], acc=0, ws=A[7], n=BIG):
     return lib.bitlinear_rms_norm_quant_backward(m, k, dn, h, rstd, w, wt, dh, dx, dw, acc, ws, n, None)
 
 
@@ -89,8 +89,8 @@ def test_norm_backward_refusals(lib):
         assert nback(lib, **bad) == EINVAL
     for name in ("dn", "h", "rstd", "w", "dh", "dx", "dw", "ws"):
         assert nback(lib, **{name: ODD}) == EALIGN, name
-    size = need(2, 64, 1)
-    assert size >= 64 * 4 and need(2, 64, 0) == 0
+    size = need(20, 64, 1)
+    assert size >= 64 * 4 and need(20, 64, 0) == 0 and need(8, 64, 1) == 0
     assert nback(lib, ws=None) == EWORKSPACE and nback(lib, n=ctypes.c_size_t(size - 1)) == EWORKSPACE
     for bad in (dict(dx=A[1]), dict(dx=P(A[0].value + 64)), dict(dw=A[0]), dict(dw=A[3]), dict(ws=A[1]), dict(ws=A[5]),
                 dict(ws=A[6])):
