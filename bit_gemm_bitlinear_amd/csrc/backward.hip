@@ -531,7 +531,7 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
       __builtin_amdgcn_sched_barrier(0);  // the reads go out ahead of this step's products
       multiply(std::false_type{}, ks, fa[ks & 1], fb[ks & 1], nullptr);
     }
-    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // LDS reads done (lgkmcnt 0)
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slab's LDS reads are done
     int8_t* st = smem + buf * kStage;
     if (ISSUE || s + 1 < nsl) {
       wait_vm<ISSUE ? (NST - 2) * D : 0>();
