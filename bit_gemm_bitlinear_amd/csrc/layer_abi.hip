@@ -63,7 +63,7 @@ struct Range {
 };
 
 bool overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p) return false;
+  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
   return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
 }

@@ -30,18 +30,28 @@ from . import bitlinear as bl
 __all__ = ["BitLinear", "linear", "norm_linear"]
 
 
-def _rows(x: torch.Tensor) -> torch.Tensor:
-    return x.reshape(-1, x.shape[-1]).contiguous()
+def _aligned(t: torch.Tensor | None):
+    """`t` as the kernels take it: contiguous, and copied where it starts off a
+    16-byte boundary (a slice of a larger tensor, the gradient that a
+    concatenation hands to its parts)."""
+    if t is None:
+        return None
+    t = t.detach().contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _rows(x: torch.Tensor | None):
+    return None if x is None else _aligned(x.reshape(-1, x.shape[-1]))
 
 
 def _project(q, x_scale, weights, biases):
     """Packs each latent weight and runs all projections on one set of codes:
     (outputs, packed weights, weight scales)."""
-    packs = [bl.pack_weights(w.detach().contiguous()) for w in weights]
+    packs = [bl.pack_weights(_aligned(w)) for w in weights]
     packed, scales = [p for p, _ in packs], [s for _, s in packs]
     count = len(weights)
     ys = bl.GroupedQuantizedCall([q] * count, [x_scale] * count, packed, scales,
-                                 biases=[None if b is None else b.detach() for b in biases])()
+                                 biases=[_aligned(b) for b in biases])()
     return ys, packed, scales
 
 
@@ -71,7 +81,7 @@ def _project_backward(ctx, first, dys, q, x_scale, packed, scales, want_dx):
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias):
-        rows = _rows(x.detach())
+        rows = _rows(x)
         q, xs = bl.act_quant(rows)
         (y,), packed, scales = _project(q, xs, [weight], [bias])
         ctx.save_for_backward(q, xs, packed[0], scales[0])
@@ -94,9 +104,7 @@ class _NormLinear(torch.autograd.Function):
         count = len(params) // 2
         weights, biases = params[:count], params[count:]
         ctx.set_materialize_grads(False)
-        normed = bl.rms_norm_quant(
-            _rows(x.detach()), None if norm_weight is None else norm_weight.detach().contiguous(),
-            None if residual is None else _rows(residual.detach()), eps)
+        normed = bl.rms_norm_quant(_rows(x), _aligned(norm_weight), _rows(residual), eps)
         ys, packed, scales = _project(normed.q, normed.x_scale, weights, biases)
         ctx.save_for_backward(normed.q, normed.x_scale, normed.h, normed.rstd, norm_weight,
                               *packed, *scales)
@@ -117,8 +125,7 @@ class _NormLinear(torch.autograd.Function):
                                          want_x or want_r or want_norm)
         dx = dweight = None
         if dn is not None:
-            dx, dweight = bl.rms_norm_quant_backward(dn, h, rstd, norm_weight,
-                                                     None if dh is None else _rows(dh))
+            dx, dweight = bl.rms_norm_quant_backward(dn, h, rstd, _aligned(norm_weight), _rows(dh))
             dx = dx.reshape(ctx.x_shape)
             if want_norm:
                 dweight = dweight.to(norm_weight.dtype)

@@ -313,3 +313,45 @@ def test_same_weight_twice_and_broadcast_input(bl, tr):
     assert x.grad.shape == x.shape
     # torch adds the 24 rows in bf16 or wider: at most a bf16 rounding a term
     assert bool(((x.grad[0].double() - s).abs() <= 24 * BF * dx.double().abs().sum(0)).all())
+
+
+def test_slices_off_the_alignment(bl, tr):
+    """Inputs and gradients that start off a 16-byte boundary or are strided
+    (slices of fused parameters, the parts of a concatenation, a norm weight
+    expanded from one value) give what aligned copies of them give."""
+    g = gen(8)
+    m, k, n = 5, 132, 33
+
+    def parts():
+        x = leaf((m + 1, k), g)                  # x[1:] starts 8 bytes past a boundary
+        w = leaf((n + 3, k + 4), g, torch.float32, 0.02)
+        b = leaf((n + 1,), g)
+        nw = leaf((1,), g, torch.float32)
+        r = leaf((m, k + 3), g)
+        return x, w, b, nw, r
+
+    x, w, b, nw, r = parts()
+    views = (x[1:], w[3:, :k], b[1:], nw.expand(k), r[:, 3:])
+    copies = [v.detach().clone(memory_format=torch.contiguous_format).requires_grad_() for v in views]
+    dys = torch.randn(2 * m + 1, n, generator=g, device=DEV).to(torch.bfloat16)
+    dhs = torch.randn(m + 1, k, generator=g, device=DEV).to(torch.bfloat16)
+
+    def run(x, w, b, nw, r, aligned):
+        h, (y,) = tr.norm_linear(x, [w], nw, r, biases=[b])
+        z = tr.linear(x, w, b)
+        # the parts' gradients are slices that start at odd rows of 33 or 132 columns
+        if aligned:
+            torch.autograd.backward([h, y, z], [dhs[1:].clone(), dys[1:m + 1].clone(), dys[m + 1:].clone()])
+        else:
+            pad = torch.zeros(1, n, dtype=torch.bfloat16, device=DEV)
+            torch.autograd.backward([torch.cat([torch.zeros(1, k, dtype=torch.bfloat16, device=DEV), h]),
+                                     torch.cat([pad, y, z])], [dhs, dys])
+        return h, y, z
+
+    for a, c in zip(run(*views, aligned=False), run(*copies, aligned=True)):
+        assert torch.equal(a, c)
+    cx, cw, cb, cn, cr = (c.grad for c in copies)
+    assert torch.equal(x.grad[1:], cx) and not bool(x.grad[0].any())
+    assert torch.equal(w.grad[3:, :k], cw) and torch.equal(b.grad[1:], cb) and torch.equal(r.grad[:, 3:], cr)
+    # 132 sums of one value, by torch: a rounding each
+    assert bool((nw.grad.double() - cn.double().sum()).abs() <= 132 * U * cn.double().abs().sum())
