@@ -186,13 +186,13 @@ __device__ __forceinline__ void store_codes(int8_t* q, int n, const Piece& v, fl
 
 // fp32(1 / sqrt(sum / k + eps)) from the hardware's fp64 estimate y and one
 // third-order step: with r = 1 - x y^2, 1 / sqrt(x) = y (1 + r / 2 + 3 r^2 / 8 + O(r^3)),
-// exact to fp64 rounding.  (Square root and divisions proper are some 80 fp64
+// exact to fp64 rounding; 0 where the residual add has overflowed to infinity.  (Square root and divisions proper are some 80 fp64
 // instructions in every wave: 2.7 us of the 12 us of 2048 rows of 2560.)
 __device__ __forceinline__ float rstd_of(double sum, double inv_k, double eps) {
   const double x = __builtin_fma(sum, inv_k, eps);
   const double y = __builtin_amdgcn_rsq(x);
   const double r = __builtin_fma(-x * y, y, 1.0);
-  return (float)__builtin_fma(y * r, __builtin_fma(r, 0.375, 0.5), y);
+  return y == 0.0 ? 0.0f : (float)__builtin_fma(y * r, __builtin_fma(r, 0.375, 0.5), y);
 }
 
 // Rows go over two grid dimensions: one alone holds 2^32 threads.

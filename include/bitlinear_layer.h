@@ -21,7 +21,9 @@
  *             (the output head).
  *
  * Shapes: as in bitlinear.h (M, N, K >= 1; K % 4 == 0; K <= 2^22; N <= 2^30;
- * M <= 2^24; products below 2^40) unless a function says otherwise.
+ * M <= 2^24; products below 2^40) unless a function says otherwise.  Inputs
+ * must be finite, as there; a value that is not spoils the outputs whose
+ * formula reads it, and no others.
  * Two launches that overlap in time must not share a workspace.
  */
 #ifndef BITLINEAR_LAYER_H

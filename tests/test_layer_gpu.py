@@ -99,6 +99,27 @@ def test_norm_quant(bl, m, k, residual, weight):
     assert torch.equal(q2, got.q) and torch.equal(s2, got.x_scale)
 
 
+@pytest.mark.parametrize("k", [64, 4100, 9000, 16388])
+def test_norm_not_finite_stays_in_its_row(bl, k):
+    """A residual add that overflows, or a NaN: 1 / rms of 0 or NaN, and no
+    other row's outputs or gradients change."""
+    rng = np.random.default_rng([6, k])
+    x, r = rows(rng, 9, k), rows(rng, 9, k)
+    wt, _ = make_weight(rng, "bf16", k)
+    dn, dh = to_dev(rows(rng, 9, k)), to_dev(rows(rng, 9, k))
+    clean = bl.rms_norm_quant(to_dev(x), wt, to_dev(r), want_norm=True)
+    cdx, _ = bl.rms_norm_quant_backward(dn, clean.h, clean.rstd, wt, dh)
+    xt, rt = to_dev(x), to_dev(r)
+    xt[2, k - 1] = rt[2, k - 1] = 3e38
+    xt[5, 1] = float("nan")
+    got = bl.rms_norm_quant(xt, wt, rt, want_norm=True)
+    assert got.rstd[2] == 0 and bool(got.rstd[5].isnan())
+    dx, _ = bl.rms_norm_quant_backward(dn, got.h, got.rstd, wt, dh)
+    keep = [0, 1, 3, 4, 6, 7, 8]
+    for a, c in zip((*got, dx), (*clean, cdx)):
+        assert torch.equal(a[keep], c[keep])
+
+
 @pytest.mark.parametrize("k", [64, 2052, 16388])
 @pytest.mark.parametrize("which", ["x", "residual"])
 def test_norm_quant_in_place(bl, k, which):
