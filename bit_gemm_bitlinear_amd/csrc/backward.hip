@@ -606,8 +606,12 @@ __device__ __forceinline__ bool tile_of(int l, const GemmJob& J, int* ti, int* t
 // each product, by four waves (two workgroups a CU), and tiles of 256 x 256 by
 // eight.  Slab rings are as deep as the LDS allows (two-bit slabs are smaller).
 // 2048 x 4096 x 14336, both gradients: 405-435 us by box, 1110-1190 TFLOP/s, the
-// matrix cores busy 61% of the cycles; 2048 x 6912 x 2560: 130 us.  A quarter of
-// the waves' time goes into waiting at the slabs' barriers.
+// matrix cores busy 61% of the cycles; 2048 x 6912 x 2560: 130 us.  What bounds
+// them is the clock that the power of the products leaves: the same launch on
+// zeros takes 329 us in place of 413, and 4096 cubed 95 in place of 112 (an 87-90
+// and 110-120 us library product).  Loads that always hit the caches gain 4% on dw
+// and nothing on dx; tiles of 128 x 256, two workgroups a CU that do not wait for
+// each other, gain nothing (4096 cubed 115 us, 2048 x 4096 x 14336 205 against 203).
 constexpr int kDeep64 = 4, kDeep64c = 8, kDeep128 = 2, kDeep128c = 4, kDeep256 = 2, kDeep256c = 4;
 constexpr int ring_bytes(int t, int deep, int deepc) {
   return std::max(deep * stage_bytes(t, t, false), deepc * stage_bytes(t, t, true));
