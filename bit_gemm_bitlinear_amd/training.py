@@ -44,6 +44,15 @@ def _rows(x: torch.Tensor | None):
     return None if x is None else _aligned(x.reshape(-1, x.shape[-1]))
 
 
+def _check_weights(weights, k):
+    """Latent weights [N_i, K] for inputs of `k` columns.  Checked here: a packed
+    weight of 16 K columns has the bytes of a tiled one with 16 N rows, and is
+    taken for it."""
+    for w in weights:
+        if w.dim() != 2 or w.shape[1] != k:
+            raise ValueError(f"a weight must have shape [N, {k}], got {list(w.shape)}")
+
+
 def _project(q, x_scale, weights, biases):
     """Packs each latent weight and runs all projections on one set of codes:
     (outputs, packed weights, weight scales)."""
@@ -138,6 +147,7 @@ class _NormLinear(torch.autograd.Function):
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
     """BitLinear of bf16 x [..., K] on latent fp32 weights [N, K] and an
     optional bf16 bias [N]: bf16 [..., N], differentiable in all three."""
+    _check_weights([weight], x.shape[-1])
     return _Linear.apply(x, weight, bias)
 
 
@@ -155,6 +165,7 @@ def norm_linear(x: torch.Tensor, weights: Sequence[torch.Tensor],
         raise ValueError("norm_linear: at least one weight, and one bias (or None) for each")
     if residual is not None and residual.shape != x.shape:
         raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
+    _check_weights(weights, x.shape[-1])
     out = _NormLinear.apply(x, residual, norm_weight, eps, *weights, *biases)
     return (x, list(out)) if residual is None else (out[0], list(out[1:]))
 

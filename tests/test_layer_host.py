@@ -265,3 +265,18 @@ def test_oracle_norm_matches_the_activation_quantization():
     assert np.array_equal(q, q2) and np.array_equal(s, s2)
     # unit root mean square, to the rounding to bf16 and eps
     assert np.all(np.abs((oracle.bf16_to_f32(n).astype(np.float64) ** 2).mean(1) - 1) <= 2 ** -6)
+
+
+# ------------------------------------------------------------------ training form
+
+def test_training_refuses_weights_of_another_width(bl):
+    """Before anything else, so host tensors show it."""
+    from bit_gemm_bitlinear_amd import training as tr
+
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    for shape in ((16, 4096), (16, 1024), (16, 64), (16, 252), (256,), (2, 16, 256)):
+        w = torch.zeros(shape)
+        for call in (lambda: tr.linear(x, w), lambda: tr.norm_linear(x, [w]), lambda: tr.norm_linear(x, [w], None, x),
+                     lambda: tr.norm_linear(x, [torch.zeros(16, 256), w])):
+            with pytest.raises(ValueError, match="weight"):
+                call()

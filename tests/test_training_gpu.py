@@ -355,3 +355,18 @@ def test_slices_off_the_alignment(bl, tr):
     assert torch.equal(w.grad[3:, :k], cw) and torch.equal(b.grad[1:], cb) and torch.equal(r.grad[:, 3:], cr)
     # 132 sums of one value, by torch: a rounding each
     assert bool((nw.grad.double() - cn.double().sum()).abs() <= 132 * U * cn.double().abs().sum())
+
+
+# ------------------------------------------------------------------ weights of another width
+
+def test_weight_of_another_width_is_refused(tr):
+    """A latent weight must have x's columns; one of sixteen times as many
+    has the bytes of a tiled weight with sixteen times the rows."""
+    g = gen(13)
+    x, r = leaf((4, 256), g), leaf((4, 256), g)
+    for shape in ((16, 4096), (16, 1024), (16, 64), (16, 252), (256,), (2, 16, 256)):
+        w = leaf(shape, g, torch.float32, 0.02)
+        for call in (lambda: tr.linear(x, w), lambda: tr.norm_linear(x, [w]), lambda: tr.norm_linear(x, [w], None, r),
+                     lambda: tr.norm_linear(x, [leaf((16, 256), g, torch.float32), w])):
+            with pytest.raises(ValueError, match="weight"):
+                call()
