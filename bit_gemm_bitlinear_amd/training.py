@@ -75,7 +75,7 @@ def _project_backward(ctx, first, dys, q, x_scale, packed, scales, want_dx):
             dws.append(None)
             dbs.append(None)
             continue
-        dy = _rows(dy)
+        dy = _aligned(dy)
         weight = want_w or want_b  # the kernel's bias sums come with the weights'
         dx, dw, db = bl.BackwardCall(
             dy, q if weight else None, x_scale if weight else None, packed[i] if want_dx else None,
@@ -88,15 +88,17 @@ def _project_backward(ctx, first, dys, q, x_scale, packed, scales, want_dx):
 
 
 class _Linear(torch.autograd.Function):
+    """Output rows [M, N], which the caller shapes: of a view made in here,
+    autograd refuses in-place operations."""
+
     @staticmethod
     def forward(ctx, x, weight, bias):
-        rows = _rows(x)
-        q, xs = bl.act_quant(rows)
+        q, xs = bl.act_quant(_rows(x))
         (y,), packed, scales = _project(q, xs, [weight], [bias])
         ctx.save_for_backward(q, xs, packed[0], scales[0])
         ctx.bias_types = [None if bias is None else bias.dtype]
         ctx.x_shape = x.shape
-        return y.reshape(*x.shape[:-1], weight.shape[0])
+        return y
 
     @staticmethod
     @once_differentiable
@@ -108,6 +110,11 @@ class _Linear(torch.autograd.Function):
 
 
 class _NormLinear(torch.autograd.Function):
+    """Rows (see _Linear) of h, with a residual, and of the outputs.  x and the
+    residual are not views of rows made outside: they get one gradient tensor,
+    which autograd copies for one of two leaves; of two views it would keep
+    both, as buffers that share memory."""
+
     @staticmethod
     def forward(ctx, x, residual, norm_weight, eps, *params):
         count = len(params) // 2
@@ -120,8 +127,7 @@ class _NormLinear(torch.autograd.Function):
         ctx.bias_types = [None if b is None else b.dtype for b in biases]
         ctx.count, ctx.x_shape = count, x.shape
         ctx.has_residual = residual is not None
-        ys = [y.reshape(*x.shape[:-1], y.shape[1]) for y in ys]
-        return (normed.h.reshape(x.shape), *ys) if residual is not None else tuple(ys)
+        return (normed.h, *ys) if residual is not None else tuple(ys)
 
     @staticmethod
     @once_differentiable
@@ -134,12 +140,12 @@ class _NormLinear(torch.autograd.Function):
                                          want_x or want_r or want_norm)
         dx = dweight = None
         if dn is not None:
-            dx, dweight = bl.rms_norm_quant_backward(dn, h, rstd, _aligned(norm_weight), _rows(dh))
+            dx, dweight = bl.rms_norm_quant_backward(dn, h, rstd, _aligned(norm_weight), _aligned(dh))
             dx = dx.reshape(ctx.x_shape)
             if want_norm:
                 dweight = dweight.to(norm_weight.dtype)
         elif dh is not None:  # no projection's output was used
-            dx = dh
+            dx = dh.reshape(ctx.x_shape)
         return (dx if want_x else None, dx if want_r else None, dweight if want_norm else None, None,
                 *dws, *dbs)
 
@@ -148,7 +154,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     """BitLinear of bf16 x [..., K] on latent fp32 weights [N, K] and an
     optional bf16 bias [N]: bf16 [..., N], differentiable in all three."""
     _check_weights([weight], x.shape[-1])
-    return _Linear.apply(x, weight, bias)
+    return _Linear.apply(x, weight, bias).reshape(*x.shape[:-1], weight.shape[0])
 
 
 def norm_linear(x: torch.Tensor, weights: Sequence[torch.Tensor],
@@ -158,7 +164,8 @@ def norm_linear(x: torch.Tensor, weights: Sequence[torch.Tensor],
     optional bf16 or fp32 weight [K], then the BitLinears `weights` (latent
     fp32 [N_i, K], up to 16) of its output.  Returns (h, outputs): h is the sum
     with the residual, what the next residual add takes (x itself without one),
-    outputs a list of bf16 [..., N_i]; differentiable throughout."""
+    outputs a list of bf16 [..., N_i]; differentiable throughout.  The backward
+    pass needs h: changed in place before it, it is refused there."""
     weights = list(weights)
     biases = [None] * len(weights) if biases is None else list(biases)
     if not weights or len(biases) != len(weights):
@@ -167,7 +174,8 @@ def norm_linear(x: torch.Tensor, weights: Sequence[torch.Tensor],
         raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
     _check_weights(weights, x.shape[-1])
     out = _NormLinear.apply(x, residual, norm_weight, eps, *weights, *biases)
-    return (x, list(out)) if residual is None else (out[0], list(out[1:]))
+    h, out = (x, out) if residual is None else (out[0].reshape(x.shape), out[1:])
+    return h, [y.reshape(*x.shape[:-1], y.shape[1]) for y in out]
 
 
 class BitLinear(torch.nn.Module):

@@ -370,3 +370,61 @@ def test_weight_of_another_width_is_refused(tr):
                      lambda: tr.norm_linear(x, [leaf((16, 256), g, torch.float32), w])):
             with pytest.raises(ValueError, match="weight"):
                 call()
+
+
+# ------------------------------------------------------------------ outputs changed in place
+
+@pytest.mark.parametrize("shape", [(6, 64), (2, 3, 64), (64,)])
+def test_outputs_change_in_place(tr, shape):
+    """Outputs take in-place operations as a torch linear's do, with the
+    gradients of the same operations out of place."""
+    g = gen(14)
+    x, r, b = leaf(shape, g), leaf(shape, g), leaf((24,), g)
+    ws = [leaf((24, 64), g, torch.float32, 0.02) for _ in range(2)]
+    leaves = (x, r, b, *ws)
+    c = torch.randn(*shape[:-1], 24, generator=g, device=DEV).to(torch.bfloat16)
+
+    def grads(in_place):
+        add = torch.Tensor.add_ if in_place else torch.Tensor.add
+        relu = torch.relu_ if in_place else torch.relu
+        y = relu(add(tr.linear(x, ws[0], b), c))
+        h, (u, v) = tr.norm_linear(x, ws, None, r)
+        u, v = add(u, c), relu(v)
+        (z,) = tr.norm_linear(x, [ws[1]])[1]
+        z = add(z, c)
+        return torch.autograd.grad([(t * t).float().sum() for t in (y, u, v, z, h)], leaves)
+
+    for got, want in zip(grads(True), grads(False)):
+        assert torch.equal(got, want)
+
+
+def test_residual_stream_changed_in_place(tr):
+    """h is kept for the backward pass: changed in place it is refused there,
+    and an in-place add is the next residual add instead."""
+    g = gen(15)
+    x, r = leaf((4, 64), g), leaf((4, 64), g)
+    w = leaf((24, 64), g, torch.float32, 0.02)
+    h, (y,) = tr.norm_linear(x, [w], None, r)
+    h.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        (y.float().sum() + h.float().sum()).backward()
+    with torch.no_grad():
+        h, _ = tr.norm_linear(x, [w], None, r)
+        assert torch.equal(h.clone().add_(1), h.add_(1))
+
+
+@pytest.mark.parametrize("shape", [(6, 64), (2, 3, 64)])
+@pytest.mark.parametrize("only_h", [False, True])
+def test_gradients_of_x_and_residual_share_no_memory(tr, shape, only_h):
+    """Equal gradients, accumulated and changed apart."""
+    g = gen(19)
+    x, r = leaf(shape, g), leaf(shape, g)
+    w = leaf((24, 64), g, torch.float32, 0.02)
+    for _ in range(2):
+        h, (y,) = tr.norm_linear(x, [w], None, r)
+        (h if only_h else y).float().sum().backward()
+    once = (torch.ones_like(x) if only_h else
+            torch.autograd.grad(tr.norm_linear(x, [w], None, r)[1][0].float().sum(), x)[0])
+    assert torch.equal(x.grad, once + once) and torch.equal(r.grad, once + once)
+    x.grad.zero_()
+    assert torch.equal(r.grad, once + once)
