@@ -150,11 +150,30 @@ class _NormLinear(torch.autograd.Function):
                 *dws, *dbs)
 
 
+class _NoTokens(torch.autograd.Function):
+    """Output rows [0, N] of each of `widths`, for inputs x without a token:
+    every gradient is zero.  (The library's calls take one token or more.)"""
+
+    @staticmethod
+    def forward(ctx, widths, x, *params):
+        bl._require(x, torch.bfloat16, x.dim(), "x")
+        ctx.like = [(t.shape, t.dtype, t.device) if t is not None else None for t in (x, *params)]
+        return tuple(x.new_empty((0, n)) for n in widths)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        return None, *(torch.zeros(like[0], dtype=like[1], device=like[2]) if want else None
+                       for like, want in zip(ctx.like, ctx.needs_input_grad[1:]))
+
+
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
     """BitLinear of bf16 x [..., K] on latent fp32 weights [N, K] and an
-    optional bf16 bias [N]: bf16 [..., N], differentiable in all three."""
+    optional bf16 bias [N]: bf16 [..., N], differentiable in all three.  Without
+    a token (a leading size of 0) y is empty and every gradient zero."""
     _check_weights([weight], x.shape[-1])
-    return _Linear.apply(x, weight, bias).reshape(*x.shape[:-1], weight.shape[0])
+    y = _Linear.apply(x, weight, bias) if x.numel() else _NoTokens.apply([weight.shape[0]], x, weight, bias)[0]
+    return y.reshape(*x.shape[:-1], weight.shape[0])
 
 
 def norm_linear(x: torch.Tensor, weights: Sequence[torch.Tensor],
@@ -165,7 +184,8 @@ def norm_linear(x: torch.Tensor, weights: Sequence[torch.Tensor],
     fp32 [N_i, K], up to 16) of its output.  Returns (h, outputs): h is the sum
     with the residual, what the next residual add takes (x itself without one),
     outputs a list of bf16 [..., N_i]; differentiable throughout.  The backward
-    pass needs h: changed in place before it, it is refused there."""
+    pass needs h: changed in place before it, it is refused there.  Without a
+    token everything is empty and every gradient zero, as in linear()."""
     weights = list(weights)
     biases = [None] * len(weights) if biases is None else list(biases)
     if not weights or len(biases) != len(weights):
@@ -173,7 +193,12 @@ def norm_linear(x: torch.Tensor, weights: Sequence[torch.Tensor],
     if residual is not None and residual.shape != x.shape:
         raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
     _check_weights(weights, x.shape[-1])
-    out = _NormLinear.apply(x, residual, norm_weight, eps, *weights, *biases)
+    if x.numel():
+        out = _NormLinear.apply(x, residual, norm_weight, eps, *weights, *biases)
+    else:
+        widths = [w.shape[0] for w in weights]
+        out = _NoTokens.apply(widths if residual is None else [x.shape[-1], *widths], x, residual, norm_weight,
+                              *weights, *biases)
     h, out = (x, out) if residual is None else (out[0].reshape(x.shape), out[1:])
     return h, [y.reshape(*x.shape[:-1], y.shape[1]) for y in out]
 

@@ -428,3 +428,34 @@ def test_gradients_of_x_and_residual_share_no_memory(tr, shape, only_h):
     assert torch.equal(x.grad, once + once) and torch.equal(r.grad, once + once)
     x.grad.zero_()
     assert torch.equal(r.grad, once + once)
+
+
+# ------------------------------------------------------------------ no tokens
+
+@pytest.mark.parametrize("shape", [(0, 64), (3, 0, 64)])
+def test_no_tokens(tr, shape):
+    """A batch without tokens has empty outputs, and every gradient is zero."""
+    g = gen(16)
+    x, r, b, nw = leaf(shape, g), leaf(shape, g), leaf((24,), g), leaf((64,), g, torch.float32)
+    ws = [leaf((24, 64), g, torch.float32, 0.02), leaf((8, 64), g, torch.float32, 0.02)]
+    leaves = (x, r, b, nw, *ws)
+    y = tr.linear(x, ws[0], b)
+    h, (u, v) = tr.norm_linear(x, ws, nw, r, biases=[b, None])
+    h2, (z,) = tr.norm_linear(x, [ws[1]], nw)
+    assert h2 is x
+    for t, n in ((y, 24), (u, 24), (v, 8), (z, 8), (h, 64)):
+        assert t.shape == (*shape[:-1], n) and t.dtype == torch.bfloat16 and t.device == x.device
+    torch.autograd.backward([y, u, v, z, h], [torch.zeros_like(t) for t in (y, u, v, z, h)])
+    for t in leaves:
+        assert t.grad.shape == t.shape and t.grad.dtype == t.dtype and not bool(t.grad.any())
+    w = leaf((24, 64), g, torch.float32)
+    w.grad = torch.ones_like(w)
+    tr.BitLinear(64, 24, device=DEV)(x).sum().backward()
+    tr.linear(x, w).sum().backward()
+    assert bool((w.grad == 1).all())
+    with torch.no_grad():
+        assert tr.linear(x, w).shape == (*shape[:-1], 24)
+    with pytest.raises(ValueError):
+        tr.linear(x, leaf((24, 68), g, torch.float32))
+    with pytest.raises(TypeError):
+        tr.linear(x.float(), w)
