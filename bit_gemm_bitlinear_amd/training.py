@@ -76,13 +76,21 @@ def _project_backward(ctx, first, dys, q, x_scale, packed, scales, want_dx):
             dbs.append(None)
             continue
         dy = _aligned(dy)
-        weight = want_w or want_b  # the kernel's bias sums come with the weights'
-        dx, dw, db = bl.BackwardCall(
-            dy, q if weight else None, x_scale if weight else None, packed[i] if want_dx else None,
-            scales[i] if want_dx else None, bias=want_b, k=q.shape[1], residual=dn, dx=dn)()
+        # The kernel's bias sums come with the weights' product: of four columns
+        # where the weights' gradient is not wanted.
+        codes, dx, dw, db = q if want_w else None, None, None, None
+        if want_b and not want_w:
+            db = bl.backward_weight(dy, q[:, :4].contiguous(), x_scale, bias=True)[1]
+        if want_w or want_dx:
+            # Layers that share an input add their gradients up in bf16, rounded
+            # after each: what autograd does with a gradient of the input's type.
+            dx, dw, sums = bl.BackwardCall(
+                dy, codes, x_scale if want_w else None, packed[i] if want_dx else None,
+                scales[i] if want_dx else None, bias=want_b and want_w, k=q.shape[1], residual=dn, dx=dn)()
+            db = sums if want_w else db
         if want_dx:
             dn = dx
-        dws.append(dw if want_w else None)
+        dws.append(dw)
         dbs.append(db.to(ctx.bias_types[i]) if want_b else None)
     return dn, dws, dbs
 

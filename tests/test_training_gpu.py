@@ -459,3 +459,32 @@ def test_no_tokens(tr, shape):
         tr.linear(x, leaf((24, 68), g, torch.float32))
     with pytest.raises(TypeError):
         tr.linear(x.float(), w)
+
+
+# ------------------------------------------------------------------ gradients that are not wanted
+
+def backward_memory(loss):
+    """Device memory that the backward pass takes at its largest."""
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    loss.backward()
+    torch.cuda.synchronize()
+    return torch.cuda.max_memory_allocated() - before
+
+
+def test_bias_gradient_alone(bl, tr):
+    """Over frozen weights the gradient of a bias does not make the weights'."""
+    g = gen(17)
+    m, n, k = 70, 2048, 4096
+    x, w, b = leaf((m, k), g), leaf((n, k), g, torch.float32, 0.02), leaf((n,), g)
+    dy = torch.randn(m, n, generator=g, device=DEV).to(torch.bfloat16)
+    for inputs in ((x.detach(), w.detach(), b), (x, w.detach(), b)):
+        b.grad = x.grad = None
+        took = backward_memory((tr.linear(*inputs) * dy).sum())
+        s = dy.double().sum(0)
+        assert bool(((b.grad.double() - s).abs() <= BF * s.abs() + (1 + BF) * (m + 2) * U * dy.double().abs().sum(0)).all())
+        assert took < 4 * n * k
+        if inputs[0] is x:
+            packed, ws = bl.pack_weights(w.detach())
+            assert torch.equal(x.grad, bl.backward_input(dy, packed, ws))
