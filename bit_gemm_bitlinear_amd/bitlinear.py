@@ -573,11 +573,12 @@ class NormQuantBackwardCall:
     norm's output (the codes pass it straight through); h, rstd: what the
     forward wrote; dh: bf16 gradient of h, or None.  A call returns (dx,
     dweight): dx bf16 [M, K] is the gradient of x and of the residual, dweight
-    fp32 [K] that of the weight (None without a weight); with accumulate it is
-    added to the given `dweight`."""
+    fp32 [K] that of the weight (None without a weight, and with want_dweight
+    False, for a frozen one); with accumulate it is added to the given
+    `dweight`."""
 
     def __init__(self, dn, h, rstd, weight=None, dh=None, dx=None, dweight=None,
-                 accumulate: bool = False, workspace=None):
+                 accumulate: bool = False, workspace=None, want_dweight: bool = True):
         _require(dn, torch.bfloat16, 2, "dn")
         (m, k), dev = dn.shape, dn.device
         _require(h, torch.bfloat16, 2, "h", shape=(m, k), device=dev)
@@ -587,10 +588,12 @@ class NormQuantBackwardCall:
             _require(dh, torch.bfloat16, 2, "dh", shape=(m, k), device=dev)
         if accumulate and dweight is None:
             raise ValueError("accumulate needs the dweight to add to")
+        if dweight is not None and not want_dweight:
+            raise ValueError("a dweight is given and want_dweight is False")
         if dx is None:
             dx = torch.empty_like(dn)
         _require(dx, torch.bfloat16, 2, "dx", shape=(m, k), device=dev)
-        if dweight is None and weight is not None:
+        if dweight is None and weight is not None and want_dweight:
             dweight = torch.empty(k, dtype=torch.float32, device=dev)
         if dweight is not None:
             _require(dweight, torch.float32, 1, "dweight", shape=(k,), device=dev)
@@ -606,9 +609,9 @@ class NormQuantBackwardCall:
         return self.dx, self.dweight
 
 
-def rms_norm_quant_backward(dn, h, rstd, weight=None, dh=None):
+def rms_norm_quant_backward(dn, h, rstd, weight=None, dh=None, want_dweight: bool = True):
     """(dx, dweight) of rms_norm_quant (see NormQuantBackwardCall)."""
-    return NormQuantBackwardCall(dn, h, rstd, weight, dh)()
+    return NormQuantBackwardCall(dn, h, rstd, weight, dh, want_dweight=want_dweight)()
 
 
 def restore_activations(q: torch.Tensor, x_scale: torch.Tensor,

@@ -148,7 +148,8 @@ class _NormLinear(torch.autograd.Function):
                                          want_x or want_r or want_norm)
         dx = dweight = None
         if dn is not None:
-            dx, dweight = bl.rms_norm_quant_backward(dn, h, rstd, _aligned(norm_weight), _aligned(dh))
+            dx, dweight = bl.rms_norm_quant_backward(dn, h, rstd, _aligned(norm_weight), _aligned(dh),
+                                                    want_dweight=want_norm)
             dx = dx.reshape(ctx.x_shape)
             if want_norm:
                 dweight = dweight.to(norm_weight.dtype)

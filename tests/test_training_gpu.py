@@ -488,3 +488,28 @@ def test_bias_gradient_alone(bl, tr):
         if inputs[0] is x:
             packed, ws = bl.pack_weights(w.detach())
             assert torch.equal(x.grad, bl.backward_input(dy, packed, ws))
+
+
+def test_frozen_norm_weight(bl, tr):
+    """A frozen norm weight's gradient is not made, nor its workspace."""
+    g = gen(18)
+    m, n, k = 1100, 16, 8192
+    x, w, nw = leaf((m, k), g), leaf((n, k), g, torch.float32, 0.02), leaf((k,), g, torch.float32)
+    dy = torch.randn(m, n, generator=g, device=DEV).to(torch.bfloat16)
+    took, grads = [], []
+    for weight in (nw, nw.detach()):
+        x.grad = None
+        _, (y,) = tr.norm_linear(x, [w.detach()], weight)
+        took.append(backward_memory((y * dy).sum()))
+        grads.append(x.grad)
+    assert torch.equal(*grads)
+    need = bl.lib().bitlinear_rms_norm_quant_backward_workspace_bytes(m, k, 1)
+    assert need >= 4 * 512 * k and took[1] <= took[0] - need
+    normed = bl.rms_norm_quant(x.detach(), nw.detach())
+    dn = torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16)
+    dx, dweight = bl.rms_norm_quant_backward(dn, normed.h, normed.rstd, nw.detach(), want_dweight=False)
+    assert dweight is None
+    assert torch.equal(dx, bl.rms_norm_quant_backward(dn, normed.h, normed.rstd, nw.detach())[0])
+    with pytest.raises(ValueError):
+        bl.NormQuantBackwardCall(dn, normed.h, normed.rstd, nw.detach(), dweight=torch.empty(k, device=DEV),
+                                 want_dweight=False)
