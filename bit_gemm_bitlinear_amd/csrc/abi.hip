@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "internal.hpp"
+#include "layer_internal.hpp"
 #include "prefill_plan.hpp"
 
 using namespace bl;
@@ -185,6 +186,29 @@ struct ProjIO {
   const float* xs_in;    // scales of caller-supplied codes q_in, or nullptr
 };
 
+// Of a forward on codes: the outputs and the workspace overlap nothing that the
+// call reads and not each other; a projection's residual may be its own output.
+// (The contraction reads the caller's scales while it writes the outputs.)
+bool outputs_apart(int32_t count, const ProjIO* io, int64_t m, const void* ws, size_t ws_bytes) {
+  const Range rws = {ws, (int64_t)ws_bytes};
+  for (int i = 0; i < count; ++i) {
+    const ProjIO& a = io[i];
+    const Range in[6] = {{a.q_in, m * a.k},  {a.xs_in, 4 * m},   {a.packed, a.n * (a.k / 4)},
+                         {a.w_scale, 4},     {a.bias, 2 * a.n},  {a.res, 2 * m * a.n}};
+    const Range ya = {a.y, 2 * m * a.n};
+    for (const Range& r : in)
+      if (overlap(rws, r)) return false;
+    if (overlap(rws, ya)) return false;
+    for (int j = 0; j < count; ++j) {
+      const Range yb = {io[j].y, 2 * m * io[j].n};
+      for (int r = 0; r < 6; ++r)
+        if (overlap(yb, in[r]) && !(r == 5 && i == j && a.res == a.y)) return false;
+      if (i != j && overlap(ya, yb)) return false;
+    }
+  }
+  return true;
+}
+
 // Diagnostics of a call: the decode kernel's wait bound and status word.
 struct CallDiag {
   int32_t* status = nullptr;
@@ -206,6 +230,7 @@ bl_status run_forward(int32_t count, const ProjIO* io, int64_t m, void* workspac
   if (!workspace) return BL_EWORKSPACE;
   if (!aligned16(workspace)) return BL_EALIGN;
   if (ws_bytes < L.total) return BL_EWORKSPACE;
+  if (io[0].xs_in && !outputs_apart(count, io, m, workspace, L.total)) return BL_EINVAL;
   if (io[0].x != nullptr) make_layout(count, ns, ks, m, true, L);
   char* ws = static_cast<char*>(workspace);
 

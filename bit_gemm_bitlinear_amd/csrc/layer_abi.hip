@@ -56,18 +56,6 @@ bl_status check_shape(int64_t m, int64_t n, int64_t k) {
   return BL_OK;
 }
 
-// A range of device memory a call reads or writes (nullptr: none).
-struct Range {
-  const void* p;
-  int64_t bytes;
-};
-
-bool overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
-}
-
 // Outputs must not overlap inputs or each other.
 bool disjoint(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
   for (const Range* o = outs.begin(); o != outs.end(); ++o) {

@@ -1,5 +1,5 @@
-// Internal launch interface of the operators of bitlinear_layer.h, between
-// their entry points (layer_abi.hip) and the kernels.
+// Internal interface of the operators of bitlinear_layer.h, between their entry
+// points (layer_abi.hip; abi.hip for the forward on codes) and the kernels.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -7,6 +7,19 @@
 #include <stdint.h>
 
 namespace bl {
+
+// A range of device memory a call reads or writes (nullptr: none),
+// for the entry points' checks.
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+
+inline bool overlap(const Range& a, const Range& b) {
+  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
 
 // ---- residual add + RMSNorm + int8 codes (norm_quant.hip) ----
 struct NormArgs {

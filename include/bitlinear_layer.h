@@ -98,6 +98,8 @@ typedef struct {
 
 /* bitlinear_forward_grouped on activations that are int8 codes already:
  * codes: HOST array of `count`; every projs[i].x must be NULL (BL_EINVAL).
+ * Outputs and workspace must not overlap an input or each other, but for a
+ * projection's residual that is its own output.
  * Results are those of bitlinear_forward_grouped on the bf16 activations
  * that the codes were made of, bit for bit.  Workspace:
  * bitlinear_forward_grouped_workspace_bytes.  The first kernel brings the

@@ -280,3 +280,32 @@ def test_training_refuses_weights_of_another_width(bl):
                      lambda: tr.norm_linear(x, [torch.zeros(16, 256), w])):
             with pytest.raises(ValueError, match="weight"):
                 call()
+
+
+def test_forward_quantized_refuses_overlaps(bl, lib):
+    """Outputs and workspace apart from what the call reads and from each
+    other; a projection's residual may be its own output, exactly."""
+    size = ctypes.c_size_t(1 << 20)
+    names = ("q", "xs", "packed", "ws", "bias", "res", "y")
+
+    def call(m=20, wsp=A[10].value, **kw):
+        p, c = (bl.Projection * 2)(), (bl.Codes * 2)()
+        for i in range(2):
+            at = {n: 0x1000000000 * (1 + len(names) * i + j) + (1 << 45) for j, n in enumerate(names)}
+            at.update({n[:-1]: v for n, v in kw.items() if n[-1] == str(i)})
+            p[i] = bl.Projection(0, at["packed"], at["ws"], at["y"], 48, 64, 0, 0, at["bias"], at["res"])
+            c[i] = bl.Codes(at["q"], at["xs"])
+        return lib.bitlinear_forward_grouped_quantized(2, p, c, m, P(wsp), size, None)
+
+    y = 1 << 44
+    sizes = dict(q=20 * 64, xs=80, packed=48 * 16, ws=4, bias=96, res=20 * 96)
+    for name, n in sizes.items():
+        for i in (0, 1):
+            last = y + (20 * 96 - 1) // 16 * 16  # the output's last 16 bytes
+            for start in (y + 16, last, y - (n - 1) // 16 * 16):
+                assert call(**{"y0": y, f"{name}{i}": start}) == EINVAL, (name, i, start - y)
+    assert call(y0=y, y1=y) == EINVAL and call(y0=y, y1=y + 20 * 96 - 16) == EINVAL
+    assert call(y0=y, res1=y) == EINVAL  # another projection's output
+    for name in ("q", "xs", "packed", "ws", "bias", "res", "y"):
+        assert call(wsp=y, **{f"{name}1": y + 64}) == EINVAL, name
+    assert call(wsp=0, y0=y, q0=y) == EWORKSPACE  # checked before
