@@ -120,13 +120,23 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _check(status: int) -> None:
-    if status != 0:
+# The current stream's handle of a device index, and the current device: what
+# torch.cuda.current_stream and current_device look up, without the objects
+# around it (1.9 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(fn, args, device: torch.device, stream=None) -> None:
+    """Calls an entry point on `device`'s current stream (or the given one),
+    with that device current: a kernel goes to the current device."""
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, _raw_stream(device.index) if stream is None else stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device.index) if stream is None else stream)
+    if status:
         raise BitLinearError(status)
-
-
-def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
 def _ptr(t: torch.Tensor):
@@ -189,8 +199,8 @@ def pack_weights(w: torch.Tensor):
     packed = torch.empty((n, k // 4), dtype=torch.uint8, device=w.device)
     w_scale = torch.empty(4, dtype=torch.float32, device=w.device)[:1]
     ws = _workspace(_lib.bitlinear_pack_workspace_bytes(n, k), w.device, None)
-    _check(_lib.bitlinear_pack_weights(_ptr(w), n, k, _ptr(packed), _ptr(w_scale), _ptr(ws),
-                                       _nbytes(ws), _stream(w)))
+    _launch(_lib.bitlinear_pack_weights,
+            (_ptr(w), n, k, _ptr(packed), _ptr(w_scale), _ptr(ws), _nbytes(ws)), w.device)
     return packed, w_scale
 
 
@@ -199,7 +209,7 @@ def unpack_weights(packed: torch.Tensor) -> torch.Tensor:
     _require(packed, torch.uint8, 2, "packed")
     n, kb = packed.shape
     u = torch.empty((n, 4 * kb), dtype=torch.int8, device=packed.device)
-    _check(_lib.bitlinear_unpack_weights(_ptr(packed), n, 4 * kb, _ptr(u), _stream(packed)))
+    _launch(_lib.bitlinear_unpack_weights, (_ptr(packed), n, 4 * kb, _ptr(u)), packed.device)
     return u
 
 
@@ -213,8 +223,8 @@ def export_bf16(packed: torch.Tensor, w_scale: torch.Tensor, k: int | None = Non
         k = 4 * packed.shape[1]
     n, layout = weight_layout(packed, k)
     out = torch.empty((n, k), dtype=torch.bfloat16, device=packed.device)
-    _check(_lib.bitlinear_export_bf16(_ptr(packed), n, k, layout, _ptr(w_scale), _ptr(out),
-                                      _stream(packed)))
+    _launch(_lib.bitlinear_export_bf16, (_ptr(packed), n, k, layout, _ptr(w_scale), _ptr(out)),
+            packed.device)
     return out
 
 
@@ -233,8 +243,8 @@ def forward_latent(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = 
     _require(out, torch.bfloat16, 2, "out", shape=(m, n), device=x.device)
     w_scale = torch.empty(4, dtype=torch.float32, device=x.device)[:1]
     ws = _workspace(int(_lib.bitlinear_forward_latent_workspace_bytes(m, n, k)), x.device, None)
-    _check(_lib.bitlinear_forward_latent(m, n, k, _ptr(x), _ptr(w), _ptr(w_scale), _ptr(out),
-                                         _ptr(ws), _nbytes(ws), _stream(x)))
+    _launch(_lib.bitlinear_forward_latent,
+            (m, n, k, _ptr(x), _ptr(w), _ptr(w_scale), _ptr(out), _ptr(ws), _nbytes(ws)), x.device)
     return out, w_scale
 
 
@@ -247,7 +257,7 @@ def tile_weights(packed: torch.Tensor) -> torch.Tensor:
     if n % 16:
         raise ValueError("the tiled layout needs N % 16 == 0")
     tiled = torch.empty((n // 16, 16 * kb), dtype=torch.uint8, device=packed.device)
-    _check(_lib.bitlinear_tile_weights(_ptr(packed), n, 4 * kb, _ptr(tiled), _stream(packed)))
+    _launch(_lib.bitlinear_tile_weights, (_ptr(packed), n, 4 * kb, _ptr(tiled)), packed.device)
     return tiled
 
 
@@ -259,7 +269,7 @@ def untile_weights(tiled: torch.Tensor) -> torch.Tensor:
         raise ValueError("a tiled weight row holds 16 rows of K/4 bytes, K % 256 == 0")
     n, k = 16 * nb, kb16 // 4
     packed = torch.empty((n, k // 4), dtype=torch.uint8, device=tiled.device)
-    _check(_lib.bitlinear_untile_weights(_ptr(tiled), n, k, _ptr(packed), _stream(tiled)))
+    _launch(_lib.bitlinear_untile_weights, (_ptr(tiled), n, k, _ptr(packed)), tiled.device)
     return packed
 
 
@@ -279,7 +289,7 @@ def act_quant(x: torch.Tensor):
     m, k = x.shape
     q = torch.empty((m, k), dtype=torch.int8, device=x.device)
     s = torch.empty(max(m, 4), dtype=torch.float32, device=x.device)[:m]
-    _check(_lib.bitlinear_act_quant(_ptr(x), m, k, _ptr(q), _ptr(s), _stream(x)))
+    _launch(_lib.bitlinear_act_quant, (_ptr(x), m, k, _ptr(q), _ptr(s)), x.device)
     return q, s
 
 
@@ -307,8 +317,8 @@ def forward(x: torch.Tensor, packed: torch.Tensor, w_scale: torch.Tensor,
     _require(out, torch.bfloat16, 2, "out", shape=(m, n), device=x.device)
     ws = _workspace(forward_workspace_bytes(m, n, k), x.device, workspace)
     fn = _lib.bitlinear_forward_tiled if layout == LAYOUT_TILED else _lib.bitlinear_forward
-    _check(fn(m, n, k, _ptr(x), _ptr(packed), _ptr(w_scale), _ptr(out),
-              _ptr(ws), _nbytes(ws), _stream(x)))
+    _launch(fn, (m, n, k, _ptr(x), _ptr(packed), _ptr(w_scale), _ptr(out), _ptr(ws), _nbytes(ws)),
+            x.device)
     return out
 
 
@@ -385,10 +395,9 @@ class GroupedCall:
         self._dev = xs[0]
 
     def __call__(self, stream=None):
-        s = ctypes.c_void_p(stream) if stream is not None else _stream(self._dev)
-        _check(_lib.bitlinear_forward_grouped(len(self._arr), self._arr, self.m,
-                                              _ptr(self.workspace),
-                                              _nbytes(self.workspace), s))
+        _launch(_lib.bitlinear_forward_grouped,
+                (len(self._arr), self._arr, self.m, _ptr(self.workspace), _nbytes(self.workspace)),
+                self._dev.device, stream)
         return self.outs
 
 
@@ -416,9 +425,9 @@ def forward_grouped_inspect(xs, packeds, w_scales, wait_polls: int = 0):
                          d["acc"].data_ptr())
         keep.append(d)
     status = torch.zeros(4, dtype=torch.int32, device=dev)
-    _check(_lib.bitlinear_forward_grouped_inspect(
-        len(xs), call._arr, m, ins, _ptr(status), int(wait_polls), _ptr(call.workspace),
-        _nbytes(call.workspace), _stream(call._dev)))
+    _launch(_lib.bitlinear_forward_grouped_inspect,
+            (len(xs), call._arr, m, ins, _ptr(status), int(wait_polls), _ptr(call.workspace),
+             _nbytes(call.workspace)), dev)
     return call.outs, keep, status[:1]
 
 
@@ -435,7 +444,7 @@ def forward_acc(q: torch.Tensor, packed: torch.Tensor, out: torch.Tensor | None 
     _require(out, torch.int32, 2, "out", shape=(m, n), device=q.device)
     ws = _workspace(forward_workspace_bytes(m, n, k), q.device, workspace)
     fn = _lib.bitlinear_forward_acc_tiled if layout == LAYOUT_TILED else _lib.bitlinear_forward_acc
-    _check(fn(m, n, k, _ptr(q), _ptr(packed), _ptr(out), _ptr(ws), _nbytes(ws), _stream(q)))
+    _launch(fn, (m, n, k, _ptr(q), _ptr(packed), _ptr(out), _ptr(ws), _nbytes(ws)), q.device)
     return out
 
 
@@ -468,25 +477,6 @@ class BitLinear:
 # Operators around the product (include/bitlinear_layer.h)
 
 WEIGHT_NONE, WEIGHT_BF16, WEIGHT_F32 = 0, 1, 2  # BL_WEIGHT_*
-
-
-# The current stream's handle of a device index, and the current device: what
-# torch.cuda.current_stream and current_device look up, without the objects
-# around it (1.9 us a call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _launch(fn, args, device: torch.device, stream=None) -> None:
-    """Calls an entry point on `device`'s current stream (or the given one),
-    with that device current: a kernel goes to the current device."""
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, _raw_stream(device.index) if stream is None else stream)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(device.index) if stream is None else stream)
-    if status:
-        raise BitLinearError(status)
 
 
 def _need(t, dtype, name, shape, device):

@@ -309,3 +309,82 @@ def test_forward_quantized_refuses_overlaps(bl, lib):
     for name in ("q", "xs", "packed", "ws", "bias", "res", "y"):
         assert call(wsp=y, **{f"{name}1": y + 64}) == EINVAL, name
     assert call(wsp=0, y0=y, q0=y) == EWORKSPACE  # checked before
+
+
+# ------------------------------------------------------------------ the device of a call
+
+class _OnDevice(torch.Tensor):
+    """A host tensor that says it is on cuda:1."""
+    device = property(lambda self: torch.device("cuda", 1))
+    is_cuda = property(lambda self: True)
+
+
+def test_calls_make_their_tensors_device_current(bl, monkeypatch):
+    """Every call of the binding enqueues on the current stream of its tensors'
+    device with that device current, whichever is current around it: the
+    library launches on the current one."""
+    class Device:
+        def __init__(self, device):
+            self.index = torch.device(device).index if not isinstance(device, int) else device
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    current, calls = [0], []
+    real = {n: getattr(bl._lib, n) for n in bl._SIGS}
+
+    class Lib:
+        def __getattr__(self, name):
+            if "bytes" in name or "launches" in name or "status" in name:
+                return real[name]
+
+            def entry(*args):
+                stream = args[-1]
+                calls.append((name, current[-1], stream.value if isinstance(stream, P) else stream))
+                return OK
+            return entry
+
+    def on_device(make):
+        return lambda *a, **kw: make(*a, **{k: v for k, v in kw.items() if k != "device"}).as_subclass(_OnDevice)
+
+    class Stream:
+        def __init__(self, index):
+            self.cuda_stream = 100 + index
+
+    monkeypatch.setattr(bl, "_lib", Lib())
+    monkeypatch.setattr(bl, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream(torch.device(d).index))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch, "empty", on_device(torch.empty))
+    monkeypatch.setattr(torch, "zeros", on_device(torch.zeros))
+    m, n, k = 3, 16, 256
+    x, y = torch.zeros(m, k, dtype=torch.bfloat16), torch.zeros(m, n, dtype=torch.bfloat16)
+    w, packed, s = torch.zeros(n, k), torch.zeros(n, k // 4, dtype=torch.uint8), torch.zeros(4)
+    q, xs, tiled = torch.zeros(m, k, dtype=torch.int8), torch.zeros(m), torch.zeros(1, 4 * k, dtype=torch.uint8)
+    bias = torch.zeros(n, dtype=torch.bfloat16)
+    made = [
+        lambda: bl.pack_weights(w), lambda: bl.unpack_weights(packed), lambda: bl.export_bf16(packed, s),
+        lambda: bl.forward_latent(x, w), lambda: bl.tile_weights(packed), lambda: bl.untile_weights(tiled),
+        lambda: bl.act_quant(x), lambda: bl.forward(x, packed, s), lambda: bl.forward(x, tiled, s),
+        lambda: bl.forward(x, packed, s, bias=bias), lambda: bl.forward_grouped([x, x], [packed, tiled], [s, s]),
+        lambda: bl.forward_grouped_inspect([x], [packed], [s]), lambda: bl.forward_acc(q, packed),
+        lambda: bl.forward_acc(q, tiled), lambda: bl.rms_norm_quant(x), lambda: bl.rms_norm_quant_backward(x, x, xs),
+        lambda: bl.restore_activations(q, xs), lambda: bl.forward_quantized(q, xs, packed, s),
+        lambda: bl.backward_input(y, packed, s), lambda: bl.backward_weight(y, q, xs),
+        lambda: bl.unpack_weights_w4(bl.pack_weights_w4(w)), lambda: bl.forward_w4(q, xs, bl.pack_weights_w4(w)),
+    ]
+    for around in (0, 1):
+        current[:] = [around]
+        for make in made:
+            calls.clear()
+            make()
+            assert calls and all(c[1:] == (1, 101) for c in calls), calls
+            assert current == [around]
+    for stream, want in ((7, 7), (0, 0)):
+        calls.clear()
+        bl.GroupedCall([x], [packed], [s])(stream)
+        assert calls[0][1] == 1 and (calls[0][2] or 0) == want
