@@ -295,7 +295,7 @@ def test_backward_not_finite_stays_in_its_row(bl):
 
 
 # Shapes by the kernels they take: one launch; operand pass and 64 or 128 tiles;
-# dx in parts; dw in parts; 256 tiles; 256 tiles with dx in parts.
+# dx in parts; dw in parts; 128 tiles; 256 tiles with dx in parts.
 PLANS = [(33, 72, 260), (512, 1024, 1024), (45, 4000, 480), (2048, 512, 512), (300, 4096, 4096), (2048, 6912, 2560)]
 
 
@@ -562,3 +562,180 @@ def test_w4_far_weights(bl):
     want, mag = w4_reference(bl, q, xs, tail)
     assert bool(((y[:, -32:].double() - want).abs() <= BF * want.abs() + (1 + BF) * (2 * (k // group) + 8) * U * mag).all())
     assert bool((y[:, :-32] == 0).all())
+
+
+# ------------------------------------------------------------------ every kernel and plan of the gradients
+
+# Per shape the plan that its gradients take, of both together, of dx alone and of
+# dw alone: "one" for the one-launch kernel, else the tiles of dx and dw and the
+# parts of their sums (None: not wanted).  test_layer_host.py holds the plan to
+# this, so that other costs in it cannot leave a kernel without a test.
+BY_PLAN = {
+    # 256 tiles, ragged in M, N and K; dy laid out; dw stored past the caches
+    (1500, 2050, 4100): ((256, 1, 256, 1), (128, 1, None, None), (None, None, 128, 1)),
+    # the same with dx past the caches too, and a last slab of one token
+    (2049, 1500, 14332): ((256, 1, 256, 1), (256, 1, None, None), (None, None, 128, 1)),
+    # 256 tiles in parts: dx, dw, either alone, whole sizes
+    (2050, 6900, 2564): ((256, 2, 256, 1), (128, 2, None, None), (None, None, 128, 1)),
+    (8190, 2050, 2500): ((256, 1, 256, 2), (128, 1, None, None), (None, None, 128, 3)),
+    (1800, 8100, 2308): ((128, 1, 128, 1), (256, 3, None, None), (None, None, 128, 1)),
+    (8300, 1900, 1924): ((128, 1, 128, 1), (128, 1, None, None), (None, None, 256, 4)),
+    (8192, 2048, 2048): ((256, 1, 256, 2), (256, 1, None, None), (None, None, 256, 4)),
+    # 128 tiles, whole sums and in parts
+    (1025, 2050, 4100): ((128, 1, 128, 1), (128, 1, None, None), (None, None, 128, 1)),
+    (4100, 700, 2052): ((128, 1, 128, 2), (128, 1, None, None), (None, None, 128, 2)),
+    (200, 5000, 1028): ((128, 8, 128, 1), (64, 6, None, None), (None, None, 128, 1)),
+    # 64 and 128 tiles in one launch
+    (700, 5000, 1284): ((64, 1, 128, 1), (64, 2, None, None), (None, None, 128, 1)),
+    (1100, 1100, 1100): ((128, 1, 64, 1), "one", (None, None, 64, 1)),
+    # 64 tiles
+    (600, 600, 600): ((64, 1, 64, 1), "one", (None, None, 64, 1)),
+    (129, 3001, 516): ((64, 6, 64, 1), (64, 8, None, None), "one"),
+    (3001, 129, 516): ((64, 1, 64, 6), "one", (None, None, 64, 8)),
+    # rows of weights shorter than a dword of the two-bit transpose's
+    (1, 2097152, 4): ((64, 16, 128, 1), (64, 16, None, None), (None, None, 128, 1)),
+    (4000, 4097, 8): ((64, 4, 64, 4), (64, 8, None, None), (None, None, 64, 6)),
+    (4000, 4097, 12): ((64, 4, 64, 4), (64, 8, None, None), (None, None, 64, 6)),
+}
+
+
+@pytest.mark.parametrize("m,n,k", list(BY_PLAN))
+def test_backward_by_plan(bl, m, n, k):
+    """Options, rows behind the outputs, and each gradient by itself."""
+    test_backward_options_on_every_plan(bl, m, n, k)
+    test_backward_leaves_what_is_behind(bl, m, n, k)
+    dy, q, xs, packed, ws = layer_case(bl, 80 + m, m, n, k)
+    check_input(bl.backward_input(dy, packed, ws), *input_gradient(bl, dy, packed, ws), n)
+    dw, db = bl.backward_weight(dy, q, xs, bias=True)
+    check_weight(dw, *weight_gradient(bl, dy, q, xs), m)
+    d = dy.double()
+    assert bool(((db.double() - d.sum(0)).abs() <= (m + 2) * U * d.abs().sum(0)).all())
+
+
+# Shapes whose gradients go through a workspace: 64 tiles, sums of dx in parts, of
+# dw in parts, 64 and 128 tiles.
+STAGED = [(600, 600, 600), (45, 4000, 480), (2048, 512, 512), (300, 1000, 2052)]
+
+
+def workspace_bytes(bl, m, n, k):
+    return bl.lib().bitlinear_backward_workspace_bytes(m, n, k, 1, 1)
+
+
+@pytest.mark.parametrize("m,n,k", STAGED)
+def test_staged_gradients_in_a_graph(bl, m, n, k):
+    """Operand pass, products and the sum of the parts, and the norm's gradient
+    with its second launch, captured with the forward calls around them and
+    replayed on new inputs: every replay against the eager result."""
+    assert workspace_bytes(bl, m, n, k) > 0
+    assert bl.lib().bitlinear_rms_norm_quant_backward_workspace_bytes(m, k, 1) > 0
+    g = torch.Generator(device=DEV).manual_seed(m)
+    x, r = (torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    dy = torch.randn(m, n, generator=g, device=DEV).to(torch.bfloat16)
+    w = 1 + 0.1 * torch.randn(k, generator=g, device=DEV)
+    packed, ws = bl.pack_weights(torch.randn(n, k, generator=g, device=DEV))
+    norm = bl.NormQuantCall(x, w, r)
+    product = bl.GroupedQuantizedCall([norm.out.q], [norm.out.x_scale], [packed], [ws])
+    back = bl.BackwardCall(dy, norm.out.q, norm.out.x_scale, packed, ws, bias=True)
+    nback = bl.NormQuantBackwardCall(back._out[0], norm.out.h, norm.out.rstd, w)
+    outs = [norm.out.q, norm.out.x_scale, norm.out.h, product.outs[0], *back._out, nback.dx, nback.dweight]
+
+    def step():
+        norm()
+        product()
+        back()
+        nback()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        x.copy_(torch.randn(m, k, generator=g, device=DEV))
+        dy.copy_(torch.randn(m, n, generator=g, device=DEV))
+        step()
+        want = [t.clone() for t in outs]
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b), i
+
+
+def test_graphs_that_share_a_workspace(bl):
+    """Gradients of several shapes captured over one workspace and replayed one
+    after the other, in changing order: each leaves nothing to the next."""
+    cases = [layer_case(bl, 90 + i, *s) for i, s in enumerate(STAGED)]
+    workspace = torch.empty(max(workspace_bytes(bl, *s) for s in STAGED), dtype=torch.uint8, device=DEV)
+    calls = [bl.BackwardCall(*c, bias=True, workspace=workspace) for c in cases]
+    want = [[t.clone() for t in call()] for call in calls]
+    graphs = []
+    for call in calls:
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for order in ([0, 1, 2, 3], [3, 1, 0, 2], [2, 2, 3, 0]):
+        for i in order:
+            for t in calls[i]._out:
+                t.zero_()
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in order:
+            assert all(torch.equal(a, b) for a, b in zip(calls[i]._out, want[i])), (order, i)
+
+
+def test_staged_gradients_on_side_streams(bl):
+    """Calls with workspaces of their own, in turn on four streams that run at
+    the same time."""
+    cases = [layer_case(bl, 95 + i, *s) for i, s in enumerate(STAGED)]
+    assert all(workspace_bytes(bl, *s) > 0 for s in STAGED)
+    want = [[t.clone() for t in bl.BackwardCall(*c, bias=True)()] for c in cases]
+    torch.cuda.synchronize()
+    streams, calls, got = [torch.cuda.Stream() for _ in cases], [], [[] for _ in cases]
+    for c, s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            calls.append(bl.BackwardCall(*c, bias=True))
+    assert len({c.workspace.data_ptr() for c in calls}) == len(calls)
+    for _ in range(20):
+        for i, (call, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i].append([t.clone() for t in call()])
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        assert all(torch.equal(a, b) for out in outs for a, b in zip(out, want[i])), STAGED[i]
+
+
+def test_staged_gradients_from_threads(bl):
+    """Host threads, each with a shape, stream and workspace of its own, every
+    call's results kept and checked."""
+    import threading
+
+    assert all(workspace_bytes(bl, *s) > 0 for s in STAGED)
+    cases = [layer_case(bl, 100 + i, *s) for i, s in enumerate(STAGED)]
+    want = [[t.clone() for t in bl.BackwardCall(*c, bias=True)()] for c in cases]
+    torch.cuda.synchronize()
+    bad, together = [], threading.Barrier(len(cases))
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                call = bl.BackwardCall(*cases[i], bias=True)
+                together.wait(timeout=30)
+                got = [[t.clone() for t in call()] for _ in range(20)]
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for out in got for a, b in zip(out, want[i])):
+                    bad.append(STAGED[i])
+        except Exception as e:  # reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad

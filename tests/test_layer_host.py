@@ -388,3 +388,89 @@ def test_calls_make_their_tensors_device_current(bl, monkeypatch):
         calls.clear()
         bl.GroupedCall([x], [packed], [s])(stream)
         assert calls[0][1] == 1 and (calls[0][2] or 0) == want
+
+
+# ------------------------------------------------------------------ plan of the gradients
+
+BACKWARD_PLAN_SRC = r'''
+#include "backward_plan.hpp"
+#include <cstdio>
+#include <cstdlib>
+
+int main(int argc, char** argv) {
+  for (int i = 1; i + 2 < argc; i += 3)
+    for (int want = 3; want >= 1; --want) {  // both, dx, dw
+      const bool dx = want != 1, dw = want != 2;
+      const bl::BackwardPlan p = bl::plan_backward(atoll(argv[i]), atoll(argv[i + 1]), atoll(argv[i + 2]), dx, dw);
+      if (p.direct)
+        printf("one\n");
+      else
+        printf("%d %d %d %d %d %d\n", dx ? bl::kConfigs[p.cfg[0]].ti : 0, p.ksplit[0], p.kspw[0],
+               dw ? bl::kConfigs[p.cfg[1]].ti : 0, p.ksplit[1], p.kspw[1]);
+    }
+  return 0;
+}
+'''
+
+
+def backward_plans(tmp_path, shapes):
+    """{shape: plans of both gradients, dx alone, dw alone}: "one" or (tile of
+    dx, parts, slabs a part, tile of dw, parts, slabs a part; tile 0: not wanted)."""
+    src, exe = tmp_path / "backward_plan.cpp", tmp_path / "backward_plan"
+    src.write_text(BACKWARD_PLAN_SRC)
+    csrc = os.path.join(ROOT, "bit_gemm_bitlinear_amd", "csrc")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe), *(str(v) for s in shapes for v in s)], capture_output=True, text=True,
+                         check=True).stdout.splitlines()
+    plans = ["one" if line == "one" else tuple(map(int, line.split())) for line in out]
+    assert len(plans) == 3 * len(shapes)
+    return {s: plans[3 * i:3 * i + 3] for i, s in enumerate(shapes)}
+
+
+def test_gradient_shapes_take_the_plans_they_are_for(tmp_path):
+    """The GPU tests' shapes by plan, every tile size and split among them."""
+    from test_layer_gpu import BY_PLAN, PLANS
+
+    tiles, parts = set(), set()
+    for shape, plans in backward_plans(tmp_path, list(BY_PLAN)).items():
+        for plan, want in zip(plans, BY_PLAN[shape]):
+            if plan == "one" or want == "one":
+                assert plan == want, (shape, plan)
+                continue
+            tx, px, _, tw, pw, _ = plan
+            assert want == (tx or None, px if tx else None, tw or None, pw if tw else None), (shape, plan)
+            for product, tile, p in (("dx", tx, px), ("dw", tw, pw)):
+                if tile:
+                    tiles.add((product, tile, p > 1, all(shape[i] % 64 for i in range(3))))
+    # either product on every tile size, whole and in parts, at ragged sizes
+    for product in ("dx", "dw"):
+        for tile in (64, 128, 256):
+            for split in (False, True):
+                assert (product, tile, split, True) in tiles, (product, tile, split)
+    got = [p[0] for p in backward_plans(tmp_path, PLANS).values()]
+    assert got[0] == "one"
+    assert [(p[0], p[1] > 1, p[3], p[4] > 1) for p in got[1:]] == [
+        (64, False, 64, False), (64, True, 64, False), (64, False, 64, True), (128, False, 128, False),
+        (256, True, 256, False)]
+
+
+def test_gradient_plans_cover_their_sums(tmp_path):
+    """Every split covers its sum with no empty part and at most 16 parts, and
+    the library's workspace queries follow the same plan."""
+    from bit_gemm_bitlinear_amd import bitlinear
+
+    need = bitlinear.lib().bitlinear_backward_workspace_bytes
+    rng = np.random.default_rng(4)
+    shapes = []
+    for _ in range(300):
+        m, n, k = (int(2 ** rng.uniform(0, 14)) for _ in range(3))
+        shapes.append((m, n, 4 * max(1, k // 4)))
+    for (m, n, k), plans in backward_plans(tmp_path, sorted(set(shapes))).items():
+        for plan, dx, dw in zip(plans, (1, 1, 0), (1, 0, 1)):
+            assert (need(m, n, k, dx, dw) == 0) == (plan == "one")
+            if plan == "one":
+                continue
+            for want, c, parts, each in ((dx, n, *plan[1:3]), (dw, m, *plan[4:6])):
+                slabs = -(-c // 64)
+                if want:
+                    assert 1 <= parts <= 16 and parts * each >= slabs > (parts - 1) * each, (m, n, k, plan)

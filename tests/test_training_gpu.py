@@ -513,3 +513,41 @@ def test_frozen_norm_weight(bl, tr):
     with pytest.raises(ValueError):
         bl.NormQuantBackwardCall(dn, normed.h, normed.rstd, nw.detach(), dweight=torch.empty(k, device=DEV),
                                  want_dweight=False)
+
+
+# ------------------------------------------------------------------ a step through workspaces
+
+def test_training_step_with_workspaces_in_a_graph(bl, tr):
+    """As test_training_step_in_a_graph, at a size whose gradients take the
+    operand pass and the norm's a second launch."""
+    g = gen(20)
+    m, k, n = 600, 600, 600
+    assert bl.lib().bitlinear_backward_workspace_bytes(m, n, k, 1, 1) > 0
+    x, nw = leaf((m, k), g), leaf((k,), g, torch.float32)
+    r, target = (torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    w = [leaf((n, k), g, torch.float32, 0.02) for _ in range(3)]
+
+    def step():
+        h, ys = tr.norm_linear(x, w, nw, r)
+        z = tr.linear(ys[0], w[1])
+        return torch.autograd.grad((*ys[1:], z, h), (x, nw, *w), (target, target, target, r))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        with torch.no_grad():
+            x.copy_(torch.randn(m, k, generator=g, device=DEV))
+            target.copy_(torch.randn(m, n, generator=g, device=DEV))
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b), i
