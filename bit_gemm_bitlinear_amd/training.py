@@ -4,7 +4,9 @@ The forward pass ternarizes the latent fp32 weights and quantizes the
 activations as the inference path does; the backward pass lets gradients pass
 straight through both roundings (the detach() form of the Falcon-Edge blog's
 BitLinear).  What is kept between the two is small: the activations as int8
-codes with a scale per token, the weights as packed ternary codes.
+codes with a scale per token, the weights as packed ternary codes; by
+norm_linear also 1 / rms per token and h in bf16, which is there anyway (the
+residual stream, or x).
 
     y = linear(x, weight)                                    # one BitLinear
     h, (q, k, v) = norm_linear(x, [wq, wk, wv], norm, residual)  # a block's entry

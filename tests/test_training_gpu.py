@@ -551,3 +551,28 @@ def test_training_step_with_workspaces_in_a_graph(bl, tr):
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b), i
+
+
+# ------------------------------------------------------------------ what a call keeps
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_linear_checkpoint_size(tr, residual):
+    """norm_linear keeps one set of codes for its projections (8 bits an
+    activation), 2 bits a weight, 1 / rms a token, and h in bf16: a tensor that
+    is there anyway, as the stream with the residual or as x."""
+    g = gen(21)
+    m, k, ns = 256, 1024, (512, 256, 256)
+    x, nw = leaf((m, k), g), leaf((k,), g, torch.float32)
+    r = leaf((m, k), g) if residual else None
+    ws = [leaf((n, k), g, torch.float32, 0.02) for n in ns]
+    kept = {}
+
+    def pack(t):
+        kept[t.data_ptr()] = t.numel() * t.element_size()
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        h, ys = tr.norm_linear(x, ws, nw, r)
+    assert kept.pop(h.data_ptr()) == 2 * m * k
+    assert kept.pop(nw.data_ptr()) == 4 * k
+    assert sum(kept.values()) == m * k + 4 * m + 4 * m + sum(n * k // 4 + 4 for n in ns)
