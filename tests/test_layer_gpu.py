@@ -739,3 +739,91 @@ def test_staged_gradients_from_threads(bl):
     for t in threads:
         t.join()
     assert not bad, bad
+
+
+# ------------------------------------------------------------------ the other kernels and rules
+
+# Rows over 32768 columns are read three times; over 256 tokens a thread takes two
+# pieces from 4096 columns on, and four from 8192.
+LONG_ROWS = [(3, 32772), (2, 65536), (5, 100004), (1, 2 ** 20 + 4), (300, 4104), (300, 8192), (260, 14332)]
+
+
+@pytest.mark.parametrize("weight", ["none", "bf16", "fp32"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("m,k", LONG_ROWS)
+def test_norm_quant_long_rows(bl, m, k, residual, weight):
+    test_norm_quant(bl, m, k, residual, weight)
+
+
+@pytest.mark.parametrize("k", [32772, 70000])
+def test_norm_long_rows_in_place_and_not_finite(bl, k):
+    for which in ("x", "residual"):
+        test_norm_quant_in_place(bl, k, which)
+    test_norm_not_finite_stays_in_its_row(bl, k)
+    # without h, the sum with the residual is made again for each reading
+    rng = np.random.default_rng([7, k])
+    x, r = to_dev(rows(rng, 3, k)), to_dev(rows(rng, 3, k, 3.0))
+    want = bl.rms_norm_quant(x, None, r, want_norm=True)
+    n, rstd = torch.empty_like(x), torch.empty(4, device=DEV)
+    bl._launch(bl.lib().bitlinear_rms_norm_quant,
+               (3, k, x.data_ptr(), r.data_ptr(), None, 0, 1e-6, None, rstd.data_ptr(), n.data_ptr(), None, None),
+               x.device)
+    assert torch.equal(n, want.n) and torch.equal(rstd[:3], want.rstd)
+
+
+def test_norm_many_rows(bl):
+    """Rows past 2^20: the grid's second dimension."""
+    m, k = 2 ** 20 + 5, 64
+    x = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+    got = bl.rms_norm_quant(x, want_norm=True)
+    for part in (slice(0, 9), slice(2 ** 20 - 4, m)):
+        few = bl.rms_norm_quant(x[part].contiguous(), want_norm=True)
+        for a, b in zip((got.q, got.x_scale, got.rstd, got.n), (few.q, few.x_scale, few.rstd, few.n)):
+            assert torch.equal(a[part], b)
+    assert bool((got.x_scale > 0).all())
+    xhat = bl.restore_activations(got.q, got.x_scale)
+    assert torch.equal(xhat[-9:], bl.restore_activations(got.q[-9:].contiguous(), got.x_scale[-9:].clone()))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,n,k", [(5, 16392, 256), (16, 16400, 4352), (7, 32776, 512), (21, 32800, 384), (16, 65544, 256)])
+def test_w4_forward_many_rows(bl, m, n, k, group):
+    """Blocks of 16 rows by four, two and one waves (more than four tokens
+    through 16384 rows and more), the last ones partly filled."""
+    test_w4_forward(bl, m, n, k, group)
+
+
+def test_w4_far_outputs(bl):
+    """Outputs past 2^31: the last tokens'."""
+    m, n, k, group = 2 ** 18 + 7, 8200, 64, 32
+    q, xs, p = w4_case(bl, 9, 23, n, k, group)
+    big = torch.zeros(m, k, dtype=torch.int8, device=DEV)
+    big[-23:] = q
+    scales = torch.ones(m, device=DEV)
+    scales[-23:] = xs
+    y = bl.forward_w4(big, scales, p)
+    assert torch.equal(y[-23:], bl.forward_w4(q, xs, p))
+    assert not bool(y[:-23].any())
+
+
+def test_backward_far_tokens(bl):
+    """Inputs past 2^31 elements: the last tokens' gradient, and a weight
+    gradient that sums over all of them."""
+    m, n, k, last = 2 ** 19 + 67, 72, 4100, 33
+    dy, q, xs, packed, ws = layer_case(bl, 110, last, n, k)
+    big_dy = torch.zeros(m, n, dtype=torch.bfloat16, device=DEV)
+    big_q = torch.ones(m, k, dtype=torch.int8, device=DEV)
+    big_xs = torch.ones(m, device=DEV)
+    big_dy[-last:], big_q[-last:], big_xs[-last:] = dy, q, xs
+    res = torch.zeros(m, k, dtype=torch.bfloat16, device=DEV)
+    res[-last:] = 2.0
+    dx, dw, db = bl.BackwardCall(big_dy, big_q, big_xs, packed, ws, bias=True, residual=res, dx=res)()
+    alone = bl.BackwardCall(dy, q, xs, packed, ws, bias=True)()
+    # rounded twice against once: both sums hold the bound before that
+    want, mag = input_gradient(bl, dy, packed, ws)
+    tol = 2 * BF * (want.abs() + 2) + (1 + 2 * BF) * (n + 2) * 2 * U * mag
+    assert bool(((dx[-last:].double() - (want + 2)).abs() <= tol).all())
+    assert not bool(dx[:-last].any())
+    check_input(alone[0], want, mag, n)
+    check_weight(dw, *weight_gradient(bl, dy, q, xs), last)
+    assert bool(((db.double() - dy.double().sum(0)).abs() <= (last + 2) * U * dy.double().abs().sum(0)).all())

@@ -576,3 +576,39 @@ def test_norm_linear_checkpoint_size(tr, residual):
     assert kept.pop(h.data_ptr()) == 2 * m * k
     assert kept.pop(nw.data_ptr()) == 4 * k
     assert sum(kept.values()) == m * k + 4 * m + 4 * m + sum(n * k // 4 + 4 for n in ns)
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 8, 16, 17, 100, 520])
+@pytest.mark.parametrize("k,ns", [(4096, (4096, 1024, 1024)), (2560, (6912, 6912)), (14336, (4096,)), (2052, (2048, 130))])
+def test_grouped_quantized_on_layers(bl, m, k, ns):
+    """Projections of layers on one set of codes, in the layouts and plans that
+    those sizes take: the grouped forward's bits."""
+    g = gen(m)
+    x = torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16)
+    packs = [bl.pack_weights(0.02 * torch.randn(n, k, generator=g, device=DEV)) for n in ns]
+    if k % 256 == 0:
+        packs = [(bl.tile_weights(p), s) for p, s in packs]
+    biases = [torch.randn(n, generator=g, device=DEV).to(torch.bfloat16) if i else None for i, n in enumerate(ns)]
+    residuals = [None if i else torch.randn(m, n, generator=g, device=DEV).to(torch.bfloat16) for i, n in enumerate(ns)]
+    ps, ss, count = [p for p, _ in packs], [s for _, s in packs], len(ns)
+    want = bl.GroupedCall([x] * count, ps, ss, biases=biases, residuals=residuals)()
+    q, xs = bl.act_quant(x)
+    kept = q.clone(), xs.clone()
+    outs = [torch.empty_like(t) if r is None else r for t, r in zip(want, residuals)]  # added in place
+    want = [t.clone() for t in want]
+    got = bl.GroupedQuantizedCall([q] * count, [xs] * count, ps, ss, outs, biases=biases, residuals=residuals)()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert torch.equal(q, kept[0]) and torch.equal(xs, kept[1])  # read where they are, and left
+
+
+def test_input_changed_in_place_is_refused(tr):
+    """Without a residual h is x itself: changed before the backward pass, the
+    gradient is refused and not made of other values."""
+    g = gen(22)
+    a, w = leaf((4, 64), g), leaf((24, 64), g, torch.float32, 0.02)
+    x = a * 2
+    _, (y,) = tr.norm_linear(x, [w])
+    x.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.float().sum().backward()
