@@ -625,7 +625,8 @@ class GroupedQuantizedCall:
     [M, K] and scales [M] (of rms_norm_quant or act_quant; projections may share
     them), the packed weights in either layout and their scale, and optionally a
     bf16 bias [N] and residual [M, N] (may be the output).  Results are those of
-    GroupedCall on the bf16 activations behind the codes."""
+    GroupedCall on the bf16 activations behind the codes (which is the faster
+    one at up to 4 tokens, where it quantizes inside its one kernel)."""
 
     def __init__(self, qs, x_scales, packeds, w_scales, outs=None, workspace=None, biases=None,
                  residuals=None):
@@ -808,7 +809,8 @@ def unpack_weights_w4(w: W4Weights) -> torch.Tensor:
 
 class W4Call:
     """A prepared product of int8 activations (codes [M, K], scales [M]) with
-    4-bit weights: y bf16 [M, N], with an optional bf16 bias [N]."""
+    4-bit weights: y bf16 [M, N], with an optional bf16 bias [N].  Made for up to
+    16 tokens: every 16 read the weights again."""
 
     def __init__(self, q, x_scale, w: W4Weights, out=None, bias=None):
         _require(q, torch.int8, 2, "q")

@@ -269,7 +269,7 @@ __device__ __forceinline__ void prepare_weights(const PrepArgs& A, int wg) {
           v4i{(int32_t)w[j], (int32_t)w[j + 1], (int32_t)w[j + 2], (int32_t)w[j + 3]};
 }
 
-// 2048 x 4096 x 14336, both gradients (150 MB moved): 30 us, 5 TB/s.
+// 2048 x 4096 x 14336, both gradients (150 MB moved): 31 us from memory, 4.9 TB/s.
 __global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs A) {
   const int wg = blockIdx.x;
   if (wg >= A.begin[2])
@@ -605,13 +605,15 @@ __device__ __forceinline__ bool tile_of(int l, const GemmJob& J, int* ti, int* t
 // The kernels: tiles of 64 x 64 and 128 x 128, whichever the plan takes for
 // each product, by four waves (two workgroups a CU), and tiles of 256 x 256 by
 // eight.  Slab rings are as deep as the LDS allows (two-bit slabs are smaller).
-// 2048 x 4096 x 14336, both gradients: 405-435 us by box, 1110-1190 TFLOP/s, the
-// matrix cores busy 61% of the cycles; 2048 x 6912 x 2560: 130 us.  What bounds
-// them is the clock that the power of the products leaves: the same launch on
-// zeros takes 329 us in place of 413, and 4096 cubed 95 in place of 112 (an 87-90
-// and 110-120 us library product).  Loads that always hit the caches gain 4% on dw
-// and nothing on dx; tiles of 128 x 256, two workgroups a CU that do not wait for
-// each other, gain nothing (4096 cubed 115 us, 2048 x 4096 x 14336 205 against 203).
+// 2048 x 4096 x 14336, both gradients: 416 us on average over 120 calls, 385 the
+// shortest (466 and 413 on another MI355X), 1156 TFLOP/s, the matrix cores busy 60%
+// of the cycles; 2048 x 6912 x 2560: 136 us, 126 the shortest.  What bounds them is
+// the clock that the power of the products leaves: the same launch on zeros takes
+// 319 us in place of 417, and the two of 4096 cubed 180 in place of 238, next to 92
+// and 125 of one bf16 library product of that size.  Loads that always hit the
+// caches gain 4% on dw and nothing on dx; tiles of 128 x 256, two workgroups a CU
+// that do not wait for each other, gain nothing (dx of 4096 cubed 115 us against
+// 112, of 2048 x 4096 x 14336 205 against 203).
 constexpr int kDeep64 = 4, kDeep64c = 8, kDeep128 = 2, kDeep128c = 4, kDeep256 = 2, kDeep256c = 4;
 constexpr int ring_bytes(int t, int deep, int deepc) {
   return std::max(deep * stage_bytes(t, t, false), deepc * stage_bytes(t, t, true));
@@ -672,8 +674,10 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const GemmArgs A, int6
 // registers to one of two LDS buffers while the other multiplies.  Operands
 // that several tiles share are laid out again by each, and a step waits for
 // its loads: worth it while there are few steps next to a second launch and the
-// trip of the operands through memory (both gradients of 16 x 480 x 960: 8.6
-// us against 12.4; of 301 x 1001 x 1284, 8 steps: 17.6 against 16.9).
+// trip of the operands through memory (both gradients of 16 x 480 x 960, whole
+// calls: 8.7 us against 11.7).  At the border the plan's estimate is off by
+// about 5%: 301 x 1001 x 1284, 8 steps, which it gives to this kernel, takes 16.8
+// us here and 16.0 in two launches.
 
 struct DirectArgs {
   int64_t m, n, k;

@@ -202,10 +202,15 @@ __device__ __forceinline__ int64_t row_index() { return (int64_t)blockIdx.y * kG
 // A workgroup a row, of as many threads as it has pieces, NCH a thread.  The
 // row stays in registers between the sum, the maximum and the codes: x and
 // the residual are read once, everything else written once.  The weights are
-// loaded with them where the registers allow: the norm then does not wait for
-// memory again after the sum.  2048 rows of 2560 with a residual (36.7 MB): 10.0-10.9 us, one round of
-// workgroups, so a chain of load, sum, maximum and store; one row of 4096:
-// 3.1 us.  A wave a row instead took 11.8 us.
+// loaded with them where the registers allow (rows of up to two pieces a
+// thread): the norm then does not wait for memory again after the sum.
+// 2048 rows of 2560 with a residual (36.7 MB): 13.8 us from memory, 10.3 where
+// the last-level cache holds the inputs.  A row is five waves, a CU holds six
+// such workgroups, 1536 rows in all: a quarter of the rows run in a second
+// round, and nothing loads for a workgroup while it reduces and stores.  777
+// rows of 14332 (33.4 MB), four pieces a thread and the weight read per row
+// after the sum: 16.5 us and 14.6.  One row of 4096: 3.4 us and 3.1.  A wave a
+// row took 11.8 us for 2048 x 2560 (next to 10.9 then).
 constexpr int kMaxT = 1024;
 template <int NCH>
 __global__ __launch_bounds__(kMaxT) void norm_quant_kernel(const NormArgs A) {
@@ -356,8 +361,10 @@ struct BwdRow {
 // grid apart, the next one loading while it works on the current, and each
 // thread fixed columns, so that it keeps its columns' sums for dweight in
 // registers over the rows.  The partial rows of the workgroups are added by a
-// second kernel, in a fixed order.  8191 rows of 2560: 33-35 us, 4.9 TB/s of the
-// 5.1 that a large copy reaches; 512 rows of 4096: 7.2 us, its two rows' latency.
+// second kernel, in a fixed order.  8191 rows of 2560 (168 MB): 34.2 us from
+// memory, 4.9 TB/s of the 5.1 that a large copy reaches, and 27.9 over and over
+// on inputs that the last-level cache (256 MB) holds; 512 rows of 4096: 8.0 us
+// and 7.2, the latency of two rows one after the other.
 constexpr int kBwdT = 512;
 template <int NCH>
 __global__ __launch_bounds__(kBwdT) void norm_backward_kernel(const NormBwdArgs A) {
@@ -500,7 +507,8 @@ __global__ __launch_bounds__(1024) void column_join_kernel(const float* __restri
 
 // ---- restored activations ----
 
-// bf16(q / s), 16 codes a thread; blockIdx.y walks the rows.  2048 x 2560: 5.4 us.
+// bf16(q / s), 16 codes a thread; blockIdx.y walks the rows.  2048 x 2560 (15.7
+// MB): 5.1 us; a row is one workgroup's, of whose 256 lanes 160 have codes there.
 __global__ __launch_bounds__(256) void restore_kernel(const int8_t* __restrict__ q,
                                                       const float* __restrict__ x_scale, int64_t m,
                                                       int k, uint16_t* __restrict__ out) {

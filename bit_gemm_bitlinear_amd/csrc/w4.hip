@@ -109,9 +109,12 @@ struct W4Chunk {
 // rows of an operand then lie in distinct banks), so a wave's memory loads are
 // the weights' alone.  It goes through its tiles U at a time, the next ones
 // loading while the current ones multiply.  GP: groups per tile (1, 2 or 4; 1
-// also where a group spans tiles).  14336 x 4096 at one token: 6.8-7.9 us for 30
-// MB; 32768 x 4096 at 16 tokens: 17 us for 72 MB, 4.3 TB/s (36 us when every wave
-// loaded its own activations from memory).
+// also where a group spans tiles).  14336 x 4096 at one token (30 MB): 8.9 us
+// from memory, 6.7 where the last-level cache holds the weights; 32768 x 4096 at
+// 16 tokens (72 MB): 21.2 us, 3.4 TB/s, and 17.3 (36 us when every wave loaded its
+// own activations from memory).  Every further 16 tokens read the weights again:
+// 14336 x 4096 at 17 tokens 22.6 us, at 2048 tokens 1353 us (the ternary product of
+// that size on the same codes: 119).
 template <int W, int GP, int U>
 __global__ __launch_bounds__(64 * W) void w4_kernel(const W4Args A) {
   extern __shared__ __align__(16) int8_t xs_lds[];
@@ -229,7 +232,8 @@ constexpr int kXBytes8 = 57000, kXBytes16 = 49000;
 //  * there are many blocks and many tokens: as few as leave 16 waves a CU, so
 //    that a workgroup stages its activations for several blocks (32768 x 4096
 //    at 16 tokens, eight waves a block 29.5 us, two 17.0; at one token, where
-//    the activations are small, 12.7 against 13.4).
+//    the activations are small, 12.7 against 13.4; the weights in the last-level
+//    cache).
 template <int GP>
 void launch_w4(W4Args a, hipStream_t s) {
   const int rows = a.m < 16 ? a.m : 16;

@@ -15,7 +15,8 @@ residual stream, or x).
 projection on the same codes.  ``BitLinear`` is ``linear`` as a module.  For
 inference pack the trained weights once: ``bitlinear.BitLinear(module.weight)``.
 
-A gradient of these gradients is not defined (asking for one raises).  To
+The gradients take up to 2^21 tokens and outputs a layer (bitlinear_backward's
+limits).  A gradient of these gradients is not defined (asking for one raises).  To
 capture a training step into a HIP graph, drop every eager graph over the same
 parameters first, as for any autograd program.
 """

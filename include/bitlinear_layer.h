@@ -21,7 +21,8 @@
  *             (the output head).
  *
  * Shapes: as in bitlinear.h (M, N, K >= 1; K % 4 == 0; K <= 2^22; N <= 2^30;
- * M <= 2^24; products below 2^40) unless a function says otherwise.  Inputs
+ * M <= 2^24; products below 2^40) unless a function says otherwise.  `stream`
+ * belongs to the device that is current in the call.  Inputs
  * must be finite, as there; a value that is not spoils the outputs whose
  * formula reads it, and no others.
  * Two launches that overlap in time must not share a workspace.
@@ -103,7 +104,9 @@ typedef struct {
  * Results are those of bitlinear_forward_grouped on the bf16 activations
  * that the codes were made of, bit for bit.  Workspace:
  * bitlinear_forward_grouped_workspace_bytes.  The first kernel brings the
- * codes into the contraction's order; then as bitlinear_forward. */
+ * codes into the contraction's order; then as bitlinear_forward.  (At M <= 4,
+ * where bitlinear_forward_grouped quantizes inside the contraction, that call
+ * on the norm's bf16 output is one launch less and faster.) */
 bl_status bitlinear_forward_grouped_quantized(int32_t count, const bl_projection *projs,
                                               const bl_codes *codes, int64_t m,
                                               void *workspace, size_t workspace_bytes,
@@ -111,8 +114,9 @@ bl_status bitlinear_forward_grouped_quantized(int32_t count, const bl_projection
 
 /* --- gradients of BitLinear -------------------------------------------- */
 
-/* Bytes of workspace bitlinear_backward needs for dx and/or dw.  Shapes: M and
- * N up to 2^21, M*N and M*K up to 2^37, M*K and N*K up to 2^36. */
+/* Bytes of workspace bitlinear_backward needs for dx and/or dw (0: none, or a
+ * shape that it refuses).  Shapes: M and N up to 2^21, M*N up to 2^37, M*K and
+ * N*K up to 2^36 (2^22 tiles of 128 x 128, the last ones counted whole). */
 size_t bitlinear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k,
                                           int32_t want_dx, int32_t want_dw);
 
@@ -146,7 +150,7 @@ bl_status bitlinear_backward(int64_t m, int64_t n, int64_t k, const uint16_t *dy
 
 /* Storage.  Weight [n][k] stands for scale * v with v in -8..7, one scale
  * (bf16) per row and group of `group` consecutive k (group a power of two,
- * 32 to 1024; K % group == 0).  N is padded to whole blocks of 16 rows and K
+ * 32 to 1024; K % group == 0; N up to 2^24).  N is padded to whole blocks of 16 rows and K
  * to whole tiles of 128, with zeros.
  *   codes : bytes [ceil(N/16)][ceil(K/128)][4][16][16]; the byte at
  *           [n/16][k/128][(k%32)/8][n%16][4*((k%128)/32) + k%4] holds the v of
@@ -173,8 +177,9 @@ bl_status bitlinear_w4_unpack(const uint8_t *codes, const uint16_t *scales, int6
  * [M][N] bf16: exact int32 sums within a group (128 of it at a time), fp32
  * over the groups.  q,
  * x_scale: int8 codes [M][K] and scales [M] of the activations.  bias: [N]
- * bf16, added to the rounded output (rounded again), or NULL.  One kernel;
- * the weights are read once for every 16 token rows. */
+ * bf16, added to the rounded output (rounded again), or NULL.  M up to 2^19.
+ * One kernel; the weights are read once for every 16 token rows, so that it is
+ * a kernel for up to 16 tokens, and right but slow for many more. */
 bl_status bitlinear_w4_forward(int64_t m, int64_t n, int64_t k, int64_t group,
                                const int8_t *q, const float *x_scale,
                                const uint8_t *codes, const uint16_t *scales,
