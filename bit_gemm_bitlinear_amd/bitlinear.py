@@ -1,5 +1,5 @@
-"""ctypes binding over libbitlinear.so (C ABI in include/bitlinear.h and
-include/bitlinear_layer.h).
+"""ctypes binding over libbitlinear.so (C ABI in include/bitlinear.h,
+include/bitlinear_layer.h and include/bitlinear_ffn.h).
 
 Argument marshalling only: every step of the BitLinear forward pass runs in
 the library's HIP kernels.  PyTorch provides device memory and the current
@@ -26,7 +26,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 _i64, _i32, _sz, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
-_dbl = ctypes.c_double
+_dbl, _flt = ctypes.c_double, ctypes.c_float
 
 
 class Projection(ctypes.Structure):
@@ -45,6 +45,11 @@ class Inspect(ctypes.Structure):
 class Codes(ctypes.Structure):
     """bl_codes: int8 activations of a projection (codes and scales)."""
     _fields_ = [("q", _vp), ("x_scale", _vp)]
+
+
+class Gradient(ctypes.Structure):
+    """bl_gradient: one tensor of a gradient norm or clipping call."""
+    _fields_ = [("g", _vp), ("out", _vp), ("numel", _i64), ("type", _i32), ("reserved", _i32)]
 
 
 LAYOUT_ROWS = 0   # BL_LAYOUT_ROWS: packed uint8 [N, K/4]
@@ -99,6 +104,26 @@ _SIGS = {
     "bitlinear_w4_unpack": (ctypes.c_int, [_vp, _vp, _i64, _i64, _i64, _vp, _vp]),
     "bitlinear_w4_forward": (ctypes.c_int, [_i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp,
                                             _vp]),
+    # include/bitlinear_ffn.h
+    "bitlinear_gated_weights_bytes": (_sz, [_i64, _i64]),
+    "bitlinear_gated_weights": (ctypes.c_int, [_i64, _i64, _vp, _i32, _vp, _i32, _vp, _vp]),
+    "bitlinear_gated_forward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "bitlinear_gated_forward": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
+                                               _vp, _vp, _vp, _sz, _vp]),
+    "bitlinear_gated_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "bitlinear_gated_backward": (ctypes.c_int, [_i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp,
+                                                _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
+                                                _sz, _vp]),
+    "bitlinear_w8_codes_bytes": (_sz, [_i64, _i64]),
+    "bitlinear_w8_pack": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "bitlinear_w8_unpack": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
+    "bitlinear_w8_forward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "bitlinear_w8_forward": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                            _vp]),
+    "bitlinear_grad_norm_workspace_bytes": (_sz, [_i32, ctypes.POINTER(Gradient)]),
+    "bitlinear_grad_norm": (ctypes.c_int, [_i32, ctypes.POINTER(Gradient), _vp, _vp, _sz, _vp]),
+    "bitlinear_clip_gradients": (ctypes.c_int, [_i32, ctypes.POINTER(Gradient), _flt, _vp, _vp, _sz,
+                                                _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -837,3 +862,333 @@ class W4Call:
 def forward_w4(q, x_scale, w: W4Weights, out=None, bias=None) -> torch.Tensor:
     """y = (codes / x_scale) . weights^T as bf16 [M, N] (see W4Call)."""
     return W4Call(q, x_scale, w, out, bias)()
+
+
+# --------------------------------------------------------------------------
+# Operators of a feed-forward block and of a training step (include/bitlinear_ffn.h)
+
+class W8Weights(NamedTuple):
+    """8-bit weights of an [N, K] matrix with an fp32 scale per row (the storage
+    of bitlinear_ffn.h): codes int8 [N/16, K/64, 4, 16, 16], N and K rounded up
+    to whole blocks; scale fp32 [N]."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    n: int
+    k: int
+
+
+def _require_w8(w: W8Weights, device=None):
+    if w.n < 1 or w.k < 1:
+        raise ValueError("W8Weights: n and k must be positive")
+    _require(w.codes, torch.int8, 5, "codes", shape=((w.n + 15) // 16, (w.k + 63) // 64, 4, 16, 16), device=device)
+    _require(w.scale, torch.float32, 1, "scale", shape=(w.n,), device=w.codes.device)
+
+
+def pack_weights_w8(w: torch.Tensor) -> W8Weights:
+    """Latent fp32 weights [N, K] -> 8-bit codes and a scale per row."""
+    _require(w, torch.float32, 2, "w")
+    n, k = w.shape
+    out = W8Weights(torch.empty(((n + 15) // 16, (k + 63) // 64, 4, 16, 16), dtype=torch.int8, device=w.device),
+                    _rows_f32(n, w.device), n, k)
+    _launch(_lib.bitlinear_w8_pack, (_ptr(w), n, k, _ptr(out.codes), _ptr(out.scale)), w.device)
+    return out
+
+
+def unpack_weights_w8(w: W8Weights) -> torch.Tensor:
+    """The fp32 weights [N, K] that 8-bit codes and scales stand for."""
+    _require_w8(w)
+    out = torch.empty((w.n, w.k), dtype=torch.float32, device=w.codes.device)
+    _launch(_lib.bitlinear_w8_unpack, (_ptr(w.codes), _ptr(w.scale), w.n, w.k, _ptr(out)), w.codes.device)
+    return out
+
+
+class W8Call:
+    """A prepared product of int8 activations (codes [M, K], scales [M]) with
+    8-bit weights: y bf16 [M, N], with an optional bf16 bias [N].  For any number
+    of tokens."""
+
+    def __init__(self, q, x_scale, w: W8Weights, out=None, bias=None, workspace=None):
+        _require(q, torch.int8, 2, "q")
+        (m, k), dev = q.shape, q.device
+        _require(x_scale, torch.float32, 1, "x_scale", shape=(m,), device=dev)
+        _require_w8(w, dev)
+        if k != w.k:
+            raise ValueError(f"q has {k} columns, the weights {w.k}")
+        if bias is not None:
+            _require(bias, torch.bfloat16, 1, "bias", shape=(w.n,), device=dev)
+        if out is None:
+            out = torch.empty((m, w.n), dtype=torch.bfloat16, device=dev)
+        _require(out, torch.bfloat16, 2, "out", shape=(m, w.n), device=dev)
+        self.workspace = _workspace(int(_lib.bitlinear_w8_forward_workspace_bytes(m, w.n, k)), dev, workspace)
+        self.out = out
+        self._dev, self._keep = dev, (q, x_scale, w, bias)
+        self._args = (m, w.n, k, _ptr(q), _ptr(x_scale), _ptr(w.codes), _ptr(w.scale), _opt(bias), _ptr(out),
+                      _ptr(self.workspace), _nbytes(self.workspace))
+
+    def __call__(self, stream=None) -> torch.Tensor:
+        _launch(_lib.bitlinear_w8_forward, self._args, self._dev, stream)
+        return self.out
+
+
+def forward_w8(q, x_scale, w: W8Weights, out=None, bias=None, workspace=None) -> torch.Tensor:
+    """y = (codes / x_scale) . weights^T as bf16 [M, N] (see W8Call)."""
+    return W8Call(q, x_scale, w, out, bias, workspace)()
+
+
+# --------------------------------------------------------------------------
+# Gated feed-forward block
+
+ACTIVATIONS = {"relu2": 1, "silu": 2}  # BL_ACT_*: max(g, 0)^2, g / (1 + exp(-g))
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+class GatedWeights(NamedTuple):
+    """Ternary weights of a feed-forward block's gate and up projections, [N, K]
+    each, laid out for GatedCall (the storage of bitlinear_ffn.h): codes uint8
+    [N/16, K/256, 2, 4, 16, 16], N and K rounded up to whole blocks; the two
+    weight scales fp32 [1]."""
+    codes: torch.Tensor
+    gate_scale: torch.Tensor
+    up_scale: torch.Tensor
+    n: int
+    k: int
+
+
+def gated_weights(gate, gate_scale, up, up_scale, k: int | None = None) -> GatedWeights:
+    """Packed ternary weights of the gate and up projections, each in either
+    layout (give K for tiled ones), laid out for GatedCall."""
+    _require(gate, torch.uint8, 2, "gate")
+    dev = gate.device
+    _require(up, torch.uint8, 2, "up", device=dev)
+    _require_scale(gate_scale, dev, "gate_scale")
+    _require_scale(up_scale, dev, "up_scale")
+    if k is None:
+        k = 4 * gate.shape[1]
+    (n, lg), (nu, lu) = weight_layout(gate, k), weight_layout(up, k)
+    if n != nu:
+        raise ValueError(f"the gate has {n} outputs, the up projection {nu}")
+    codes = torch.empty(((n + 15) // 16, (k + 255) // 256, 2, 4, 16, 16), dtype=torch.uint8, device=dev)
+    _launch(_lib.bitlinear_gated_weights, (n, k, _ptr(gate), lg, _ptr(up), lu, _ptr(codes)), dev)
+    return GatedWeights(codes, gate_scale, up_scale, n, k)
+
+
+class Gated(NamedTuple):
+    """What a GatedCall writes: a = act(g) * u, and where they are kept g and u
+    themselves, bf16 [M, N] each."""
+    a: torch.Tensor
+    g: torch.Tensor | None
+    u: torch.Tensor | None
+
+
+class GatedCall:
+    """A prepared gated feed-forward entry: both projections of int8 activations
+    (codes [M, K], scales [M]), the activation function ("relu2" or "silu") and
+    the product, in one kernel.  `keep` also writes g and u, which the gradients
+    read.  Outputs (or `out`, a Gated) and workspace are allocated once."""
+
+    def __init__(self, q, x_scale, w: GatedWeights, activation: str, keep: bool = False, out: Gated | None = None,
+                 workspace=None):
+        _require(q, torch.int8, 2, "q")
+        (m, k), dev, act = q.shape, q.device, _activation(activation)
+        _require(x_scale, torch.float32, 1, "x_scale", shape=(m,), device=dev)
+        if w.n < 1 or w.k < 1:
+            raise ValueError("GatedWeights: n and k must be positive")
+        _require(w.codes, torch.uint8, 6, "codes", shape=((w.n + 15) // 16, (w.k + 255) // 256, 2, 4, 16, 16),
+                 device=dev)
+        _require_scale(w.gate_scale, dev, "gate_scale")
+        _require_scale(w.up_scale, dev, "up_scale")
+        if k != w.k:
+            raise ValueError(f"q has {k} columns, the weights {w.k}")
+        if out is None:
+            out = Gated(*(torch.empty((m, w.n), dtype=torch.bfloat16, device=dev) if i == 0 or keep else None
+                          for i in range(3)))
+        _require(out.a, torch.bfloat16, 2, "out.a", shape=(m, w.n), device=dev)
+        if (out.g is None) != (out.u is None) or (keep and out.g is None):
+            raise ValueError("out.g and out.u are kept together (and needed with keep)")
+        for t, name in ((out.g, "out.g"), (out.u, "out.u")):
+            if t is not None:
+                _require(t, torch.bfloat16, 2, name, shape=(m, w.n), device=dev)
+        self.workspace = _workspace(int(_lib.bitlinear_gated_forward_workspace_bytes(m, w.n, k)), dev, workspace)
+        self.out = out
+        self._dev, self._keep = dev, (q, x_scale, w)
+        self._args = (m, w.n, k, _ptr(q), _ptr(x_scale), _ptr(w.codes), _ptr(w.gate_scale), _ptr(w.up_scale), act,
+                      _ptr(out.a), _opt(out.g), _opt(out.u), _ptr(self.workspace), _nbytes(self.workspace))
+
+    def __call__(self, stream=None) -> Gated:
+        _launch(_lib.bitlinear_gated_forward, self._args, self._dev, stream)
+        return self.out
+
+
+def forward_gated(q, x_scale, w: GatedWeights, activation: str, keep: bool = False) -> Gated:
+    """The gate and up projections, the activation function and the product (see
+    GatedCall)."""
+    return GatedCall(q, x_scale, w, activation, keep)()
+
+
+class GatedBackwardCall:
+    """Prepared gradients of a gated feed-forward entry, from da bf16 [M, N] and
+    the g and u that the forward kept: of the input (packed weights of both
+    projections, each in either layout, and their scales), dx bf16 [M, K], and of
+    both latent weights (the input's int8 codes and scales), dw_gate and dw_up
+    fp32 [N, K].  Leave `gate` and `up` out for no dx, or `q` for no weights'
+    gradients.  `residual` (bf16 [M, K], may be dx) is added to dx; with
+    accumulate the weights' gradients are added to the given tensors.  A call
+    returns (dx, dw_gate, dw_up), None for what is left out."""
+
+    def __init__(self, da, g, u, activation: str, q=None, x_scale=None, gate=None, gate_scale=None, up=None,
+                 up_scale=None, k: int | None = None, residual=None, dx=None, dw_gate=None, dw_up=None,
+                 accumulate: bool = False, workspace=None):
+        _require(da, torch.bfloat16, 2, "da")
+        (m, n), dev, act = da.shape, da.device, _activation(activation)
+        _require(g, torch.bfloat16, 2, "g", shape=(m, n), device=dev)
+        _require(u, torch.bfloat16, 2, "u", shape=(m, n), device=dev)
+        if (gate is None) != (up is None):
+            raise ValueError("gate and up are given together")
+        if q is None and gate is None:
+            raise ValueError("nothing to do: give gate and up (for dx) or q (for the weights' gradients)")
+        if q is not None:
+            _require(q, torch.int8, 2, "q", device=dev)
+            if k is not None and k != q.shape[1]:
+                raise ValueError(f"q has {q.shape[1]} columns, k is {k}")
+            k = q.shape[1]
+            _require(q, torch.int8, 2, "q", shape=(m, k))
+            _require(x_scale, torch.float32, 1, "x_scale", shape=(m,), device=dev)
+            if (dw_gate is None) != (dw_up is None):
+                raise ValueError("dw_gate and dw_up are given together")
+            if accumulate and dw_gate is None:
+                raise ValueError("accumulate needs the tensors to add to")
+            if dw_gate is None:
+                dw_gate, dw_up = (torch.empty((n, k), dtype=torch.float32, device=dev) for _ in range(2))
+            _require(dw_gate, torch.float32, 2, "dw_gate", shape=(n, k), device=dev)
+            _require(dw_up, torch.float32, 2, "dw_up", shape=(n, k), device=dev)
+        elif dw_gate is not None or dw_up is not None:
+            raise ValueError("dw_gate and dw_up need q and x_scale")
+        lg = lu = LAYOUT_ROWS
+        if gate is not None:
+            _require(gate, torch.uint8, 2, "gate", device=dev)
+            _require(up, torch.uint8, 2, "up", device=dev)
+            _require_scale(gate_scale, dev, "gate_scale")
+            _require_scale(up_scale, dev, "up_scale")
+            if k is None:
+                k = 4 * gate.shape[1]
+            (ng, lg), (nu, lu) = weight_layout(gate, k), weight_layout(up, k)
+            if ng != n or nu != n:
+                raise ValueError(f"the packed weights have {ng} and {nu} rows, da {n} columns")
+            if residual is not None:
+                _require(residual, torch.bfloat16, 2, "residual", shape=(m, k), device=dev)
+            if dx is None:
+                dx = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
+            _require(dx, torch.bfloat16, 2, "dx", shape=(m, k), device=dev)
+        elif dx is not None or residual is not None:
+            raise ValueError("dx needs gate and up")
+        need = int(_lib.bitlinear_gated_backward_workspace_bytes(m, n, k, dx is not None, dw_gate is not None))
+        self.workspace = _workspace(need, dev, workspace)
+        self._out = (dx, dw_gate, dw_up)
+        self._dev, self._keep = dev, (da, g, u, q, x_scale, gate, gate_scale, up, up_scale, residual)
+        self._args = (m, n, k, act, _ptr(da), _ptr(g), _ptr(u), _opt(gate), lg, _opt(up), lu, _opt(gate_scale),
+                      _opt(up_scale), _opt(residual), _opt(dx), _opt(q), _opt(x_scale), _opt(dw_gate), _opt(dw_up),
+                      int(accumulate), _ptr(self.workspace), _nbytes(self.workspace))
+
+    def __call__(self, stream=None):
+        _launch(_lib.bitlinear_gated_backward, self._args, self._dev, stream)
+        return self._out
+
+
+# --------------------------------------------------------------------------
+# Gradient norm and clipping
+
+GRAD_BF16, GRAD_F32 = 1, 2  # BL_GRAD_*
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill its piece of memory, in some order of its
+    dimensions."""
+    want = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != want and t.numel():
+            return False
+        want *= size
+    return True
+
+
+def _gradients(grads, outs):
+    """Descriptors of the gradients, and their device."""
+    if not grads:
+        raise ValueError("at least one gradient")
+    if outs is not None and len(outs) != len(grads):
+        raise ValueError("outs: one tensor per gradient")
+    arr = (Gradient * len(grads))()
+    dev = grads[0].device if isinstance(grads[0], torch.Tensor) else None
+    for i, g in enumerate(grads):
+        o = g if outs is None else outs[i]
+        for t, name in ((g, "a gradient"), (o, "an output")):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+            if t.dtype not in (torch.float32, torch.bfloat16):
+                raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, expected {dev}")
+            if not _dense(t):
+                raise ValueError(f"{name} must fill its memory (a slice of a larger tensor does not)")
+        if o is not g and (o.shape != g.shape or o.dtype != g.dtype or (o.numel() > 1 and o.stride() != g.stride())):
+            raise ValueError("an output must have its gradient's shape, type and strides")
+        arr[i] = Gradient(g.data_ptr(), o.data_ptr(), g.numel(), GRAD_BF16 if g.dtype == torch.bfloat16 else GRAD_F32, 0)
+    return arr, dev
+
+
+class GradNormCall:
+    """A prepared norm of many gradients together (fp32 or bf16 tensors of any
+    shapes on one device): fp32 [1], on the device."""
+
+    def __init__(self, grads, workspace=None):
+        self._arr, self._dev = _gradients(list(grads), None)
+        self.norm = _rows_f32(1, self._dev)
+        need = int(_lib.bitlinear_grad_norm_workspace_bytes(len(self._arr), self._arr))
+        self.workspace = _workspace(need, self._dev, workspace)
+        self._keep = list(grads)
+        self._args = (len(self._arr), self._arr, _ptr(self.norm), _ptr(self.workspace), _nbytes(self.workspace))
+
+    def __call__(self, stream=None) -> torch.Tensor:
+        _launch(_lib.bitlinear_grad_norm, self._args, self._dev, stream)
+        return self.norm
+
+
+class ClipGradsCall:
+    """Prepared clipping of many gradients to a norm of all of them together:
+    each is multiplied by min(1, max_norm / (norm + 1e-6)), in place or into
+    `outs`.  No gradient may be listed twice.  A call returns (norm, outs), norm
+    fp32 [1] on the device: that before clipping.  Nothing waits for it: a norm
+    that is not finite is the caller's to look at."""
+
+    def __init__(self, grads, max_norm: float, outs=None, workspace=None):
+        grads = list(grads)
+        max_norm = float(max_norm)
+        if not max_norm >= 0:
+            raise ValueError(f"max_norm must be 0 or more, got {max_norm}")
+        self._arr, self._dev = _gradients(grads, outs)
+        self.norm = _rows_f32(1, self._dev)
+        need = int(_lib.bitlinear_grad_norm_workspace_bytes(len(self._arr), self._arr))
+        self.workspace = _workspace(need, self._dev, workspace)
+        self._keep = grads
+        self.outs = grads if outs is None else list(outs)
+        self._args = (len(self._arr), self._arr, max_norm, _ptr(self.norm), _ptr(self.workspace),
+                      _nbytes(self.workspace))
+
+    def __call__(self, stream=None):
+        _launch(_lib.bitlinear_clip_gradients, self._args, self._dev, stream)
+        return self.norm, self.outs
+
+
+def grad_norm(grads) -> torch.Tensor:
+    """The norm of all gradients together, fp32 [1] (see GradNormCall)."""
+    return GradNormCall(grads)()
+
+
+def clip_grads(grads, max_norm: float, outs=None):
+    """(norm, clipped gradients), in place unless `outs` (see ClipGradsCall)."""
+    return ClipGradsCall(grads, max_norm, outs)()

@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbitlinear.so")
 SOURCES = ["abi.hip", "act_quant.hip", "decode.hip", "decode_fused.hip", "prefill.hip", "pack.hip",
-           "layer_abi.hip", "norm_quant.hip", "backward.hip", "w4.hip"]
+           "layer_abi.hip", "norm_quant.hip", "backward.hip", "w4.hip",
+           "gated.hip", "w8.hip", "grad_norm.hip"]
 # measurement kernels (include/bitlinear_probes.h), a library of their own
 PROBE_LIB = os.path.join(PKG, "libbitlinear_probes.so")
 PROBE_SOURCES = ["probes.hip"]

@@ -4,7 +4,10 @@
 //   dw[n][k] = sum_m dy[m][n] * xhat[m][k],  xhat = bf16(q / x_scale)
 //   db[n]    = sum_m dy[m][n]
 //
-// Both are matrix products C[i][j] = sum_c A[i][c] B[j][c].  u in {-1, 0, 1}
+// and those of a gated feed-forward block's two projections (bitlinear_ffn.h),
+// whose dg and du are made on the way: dx sums over both, dw has both's rows.
+//
+// All are matrix products C[i][j] = sum_c A[i][c] B[j][c].  u in {-1, 0, 1}
 // and xhat are bf16 values, so every product is exact on the bf16 matrix cores
 // and the sums are fp32.  A call is two launches (three where a product's c is
 // split): one prepares the operands, one multiplies, dx and dw in one grid.
@@ -18,6 +21,8 @@
 //   dy  as A of dx: rows m, c = n;    dy^T as A of dw: rows n, c = m
 //   xhat^T as B of dw: rows k, c = m (bf16)
 //   u^T as B of dx: rows k, c = n, two bits a weight (16 bytes a row and slab)
+// Of a gated block the slabs of du and the up weights follow those of dg and the
+// gate's (dx), and the rows of du^T those of dg^T (dw).
 #include "../../include/bitlinear_layer.h"
 #include "backward_plan.hpp"
 #include "common.hpp"
@@ -65,6 +70,12 @@ struct PrepArgs {
   const uint8_t* packed;
   int32_t tiled;
   uint8_t* ut;  // [ceil(n/64)][k][16]
+  // gated: begin[2] is the gate's weights, begin_up the up projection's
+  int32_t begin_up;
+  const uint16_t* g;
+  const uint16_t* u;
+  const uint8_t* packed_up;
+  int32_t tiled_up;
 };
 
 // Column j of eight rows of eight bf16 values: a byte select per pair of rows.
@@ -201,7 +212,8 @@ __device__ __forceinline__ void prepare_xhat(const PrepArgs& A, int wg) {
 // smaller blocks.  In the result the codes of n = 2a and n = 2a + 1 sit at bits
 // 2a and 16 + 2a (the rows are loaded in that order), where the product's
 // expansion takes them as pairs.  Rows past N are code 1 (u = 0).
-__device__ __forceinline__ void prepare_weights(const PrepArgs& A, int wg) {
+__device__ __forceinline__ void prepare_weights(const PrepArgs& A, const uint8_t* __restrict__ packed, bool tiled,
+                                                uint8_t* __restrict__ ut, int wg) {
   const int cols = (int)((A.k + 1023) >> 10);
   const int64_t slab = wg / cols;
   const int d = threadIdx.x & 3;
@@ -217,8 +229,8 @@ __device__ __forceinline__ void prepare_weights(const PrepArgs& A, int wg) {
 #pragma unroll
     for (int p = 0; p < 16; ++p) {
       const int64_t n = min(n0 + (p < 8 ? 2 * p : 2 * (p - 8) + 1), A.n - 1);
-      const int64_t at = A.tiled ? tiled_chunk_offset(n, o & ~(int64_t)15, rb) + (o & 15) : n * rb + oc;
-      w[p] = *G(reinterpret_cast<const u32_any*>(A.packed + at));
+      const int64_t at = tiled ? tiled_chunk_offset(n, o & ~(int64_t)15, rb) + (o & 15) : n * rb + oc;
+      w[p] = *G(reinterpret_cast<const u32_any*>(packed + at));
     }
 #pragma unroll
     for (int p = 0; p < 16; ++p) w[p] >>= sh;
@@ -228,7 +240,7 @@ __device__ __forceinline__ void prepare_weights(const PrepArgs& A, int wg) {
       const int64_t n = min(n0 + (p < 8 ? 2 * p : 2 * (p - 8) + 1), A.n - 1);
       w[p] = 0;
 #pragma unroll
-      for (int b = 0; b < 3; ++b) w[p] |= (uint32_t)*G(A.packed + n * rb + min((int64_t)b, rb - 1)) << (8 * b);
+      for (int b = 0; b < 3; ++b) w[p] |= (uint32_t)*G(packed + n * rb + min((int64_t)b, rb - 1)) << (8 * b);
     }
   }
 #pragma unroll
@@ -265,19 +277,98 @@ __device__ __forceinline__ void prepare_weights(const PrepArgs& A, int wg) {
 #pragma unroll
   for (int j = 0; j < 16; j += 4)
     if (k + j < A.k)  // K % 4 == 0
-      *G(reinterpret_cast<v4i*>(A.ut + (slab * A.k + k + j + d) * kCodes)) =
+      *G(reinterpret_cast<v4i*>(ut + (slab * A.k + k + j + d) * kCodes)) =
           v4i{(int32_t)w[j], (int32_t)w[j + 1], (int32_t)w[j + 2], (int32_t)w[j + 3]};
+}
+
+// dg and du of a gated block's elements, from da and the kept g and u, as
+// bitlinear_gated_backward states them.  Of relu2 every product is exact in
+// fp32 (three significands of eight bits); of silu they are made in fp64: a
+// last bit of fp32 at a border of bf16 would be a whole step of the operand.
+template <bool SILU>
+__device__ __forceinline__ void gate_grads(float da, float g, float u, float* dg, float* du) {
+  if constexpr (!SILU) {
+    const float r = fmaxf(g, 0.0f);
+    *dg = 2.0f * ((da * u) * r);
+    *du = (da * r) * r;
+  } else {
+    const double x = g, e = exp(-fabs(x)), p = 1.0 / (1.0 + e);
+    const double s = x >= 0.0 ? p : e * p, t = x >= 0.0 ? e * p : p;  // sigmoid(g), sigmoid(-g)
+    *dg = (float)(((double)da * u) * (s * (1.0 + x * t)));
+    *du = (float)((double)da * (x * s));
+  }
+}
+
+// As prepare_dy, dg and du made of the tokens' da, g and u on the way.
+template <bool SILU>
+__device__ __forceinline__ void prepare_gated(const PrepArgs& A, int wg) {
+  const int cols = (int)((A.n + 255) >> 8);
+  const int64_t ms = wg / cols, n0 = (int64_t)(wg - (int)ms * cols) * 256;
+  const int mi = threadIdx.x & 7, ni = threadIdx.x >> 3;
+  const int64_t m0 = ms * 64 + 8 * mi, n = n0 + 8 * ni;
+  const int mv = (int)min((int64_t)8, A.m - m0);  // rows of the eight that exist (may be <= 0)
+  v4i rg[8], ru[8];
+  {
+    v4i rd[8];
+    load_dy8(A.dy, A.m, A.n, m0, n, rd);
+    load_dy8(A.g, A.m, A.n, m0, n, rg);
+    load_dy8(A.u, A.m, A.n, m0, n, ru);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t d = (uint32_t)rd[i][e], g = (uint32_t)rg[i][e], u = (uint32_t)ru[i][e];
+        float g0, g1, u0, u1;
+        gate_grads<SILU>(__uint_as_float(d << 16), __uint_as_float(g << 16), __uint_as_float(u << 16), &g0, &u0);
+        gate_grads<SILU>(__uint_as_float(d & 0xFFFF0000u), __uint_as_float(g & 0xFFFF0000u),
+                         __uint_as_float(u & 0xFFFF0000u), &g1, &u1);
+        rg[i][e] = (int32_t)pack_bf16x2(g0, g1);
+        ru[i][e] = (int32_t)pack_bf16x2(u0, u1);
+      }
+  }
+  if (A.dys && n < ((A.n + 63) & ~(int64_t)63)) {
+    const int64_t ns = (A.n + 63) >> 6;
+    uint16_t* d = A.dys + ((n >> 6) * A.m + m0) * 64 + (n & 63);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < mv) {
+        *G(reinterpret_cast<v4i*>(d + 64 * i)) = rg[i];
+        *G(reinterpret_cast<v4i*>(d + ns * A.m * 64 + 64 * i)) = ru[i];
+      }
+  }
+  if (A.dyt) {
+    uint16_t* d = A.dyt + (ms * 2 * A.n + n) * 64 + 8 * mi;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j < A.n) {
+        *G(reinterpret_cast<v4i*>(d + 64 * j)) = column8(rg, j);
+        *G(reinterpret_cast<v4i*>(d + (A.n + j) * 64)) = column8(ru, j);
+      }
+  }
 }
 
 // 2048 x 4096 x 14336, both gradients (150 MB moved): 31 us from memory, 4.9 TB/s.
 __global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs A) {
   const int wg = blockIdx.x;
   if (wg >= A.begin[2])
-    prepare_weights(A, wg - A.begin[2]);
+    prepare_weights(A, A.packed, A.tiled, A.ut, wg - A.begin[2]);
   else if (wg >= A.begin[1])
     prepare_xhat(A, wg - A.begin[1]);
   else
     prepare_dy(A, wg);
+}
+
+template <bool SILU>
+__global__ __launch_bounds__(256) void prepare_gated_kernel(const PrepArgs A) {
+  const int wg = blockIdx.x;
+  if (wg >= A.begin_up)
+    prepare_weights(A, A.packed_up, A.tiled_up, A.ut + ((A.n + 63) >> 6) * A.k * kCodes, wg - A.begin_up);
+  else if (wg >= A.begin[2])
+    prepare_weights(A, A.packed, A.tiled, A.ut, wg - A.begin[2]);
+  else if (wg >= A.begin[1])
+    prepare_xhat(A, wg - A.begin[1]);
+  else
+    prepare_gated<SILU>(A, wg);
 }
 
 // ---------------------------------------------------------------------------
@@ -303,6 +394,12 @@ struct GemmJob {
   // them: kept there it would push out the operands, and be written back at
   // the kernel's end (2048 x 4096 x 14336: 472 -> 437 us for both gradients)
   int32_t past_cache;
+  // gated: dx's c is the gate's outputs up to slab `split`, and the up
+  // projection's from there on; dw's rows are the gate's up to row `split`, and
+  // from there on those of cf_up.  *scale_gate: the gate's weight scale
+  int32_t split;
+  float* cf_up;
+  const float* scale_gate;
 };
 
 struct GemmArgs {
@@ -378,10 +475,17 @@ __device__ __forceinline__ void put(V v, P* p, bool past_cache) {
   }
 }
 
-__device__ __forceinline__ void put4(const GemmJob& J, int64_t o, v4f v, float scale) {
+// At offset o of C, in row r (which only GATED asks for).
+template <bool GATED>
+__device__ __forceinline__ void put4(const GemmJob& J, int64_t r, int64_t o, v4f v, float scale) {
   if (J.cf) {
-    if (J.accumulate) v += *G(reinterpret_cast<const v4f*>(J.cf + o));
-    put(v, J.cf + o, J.past_cache);
+    float* cf = J.cf;
+    if (GATED && r >= J.split) {
+      cf = J.cf_up;
+      o -= (int64_t)J.split * J.rb;
+    }
+    if (J.accumulate) v += *G(reinterpret_cast<const v4f*>(cf + o));
+    put(v, cf + o, J.past_cache);
     return;
   }
   v2i w;
@@ -403,7 +507,8 @@ constexpr int stage_bytes(int ti, int tj, bool codes) { return ti * kRow + tj * 
 // global memory straight into a ring of NST buffers in LDS.  Chunk c (16
 // bytes) of row r of a slab sits at chunk c ^ ((r / 2) & 7) of its 128-byte
 // row, so that the 16 rows that LDS serves together lie in distinct banks.
-template <int TI, int TJ, int WI, int WJ, int NST, bool CODES>
+// GATED: C is of a gated block's two projections (GemmJob::split).
+template <int TI, int TJ, int WI, int WJ, int NST, bool CODES, bool GATED>
 __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int kp, int8_t* smem) {
   constexpr int NW = WI * WJ;
   constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;
@@ -542,6 +647,16 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
     }
     __builtin_amdgcn_sched_barrier(0);
     multiply(issue, KS - 1, fa[(KS - 1) & 1], fb[(KS - 1) & 1], st);
+    // The gate's sum is to be divided by its weight scale and the up projection's
+    // by its own: times their ratio, it is divided with the other at the end.
+    if constexpr (GATED && CODES)
+      if (s + 1 == min(J.split - s0, nsl)) {  // the last of the gate's slabs in this part
+        const float f = load_f32_vmem(J.scale) / load_f32_vmem(J.scale_gate);
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+#pragma unroll
+          for (int j = 0; j < FJ; ++j) acc[i][j] *= f;
+      }
   };
   int s = 0;
   for (; s + NST < nsl; ++s) slab(std::true_type{}, s);
@@ -578,7 +693,7 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
       if (J.ksplit > 1)
         *G(reinterpret_cast<v4f*>(J.part + (int64_t)kp * J.ra * J.rb + o)) = v;
       else
-        put4(J, o, v, sc);
+        put4<GATED>(J, r, o, v, sc);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -622,7 +737,7 @@ constexpr size_t kLdsSmall = std::max(ring_bytes(64, kDeep64, kDeep64c), ring_by
 constexpr size_t kLdsBig = ring_bytes(256, kDeep256, kDeep256c);
 static_assert(2 * kLdsSmall <= 160 * 1024 && kLdsBig <= 160 * 1024, "LDS of a CU");
 
-template <bool BIG>
+template <bool BIG, bool GATED>
 __global__ __launch_bounds__(BIG ? 512 : 256, 2) void gemm_kernel(const GemmArgs A) {
   extern __shared__ __align__(16) int8_t smem[];
   const int wg = blockIdx.x;
@@ -640,23 +755,24 @@ __global__ __launch_bounds__(BIG ? 512 : 256, 2) void gemm_kernel(const GemmArgs
   if (!tile_of(wg - A.begin[ji], J, &ti, &tj, &kp)) return;
   if constexpr (BIG) {
     if (J.codes)
-      gemm_tile<256, 256, 2, 4, kDeep256c, true>(J, ti, tj, kp, smem);
+      gemm_tile<256, 256, 2, 4, kDeep256c, true, GATED>(J, ti, tj, kp, smem);
     else
-      gemm_tile<256, 256, 2, 4, kDeep256, false>(J, ti, tj, kp, smem);
+      gemm_tile<256, 256, 2, 4, kDeep256, false, GATED>(J, ti, tj, kp, smem);
   } else if (J.cfg == 1) {
     if (J.codes)
-      gemm_tile<128, 128, 2, 2, kDeep128c, true>(J, ti, tj, kp, smem);
+      gemm_tile<128, 128, 2, 2, kDeep128c, true, GATED>(J, ti, tj, kp, smem);
     else
-      gemm_tile<128, 128, 2, 2, kDeep128, false>(J, ti, tj, kp, smem);
+      gemm_tile<128, 128, 2, 2, kDeep128, false, GATED>(J, ti, tj, kp, smem);
   } else {
     if (J.codes)
-      gemm_tile<64, 64, 2, 2, kDeep64c, true>(J, ti, tj, kp, smem);
+      gemm_tile<64, 64, 2, 2, kDeep64c, true, GATED>(J, ti, tj, kp, smem);
     else
-      gemm_tile<64, 64, 2, 2, kDeep64, false>(J, ti, tj, kp, smem);
+      gemm_tile<64, 64, 2, 2, kDeep64, false, GATED>(J, ti, tj, kp, smem);
   }
 }
 
 // Adds the parts of the split products, in order: four columns a thread.
+template <bool GATED>
 __global__ __launch_bounds__(256) void gemm_finish_kernel(const GemmArgs A, int64_t first1, int64_t total) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= total) return;
@@ -664,7 +780,7 @@ __global__ __launch_bounds__(256) void gemm_finish_kernel(const GemmArgs A, int6
   const int64_t o = 4 * (id - (id >= first1 ? first1 : 0)), slice = (int64_t)J.ra * J.rb;
   v4f v = *G(reinterpret_cast<const v4f*>(J.part + o));
   for (int p = 1; p < J.ksplit; ++p) v += *G(reinterpret_cast<const v4f*>(J.part + p * slice + o));
-  put4(J, o, v, !J.cf ? load_f32_vmem(J.scale) : 1.0f);
+  put4<GATED>(J, GATED ? o / J.rb : 0, o, v, !J.cf ? load_f32_vmem(J.scale) : 1.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -935,7 +1051,7 @@ __device__ __forceinline__ void direct_tile(const DirectArgs& A, const GemmJob& 
   for (int e = 0; e < 4; ++e) {
     const int64_t c = op.j0 + wj0 + 8 * e + 4 * lg;
     if (c >= J.rb) continue;
-    put4(J, r * J.rb + c, v4f{acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]}, sc);
+    put4<false>(J, r, r * J.rb + c, v4f{acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]}, sc);
   }
 }
 
@@ -961,49 +1077,50 @@ struct WsLayout {
   size_t dys, dyt, dbp, xt, ut, part[2], total;
 };
 
-WsLayout layout(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
+WsLayout layout(int64_t m, int64_t n, int64_t k, bool dx, bool dw, bool gated) {
   WsLayout L = {};
-  const BackwardPlan p = L.plan = plan_backward(m, n, k, dx, dw);
+  const BackwardPlan p = L.plan = plan_backward(m, n, k, dx, dw, gated);
+  const int64_t both = gated ? 2 : 1;
   if (p.direct) return L;  // no workspace
   auto take = [&](size_t& off, bool want, int64_t bytes) {
     off = L.total;
     if (want) L.total = align256(L.total + (size_t)bytes);
   };
-  take(L.dys, dx && !dy_as_is(n), slabs_of(n) * m * kRow);
-  take(L.ut, dx, slabs_of(n) * k * kCodes);
-  take(L.dyt, dw, slabs_of(m) * n * kRow);
+  take(L.dys, dx && (gated || !dy_as_is(n)), both * slabs_of(n) * m * kRow);
+  take(L.ut, dx, both * slabs_of(n) * k * kCodes);
+  take(L.dyt, dw, slabs_of(m) * both * n * kRow);
   take(L.xt, dw, slabs_of(m) * k * kRow);
-  take(L.dbp, dw, slabs_of(m) * n * 4);
+  take(L.dbp, dw && !gated, slabs_of(m) * n * 4);
   take(L.part[0], dx && p.ksplit[0] > 1, 4 * p.ksplit[0] * m * k);
-  take(L.part[1], dw && p.ksplit[1] > 1, 4 * p.ksplit[1] * n * k);
+  take(L.part[1], dw && p.ksplit[1] > 1, 4 * p.ksplit[1] * both * n * k);
   return L;
 }
 
-template <bool BIG>
+template <bool BIG, bool GATED>
 hipError_t launch_gemm(const GemmArgs& a, int64_t wgs, hipStream_t s) {
   constexpr size_t lds = BIG ? kLdsBig : kLdsSmall;
   static_assert(lds > 64 * 1024, "the attribute is needed above 64 KB");
   static std::atomic<bool> done[kMaxDevices];  // once per device
   const int dev = current_device_index();
   if (!done[dev].load(std::memory_order_acquire)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gemm_kernel<BIG>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gemm_kernel<BIG, GATED>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
     done[dev].store(true, std::memory_order_release);
   }
-  gemm_kernel<BIG><<<(unsigned)wgs, BIG ? 512 : 256, lds, s>>>(a);
+  gemm_kernel<BIG, GATED><<<(unsigned)wgs, BIG ? 512 : 256, lds, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t backward_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
-  return layout(m, n, k, dx, dw).total;
+  return layout(m, n, k, dx, dw, false).total;
 }
 
 hipError_t launch_backward(const BackwardArgs& b, char* ws, size_t ws_bytes, hipStream_t s) {
   const bool dx = b.dx != nullptr, dw = b.dw != nullptr;
-  const WsLayout L = layout(b.m, b.n, b.k, dx, dw);
+  const WsLayout L = layout(b.m, b.n, b.k, dx, dw, false);
   const BackwardPlan& p = L.plan;
   if (ws_bytes < L.total) return hipErrorInvalidValue;
   if (p.direct) {
@@ -1105,10 +1222,98 @@ hipError_t launch_backward(const BackwardArgs& b, char* ws, size_t ws_bytes, hip
     const int threads = big ? 512 : 256;
     grid += (b.n + threads - 1) / threads;
   }
-  e = big ? launch_gemm<true>(g, grid, s) : launch_gemm<false>(g, grid, s);
+  e = big ? launch_gemm<true, false>(g, grid, s) : launch_gemm<false, false>(g, grid, s);
   const int64_t total = finish[0] + finish[1];
   if (e != hipSuccess || total == 0) return e;
-  gemm_finish_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(g, finish[0], total);
+  gemm_finish_kernel<false><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(g, finish[0], total);
+  return hipGetLastError();
+}
+
+size_t gated_backward_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
+  return layout(m, n, k, dx, dw, true).total;
+}
+
+// Two launches (three where a product's sum is split): operands, products.
+hipError_t launch_gated_backward(const GatedBackwardArgs& b, char* ws, size_t ws_bytes, hipStream_t s) {
+  const bool dx = b.dx != nullptr, dw = b.dw_gate != nullptr;
+  const WsLayout L = layout(b.m, b.n, b.k, dx, dw, true);
+  const BackwardPlan& p = L.plan;
+  if (ws_bytes < L.total) return hipErrorInvalidValue;
+  const int64_t ms = slabs_of(b.m), ns = slabs_of(b.n);
+
+  PrepArgs pa = {};
+  pa.m = b.m;
+  pa.n = b.n;
+  pa.k = b.k;
+  pa.dy = b.da;
+  pa.g = b.g;
+  pa.u = b.u;
+  pa.dys = dx ? reinterpret_cast<uint16_t*>(ws + L.dys) : nullptr;
+  pa.dyt = dw ? reinterpret_cast<uint16_t*>(ws + L.dyt) : nullptr;
+  pa.q = b.q;
+  pa.x_scale = b.x_scale;
+  pa.xt = reinterpret_cast<uint16_t*>(ws + L.xt);
+  pa.packed = b.gate;
+  pa.tiled = b.gate_tiled ? 1 : 0;
+  pa.packed_up = b.up;
+  pa.tiled_up = b.up_tiled ? 1 : 0;
+  pa.ut = reinterpret_cast<uint8_t*>(ws + L.ut);
+  int64_t wgs = ms * ((b.n + 255) / 256);
+  pa.begin[1] = (int32_t)wgs;
+  if (dw) wgs += ms * ((b.k + 255) / 256);
+  pa.begin[2] = (int32_t)wgs;
+  if (dx) wgs += ns * ((b.k + 1023) / 1024);
+  pa.begin_up = (int32_t)wgs;
+  if (dx) wgs += ns * ((b.k + 1023) / 1024);
+  if (b.silu)
+    prepare_gated_kernel<true><<<(unsigned)wgs, 256, 0, s>>>(pa);
+  else
+    prepare_gated_kernel<false><<<(unsigned)wgs, 256, 0, s>>>(pa);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+
+  GemmArgs g = {};
+  const int64_t rows[2] = {b.m, 2 * b.n}, slabs[2] = {2 * ns, ms};
+  const bool want[2] = {dx, dw};
+  const bool big = p.cfg[0] == 2;
+  int64_t grid = 0, finish[2] = {0, 0};
+  for (int o = 0; o < 2; ++o) {
+    const int j = o == 0 ? p.order : 1 - p.order;  // 0: dx, 1: dw
+    GemmJob& J = g.j[o];
+    g.begin[o] = (int32_t)grid;
+    if (!want[j]) continue;
+    const Config& C = kConfigs[p.cfg[j]];
+    J.a = reinterpret_cast<const uint8_t*>(ws + (j ? L.dyt : L.dys));
+    J.a_row = kRow;
+    J.a_slab = rows[j] * kRow;
+    J.b = reinterpret_cast<const uint8_t*>(ws + (j ? L.xt : L.ut));
+    J.ra = (int32_t)rows[j];
+    J.rb = (int32_t)b.k;
+    J.slabs = (int32_t)slabs[j];
+    J.tiles_i = (int32_t)((rows[j] + C.ti - 1) / C.ti);
+    J.tiles_j = (int32_t)((b.k + C.tj - 1) / C.tj);
+    J.ksplit = p.ksplit[j];
+    J.kspw = p.kspw[j];
+    J.cfg = p.cfg[j];
+    J.codes = j == 0;
+    J.part = reinterpret_cast<float*>(ws + L.part[j]);
+    J.cf = j ? b.dw_gate : nullptr;
+    J.cf_up = b.dw_up;
+    J.accumulate = b.accumulate ? 1 : 0;
+    J.cb = j ? nullptr : b.dx;
+    J.scale = b.up_scale;
+    J.scale_gate = b.gate_scale;
+    J.split = (int32_t)(j ? b.n : ns);
+    J.res = j ? nullptr : b.residual;
+    J.past_cache = rows[j] * b.k * (j ? 4 : 2) > kL2Bytes ? 1 : 0;
+    if (J.ksplit > 1) finish[o] = rows[j] * (b.k / 4);
+    grid += round_up((int64_t)J.tiles_i * J.tiles_j * J.ksplit, 8);
+  }
+  g.begin[2] = (int32_t)grid;
+  e = big ? launch_gemm<true, true>(g, grid, s) : launch_gemm<false, true>(g, grid, s);
+  const int64_t total = finish[0] + finish[1];
+  if (e != hipSuccess || total == 0) return e;
+  gemm_finish_kernel<true><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(g, finish[0], total);
   return hipGetLastError();
 }
 

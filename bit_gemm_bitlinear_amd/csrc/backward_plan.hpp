@@ -62,8 +62,11 @@ inline float makespan(int64_t na, float a, int64_t nb, float b) {
 
 // Per product the tile size and the parts of its sum, with the smallest
 // estimated time of all together.  256 x 256 tiles are a kernel of their own.
-inline BackwardPlan plan_backward(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
-  const int64_t rows[2] = {m, n}, slabs[2] = {slabs_of(n), slabs_of(m)};
+// gated: two projections of n outputs each, dx's sum and dw's rows those of both
+// (no one-launch kernel).
+inline BackwardPlan plan_backward(int64_t m, int64_t n, int64_t k, bool dx, bool dw, bool gated = false) {
+  const int64_t both = gated ? 2 : 1;
+  const int64_t rows[2] = {m, both * n}, slabs[2] = {both * slabs_of(n), slabs_of(m)};
   const bool want[2] = {dx, dw};
   struct Option {
     int cfg, ksplit, kspw;
@@ -126,6 +129,9 @@ inline BackwardPlan plan_backward(int64_t m, int64_t n, int64_t k, bool dx, bool
       best0 = &a;
       best1 = &b;
     }
+  if (gated)
+    return BackwardPlan{{best0->cfg, best1->cfg}, {best0->ksplit, best1->ksplit}, {best0->kspw, best1->kspw},
+                        best0->us >= best1->us ? 0 : 1, false};
   const float operands = (dx ? 2.0f * m * n + 0.25f * n * k : 0.0f) + (dw ? 2.0f * m * n + 2.0f * m * k : 0.0f);
   if (direct <= best + kPrepareUs + 2.0f * operands / kBytesPerUs) return BackwardPlan{{0, 0}, {1, 1}, {1, 1}, 0, true};
   return BackwardPlan{{best0->cfg, best1->cfg}, {best0->ksplit, best1->ksplit}, {best0->kspw, best1->kspw},

@@ -1,4 +1,4 @@
-// Internal interface of the operators of bitlinear_layer.h, between their entry
+// Internal interface of the operators of bitlinear_layer.h and bitlinear_ffn.h, between their entry
 // points (layer_abi.hip; abi.hip for the forward on codes) and the kernels.
 #pragma once
 
@@ -77,6 +77,77 @@ struct BackwardArgs {
 };
 size_t backward_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw);
 hipError_t launch_backward(const BackwardArgs& a, char* ws, size_t ws_bytes, hipStream_t s);
+
+// Those of a gated block's two projections (backward.hip).
+struct GatedBackwardArgs {
+  int64_t m, n, k;
+  bool silu;
+  const uint16_t* da;
+  const uint16_t* g;
+  const uint16_t* u;
+  // dx (nullptr: not wanted)
+  const uint8_t* gate;
+  const uint8_t* up;
+  bool gate_tiled, up_tiled;
+  const float* gate_scale;
+  const float* up_scale;
+  const uint16_t* residual;
+  uint16_t* dx;
+  // both or neither
+  const int8_t* q;
+  const float* x_scale;
+  float* dw_gate;
+  float* dw_up;
+  bool accumulate;
+};
+size_t gated_backward_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw);
+hipError_t launch_gated_backward(const GatedBackwardArgs& a, char* ws, size_t ws_bytes, hipStream_t s);
+
+// ---- gated feed-forward projections (gated.hip) ----
+struct GatedArgs {
+  int64_t m, n, k;
+  const int8_t* q;
+  const float* x_scale;
+  const uint8_t* codes;  // the storage of bitlinear_ffn.h
+  const float* gate_scale;
+  const float* up_scale;
+  bool silu;
+  uint16_t* a;
+  uint16_t* g;  // or nullptr
+  uint16_t* u;
+};
+hipError_t launch_gated_weights(const uint8_t* gate, bool gate_tiled, const uint8_t* up, bool up_tiled,
+                                int64_t n, int64_t k, uint8_t* codes, hipStream_t s);
+size_t gated_forward_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_gated_forward(const GatedArgs& a, char* ws, hipStream_t s);
+
+// ---- 8-bit weights (w8.hip) ----
+hipError_t launch_w8_pack(const float* w, int64_t n, int64_t k, int8_t* codes, float* scale, hipStream_t s);
+hipError_t launch_w8_unpack(const int8_t* codes, const float* scale, int64_t n, int64_t k, float* out,
+                            hipStream_t s);
+struct W8Args {
+  int64_t m, n, k;
+  const int8_t* q;
+  const float* x_scale;
+  const int8_t* codes;
+  const float* scale;
+  const uint16_t* bias;  // or nullptr
+  uint16_t* y;
+};
+size_t w8_forward_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_w8_forward(const W8Args& a, char* ws, hipStream_t s);
+
+// ---- gradient norm and clipping (grad_norm.hip) ----
+struct Gradient {
+  const void* g;
+  void* out;
+  int64_t numel;
+  bool bf16;
+};
+size_t grad_norm_bytes(int32_t count, const int64_t* numel);
+// norm: 1 float.  clip: out = g * min(1, max_norm / (norm + 1e-6)) as well.
+hipError_t launch_grad_norm(int32_t count, const Gradient* t, bool clip, float max_norm, float* norm, char* ws,
+                            hipStream_t s);
 
 // ---- 4-bit weights (w4.hip) ----
 hipError_t launch_w4_pack(const float* w, int64_t n, int64_t k, int group, uint8_t* codes,

@@ -10,9 +10,14 @@ residual stream, or x).
 
     y = linear(x, weight)                                    # one BitLinear
     h, (q, k, v) = norm_linear(x, [wq, wk, wv], norm, residual)  # a block's entry
+    h, a = norm_gated(x, w_gate, w_up, norm, residual)       # a feed-forward block's
+    norm = clip_grad_norm(model.parameters(), 1.0)           # after the backward pass
 
 ``norm_linear`` adds the residual, normalizes, quantizes once, and runs every
-projection on the same codes.  ``BitLinear`` is ``linear`` as a module.  For
+projection on the same codes; ``norm_gated`` runs the gate and up projections,
+the activation function and the product in one kernel, and its backward pass
+keeps g and u in bf16.  ``BitLinear`` is ``linear`` as a module, ``FeedForward``
+a whole feed-forward block.  For
 inference pack the trained weights once: ``bitlinear.BitLinear(module.weight)``.
 
 The gradients take up to 2^21 tokens and outputs a layer (bitlinear_backward's
@@ -30,7 +35,7 @@ from torch.autograd.function import once_differentiable
 
 from . import bitlinear as bl
 
-__all__ = ["BitLinear", "linear", "norm_linear"]
+__all__ = ["BitLinear", "FeedForward", "clip_grad_norm", "linear", "norm_gated", "norm_linear"]
 
 
 def _aligned(t: torch.Tensor | None):
@@ -162,6 +167,46 @@ class _NormLinear(torch.autograd.Function):
                 *dws, *dbs)
 
 
+class _NormGated(torch.autograd.Function):
+    """Rows of h, with a residual, and of a (see _NormLinear)."""
+
+    @staticmethod
+    def forward(ctx, x, residual, norm_weight, eps, activation, keep, w_gate, w_up):
+        ctx.set_materialize_grads(False)
+        normed = bl.rms_norm_quant(_rows(x), _aligned(norm_weight), _rows(residual), eps)
+        (pg, sg), (pu, su) = (bl.pack_weights(_aligned(w)) for w in (w_gate, w_up))
+        out = bl.forward_gated(normed.q, normed.x_scale, bl.gated_weights(pg, sg, pu, su), activation, keep)
+        if keep:
+            ctx.save_for_backward(normed.q, normed.x_scale, normed.h, normed.rstd, norm_weight, out.g, out.u,
+                                  pg, sg, pu, su)
+        ctx.activation, ctx.x_shape, ctx.has_residual = activation, x.shape, residual is not None
+        return (normed.h, out.a) if residual is not None else (out.a,)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        q, xs, h, rstd, norm_weight, g, u, pg, sg, pu, su = ctx.saved_tensors
+        dh, da = grads if ctx.has_residual else (None, *grads)
+        want_x, want_r, want_norm = ctx.needs_input_grad[:3]
+        want_g, want_u = ctx.needs_input_grad[6:]
+        want_dn, want_w = want_x or want_r or want_norm, want_g or want_u
+        dx = dweight = dwg = dwu = None
+        if da is not None and (want_dn or want_w):
+            weights = (pg, sg, pu, su) if want_dn else (None,) * 4
+            dn, dwg, dwu = bl.GatedBackwardCall(_aligned(da), g, u, ctx.activation, q if want_w else None,
+                                                xs if want_w else None, *weights, k=q.shape[1])()
+            if want_dn:
+                dx, dweight = bl.rms_norm_quant_backward(dn, h, rstd, _aligned(norm_weight), _aligned(dh),
+                                                        want_dweight=want_norm)
+                dx = dx.reshape(ctx.x_shape)
+                if want_norm:
+                    dweight = dweight.to(norm_weight.dtype)
+        elif dh is not None:  # a was not used
+            dx = dh.reshape(ctx.x_shape)
+        return (dx if want_x else None, dx if want_r else None, dweight if want_norm else None, None, None, None,
+                dwg if want_g else None, dwu if want_u else None)
+
+
 class _NoTokens(torch.autograd.Function):
     """Output rows [0, N] of each of `widths`, for inputs x without a token:
     every gradient is zero.  (The library's calls take one token or more.)"""
@@ -215,6 +260,46 @@ def norm_linear(x: torch.Tensor, weights: Sequence[torch.Tensor],
     return h, [y.reshape(*x.shape[:-1], y.shape[1]) for y in out]
 
 
+def norm_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+               norm_weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+               activation: str = "relu2", eps: float = 1e-6):
+    """RMSNorm of bf16 x [..., K] (plus a residual of the same shape) with an
+    optional bf16 or fp32 weight [K], then act(gate) * up of its output: the
+    BitLinears w_gate and w_up (latent fp32 [N, K] each) and the activation
+    function, "relu2" or "silu".  Returns (h, a): h as norm_linear's, a bf16
+    [..., N]; differentiable throughout, without a token empty, as there."""
+    bl._activation(activation)
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
+    _check_weights([w_gate, w_up], x.shape[-1])
+    if w_gate.shape != w_up.shape:
+        raise ValueError(f"the gate has shape {list(w_gate.shape)}, the up projection {list(w_up.shape)}")
+    inputs = [t for t in (x, residual, norm_weight, w_gate, w_up) if t is not None]
+    if x.numel():
+        keep = torch.is_grad_enabled() and any(t.requires_grad for t in inputs)
+        out = _NormGated.apply(x, residual, norm_weight, eps, activation, keep, w_gate, w_up)
+    else:
+        n = w_gate.shape[0]
+        out = _NoTokens.apply([n] if residual is None else [x.shape[-1], n], x, residual, norm_weight, w_gate, w_up)
+    a = out[-1].reshape(*x.shape[:-1], w_gate.shape[0])
+    return (x if residual is None else out[0].reshape(x.shape)), a
+
+
+def clip_grad_norm(parameters, max_norm: float) -> torch.Tensor:
+    """Scales the gradients (.grad, fp32 or bf16, on one device) of the
+    parameters in place, so that their norm, taken over all of them together, is
+    at most max_norm; returns the norm before, a 0-d fp32 tensor on the device.
+    Two passes over the gradients, and nothing waits for them: where the norm is
+    not finite, the gradients are spoiled as bitlinear.ClipGradsCall says, and the
+    caller's to look at.  A parameter listed twice counts once."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = list({id(p): p.grad for p in parameters if p.grad is not None}.values())
+    if not grads:
+        return torch.zeros(())
+    return bl.clip_grads(grads, max_norm)[0].reshape(())
+
+
 class BitLinear(torch.nn.Module):
     """A trainable BitLinear: latent fp32 weight [out, in], optional bf16
     bias."""
@@ -232,3 +317,35 @@ class BitLinear(torch.nn.Module):
 
     def extra_repr(self) -> str:
         return f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}"
+
+
+class FeedForward(torch.nn.Module):
+    """A trainable gated feed-forward block: norm, gate and up projections,
+    activation function ("relu2" or "silu") and product, with `sub_norm` another
+    norm, and the down projection; latent fp32 weights, fp32 norm weights."""
+
+    def __init__(self, features: int, hidden: int, activation: str = "relu2", sub_norm: bool = True,
+                 eps: float = 1e-6, device=None):
+        super().__init__()
+        bl._activation(activation)
+        self.activation, self.eps = activation, eps
+
+        def weight(n, k):
+            return torch.nn.Parameter(torch.randn(n, k, dtype=torch.float32, device=device) * k ** -0.5)
+
+        self.gate, self.up, self.down = weight(hidden, features), weight(hidden, features), weight(features, hidden)
+        self.norm = torch.nn.Parameter(torch.ones(features, dtype=torch.float32, device=device))
+        self.sub_norm = (torch.nn.Parameter(torch.ones(hidden, dtype=torch.float32, device=device))
+                         if sub_norm else None)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        """(h, y) of bf16 x [..., features]: h = x + residual (x without one), and
+        the block's output y, which the next residual add takes."""
+        h, a = norm_gated(x, self.gate, self.up, self.norm, residual, self.activation, self.eps)
+        if self.sub_norm is None:
+            return h, linear(a, self.down)
+        return h, norm_linear(a, [self.down], self.sub_norm, eps=self.eps)[1][0]
+
+    def extra_repr(self) -> str:
+        return (f"features={self.down.shape[0]}, hidden={self.down.shape[1]}, activation={self.activation!r}, "
+                f"sub_norm={self.sub_norm is not None}")

@@ -26,3 +26,4 @@ from .bitlinear_oracle import (  # noqa: F401
     weight_scale,
 )
 from . import layer_oracle as layer  # noqa: F401
+from . import ffn_oracle as ffn  # noqa: F401

@@ -1,0 +1,709 @@
+"""The operators of a feed-forward block and of a training step
+(bitlinear_ffn.h) on the GPU, against plain float64 forms
+(oracle/ffn_oracle.py).
+
+What a definition rounds is compared bit for bit; sums are held to bounds by
+arithmetic: U = 2^-24 is half a step of fp32, a result rounded to bf16 is off by
+2^-8 of itself (half a step, relative), and the matrix cores' fp32 sums count a
+whole step (2^-23) per term, as their rounding mode is not ours to choose.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import ffn as ref
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+U = 2.0 ** -24
+BF = 2.0 ** -8
+TINY = 2.0 ** -126  # the smallest normal number of fp32 and bf16
+
+
+@pytest.fixture(scope="module")
+def bl():
+    from bit_gemm_bitlinear_amd import bitlinear
+
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    return bitlinear
+
+
+@pytest.fixture(scope="module")
+def tr():
+    from bit_gemm_bitlinear_amd import training
+
+    return training
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def to_dev(bits):
+    return dev(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16)
+
+
+def bits_of(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def bf16(a):
+    """fp32 values of a rounded to bf16."""
+    return oracle.bf16_to_f32(oracle.f32_to_bf16(np.asarray(a, np.float32)))
+
+
+def codes(rng, m, k):
+    """int8 codes (the whole range, -128 among them) and scales (one of a tiny
+    row); every fifth row is zeros."""
+    q = rng.integers(-128, 128, (m, k)).astype(np.int8)
+    q[3::5] = 0
+    s = np.exp(rng.standard_normal(m)).astype(np.float32) * 20
+    s[1::7] = 1.27e7
+    return q, s
+
+
+def ternary(rng, n, k):
+    """Ternary weights with whole zero rows, their packed form's bits and scale."""
+    u = rng.integers(-1, 2, (n, k)).astype(np.int8)
+    u[2::11] = 0
+    return u, oracle.pack(u), np.float32(rng.uniform(20, 90))
+
+
+def guarded(shape, dtype):
+    """A tensor in the middle of a larger one filled with a pattern, and a check
+    that the rest is as it was."""
+    n = int(np.prod(shape))
+    pad = 256
+    whole = torch.full((n + 2 * pad,), 7, dtype=dtype, device=DEV)
+    inner = whole[pad:pad + n].view(shape)
+
+    def check():
+        assert bool((whole[:pad] == 7).all()) and bool((whole[pad + n:] == 7).all()), "written outside the output"
+
+    return inner, check
+
+
+# ----------------------------------------------------------------- gated
+
+SHAPES = [(1, 16, 256), (1, 1, 4), (2, 17, 260), (5, 40, 2084), (16, 33, 512), (17, 100, 1028), (31, 259, 252),
+          (64, 130, 640), (77, 1003, 2084), (129, 300, 1280), (257, 515, 388), (300, 64, 4096), (1, 6912, 2560),
+          (4, 4096, 1024), (513, 1024, 128)]
+
+
+def gated_inputs(bl, seed, m, n, k, tiled=False):
+    rng = np.random.default_rng(seed)
+    q, xs = codes(rng, m, k)
+    (ug, pg, sg), (uu, pu, su) = ternary(rng, n, k), ternary(rng, n, k)
+    tg, tu, dsg, dsu = dev(pg), dev(pu), dev(np.array([sg])), dev(np.array([su]))
+    return q, xs, ug, sg, uu, su, tg, dsg, tu, dsu
+
+
+def check_gated(a, g, u, want_a, act):
+    """a against its float64 form.  g and u of that form are the kernel's own
+    fp32 values.  relu2: three products, 3 U; silu: exp2's argument is rounded
+    (|g| log2(e) at 2 U, times ln 2: 2 |g| U of e), exp2, the sum, the reciprocal
+    and three products a step (2 U) each at most; the rounding to bf16.  exp2
+    gives no value below the normal range but 0: exp(-|g|) is then off by TINY at
+    most, and a = g u exp(-|g|) / (1 + exp(-|g|)) by |g u| TINY."""
+    rel = 3 * U if act == "relu2" else (14 + 2 * np.abs(g.astype(np.float64))) * U
+    tol = np.abs(want_a) * (BF * (1 + rel) + rel) + TINY
+    if act == "silu":
+        tol = tol + np.abs(g.astype(np.float64) * u) * TINY
+    assert np.all(np.abs(a - want_a) <= tol), np.max(np.abs(a - want_a) / np.maximum(tol, 1e-300))
+
+
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gated(bl, m, n, k, act):
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu = gated_inputs(bl, 11, m, n, k)
+    w = bl.gated_weights(tg, dsg, tu, dsu)
+    if n * k < 20000:
+        assert np.array_equal(w.codes.flatten().cpu().numpy(), ref.gated_pack(ug, uu))
+    outs, checks = zip(*(guarded((m, n), torch.bfloat16) for _ in range(3)))
+    dq, dxs = dev(q), dev(xs)
+    r = bl.GatedCall(dq, dxs, w, act, keep=True, out=bl.Gated(*outs))()
+    for c in checks:
+        c()
+    want_a, g, u = ref.gated_forward(q, xs, ug, sg, uu, su, act)
+    assert np.array_equal(bits_of(r.g), oracle.f32_to_bf16(g)) and np.array_equal(bits_of(r.u), oracle.f32_to_bf16(u))
+    check_gated(f64(r.a), g, u, want_a, act)
+    alone = bl.forward_gated(dq, dxs, w, act)
+    assert alone.g is None and torch.equal(alone.a.view(torch.int16), r.a.view(torch.int16))
+
+
+def test_gated_layouts_and_projections(bl):
+    """Either layout of the packed weights, and g and u of the BitLinear calls."""
+    m, n, k = 40, 96, 768
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu = gated_inputs(bl, 12, m, n, k)
+    q = np.maximum(q, -127)  # codes as the quantizer writes them
+    dq, dxs = dev(q), dev(xs)
+    w = bl.gated_weights(tg, dsg, tu, dsu)
+    for pg in (tg, bl.tile_weights(tg)):
+        for pu in (tu, bl.tile_weights(tu)):
+            assert torch.equal(bl.gated_weights(pg, dsg, pu, dsu, k=k).codes, w.codes)
+    r = bl.forward_gated(dq, dxs, w, "silu", keep=True)
+    ys = bl.GroupedQuantizedCall([dq] * 2, [dxs] * 2, [tg, tu], [dsg, dsu])()
+    assert torch.equal(r.g, ys[0]) and torch.equal(r.u, ys[1])
+
+
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+def test_gated_extremes(bl, act):
+    """Projections far outside silu's and relu2's ordinary range, from scales."""
+    m, n, k = 20, 48, 256
+    q, xs, ug, sg, uu, su, tg, _, tu, _ = gated_inputs(bl, 13, m, n, k)
+    xs[:] = 1.0
+    for gs, us in ((1e-6, 1e-9), (1e6, 1.0), (1e-2, 1e12), (1e12, 1e-12), (3e-17, 1e3)):
+        gs, us = np.float32(gs), np.float32(us)
+        r = bl.forward_gated(dev(q), dev(xs), bl.gated_weights(tg, dev(np.array([gs])), tu, dev(np.array([us]))), act,
+                             keep=True)
+        with np.errstate(over="ignore"):
+            want_a, g, u = ref.gated_forward(q, xs, ug, gs, uu, us, act)
+        a = f64(r.a)
+        fine = np.abs(want_a) < 3e38
+        if act == "relu2":
+            assert np.all(np.isfinite(a[fine]))
+            # r * u may be below the normal range where the result is not
+            fine &= (np.abs(g.astype(np.float64) * u) > TINY) | (g <= 0) | (u == 0)
+        check_gated(a[fine], g[fine], u[fine], want_a[fine], act)
+
+
+def test_gated_one_bad_row(bl):
+    """A scale that is not finite spoils its row and no other."""
+    for m in (3, 40):
+        q, xs, ug, sg, uu, su, tg, dsg, tu, dsu = gated_inputs(bl, 14, m, 64, 512)
+        w = bl.gated_weights(tg, dsg, tu, dsu)
+        good = bl.forward_gated(dev(q), dev(xs), w, "silu").a
+        xs[1] = np.nan
+        bad = bl.forward_gated(dev(q), dev(xs), w, "silu").a
+        keep = [i for i in range(m) if i != 1]
+        assert torch.equal(bad[keep], good[keep]) and not bool(torch.isfinite(bad[1]).any())
+
+
+BACK = [(1, 1, 4), (1, 16, 64), (3, 5, 8), (64, 64, 64), (65, 67, 68), (40, 1000, 260), (301, 1001, 1284), (130, 520, 640),
+        (700, 200, 520), (520, 2048, 516)]
+
+
+def backward_inputs(bl, seed, m, n, k):
+    rng = np.random.default_rng(seed)
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu = gated_inputs(bl, seed, m, n, k)
+    da, g, u = (bf16(rng.standard_normal((m, n)) * s) for s in (1e-3, 1.5, 1.5))
+    da[2::5] = 0
+    g[:, ::13] = 0
+    return q, xs, ug, sg, uu, su, tg, dsg, tu, dsu, da, g, u
+
+
+def check_backward(out, want, m, n, res=None):
+    dx, dwg, dwu = out
+    if dx is not None:
+        # 2 n terms; the ratio of the scales, the gate's sum times it and the
+        # quotient: four more roundings; the rounding to bf16
+        tol = want["dx_abs"] * ((2 * n + 4) * 2 * U) + TINY
+        w = want["dx"] if res is None else want["dx"] + res
+        tol = tol + BF * (np.abs(want["dx"]) + tol) + (0 if res is None else BF * (np.abs(w) + tol) * (1 + BF))
+        assert np.all(np.abs(f64(dx) - w) <= tol), np.max(np.abs(f64(dx) - w) / tol)
+    for got, name in ((dwg, "dw_gate"), (dwu, "dw_up")):
+        if got is not None:
+            tol = want[name + "_abs"] * ((m + 2) * 2 * U) + TINY
+            assert np.all(np.abs(f64(got) - want[name]) <= tol), (name, np.max(np.abs(f64(got) - want[name]) / tol))
+
+
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+@pytest.mark.parametrize("m,n,k", BACK)
+def test_gated_backward(bl, m, n, k, act):
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu, da, g, u = backward_inputs(bl, 21, m, n, k)
+    xhat = oracle.bf16_to_f32(layer.restore_activations(q, xs))
+    want = ref.gated_backward(*(t.astype(np.float64) for t in (da, g, u)), act, ug, sg, uu, su, xhat)
+    dda, dg, du = (to_dev(oracle.f32_to_bf16(t)) for t in (da, g, u))
+    dx, ck0 = guarded((m, k), torch.bfloat16)
+    dwg, ck1 = guarded((n, k), torch.float32)
+    dwu, ck2 = guarded((n, k), torch.float32)
+    call = bl.GatedBackwardCall(dda, dg, du, act, dev(q), dev(xs), tg, dsg, tu, dsu, dx=dx, dw_gate=dwg, dw_up=dwu)
+    check_backward(call(), want, m, n)
+    for c in (ck0, ck1, ck2):
+        c()
+    first = [t.clone() for t in call._out]
+    for a, b in zip(first, call()):
+        assert torch.equal(a, b)  # the same again
+    # either part alone, and added to what is there
+    alone = bl.GatedBackwardCall(dda, dg, du, act, gate=tg, gate_scale=dsg, up=tu, up_scale=dsu)()
+    check_backward(alone, want, m, n)
+    assert alone[1] is None and alone[2] is None
+    alone = bl.GatedBackwardCall(dda, dg, du, act, dev(q), dev(xs))()
+    check_backward(alone, want, m, n)
+    assert alone[0] is None
+    rng = np.random.default_rng(22)
+    res = bf16(rng.standard_normal((m, k)) * 1e-3)
+    dx = to_dev(oracle.f32_to_bf16(res))
+    had = [torch.randn(n, k, device=DEV) for _ in range(2)]
+    acc = [t.clone() for t in had]
+    out = bl.GatedBackwardCall(dda, dg, du, act, dev(q), dev(xs), tg, dsg, tu, dsu, residual=dx, dx=dx, dw_gate=acc[0],
+                               dw_up=acc[1], accumulate=True)()
+    check_backward((out[0], None, None), want, m, n, res.astype(np.float64))
+    for got, was, name in ((out[1], had[0], "dw_gate"), (out[2], had[1], "dw_up")):
+        w = want[name] + f64(was)
+        tol = want[name + "_abs"] * ((m + 2) * 2 * U) + U * np.abs(w) * 2 + TINY
+        assert np.all(np.abs(f64(got) - w) <= tol), name
+
+
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+def test_gate_gradients_bit_for_bit(bl, act):
+    """One token whose restored activation is 1 in column 0: dw[:, 0] is dg and
+    du.  (silu's float64 forms may differ in their last bits: a value at a border
+    of fp32, one in 2^28, would be seen here.)"""
+    n = 6000
+    rng = np.random.default_rng(23)
+    g = np.concatenate([rng.standard_normal(n - 20) * 4, [0, -0.0, 1e-30, -1e-30, 50, -50, 88, -88, 89, -89, 100, -100, 500,
+                                                          -500, 1e4, -1e4, 1.2785, -1.2785, 3e-39, 1e-10]])
+    g, da, u = bf16(g)[None], bf16(rng.standard_normal(n))[None], bf16(rng.standard_normal(n))[None]
+    q = np.zeros((1, 4), np.int8)
+    q[0, 0] = 127
+    out = bl.GatedBackwardCall(*(to_dev(oracle.f32_to_bf16(t)) for t in (da, g, u)), act, dev(q),
+                               dev(np.array([127], np.float32)))()
+    dg, du = ref.gate_gradients(*(t.astype(np.float64) for t in (da, g, u)), act)
+    for got, want in ((out[1], dg[0]), (out[2], du[0])):
+        got = f64(got)[:, 0]
+        same = (got == want) | (np.abs(want) < TINY)  # below the normal range the matrix cores may flush
+        assert np.all(same), (got[~same], want[~same])
+        assert not np.any(f64(out[1])[:, 1:])
+
+
+def test_gated_backward_tiled_weights(bl):
+    m, n, k = 70, 96, 512
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu, da, g, u = backward_inputs(bl, 24, m, n, k)
+    dda, dg, du = (to_dev(oracle.f32_to_bf16(t)) for t in (da, g, u))
+    want = bl.GatedBackwardCall(dda, dg, du, "silu", gate=tg, gate_scale=dsg, up=tu, up_scale=dsu)()[0]
+    for pg in (tg, bl.tile_weights(tg)):
+        for pu in (tu, bl.tile_weights(tu)):
+            got = bl.GatedBackwardCall(dda, dg, du, "silu", gate=pg, gate_scale=dsg, up=pu, up_scale=dsu, k=k)()[0]
+            assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+def test_gated_backward_against_differences(bl, act):
+    """The directional derivatives of <da, act(g) u> along the restored
+    activations and along the (unrounded) weights, in float64, against the
+    gradients: what g and u are rounded to (bf16) and dg and du cost at most 2^-8
+    each of every term's magnitude, to which act'(g) answers with its own slope
+    (2 at most for relu2 near 0 relative to itself, |g act''| for silu)."""
+    m, n, k = 24, 40, 64
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu, da, _, _ = backward_inputs(bl, 25, m, n, k)
+    rng = np.random.default_rng(26)
+    xs[:] = 40.0
+    xhat = oracle.bf16_to_f32(layer.restore_activations(q, xs)).astype(np.float64)
+    wg, wu = ug / np.float64(sg) + 0, uu / np.float64(su) + 0
+    g, u = bf16(xhat @ wg.T), bf16(xhat @ wu.T)
+    out = bl.GatedBackwardCall(*(to_dev(oracle.f32_to_bf16(t)) for t in (da, g, u)), act, dev(q), dev(xs), tg, dsg, tu,
+                               dsu)()
+
+    def value(x, a, b):
+        return np.sum(da * ref.activation(act, x @ a.T)[0] * (x @ b.T))
+
+    t = 1e-5
+    # the magnitudes that the roundings act on
+    g64, u64 = xhat @ wg.T, xhat @ wu.T
+    h, dh = ref.activation(act, g64)
+    mag_g = np.abs(da) * (np.abs(u64) * (np.abs(dh) + np.abs(g64) * (2 if act == "relu2" else 1)))
+    mag_u = np.abs(da) * (np.abs(h) + np.abs(g64 * dh))
+    for which in range(3):
+        d = rng.standard_normal(((m, k), (n, k), (n, k))[which])
+        args = [xhat, wg, wu]
+        up, down = list(args), list(args)
+        up[which], down[which] = args[which] + t * d, args[which] - t * d
+        num = (value(*up) - value(*down)) / (2 * t)
+        got = np.sum(f64(out[which]) * d)
+        if which == 0:
+            mag = np.sum(mag_g * np.abs(d @ wg.T) + mag_u * np.abs(d @ wu.T)) + np.sum(np.abs(f64(out[0]) * d))
+        else:
+            mag = np.sum((mag_g, mag_u)[which - 1] * np.abs(xhat @ d.T))
+        assert abs(got - num) <= 3 * BF * mag, (which, got, num, mag)
+
+
+# -------------------------------------------------------------------- w8
+
+W8_SHAPES = [(1, 1, 4), (1, 16, 64), (1, 4096, 1024), (2, 17, 68), (5, 40, 2084), (9, 1003, 2084), (16, 33, 512),
+             (17, 100, 1028), (33, 64, 4096), (64, 130, 640), (77, 515, 388), (129, 300, 1280), (257, 259, 252),
+             (300, 600, 2048), (600, 1030, 512), (3, 200, 16384)]
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("m,n,k", W8_SHAPES)
+def test_w8(bl, m, n, k, bias):
+    rng = np.random.default_rng(31)
+    q, xs = codes(rng, m, k)
+    w = (0.02 * rng.standard_normal((n, k)) * np.exp(rng.standard_normal((n, 1)))).astype(np.float32)
+    w[n // 2] = 0
+    v, s = ref.w8_quant(w)
+    packed = bl.pack_weights_w8(dev(w))
+    assert np.array_equal(packed.codes.flatten().cpu().numpy(), ref.w8_pack(v))
+    assert np.array_equal(packed.scale.cpu().numpy(), s)
+    assert np.array_equal(bl.unpack_weights_w8(packed).cpu().numpy(), (v * s[:, None]).astype(np.float32))
+    b = bf16(rng.standard_normal(n)) if bias else None
+    want = ref.w8_forward(q, xs, v, s)
+    if bias:
+        want = oracle.add_bf16(want, np.broadcast_to(oracle.f32_to_bf16(b), want.shape))
+    out, check = guarded((m, n), torch.bfloat16)
+    call = bl.W8Call(dev(q), dev(xs), packed, out=out, bias=to_dev(oracle.f32_to_bf16(b)) if bias else None)
+    for _ in range(2):
+        assert np.array_equal(bits_of(call()), want)
+    check()
+
+
+def test_w8_extreme_weights(bl):
+    """Rows of the smallest and largest magnitudes, and whole sums of the largest
+    codes over the longest K."""
+    w = np.zeros((5, 64), np.float32)
+    w[0, 3], w[1, :], w[2, ::2], w[3, 7], w[4, :2] = 3e38, 1e-44, -1e-38, 1e-45, (1.0, -2.0)
+    p = bl.pack_weights_w8(dev(w))
+    v, s = ref.w8_quant(w)
+    assert np.array_equal(p.scale.cpu().numpy(), s)
+    assert np.array_equal(p.codes.flatten().cpu().numpy(), ref.w8_pack(v))
+    for m in (1, 20):
+        k = 2 ** 17
+        q = torch.full((m, k), -128, dtype=torch.int8, device=DEV)
+        wl = torch.ones(16, k, device=DEV)
+        wl[1::2] *= -1
+        y = bl.forward_w8(q, torch.full((m,), 128.0, device=DEV), bl.pack_weights_w8(wl))
+        scale = np.float32(1) / np.float32(127)
+        want = bf16([np.float32(np.float32(np.float32(-128 * 127 * k) * scale) / np.float32(128))])[0]
+        assert bool((y[:, 0::2] == float(want)).all()) and bool((y[:, 1::2] == -float(want)).all())
+
+
+# ------------------------------------------------------------------ clip
+
+def gradient_set(rng, shapes, scale=1.0):
+    """fp32 and bf16 gradients in turn: (device tensors, their fp32 values)."""
+    out = []
+    for i, s in enumerate(shapes):
+        a = (rng.standard_normal(s) * scale).astype(np.float32)
+        out.append(dev(a) if i % 2 == 0 else to_dev(oracle.f32_to_bf16(a)).view(s))
+    return out, [t.float().cpu().numpy() for t in out]
+
+
+def check_clip(norm, outs, vals, max_norm):
+    want, c = ref.clip(vals, max_norm)
+    assert abs(float(norm) - want) <= 2 * U * want + 1e-45
+    for o, v in zip(outs, vals):
+        w = v.astype(np.float64) * c
+        tol = np.abs(w) * (2 * U if o.dtype == torch.float32 else BF + 2 * U) + TINY
+        if c == 1.0:
+            assert np.array_equal(o.float().cpu().numpy(), v)
+        assert np.all(np.abs(f64(o) - w) <= tol)
+
+
+CLIP_SETS = [[(1,)], [(3, 5), (7,)], [(0,), (5,), (0, 4)], [(1000, 333), (333,), (17, 5, 3), (4096, 64)],
+             [(i % 37 + 1, 13) for i in range(250)], [(16384,), (16385,), (16383,), (1 << 20,), (5, 100003)]]
+
+
+@pytest.mark.parametrize("max_norm", [0.0, 0.5, 1e9, float("inf")])
+@pytest.mark.parametrize("shapes", CLIP_SETS, ids=range(len(CLIP_SETS)))
+def test_clip(bl, shapes, max_norm):
+    grads, vals = gradient_set(np.random.default_rng(41), shapes)
+    assert abs(float(bl.grad_norm(grads)) - ref.clip(vals, 1.0)[0]) <= 2 * U * ref.clip(vals, 1.0)[0]
+    outs = [torch.empty_like(g) for g in grads]
+    call = bl.ClipGradsCall(grads, max_norm, outs=outs)
+    for _ in range(2):
+        norm, got = call()
+        check_clip(norm, got, vals, max_norm)
+    for g, v in zip(grads, vals):  # the gradients are as they were
+        assert np.array_equal(g.float().cpu().numpy(), v)
+    norm, got = bl.clip_grads(grads, max_norm)
+    check_clip(norm, got, vals, max_norm)
+    for g, o in zip(grads, outs):
+        assert torch.equal(g, o)  # in place, the same bits
+
+
+def test_clip_alignment_and_order(bl):
+    """Tensors that start at any element and dense tensors of any order of
+    dimensions; what lies beside them is left alone."""
+    rng = np.random.default_rng(42)
+    grads, vals, checks = [], [], []
+    for i, n in enumerate((5, 1000, 40001, 7, 16384 + 3)):
+        for dtype in (torch.float32, torch.bfloat16):
+            base = torch.full((n + 40,), 3.0, dtype=dtype, device=DEV)
+            g = base[i + 1:i + 1 + n]
+            g.copy_(torch.from_numpy(rng.standard_normal(n).astype(np.float32)))
+            grads.append(g)
+            checks.append((base, i + 1, n))
+    t = torch.randn(60, 70, device=DEV)
+    grads += [t.t(), torch.randn(3, 8, 5, 6, device=DEV).contiguous(memory_format=torch.channels_last)]
+    vals = [g.float().cpu().numpy() for g in grads]
+    norm, got = bl.clip_grads(grads, 0.7)
+    check_clip(norm, got, vals, 0.7)
+    for base, at, n in checks:
+        assert bool((base[:at] == 3).all()) and bool((base[at + n:] == 3).all())
+    with pytest.raises(ValueError):
+        bl.clip_grads([torch.zeros(8, 8, device=DEV)[:, :4]], 1.0)
+    with pytest.raises(TypeError):
+        bl.clip_grads([torch.zeros(8, device=DEV, dtype=torch.float16)], 1.0)
+    with pytest.raises(ValueError):
+        bl.clip_grads([torch.zeros(8, 4, device=DEV)], 1.0, outs=[torch.zeros(4, 8, device=DEV)])
+    with pytest.raises(bl.BitLinearError):  # the same gradient twice
+        bl.clip_grads([t, t], 1.0)
+
+
+def test_clip_extremes(bl):
+    """Magnitudes whose squares leave fp32, values that are not finite, zeros."""
+    big = torch.full((1000,), 2e38, device=DEV)
+    norm, (o,) = bl.clip_grads([big], 1.0, outs=[torch.empty_like(big)])
+    assert float(norm) == float("inf")  # 6.3e39 in fp32
+    c = np.float32(1 / (np.sqrt(1000 * float(np.float32(2e38)) ** 2) + 1e-6))
+    assert c == 0 or np.all(np.abs(f64(o) - float(np.float32(2e38)) * float(c)) <= 4 * U * 0.04)
+    small = torch.full((1000,), 1e-30, device=DEV)
+    norm, (o,) = bl.clip_grads([small], 1e-31, outs=[torch.empty_like(small)])
+    want = np.sqrt(1000) * float(np.float32(1e-30))
+    assert abs(float(norm) - want) <= 2 * U * want
+    assert np.all(np.abs(f64(o) - 1e-30 * 1e-31 / (want + 1e-6)) <= TINY)
+    z = torch.zeros(77, device=DEV)
+    norm, (o,) = bl.clip_grads([z], 0.0, outs=[torch.empty_like(z)])
+    assert float(norm) == 0 and not bool(o.any())
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        g = [torch.ones(100, device=DEV), torch.ones(50, device=DEV, dtype=torch.bfloat16)]
+        g[0][7] = bad
+        norm, o = bl.clip_grads(g, 1.0)
+        if bad != bad:
+            assert bool(torch.isnan(norm).all()) and all(bool(torch.isnan(t).all()) for t in o)
+        else:
+            assert float(norm) == float("inf")
+            assert bool(torch.isnan(o[0][7])) and not bool(o[1].any()) and int(torch.count_nonzero(o[0])) == 1
+
+
+def test_clip_grad_norm_of_a_module(tr):
+    torch.manual_seed(43)
+    ffn = tr.FeedForward(256, 512, device=DEV)
+    x = torch.randn(30, 256, device=DEV).to(torch.bfloat16)
+    _, y = ffn(x)
+    y.float().square().sum().backward()
+    params = list(ffn.parameters())
+    want = [p.grad.clone() for p in params]
+    total = float(torch.sqrt(sum(g.double().square().sum() for g in want)))
+    norm = tr.clip_grad_norm(params + params[:1], 0.25 * total)  # a parameter listed twice counts once
+    assert norm.dim() == 0 and abs(float(norm) - total) <= 2 * U * total
+    for p, g in zip(params, want):
+        assert torch.allclose(p.grad.double(), g.double() * (0.25 * total / (total + 1e-6)), rtol=4 * U, atol=0)
+
+
+# ------------------------------------------------------------- together
+
+def numpy_norm(h, rstd, w):
+    return bf16((h * rstd[:, None]).astype(np.float32) * (1 if w is None else w))
+
+
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_gated(bl, tr, act, residual):
+    """The block's entry and its gradients, from the formulas of its steps."""
+    torch.manual_seed(51)
+    m, n, k = 45, 200, 260
+    x = torch.randn(5, 9, k, device=DEV).to(torch.bfloat16).requires_grad_()
+    r = torch.randn(5, 9, k, device=DEV).to(torch.bfloat16).requires_grad_() if residual else None
+    nw = (1 + 0.1 * torch.randn(k, device=DEV)).requires_grad_()
+    wg, wu = ((0.05 * torch.randn(n, k, device=DEV)).requires_grad_() for _ in range(2))
+    h, a = tr.norm_gated(x, wg, wu, nw, r, act, 1e-5)
+    assert a.shape == (5, 9, n) and h.shape == x.shape
+    da = (torch.randn(5, 9, n, device=DEV) * 1e-2).to(torch.bfloat16)
+    dh = (torch.randn(5, 9, k, device=DEV) * 1e-2).to(torch.bfloat16)
+    torch.autograd.backward([a, h], [da, dh]) if residual else a.backward(da)
+    # the same steps by the library's calls, whose own tests hold them
+    normed = bl.rms_norm_quant(x.detach().reshape(m, k), nw.detach(), None if r is None else r.detach().reshape(m, k), 1e-5)
+    (pg, sg), (pu, su) = bl.pack_weights(wg.detach()), bl.pack_weights(wu.detach())
+    out = bl.forward_gated(normed.q, normed.x_scale, bl.gated_weights(pg, sg, pu, su), act, keep=True)
+    assert torch.equal(a.reshape(m, n), out.a) and torch.equal(h.reshape(m, k), normed.h)
+    xhat = f64(bl.restore_activations(normed.q, normed.x_scale))
+    want = ref.gated_backward(f64(da).reshape(m, n), f64(out.g), f64(out.u), act, f64(bl.unpack_weights(pg)), float(sg),
+                              f64(bl.unpack_weights(pu)), float(su), xhat)
+    check_backward((None, wg.grad, wu.grad), want, m, n)
+    dn, _, _ = bl.GatedBackwardCall(da.reshape(m, n), out.g, out.u, act, gate=pg, gate_scale=sg, up=pu, up_scale=su)()
+    check_backward((dn, None, None), want, m, n)
+    dx, dweight = bl.rms_norm_quant_backward(dn, normed.h, normed.rstd, nw.detach(), dh.reshape(m, k) if residual else None)
+    assert torch.equal(x.grad.reshape(m, k), dx) and torch.equal(nw.grad, dweight)
+    if residual:
+        assert torch.equal(r.grad, x.grad) and r.grad.data_ptr() != x.grad.data_ptr()
+
+
+@pytest.mark.parametrize("sub_norm", [False, True])
+def test_feed_forward_block(bl, tr, sub_norm):
+    """A whole block forward and backward: what it gives is what its calls give,
+    and every parameter gets a gradient."""
+    torch.manual_seed(52)
+    ffn = tr.FeedForward(256, 680, "silu", sub_norm=sub_norm, device=DEV)
+    x, r = (torch.randn(2, 21, 256, device=DEV).to(torch.bfloat16) for _ in range(2))
+    h, y = ffn(x, r)
+    assert torch.equal(h, x + r) and y.shape == x.shape
+    (y.float() * torch.randn_like(y.float())).sum().backward()
+    for name, p in ffn.named_parameters():
+        assert p.grad is not None and bool(torch.isfinite(p.grad).all()) and bool(p.grad.any()), name
+    norm = tr.clip_grad_norm(ffn.parameters(), 1.0)
+    after = torch.sqrt(sum(p.grad.double().square().sum() for p in ffn.parameters()))
+    assert float(after) <= max(1.0, float(norm)) * (1 + 1e-6)
+    with torch.no_grad():
+        h2, y2 = ffn(x, r)
+        normed = bl.rms_norm_quant(x.reshape(42, -1), ffn.norm, r.reshape(42, -1), ffn.eps)
+        w = bl.gated_weights(*bl.pack_weights(ffn.gate), *bl.pack_weights(ffn.up))
+        a = bl.forward_gated(normed.q, normed.x_scale, w, "silu").a
+        q, xs = (bl.rms_norm_quant(a, ffn.sub_norm, eps=ffn.eps)[:2] if sub_norm else bl.act_quant(a))
+        want = bl.forward_quantized(q, xs, *bl.pack_weights(ffn.down))
+    assert torch.equal(y2, y) and torch.equal(y2.reshape(42, -1), want) and torch.equal(h2, h)
+
+
+def test_norm_gated_frozen_and_empty(tr):
+    torch.manual_seed(53)
+    n, k = 70, 128
+    wg, wu = (0.05 * torch.randn(n, k, device=DEV) for _ in range(2))
+    x = torch.randn(9, k, device=DEV).to(torch.bfloat16)
+    for want in range(3):
+        ts = [t.clone().requires_grad_(i == want) for i, t in enumerate((x, wg, wu))]
+        _, a = tr.norm_gated(*ts)
+        a.float().sum().backward()
+        assert [t.grad is not None for t in ts] == [i == want for i in range(3)]
+    _, a = tr.norm_gated(x, wg, wu)
+    assert not a.requires_grad
+    e = torch.zeros(0, 3, k, device=DEV, dtype=torch.bfloat16, requires_grad=True)
+    w = wg.clone().requires_grad_()
+    h, a = tr.norm_gated(e, w, wu, residual=e)
+    assert a.shape == (0, 3, n) and h.shape == e.shape
+    a.sum().backward()
+    assert not bool(w.grad.any()) and w.grad.shape == w.shape
+    # a not used: the gradient of h alone
+    x2, r2 = x.clone().requires_grad_(), x.clone().requires_grad_()
+    h, _ = tr.norm_gated(x2, w, wu, residual=r2)
+    h.float().sum().backward()
+    assert bool((x2.grad == 1).all()) and bool((r2.grad == 1).all())
+
+
+def serving_calls(bl, m, seed=61):
+    """A feed-forward block and an 8-bit head at m tokens, prepared."""
+    torch.manual_seed(seed)
+    k, n, v = 512, 1408, 1000
+    x = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+    (pg, sg), (pu, su), (pd, sd) = (bl.pack_weights(0.05 * torch.randn(a, b, device=DEV)) for a, b in ((n, k), (n, k), (k, n)))
+    head = bl.pack_weights_w8(0.05 * torch.randn(v, k, device=DEV))
+    norm = bl.NormQuantCall(x)
+    gated = bl.GatedCall(norm.out.q, norm.out.x_scale, bl.gated_weights(pg, sg, pu, su), "relu2")
+    sub = bl.NormQuantCall(gated.out.a)
+    down = bl.GroupedQuantizedCall([sub.out.q], [sub.out.x_scale], [pd], [sd], residuals=[x])
+    last = bl.NormQuantCall(down.outs[0])
+    logits = bl.W8Call(last.out.q, last.out.x_scale, head)
+    calls = [norm, gated, sub, down, last, logits]
+    return x, calls, logits.out
+
+
+@pytest.mark.parametrize("m", [1, 4, 16, 17, 200])
+def test_serving_block_in_a_graph(bl, m):
+    """norm, gated projections, norm, down projection, norm, 8-bit head: captured,
+    replayed with other tokens and eager work between, against eager runs."""
+    x, calls, out = serving_calls(bl, m)
+    x2, calls2, out2 = serving_calls(bl, m)
+    for c in calls:
+        c()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c in calls:
+            c()
+    for i in range(4):
+        new = torch.randn(x.shape, device=DEV).to(torch.bfloat16)
+        x.copy_(new)
+        x2.copy_(new)
+        out.zero_()
+        graph.replay()
+        for c in calls2:
+            c()
+        torch.cuda.synchronize()
+        assert torch.equal(out, out2), i
+
+
+def test_training_step_in_a_graph(bl, tr):
+    """Forward, backward and clipping, captured and replayed."""
+    m, n, k = 33, 300, 256
+    rng = np.random.default_rng(62)
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu, da, g, u = backward_inputs(bl, 62, m, n, k)
+    w = bl.gated_weights(tg, dsg, tu, dsu)
+    dda = to_dev(oracle.f32_to_bf16(da))
+    dq, dxs = dev(q), dev(xs)
+    fwd = bl.GatedCall(dq, dxs, w, "silu", keep=True)
+    back = bl.GatedBackwardCall(dda, fwd.out.g, fwd.out.u, "silu", dq, dxs, tg, dsg, tu, dsu)
+    clip = bl.ClipGradsCall(list(back._out[1:]), 0.01)
+
+    def step():
+        fwd()
+        back()
+        return clip()
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(3):
+        dda.copy_(to_dev(oracle.f32_to_bf16((rng.standard_normal((m, n)) * 1e-3).astype(np.float32))))
+        dq.copy_(dev(codes(rng, m, k)[0]))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (fwd.out.a, *back._out, clip.norm)]
+        f2 = bl.GatedCall(dq, dxs, w, "silu", keep=True)()
+        b2 = bl.GatedBackwardCall(dda, f2.g, f2.u, "silu", dq, dxs, tg, dsg, tu, dsu)()
+        norm, _ = bl.clip_grads(list(b2[1:]), 0.01)
+        for a, b in zip(got, (f2.a, *b2, norm)):
+            assert torch.equal(a, b)
+
+
+def test_side_stream(bl):
+    """Calls go to the current stream, in order with the work around them."""
+    x, calls, out = serving_calls(bl, 24)
+    for c in calls:
+        c()
+    want = out.clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    new = x.clone()
+    x.zero_()
+    out.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(2_000_000)
+        x.copy_(new)
+        for c in calls:
+            c()
+        got = out.clone()
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_large_offsets(bl):
+    """Outputs and weights of more than 2^31 elements, and gradients too."""
+    m, n, k = 70000, 32768, 64
+    q = torch.randint(-127, 128, (m, k), device=DEV, dtype=torch.int8)
+    xs = torch.full((m,), 50.0, device=DEV)
+    w = 0.05 * torch.randn(n, k, device=DEV)
+    p = bl.pack_weights_w8(w)
+    y = bl.forward_w8(q, xs, p)
+    rows = [0, 1, 32767, 65535, 65536, m - 1]
+    assert torch.equal(y[rows], bl.forward_w8(q[rows].contiguous(), xs[:6].contiguous(), p))
+    del y
+    (pg, sg), (pu, su) = bl.pack_weights(w), bl.pack_weights(w.flip(0).contiguous())
+    gw = bl.gated_weights(pg, sg, pu, su)
+    a = bl.forward_gated(q, xs, gw, "relu2").a
+    assert torch.equal(a[rows], bl.forward_gated(q[rows].contiguous(), xs[:6].contiguous(), gw, "relu2").a)
+    del a
+    g = torch.zeros(2 ** 31 + 5, device=DEV, dtype=torch.bfloat16)
+    g[-1], g[2 ** 31], g[0] = 3.0, 4.0, 12.0
+    norm, (o,) = bl.clip_grads([g], 6.5)
+    assert float(norm) == 13.0
+    assert [float(o[i]) for i in (0, 2 ** 31, 2 ** 31 + 4)] == [6.0, 2.0, 1.5]
+    del g, o
+    n, k = 32768, 65536 + 256
+    codes_ = torch.zeros(n // 16, k // 64, 4, 16, 16, dtype=torch.int8, device=DEV)
+    codes_[-1, -1, 3, 15, 15] = 5  # weight [n - 1][k - 1]
+    codes_[0, 0, 0, 0, 0] = 7
+    w8 = bl.W8Weights(codes_, torch.ones(n, device=DEV), n, k)
+    q = torch.full((1, k), 2, device=DEV, dtype=torch.int8)
+    y = bl.forward_w8(q, torch.ones(1, device=DEV), w8)
+    assert float(y[0, -1]) == 10 and float(y[0, 0]) == 14 and int(torch.count_nonzero(y)) == 2
