@@ -1,0 +1,410 @@
+// Tiles of products of int8 activations, in their own row-major order, with the
+// 8-bit weights (w8.hip) or the two ternary weights of a gated block (gated.hip)
+// on the int8 matrix cores: C[i][j] = sum_k q[i][k] * w[j][k], exact in int32.
+//
+// K goes in slabs of 128.  Both operands go from global memory straight into a
+// ring of buffers in LDS:
+//   activations     rows of 128 bytes; chunk c (16 bytes) of row r at chunk
+//                   c ^ ((r / 2) & 7), so that the 16 rows that LDS serves
+//                   together lie in distinct banks
+//   8-bit weights   the same, gathered from the storage's kilobytes (a wave's
+//                   load takes eight pieces of 128 bytes)
+//   ternary weights 32 bytes a row; chunk h (64 weights) of row r at chunk
+//                   h ^ ((r / 8) & 1).  Expanded in registers (expand16)
+// The weights are the matrix core's first operand, so that a lane's sums belong
+// to one token: lane (lr, lg) = (lane % 32, lane / 32) holds, of a 32 x 32
+// subtile, row lr at columns 8 a + 4 lg .. + 3 in elements 4 a .. 4 a + 3.
+//
+// What lies past K in the activations' rows is read (the last chunk again) and
+// meets zeros of the weights' padding.  Rows past the end read the last one; their
+// sums are not stored.
+#pragma once
+
+#include "codes_plan.hpp"
+#include "common.hpp"
+#include "internal.hpp"
+
+#include <atomic>
+#include <type_traits>
+
+namespace bl {
+
+typedef int32_t v16i __attribute__((ext_vector_type(16)));
+
+struct CodesJob {
+  const int8_t* q;  // rows of ldq bytes, 16-byte aligned
+  int32_t ldq;      // ldq % 16 == 0
+  int32_t m, n, k;
+  const uint8_t* w;
+  int32_t ktiles, blocks;  // of the weights' storage
+  int32_t slabs;           // ceil(k / 128)
+  int32_t tiles_i, tiles_j;
+  int32_t ksplit, kspw;  // parts of k, and slabs a part
+  int32_t* part;         // ksplit > 1: int32 sums [ksplit][m][n] (gated: [ksplit][2][m][n])
+};
+
+constexpr int kCodesRow = 128;                           // bytes of a row of a slab
+constexpr int codes_b_row(bool ternary) { return ternary ? 32 : 128; }
+constexpr int codes_stage(int ti, int tj, bool ternary) { return ti * kCodesRow + tj * codes_b_row(ternary); }
+
+namespace codes_gemm {
+
+__device__ __forceinline__ v16i mfma_32x32x32_i8(v4i a, v4i b, v16i c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// Waits until at most `ahead` slabs of D loads each are still in flight.
+template <int D, int C>
+__device__ __forceinline__ void wait_slabs(int ahead) {
+  if constexpr (C == 0) {
+    wait_vm<0>();
+  } else {
+    if (ahead >= C)
+      wait_vm<C * D>();
+    else
+      wait_slabs<D, C - 1>(ahead);
+  }
+}
+
+__device__ __forceinline__ void dma16(const void* src, int8_t* lds_dst) {
+  __builtin_amdgcn_global_load_lds((const BL_GLOBAL void*)src,
+                                   (__attribute__((address_space(3))) void*)lds_dst, 16, 0, 0);
+}
+
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");  // no LDS access moves across
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+}  // namespace codes_gemm
+
+// int8 values 64 u of the 16 weights of a dword of the gated storage, four a
+// dword, in order.
+__device__ __forceinline__ v4i expand16(uint32_t p) {
+  v4i r;
+  r.x = (int32_t)(p & 0xC0C0C0C0u);
+  r.y = (int32_t)((p << 2) & 0xC0C0C0C0u);
+  r.z = (int32_t)((p << 4) & 0xC0C0C0C0u);
+  r.w = (int32_t)((p << 6) & 0xC0C0C0C0u);
+  return r;
+}
+
+// One tile of TI tokens x TJ weight rows by WI x WJ waves.  TERNARY: the first
+// half of the TJ rows is the gate's, the second the up projection's of the same
+// TJ / 2 outputs, and so is each wave's share.
+template <int TI_, int TJ_, int WI_, int WJ_, int NST_, bool TERNARY>
+struct CodesTile {
+  static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, NST = NST_, NW = WI * WJ;
+  static constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;
+  static constexpr int kStage = codes_stage(TI, TJ, TERNARY);
+  static constexpr int kLds = NST * kStage;
+  static constexpr int DA = TI / 8 / NW;  // loads of a slab, per wave
+  static constexpr int CB = TJ * codes_b_row(TERNARY) / 1024;  // of the weights, all waves
+  static constexpr int DB = CB < NW ? 1 : CB / NW;
+  static constexpr int D = DA + DB;
+  static constexpr int kCols = TERNARY ? TJ / 2 : TJ;  // outputs of a tile
+  static_assert(DA * 8 * NW == TI && (DB * NW == CB || NW % CB == 0), "whole loads");
+  static_assert(FI * WI * 32 == TI && FJ * WJ * 32 == TJ && (!TERNARY || FJ % 2 == 0), "whole subtiles");
+
+  // First row and (outputs') first column of the wave's share.
+  static __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6); }
+  static __device__ __forceinline__ int row0() { return (wave() % WI) * (TI / WI); }
+  static __device__ __forceinline__ int col0() { return (wave() / WI) * (kCols / WJ); }
+  // Weight row (of the tile) of fragment j.
+  static __device__ __forceinline__ int brow(int j) {
+    if constexpr (TERNARY) return (j < FJ / 2 ? 0 : TJ / 2) + col0() + 32 * (j % (FJ / 2));
+    return col0() + 32 * j;
+  }
+
+  static __device__ __forceinline__ void run(const CodesJob& J, int ti, int tj, int kp, int8_t* smem,
+                                             v16i (&acc)[FI][FJ]) {
+    using namespace codes_gemm;
+    const int lane = threadIdx.x & 63, wv = wave();
+    const int lr = lane & 31, lg = lane >> 5;
+    const int i0 = ti * TI, wi0 = row0();
+    const int s0 = kp * J.kspw, nsl = min(J.slabs - s0, J.kspw);
+    const int blk0 = tj * (kCols / 16);
+
+    // Per lane the offsets of a load's row and of its chunk in the slab.
+    uint32_t ar[DA], ac[DA], br[DB], bc[DB];
+#pragma unroll
+    for (int i = 0; i < DA; ++i) {
+      const int pos = (wv * DA + i) * 64 + lane, r = pos >> 3;
+      ar[i] = (uint32_t)min(r, J.m - 1 - i0) * (uint32_t)J.ldq;
+      ac[i] = 16 * ((pos & 7) ^ ((r >> 1) & 7));
+    }
+#pragma unroll
+    for (int i = 0; i < DB; ++i) {  // waves past the last piece load one again, so that all wait alike
+      const int pos = ((wv % CB) * DB + i) * 64 + lane;
+      if constexpr (TERNARY) {
+        const int r = pos >> 1, h = (pos & 1) ^ ((r >> 3) & 1), up = r >= TJ / 2, o = r - up * (TJ / 2);
+        br[i] = (uint32_t)min(o >> 4, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 2048) + 1024 * up + 16 * (o & 15);
+        bc[i] = 256 * h;
+      } else {
+        const int r = pos >> 3, c = (pos & 7) ^ ((r >> 1) & 7);
+        br[i] = (uint32_t)min(r >> 4, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 1024) + 256 * (c & 3) + 16 * (r & 15);
+        bc[i] = 1024 * (c >> 2);
+      }
+    }
+    const int8_t* pa = J.q + (int64_t)i0 * J.ldq;
+    const uint8_t* pb = J.w + (int64_t)blk0 * J.ktiles * (TERNARY ? 2048 : 1024);
+    int next = s0;  // the slab that is loaded next
+    // Load d (of D) of the next slab into the buffer st.
+    auto issue_one = [&](int d, int8_t* st) {
+      if (d < DA) {
+        // the row's last chunk for those past it
+        const uint32_t last = (uint32_t)(J.ldq - 16 - next * kCodesRow);
+        dma16(pa + (int64_t)next * kCodesRow + ar[d] + min(ac[d], last), st + (wv * DA + d) * 1024);
+      } else {
+        const int e = d - DA;
+        int8_t* dst = st + TI * kCodesRow + ((wv % CB) * DB + e) * 1024;
+        if constexpr (TERNARY) {
+          dma16(pb + (int64_t)(next >> 1) * 2048 + 512 * (next & 1) + br[e] + bc[e], dst);
+        } else {
+          // an odd last tile's half of the slab again
+          const uint32_t last = (uint32_t)(J.ktiles - 1 - 2 * next) * 1024;
+          dma16(pb + (int64_t)next * 2048 + br[e] + min(bc[e], last), dst);
+        }
+      }
+      if (d == D - 1) ++next;
+    };
+
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+      for (int j = 0; j < FJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+
+    // Fragments of step ks of a slab: 32 k, 16 a lane half (chunk 2 ks + lg of a
+    // row; TERNARY: chunk 4 lg + ks, dword ks of the weights' chunk lg).
+    v4i fa[2][FI], fb[2][FJ], cj[FJ];
+    const int8_t* sa = smem;  // the current slab's buffer
+    auto load = [&](int ks, v4i (&a)[FI], v4i (&b)[FJ]) {
+#pragma unroll
+      for (int i = 0; i < FI; ++i) {
+        const int r = wi0 + 32 * i + lr, c = TERNARY ? 4 * lg + ks : 2 * ks + lg;
+        a[i] = *reinterpret_cast<const v4i*>(sa + kCodesRow * r + 16 * (c ^ ((r >> 1) & 7)));
+      }
+#pragma unroll
+      for (int j = 0; j < FJ; ++j) {
+        const int r = brow(j) + lr;
+        const int8_t* sb = sa + TI * kCodesRow + codes_b_row(TERNARY) * r;
+        if constexpr (!TERNARY)
+          b[j] = *reinterpret_cast<const v4i*>(sb + 16 * ((2 * ks + lg) ^ ((r >> 1) & 7)));
+        else if (ks == 0)
+          b[j] = *reinterpret_cast<const v4i*>(sb + 16 * (lg ^ ((r >> 3) & 1)));
+      }
+    };
+    // Products of step ks; with ISSUE, a load of the slab that goes to `st`
+    // between any two of them.
+    auto multiply = [&](auto issue, int ks, const v4i (&a)[FI], const v4i (&b)[FJ], int8_t* st) {
+      constexpr bool ISSUE = decltype(issue)::value;
+      constexpr int P = FI * FJ;
+#pragma unroll
+      for (int j = 0; j < FJ; ++j) {
+        v4i w;
+        if constexpr (TERNARY)
+          w = expand16((uint32_t)cj[j][ks]);
+        else
+          w = b[j];
+#pragma unroll
+        for (int i = 0; i < FI; ++i) {
+          acc[i][j] = mfma_32x32x32_i8(w, a[i], acc[i][j]);
+          if constexpr (ISSUE) {
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+              if (d * P / D == j * FI + i) {
+                __builtin_amdgcn_sched_barrier(0);
+                issue_one(d, st);
+                __builtin_amdgcn_sched_barrier(0);
+              }
+          }
+        }
+      }
+    };
+
+    constexpr int KS = 4;
+#pragma unroll
+    for (int p = 0; p < NST; ++p)
+      if (p < nsl) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) issue_one(d, smem + p * kStage);
+      }
+    wait_slabs<D, NST - 1>(min(nsl - 1, NST - 1));
+    barrier();
+    load(0, fa[0], fb[0]);
+    int buf = 0;
+    // 8-bit weights of an odd number of tiles: the last slab's second half is not there
+    const int half = !TERNARY && (J.ktiles & 1) && s0 + nsl == J.slabs ? nsl - 1 : -1;
+    // A slab: its first steps, then, when its last fragments are in registers
+    // and every wave is there, its buffer is free.  The next slab's first
+    // fragments are read ahead of the last products, and the buffer refilled
+    // between them.
+    auto slab = [&](auto issue, int s) {
+      constexpr bool ISSUE = decltype(issue)::value;
+      if constexpr (TERNARY) {
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) cj[j] = fb[0][j];
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS - 1; ++ks) {
+        load(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);  // the reads go out ahead of this step's products
+        if (ISSUE || ks < KS / 2 || s != half) multiply(std::false_type{}, ks, fa[ks & 1], fb[ks & 1], nullptr);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slab's LDS reads are done
+      int8_t* st = smem + buf * kStage;
+      if (ISSUE || s + 1 < nsl) {
+        wait_vm<ISSUE ? (NST - 2) * D : 0>();
+        barrier();
+        buf = buf + 1 == NST ? 0 : buf + 1;
+        sa = smem + buf * kStage;
+        load(0, fa[0], fb[0]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (ISSUE || s != half) multiply(issue, KS - 1, fa[(KS - 1) & 1], fb[(KS - 1) & 1], st);
+    };
+    int s = 0;
+    for (; s + NST < nsl; ++s) slab(std::true_type{}, s);
+    for (; s < nsl; ++s) slab(std::false_type{}, s);
+  }
+};
+
+// Workgroups go to the 8 XCDs round-robin and each has its own L2, so each XCD
+// takes one contiguous share of the tiles, walked in groups of up to four tile
+// rows so that neighbours in time share operands both ways.
+__device__ __forceinline__ bool codes_tile_of(int l, const CodesJob& J, int* ti, int* tj, int* kp) {
+  const int T = J.tiles_i * J.tiles_j * J.ksplit, chunk = (T + 7) >> 3;
+  const int w = l >> 3;
+  int t = (l & 7) * chunk + w;
+  if (w >= chunk || t >= T) return false;
+  const int per = J.tiles_i * J.tiles_j;
+  *kp = t / per;
+  t -= *kp * per;
+  const int g = t / (4 * J.tiles_j), rows = min(4, J.tiles_i - 4 * g);
+  t -= g * 4 * J.tiles_j;
+  *ti = 4 * g + t % rows;
+  *tj = t / rows;
+  return true;
+}
+
+// 16 sums of a 32 x 32 subtile's row as bf16 pairs pk[8] (columns 8 a + 4 lg + 0..3
+// in pk[2 a], pk[2 a + 1]) to 8 consecutive columns twice: lanes of lg = 0 get
+// columns 0-7 in pk[0..3] and 16-23 in pk[4..7], those of lg = 1 8-15 and 24-31.
+__device__ __forceinline__ void codes_rows8(uint32_t (&pk)[8]) {
+#pragma unroll
+  for (int h = 0; h < 8; h += 4)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const auto sw = __builtin_amdgcn_permlane32_swap(pk[h + t], pk[h + 2 + t], false, false);
+      pk[h + t] = sw[0];
+      pk[h + 2 + t] = sw[1];
+    }
+}
+
+// Up to eight bf16 outputs of one row from column n on.
+__device__ __forceinline__ void codes_put8(uint16_t* row, int n, int cols, bool wide, const uint32_t* w) {
+  if (wide && n + 8 <= cols) {
+    *G(reinterpret_cast<v4i*>(row + n)) = v4i{(int32_t)w[0], (int32_t)w[1], (int32_t)w[2], (int32_t)w[3]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (n + e < cols) *G(row + n + e) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+// int32 sums of a part (32 x 32 subtile: one row a lane).
+__device__ __forceinline__ void codes_put_part(int32_t* row, int n0, int cols, const v16i& acc) {
+  const int lg = (threadIdx.x >> 5) & 1;
+  const bool wide = (cols & 3) == 0;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int n = n0 + 8 * a + 4 * lg;
+    if (wide && n + 4 <= cols) {
+      *G(reinterpret_cast<v4i*>(row + n)) = v4i{acc[4 * a], acc[4 * a + 1], acc[4 * a + 2], acc[4 * a + 3]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < cols) *G(row + n + e) = acc[4 * a + e];
+    }
+  }
+}
+
+// Adds eight columns' sums of the parts, in order (`left`: columns that exist).
+__device__ __forceinline__ void codes_add_parts(const int32_t* src, int64_t slice, int ksplit, int left, bool wide,
+                                                int32_t (&v)[8]) {
+  if (wide && left >= 8) {
+    for (int p = 0; p < ksplit; ++p) {
+      const v4i lo = *G(reinterpret_cast<const v4i*>(src + p * slice));
+      const v4i hi = *G(reinterpret_cast<const v4i*>(src + p * slice + 4));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += lo[e];
+        v[4 + e] += hi[e];
+      }
+    }
+  } else {
+    for (int p = 0; p < ksplit; ++p)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) v[e] += *G(src + p * slice + e);
+  }
+}
+
+// Activations whose rows do not start at a multiple of 16 bytes, in rows that do
+// (K rounded up to 16, the rest zeros): 16 bytes a thread.
+static __global__ __launch_bounds__(256) void codes_rows_kernel(const int8_t* __restrict__ q, int64_t total,
+                                                                int32_t k, int32_t ldq, int8_t* __restrict__ out) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= total) return;
+  const int cpr = ldq >> 4;
+  const int64_t m = id / cpr;
+  const int c = 16 * (int)(id - m * cpr);
+  v4i v;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) v[d] = c + 4 * d < k ? *G(reinterpret_cast<const int32_t*>(q + m * k + c + 4 * d)) : 0;
+  *G(reinterpret_cast<v4i*>(out + 16 * id)) = v;
+}
+
+inline hipError_t codes_rows(const int8_t* q, int64_t m, int64_t k, int32_t ldq, int8_t* out, hipStream_t s) {
+  const int64_t total = m * (ldq >> 4);
+  codes_rows_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(q, total, (int32_t)k, ldq, out);
+  return hipGetLastError();
+}
+
+inline void set_plan(CodesJob& J, const CodesPlan& p, int32_t* part) {
+  J.slabs = p.slabs;
+  J.tiles_i = p.tiles_i;
+  J.tiles_j = p.tiles_j;
+  J.ksplit = p.ksplit;
+  J.kspw = p.kspw;
+  J.part = part;
+}
+
+// Launches a kernel with the dynamic LDS it needs (an attribute above 64 KB, set
+// once per device and kernel: `done` is the caller's).
+template <typename Kernel, typename Args>
+hipError_t codes_launch(Kernel kernel, std::atomic<bool>* done, unsigned grid, unsigned threads, size_t lds,
+                        hipStream_t s, const Args& args) {
+  if (lds > 64 * 1024) {
+    const int dev = current_device_index();
+    if (!done[dev].load(std::memory_order_acquire)) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return e;
+      done[dev].store(true, std::memory_order_release);
+    }
+  }
+  kernel<<<grid, threads, lds, s>>>(args);
+  return hipGetLastError();
+}
+
+}  // namespace bl

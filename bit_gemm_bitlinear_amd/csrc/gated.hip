@@ -10,6 +10,8 @@
 // codes to subtract, no activations to reorder.  The sums come out 64 times too
 // large, exactly; the factor leaves in the epilogue.
 #include "../../include/bitlinear_ffn.h"
+#include "codes_gemm.hpp"
+#include "codes_plan.hpp"
 #include "common.hpp"
 #include "internal.hpp"
 #include "layer_internal.hpp"
@@ -63,16 +65,6 @@ __global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __res
     }
     *G(reinterpret_cast<v4i*>(codes + 16 * id)) = v;
   }
-}
-
-// int8 values 64 u of the 16 weights of a dword, four a dword, in order.
-__device__ __forceinline__ v4i expand16(uint32_t p) {
-  v4i r;
-  r.x = (int32_t)(p & 0xC0C0C0C0u);
-  r.y = (int32_t)((p << 2) & 0xC0C0C0C0u);
-  r.z = (int32_t)((p << 4) & 0xC0C0C0C0u);
-  r.w = (int32_t)((p << 6) & 0xC0C0C0C0u);
-  return r;
 }
 
 // act(g) * u.  exp(-|g|) is at most 1, so nothing overflows that the result
@@ -143,6 +135,168 @@ __global__ __launch_bounds__(64) void gated_kernel(const GatedKernelArgs A) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// More than 16 tokens: tiles on the int8 matrix cores (codes_gemm.hpp), the
+// gate's and the up projection's columns of the same outputs in one wave.
+
+struct GatedGemmArgs {
+  CodesJob j;
+  const float* x_scale;
+  const float* gate_scale;
+  const float* up_scale;
+  uint16_t* a;
+  uint16_t* g;
+  uint16_t* u;
+};
+
+template <typename T, bool SILU>
+__global__ __launch_bounds__(64 * T::NW, 2) void gated_gemm_kernel(const GatedGemmArgs A) {
+  extern __shared__ __align__(16) int8_t smem[];
+  const CodesJob& J = A.j;
+  int ti, tj, kp;
+  if (!codes_tile_of((int)blockIdx.x, J, &ti, &tj, &kp)) return;
+  v16i acc[T::FI][T::FJ];
+  T::run(J, ti, tj, kp, smem, acc);
+  constexpr int FO = T::FJ / 2;  // subtiles of outputs
+  const int lane = threadIdx.x & 63, lr = lane & 31, lg = lane >> 5;
+  const int m0 = ti * T::TI + T::row0() + lr, n0 = tj * T::kCols + T::col0();
+  if (J.ksplit > 1) {
+#pragma unroll
+    for (int i = 0; i < T::FI; ++i) {
+      const int m = m0 + 32 * i;
+      if (m >= J.m) continue;
+#pragma unroll
+      for (int j = 0; j < T::FJ; ++j) {
+        int32_t* row = J.part + ((int64_t)(2 * kp + (j >= FO)) * J.m + m) * J.n;
+        codes_put_part(row, n0 + 32 * (j % FO), J.n, acc[i][j]);
+      }
+    }
+    return;
+  }
+  const bool wide = (J.n & 7) == 0;  // output rows are 16-byte aligned
+  const float gs = load_f32_vmem(A.gate_scale), us = load_f32_vmem(A.up_scale);
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i) {
+    const int m = m0 + 32 * i;
+    const float xs = *G(A.x_scale + min(m, J.m - 1));
+    const RowDiv dg = row_div_setup(xs * gs), du = row_div_setup(xs * us);
+    const int64_t at = (int64_t)m * J.n;
+#pragma unroll
+    for (int j = 0; j < FO; ++j) {
+      uint32_t pa[8], pg[8], pu[8];
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        float g[2], u[2], a[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          g[e] = row_div((float)acc[i][j][2 * h + e] * 0.015625f, dg);
+          u[e] = row_div((float)acc[i][j + FO][2 * h + e] * 0.015625f, du);
+          a[e] = gate_value<SILU>(g[e], u[e]);
+        }
+        pa[h] = pack_bf16x2(a[0], a[1]);
+        if (A.g) {
+          pg[h] = pack_bf16x2(g[0], g[1]);
+          pu[h] = pack_bf16x2(u[0], u[1]);
+        }
+      }
+      codes_rows8(pa);
+      if (A.g) {
+        codes_rows8(pg);
+        codes_rows8(pu);
+      }
+      if (m >= J.m) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = n0 + 32 * j + 16 * h + 8 * lg;
+        codes_put8(A.a + at, n, J.n, wide, pa + 4 * h);
+        if (A.g) {
+          codes_put8(A.g + at, n, J.n, wide, pg + 4 * h);
+          codes_put8(A.u + at, n, J.n, wide, pu + 4 * h);
+        }
+      }
+    }
+  }
+}
+
+// Adds the parts of split sums: eight outputs of a row a thread.
+template <bool SILU>
+__global__ __launch_bounds__(256) void gated_finish_kernel(const GatedGemmArgs A, int64_t total) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= total) return;
+  const CodesJob& J = A.j;
+  const int cpr = (J.n + 7) >> 3;
+  const int64_t m = id / cpr;
+  const int n = 8 * (int)(id - m * cpr);
+  const int64_t slice = (int64_t)J.m * J.n;
+  const int32_t* src = J.part + m * J.n + n;
+  int32_t vg[8] = {0, 0, 0, 0, 0, 0, 0, 0}, vu[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  codes_add_parts(src, 2 * slice, J.ksplit, J.n - n, (J.n & 3) == 0, vg);
+  codes_add_parts(src + slice, 2 * slice, J.ksplit, J.n - n, (J.n & 3) == 0, vu);
+  const float xs = *G(A.x_scale + m);
+  const RowDiv dg = row_div_setup(xs * *G(A.gate_scale)), du = row_div_setup(xs * *G(A.up_scale));
+  uint32_t pa[4], pg[4], pu[4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    float g[2], u[2], a[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      g[e] = row_div((float)vg[2 * h + e] * 0.015625f, dg);
+      u[e] = row_div((float)vu[2 * h + e] * 0.015625f, du);
+      a[e] = gate_value<SILU>(g[e], u[e]);
+    }
+    pa[h] = pack_bf16x2(a[0], a[1]);
+    pg[h] = pack_bf16x2(g[0], g[1]);
+    pu[h] = pack_bf16x2(u[0], u[1]);
+  }
+  const bool wide = (J.n & 7) == 0;
+  codes_put8(A.a + m * J.n, n, J.n, wide, pa);
+  if (A.g) {
+    codes_put8(A.g + m * J.n, n, J.n, wide, pg);
+    codes_put8(A.u + m * J.n, n, J.n, wide, pu);
+  }
+}
+
+using GatedTile256 = CodesTile<256, 256, 2, 4, 3, true>;
+using GatedTile128 = CodesTile<128, 256, 2, 2, 3, true>;
+using GatedTile64 = CodesTile<64, 128, 2, 2, 6, true>;
+using GatedTile32 = CodesTile<32, 256, 1, 4, 6, true>;
+
+template <typename T, bool SILU>
+hipError_t gated_gemm(const GatedGemmArgs& a, hipStream_t s) {
+  static std::atomic<bool> done[kMaxDevices];
+  const int64_t grid = round_up((int64_t)a.j.tiles_i * a.j.tiles_j * a.j.ksplit, 8);
+  return codes_launch(&gated_gemm_kernel<T, SILU>, done, (unsigned)grid, 64 * T::NW, T::kLds, s, a);
+}
+
+template <bool SILU>
+hipError_t launch_gated_gemm(const GatedGemmArgs& a, int cfg, hipStream_t s) {
+  const hipError_t e = cfg == 3   ? gated_gemm<GatedTile256, SILU>(a, s)
+                       : cfg == 2 ? gated_gemm<GatedTile128, SILU>(a, s)
+                       : cfg == 1 ? gated_gemm<GatedTile64, SILU>(a, s)
+                                  : gated_gemm<GatedTile32, SILU>(a, s);
+  if (e != hipSuccess || a.j.ksplit == 1) return e;
+  const int64_t total = (int64_t)a.j.m * ((a.j.n + 7) / 8);
+  gated_finish_kernel<SILU><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, total);
+  return hipGetLastError();
+}
+
+struct GatedLayout {
+  CodesPlan plan;
+  int32_t ldq;
+  size_t part, total;
+};
+
+GatedLayout gated_layout(int64_t m, int64_t n, int64_t k) {
+  GatedLayout L = {};
+  if (m <= 16) return L;
+  L.plan = plan_codes(m, n, (k + 127) / 128, true);
+  L.ldq = (int32_t)round_up(k, 16);
+  if (k % 16) L.total = align256((size_t)m * L.ldq);
+  L.part = L.total;
+  if (L.plan.ksplit > 1) L.total = align256(L.total + 8 * (size_t)L.plan.ksplit * m * n);
+  return L;
+}
+
 }  // namespace
 
 hipError_t launch_gated_weights(const uint8_t* gate, bool gate_tiled, const uint8_t* up, bool up_tiled,
@@ -154,9 +308,35 @@ hipError_t launch_gated_weights(const uint8_t* gate, bool gate_tiled, const uint
   return hipGetLastError();
 }
 
-size_t gated_forward_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t gated_forward_bytes(int64_t m, int64_t n, int64_t k) { return gated_layout(m, n, k).total; }
 
-hipError_t launch_gated_forward(const GatedArgs& b, char*, hipStream_t s) {
+hipError_t launch_gated_forward(const GatedArgs& b, char* ws, hipStream_t s) {
+  if (b.m > 16) {
+    const GatedLayout L = gated_layout(b.m, b.n, b.k);
+    GatedGemmArgs a = {};
+    CodesJob& J = a.j;
+    J.q = b.q;
+    J.ldq = L.ldq;
+    J.m = (int32_t)b.m;
+    J.n = (int32_t)b.n;
+    J.k = (int32_t)b.k;
+    J.w = b.codes;
+    J.ktiles = (int32_t)((b.k + 255) / 256);
+    J.blocks = (int32_t)((b.n + 15) / 16);
+    set_plan(J, L.plan, reinterpret_cast<int32_t*>(ws + L.part));
+    a.x_scale = b.x_scale;
+    a.gate_scale = b.gate_scale;
+    a.up_scale = b.up_scale;
+    a.a = b.a;
+    a.g = b.g;
+    a.u = b.u;
+    if (b.k % 16) {
+      const hipError_t e = codes_rows(b.q, b.m, b.k, L.ldq, reinterpret_cast<int8_t*>(ws), s);
+      if (e != hipSuccess) return e;
+      J.q = reinterpret_cast<const int8_t*>(ws);
+    }
+    return b.silu ? launch_gated_gemm<true>(a, L.plan.cfg, s) : launch_gated_gemm<false>(a, L.plan.cfg, s);
+  }
   GatedKernelArgs a = {};
   a.q = b.q;
   a.x_scale = b.x_scale;

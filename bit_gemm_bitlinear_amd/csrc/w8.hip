@@ -7,6 +7,8 @@
 // bytes (consecutive k of one row) a lane of a wavefront: an operand of the
 // 16x16x64 int8 matrix-core op.  Sums are exact in int32.
 #include "../../include/bitlinear_ffn.h"
+#include "codes_gemm.hpp"
+#include "codes_plan.hpp"
 #include "common.hpp"
 #include "internal.hpp"
 #include "layer_internal.hpp"
@@ -106,6 +108,155 @@ __global__ __launch_bounds__(64) void w8_kernel(const W8KernelArgs A) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// More than 16 tokens: tiles on the int8 matrix cores (codes_gemm.hpp).
+
+struct W8GemmArgs {
+  CodesJob j;
+  const float* x_scale;
+  const float* scale;
+  const uint16_t* bias;
+  uint16_t* y;
+};
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// (acc * s) / xs by one product and one division.  With both scales in a middle
+// range (xs in 2^-40..2^40, s in 2^-60..2^40) nothing in the division's fast form
+// leaves fp32's.
+__device__ __forceinline__ bool w8_fast_row(float xs) { return xs >= 9.094947e-13f && xs <= 1.0995116e12f; }
+__device__ __forceinline__ bool w8_fast_scale(float s) { return s >= 8.6736174e-19f && s <= 1.0995116e12f; }
+__device__ __forceinline__ float w8_value(int32_t acc, float s, float xs, float y, bool fast) {
+  const float t = (float)acc * s;
+  return fast ? row_div_fast(t, xs, y) : t / xs;
+}
+
+template <typename T>
+__global__ __launch_bounds__(64 * T::NW, 2) void w8_gemm_kernel(const W8GemmArgs A) {
+  extern __shared__ __align__(16) int8_t smem[];
+  const CodesJob& J = A.j;
+  int ti, tj, kp;
+  if (!codes_tile_of((int)blockIdx.x, J, &ti, &tj, &kp)) return;
+  v16i acc[T::FI][T::FJ];
+  T::run(J, ti, tj, kp, smem, acc);
+  const int lane = threadIdx.x & 63, lr = lane & 31, lg = lane >> 5;
+  const int m0 = ti * T::TI + T::row0() + lr, n0 = tj * T::kCols + T::col0();
+  if (J.ksplit > 1) {
+#pragma unroll
+    for (int i = 0; i < T::FI; ++i) {
+      const int m = m0 + 32 * i;
+      if (m >= J.m) continue;
+      int32_t* row = J.part + ((int64_t)kp * J.m + m) * J.n;
+#pragma unroll
+      for (int j = 0; j < T::FJ; ++j) codes_put_part(row, n0 + 32 * j, J.n, acc[i][j]);
+    }
+    return;
+  }
+  const bool wide = (J.n & 7) == 0;  // output rows are 16-byte aligned
+  float xs[T::FI], y[T::FI];
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i) {
+    xs[i] = *G(A.x_scale + min(m0 + 32 * i, J.m - 1));
+    y[i] = 1.0f / xs[i];
+  }
+#pragma unroll
+  for (int j = 0; j < T::FJ; ++j) {
+    float s[16];  // scales of the lane's columns
+    bool fast = true;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[4 * a + e] = *G(A.scale + min(n0 + 32 * j + 8 * a + 4 * lg + e, J.n - 1));
+        fast = fast && w8_fast_scale(s[4 * a + e]);
+      }
+#pragma unroll
+    for (int i = 0; i < T::FI; ++i) {
+      const int m = m0 + 32 * i;
+      const bool f = fast && w8_fast_row(xs[i]);
+      uint32_t pk[8];
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        pk[h] = pack_bf16x2(w8_value(acc[i][j][2 * h], s[2 * h], xs[i], y[i], f),
+                            w8_value(acc[i][j][2 * h + 1], s[2 * h + 1], xs[i], y[i], f));
+      codes_rows8(pk);
+      if (m >= J.m) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = n0 + 32 * j + 16 * h + 8 * lg;
+        if (A.bias) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t b0 = *G(A.bias + min(n + 2 * e, J.n - 1)), b1 = *G(A.bias + min(n + 2 * e + 1, J.n - 1));
+            pk[4 * h + e] = add_bf16x2(pk[4 * h + e], b0 | (b1 << 16));
+          }
+        }
+        codes_put8(A.y + (int64_t)m * J.n, n, J.n, wide, pk + 4 * h);
+      }
+    }
+  }
+}
+
+// Adds the parts of a split product: eight outputs of a row a thread.
+__global__ __launch_bounds__(256) void w8_finish_kernel(const W8GemmArgs A, int64_t total) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= total) return;
+  const CodesJob& J = A.j;
+  const int cpr = (J.n + 7) >> 3;
+  const int64_t m = id / cpr;
+  const int n = 8 * (int)(id - m * cpr);
+  const int64_t slice = (int64_t)J.m * J.n;
+  const int32_t* src = J.part + m * J.n + n;
+  int32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  codes_add_parts(src, slice, J.ksplit, J.n - n, (J.n & 3) == 0, v);
+  const float xs = *G(A.x_scale + m), y = 1.0f / xs;
+  float t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float s = *G(A.scale + min(n + e, J.n - 1));
+    t[e] = w8_value(v[e], s, xs, y, w8_fast_row(xs) && w8_fast_scale(s));
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    w[e] = pack_bf16x2(t[2 * e], t[2 * e + 1]);
+    if (A.bias) {
+      const uint32_t b0 = *G(A.bias + min(n + 2 * e, J.n - 1)), b1 = *G(A.bias + min(n + 2 * e + 1, J.n - 1));
+      w[e] = add_bf16x2(w[e], b0 | (b1 << 16));
+    }
+  }
+  codes_put8(A.y + m * J.n, n, J.n, (J.n & 7) == 0, w);
+}
+
+using W8Tile256 = CodesTile<256, 256, 2, 4, 2, false>;
+using W8Tile128 = CodesTile<128, 128, 2, 2, 2, false>;
+using W8Tile64 = CodesTile<64, 128, 2, 2, 3, false>;
+using W8Tile32 = CodesTile<32, 128, 1, 4, 4, false>;
+
+template <typename T>
+hipError_t w8_gemm(const W8GemmArgs& a, hipStream_t s) {
+  static std::atomic<bool> done[kMaxDevices];
+  const int64_t grid = round_up((int64_t)a.j.tiles_i * a.j.tiles_j * a.j.ksplit, 8);
+  return codes_launch(&w8_gemm_kernel<T>, done, (unsigned)grid, 64 * T::NW, T::kLds, s, a);
+}
+
+struct W8Layout {
+  CodesPlan plan;
+  int32_t ldq;
+  size_t part, total;
+};
+
+W8Layout w8_layout(int64_t m, int64_t n, int64_t k) {
+  W8Layout L = {};
+  if (m <= 16) return L;
+  L.plan = plan_codes(m, n, (k + 127) / 128, false);
+  L.ldq = (int32_t)round_up(k, 16);
+  if (k % 16) L.total = align256((size_t)m * L.ldq);
+  L.part = L.total;
+  if (L.plan.ksplit > 1) L.total = align256(L.total + 4 * (size_t)L.plan.ksplit * m * n);
+  return L;
+}
+
 }  // namespace
 
 hipError_t launch_w8_pack(const float* w, int64_t n, int64_t k, int8_t* codes, float* scale, hipStream_t s) {
@@ -121,9 +272,41 @@ hipError_t launch_w8_unpack(const int8_t* codes, const float* scale, int64_t n, 
   return hipGetLastError();
 }
 
-size_t w8_forward_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t w8_forward_bytes(int64_t m, int64_t n, int64_t k) { return w8_layout(m, n, k).total; }
 
-hipError_t launch_w8_forward(const W8Args& b, char*, hipStream_t s) {
+hipError_t launch_w8_forward(const W8Args& b, char* ws, hipStream_t s) {
+  if (b.m > 16) {
+    const W8Layout L = w8_layout(b.m, b.n, b.k);
+    W8GemmArgs a = {};
+    CodesJob& J = a.j;
+    J.q = b.q;
+    J.ldq = L.ldq;
+    J.m = (int32_t)b.m;
+    J.n = (int32_t)b.n;
+    J.k = (int32_t)b.k;
+    J.w = reinterpret_cast<const uint8_t*>(b.codes);
+    J.ktiles = (int32_t)((b.k + 63) / 64);
+    J.blocks = (int32_t)((b.n + 15) / 16);
+    set_plan(J, L.plan, reinterpret_cast<int32_t*>(ws + L.part));
+    a.x_scale = b.x_scale;
+    a.scale = b.scale;
+    a.bias = b.bias;
+    a.y = b.y;
+    hipError_t e = hipSuccess;
+    if (b.k % 16) {
+      e = codes_rows(b.q, b.m, b.k, L.ldq, reinterpret_cast<int8_t*>(ws), s);
+      if (e != hipSuccess) return e;
+      J.q = reinterpret_cast<const int8_t*>(ws);
+    }
+    e = L.plan.cfg == 3   ? w8_gemm<W8Tile256>(a, s)
+        : L.plan.cfg == 2 ? w8_gemm<W8Tile128>(a, s)
+        : L.plan.cfg == 1 ? w8_gemm<W8Tile64>(a, s)
+                          : w8_gemm<W8Tile32>(a, s);
+    if (e != hipSuccess || J.ksplit == 1) return e;
+    const int64_t total = b.m * ((b.n + 7) / 8);
+    w8_finish_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, total);
+    return hipGetLastError();
+  }
   W8KernelArgs a = {};
   a.q = b.q;
   a.x_scale = b.x_scale;
