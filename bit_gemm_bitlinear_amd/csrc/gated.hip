@@ -12,6 +12,7 @@
 #include "../../include/bitlinear_ffn.h"
 #include "codes_gemm.hpp"
 #include "codes_plan.hpp"
+#include "codes_rows.hpp"
 #include "common.hpp"
 #include "internal.hpp"
 #include "layer_internal.hpp"
@@ -46,23 +47,18 @@ __global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __res
     const int64_t row = 16 * b + (lane & 15), o = 64 * t + 16 * (lane >> 4);
     const uint8_t* src = p ? up : gate;
     const bool tiled = p ? up_tiled : gate_tiled;
-    v4i v;
+    v4i v = {0x55555555, 0x55555555, 0x55555555, 0x55555555};
+    if (row < n && tiled) {
+      v = *G(reinterpret_cast<const v4i*>(src + tiled_chunk_offset(row, o, rb)));
+    } else if (row < n && (rb & 15) == 0) {
+      if (o < rb) v = *G(reinterpret_cast<const v4i*>(src + row * rb + o));
+    } else if (row < n) {
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      uint32_t w = 0x55555555u;
-      if (row < n) {
-        if (tiled) {
-          w = *G(reinterpret_cast<const uint32_t*>(src + tiled_chunk_offset(row, o, rb) + 4 * d));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int64_t at = o + 4 * d + e;
-            if (at < rb) w = (w & ~(0xFFu << (8 * e))) | ((uint32_t)*G(src + row * rb + at) << (8 * e));
-          }
-        }
-      }
-      v[d] = (int32_t)gated_dword(w);
+      for (int e = 0; e < 16; ++e)
+        if (o + e < rb) v[e >> 2] = (v[e >> 2] & ~(0xFF << (8 * (e & 3)))) | ((int)*G(src + row * rb + o + e) << (8 * (e & 3)));
     }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d] = (int32_t)gated_dword((uint32_t)v[d]);
     *G(reinterpret_cast<v4i*>(codes + 16 * id)) = v;
   }
 }
@@ -81,58 +77,50 @@ __device__ __forceinline__ float gate_value(float g, float u) {
   }
 }
 
-struct GatedKernelArgs {
-  const int8_t* q;
+// ---------------------------------------------------------------------------
+// Up to 16 tokens (codes_rows.hpp).
+
+struct GatedRowsArgs {
+  RowsJob j;
   const float* x_scale;
-  const uint8_t* codes;
   const float* gate_scale;
   const float* up_scale;
   uint16_t* a;
   uint16_t* g;
   uint16_t* u;
-  int32_t m, n, k;
-  int32_t ktiles, blocks;
 };
 
-// One wave: 16 outputs of 16 tokens.
-template <bool SILU>
-__global__ __launch_bounds__(64) void gated_kernel(const GatedKernelArgs A) {
-  const int lane = threadIdx.x, lr = lane & 15, lg = lane >> 4;
-  const int blk = blockIdx.x, m0 = (int)blockIdx.y * 16;
-  const uint8_t* cp = A.codes + (int64_t)blk * A.ktiles * 2048 + 16 * lane;
-  const int64_t m = min(m0 + lr, A.m - 1);
-  const int8_t* qp = A.q + m * A.k;
-  v4i ag = {0, 0, 0, 0}, au = {0, 0, 0, 0};
-  for (int t = 0; t < A.ktiles; ++t) {
-    const v4i wg = *G(reinterpret_cast<const v4i*>(cp + (int64_t)t * 2048));
-    const v4i wu = *G(reinterpret_cast<const v4i*>(cp + (int64_t)t * 2048 + 1024));
+template <int W, int U, bool SILU>
+__global__ __launch_bounds__(64 * W) void gated_rows_kernel(const GatedRowsArgs A) {
+  extern __shared__ __align__(16) int8_t smem[];
+  codes_rows_product<W, U, true>(A.j, smem, [&](int m, int n, const v4i (&acc)[2]) {
+    const float xs = *G(A.x_scale + m);
+    const RowDiv dg = row_div_setup(xs * *G(A.gate_scale)), du = row_div_setup(xs * *G(A.up_scale));
+    float g[4], u[4], a[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      v4i x;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const int k = 256 * t + 64 * lg + 16 * s + 4 * d;
-        x[d] = k < A.k ? *G(reinterpret_cast<const int32_t*>(qp + k)) : 0;
-      }
-      ag = mfma_16x16x64_i8(expand16((uint32_t)wg[s]), x, ag);
-      au = mfma_16x16x64_i8(expand16((uint32_t)wu[s]), x, au);
+    for (int e = 0; e < 4; ++e) {
+      g[e] = row_div((float)acc[0][e] * 0.015625f, dg);
+      u[e] = row_div((float)acc[1][e] * 0.015625f, du);
+      a[e] = gate_value<SILU>(g[e], u[e]);
     }
-  }
-  if (m0 + lr >= A.m) return;
-  const float xs = *G(A.x_scale + m);
-  const RowDiv dg = row_div_setup(xs * *G(A.gate_scale)), du = row_div_setup(xs * *G(A.up_scale));
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int n = 16 * blk + 4 * lg + e;
-    if (n >= A.n) continue;
-    const float g = row_div((float)ag[e] * 0.015625f, dg), u = row_div((float)au[e] * 0.015625f, du);
-    const int64_t o = m * A.n + n;
-    *G(A.a + o) = f32_to_bf16(gate_value<SILU>(g, u));
+    const int64_t at = (int64_t)m * A.j.n;
+    codes_put4(A.a + at, n, A.j.n, pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
     if (A.g) {
-      *G(A.g + o) = f32_to_bf16(g);
-      *G(A.u + o) = f32_to_bf16(u);
+      codes_put4(A.g + at, n, A.j.n, pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
+      codes_put4(A.u + at, n, A.j.n, pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]));
     }
-  }
+  });
+}
+
+template <bool SILU>
+hipError_t launch_gated_rows(const GatedRowsArgs& a, const RowsPlan& p, hipStream_t s) {
+  const int per = p.waves / p.wk;
+  const dim3 grid((unsigned)((a.j.blocks + per - 1) / per), (unsigned)((a.j.m + 15) / 16));
+  if (p.waves == 16)
+    gated_rows_kernel<16, 1, SILU><<<grid, 1024, p.lds, s>>>(a);
+  else
+    gated_rows_kernel<8, 2, SILU><<<grid, 512, p.lds, s>>>(a);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -337,26 +325,24 @@ hipError_t launch_gated_forward(const GatedArgs& b, char* ws, hipStream_t s) {
     }
     return b.silu ? launch_gated_gemm<true>(a, L.plan.cfg, s) : launch_gated_gemm<false>(a, L.plan.cfg, s);
   }
-  GatedKernelArgs a = {};
-  a.q = b.q;
+  const RowsPlan p = plan_rows(b.m, b.n, b.k, true);
+  GatedRowsArgs a = {};
+  a.j.q = b.q;
+  a.j.m = (int32_t)b.m;
+  a.j.n = (int32_t)b.n;
+  a.j.k = (int32_t)b.k;
+  a.j.w = b.codes;
+  a.j.ktiles = (int32_t)((b.k + 255) / 256);
+  a.j.blocks = (int32_t)((b.n + 15) / 16);
+  a.j.wk = p.wk;
+  a.j.seg = p.seg;
   a.x_scale = b.x_scale;
-  a.codes = b.codes;
   a.gate_scale = b.gate_scale;
   a.up_scale = b.up_scale;
   a.a = b.a;
   a.g = b.g;
   a.u = b.u;
-  a.m = (int32_t)b.m;
-  a.n = (int32_t)b.n;
-  a.k = (int32_t)b.k;
-  a.ktiles = (int32_t)((b.k + 255) / 256);
-  a.blocks = (int32_t)((b.n + 15) / 16);
-  const dim3 grid((unsigned)a.blocks, (unsigned)((b.m + 15) / 16));
-  if (b.silu)
-    gated_kernel<true><<<grid, 64, 0, s>>>(a);
-  else
-    gated_kernel<false><<<grid, 64, 0, s>>>(a);
-  return hipGetLastError();
+  return b.silu ? launch_gated_rows<true>(a, p, s) : launch_gated_rows<false>(a, p, s);
 }
 
 }  // namespace bl

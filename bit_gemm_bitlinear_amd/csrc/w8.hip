@@ -9,6 +9,7 @@
 #include "../../include/bitlinear_ffn.h"
 #include "codes_gemm.hpp"
 #include "codes_plan.hpp"
+#include "codes_rows.hpp"
 #include "common.hpp"
 #include "internal.hpp"
 #include "layer_internal.hpp"
@@ -67,45 +68,45 @@ __global__ __launch_bounds__(256) void w8_unpack_kernel(const int8_t* __restrict
   }
 }
 
-struct W8KernelArgs {
-  const int8_t* q;
+// (acc * s) / xs by one product and one division.  With both scales in a middle
+// range (xs in 2^-40..2^40, s in 2^-60..2^40) nothing in the division's fast form
+// leaves fp32's.
+__device__ __forceinline__ bool w8_fast_row(float xs) { return xs >= 9.094947e-13f && xs <= 1.0995116e12f; }
+__device__ __forceinline__ bool w8_fast_scale(float s) { return s >= 8.6736174e-19f && s <= 1.0995116e12f; }
+__device__ __forceinline__ float w8_value(int32_t acc, float s, float xs, float y, bool fast) {
+  const float t = (float)acc * s;
+  return fast ? row_div_fast(t, xs, y) : t / xs;
+}
+
+// ---------------------------------------------------------------------------
+// Up to 16 tokens (codes_rows.hpp).
+
+struct W8RowsArgs {
+  RowsJob j;
   const float* x_scale;
-  const int8_t* codes;
   const float* scale;
   const uint16_t* bias;
   uint16_t* y;
-  int32_t m, n, k;
-  int32_t ktiles, blocks;
 };
 
-// One wave: 16 outputs of 16 tokens.
-__global__ __launch_bounds__(64) void w8_kernel(const W8KernelArgs A) {
-  const int lane = threadIdx.x, lr = lane & 15, lg = lane >> 4;
-  const int blk = blockIdx.x, m0 = (int)blockIdx.y * 16;
-  const int8_t* cp = A.codes + (int64_t)blk * A.ktiles * 1024 + 16 * lane;
-  const int64_t m = min(m0 + lr, A.m - 1);
-  const int8_t* qp = A.q + m * A.k;
-  v4i acc = {0, 0, 0, 0};
-  for (int t = 0; t < A.ktiles; ++t) {
-    const v4i w = *G(reinterpret_cast<const v4i*>(cp + (int64_t)t * 1024));
-    v4i x;
+template <int W, int U>
+__global__ __launch_bounds__(64 * W) void w8_rows_kernel(const W8RowsArgs A) {
+  extern __shared__ __align__(16) int8_t smem[];
+  codes_rows_product<W, U, false>(A.j, smem, [&](int m, int n, const v4i (&acc)[1]) {
+    const float xs = *G(A.x_scale + m);
+    float v[4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const int k = 64 * t + 16 * lg + 4 * d;
-      x[d] = k < A.k ? *G(reinterpret_cast<const int32_t*>(qp + k)) : 0;
+    for (int e = 0; e < 4; ++e) v[e] = (float)acc[0][e] * *G(A.scale + min(n + e, A.j.n - 1)) / xs;
+    uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
+    if (A.bias) {
+      uint32_t b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = *G(A.bias + min(n + e, A.j.n - 1));
+      lo = add_bf16x2(lo, b[0] | (b[1] << 16));
+      hi = add_bf16x2(hi, b[2] | (b[3] << 16));
     }
-    acc = mfma_16x16x64_i8(w, x, acc);
-  }
-  if (m0 + lr >= A.m) return;
-  const float xs = *G(A.x_scale + m);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int n = 16 * blk + 4 * lg + e;
-    if (n >= A.n) continue;
-    uint16_t y = f32_to_bf16((float)acc[e] * *G(A.scale + n) / xs);
-    if (A.bias) y = add_bf16(y, *G(A.bias + n));
-    *G(A.y + m * A.n + n) = y;
-  }
+    codes_put4(A.y + (int64_t)m * A.j.n, n, A.j.n, lo, hi);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -120,16 +121,6 @@ struct W8GemmArgs {
 };
 
 typedef float v4f __attribute__((ext_vector_type(4)));
-
-// (acc * s) / xs by one product and one division.  With both scales in a middle
-// range (xs in 2^-40..2^40, s in 2^-60..2^40) nothing in the division's fast form
-// leaves fp32's.
-__device__ __forceinline__ bool w8_fast_row(float xs) { return xs >= 9.094947e-13f && xs <= 1.0995116e12f; }
-__device__ __forceinline__ bool w8_fast_scale(float s) { return s >= 8.6736174e-19f && s <= 1.0995116e12f; }
-__device__ __forceinline__ float w8_value(int32_t acc, float s, float xs, float y, bool fast) {
-  const float t = (float)acc * s;
-  return fast ? row_div_fast(t, xs, y) : t / xs;
-}
 
 template <typename T>
 __global__ __launch_bounds__(64 * T::NW, 2) void w8_gemm_kernel(const W8GemmArgs A) {
@@ -307,19 +298,27 @@ hipError_t launch_w8_forward(const W8Args& b, char* ws, hipStream_t s) {
     w8_finish_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, total);
     return hipGetLastError();
   }
-  W8KernelArgs a = {};
-  a.q = b.q;
+  const RowsPlan p = plan_rows(b.m, b.n, b.k, false);
+  W8RowsArgs a = {};
+  a.j.q = b.q;
+  a.j.m = (int32_t)b.m;
+  a.j.n = (int32_t)b.n;
+  a.j.k = (int32_t)b.k;
+  a.j.w = reinterpret_cast<const uint8_t*>(b.codes);
+  a.j.ktiles = (int32_t)((b.k + 63) / 64);
+  a.j.blocks = (int32_t)((b.n + 15) / 16);
+  a.j.wk = p.wk;
+  a.j.seg = p.seg;
   a.x_scale = b.x_scale;
-  a.codes = b.codes;
   a.scale = b.scale;
   a.bias = b.bias;
   a.y = b.y;
-  a.m = (int32_t)b.m;
-  a.n = (int32_t)b.n;
-  a.k = (int32_t)b.k;
-  a.ktiles = (int32_t)((b.k + 63) / 64);
-  a.blocks = (int32_t)((b.n + 15) / 16);
-  w8_kernel<<<dim3((unsigned)a.blocks, (unsigned)((b.m + 15) / 16)), 64, 0, s>>>(a);
+  const int per = p.waves / p.wk;
+  const dim3 grid((unsigned)((a.j.blocks + per - 1) / per), (unsigned)((b.m + 15) / 16));
+  if (p.waves == 16)
+    w8_rows_kernel<16, 2><<<grid, 1024, p.lds, s>>>(a);
+  else
+    w8_rows_kernel<8, 4><<<grid, 512, p.lds, s>>>(a);
   return hipGetLastError();
 }
 
