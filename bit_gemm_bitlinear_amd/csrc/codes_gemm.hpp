@@ -361,7 +361,7 @@ __device__ __forceinline__ void codes_add_parts(const int32_t* src, int64_t slic
 
 // Activations whose rows do not start at a multiple of 16 bytes, in rows that do
 // (K rounded up to 16, the rest zeros): 16 bytes a thread.
-static __global__ __launch_bounds__(256) void codes_rows_kernel(const int8_t* __restrict__ q, int64_t total,
+static __global__ __launch_bounds__(256) void codes_pad_kernel(const int8_t* __restrict__ q, int64_t total,
                                                                 int32_t k, int32_t ldq, int8_t* __restrict__ out) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= total) return;
@@ -374,9 +374,9 @@ static __global__ __launch_bounds__(256) void codes_rows_kernel(const int8_t* __
   *G(reinterpret_cast<v4i*>(out + 16 * id)) = v;
 }
 
-inline hipError_t codes_rows(const int8_t* q, int64_t m, int64_t k, int32_t ldq, int8_t* out, hipStream_t s) {
+inline hipError_t codes_pad(const int8_t* q, int64_t m, int64_t k, int32_t ldq, int8_t* out, hipStream_t s) {
   const int64_t total = m * (ldq >> 4);
-  codes_rows_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(q, total, (int32_t)k, ldq, out);
+  codes_pad_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(q, total, (int32_t)k, ldq, out);
   return hipGetLastError();
 }
 
@@ -389,16 +389,16 @@ inline void set_plan(CodesJob& J, const CodesPlan& p, int32_t* part) {
   J.part = part;
 }
 
-// Launches a kernel with the dynamic LDS it needs (an attribute above 64 KB, set
-// once per device and kernel: `done` is the caller's).
+// Launches a kernel with `lds` bytes of dynamic LDS, of at most `most`: an attribute
+// above 64 KB, set once per device and kernel (`done` is the caller's).
 template <typename Kernel, typename Args>
-hipError_t codes_launch(Kernel kernel, std::atomic<bool>* done, unsigned grid, unsigned threads, size_t lds,
+hipError_t codes_launch(Kernel kernel, std::atomic<bool>* done, dim3 grid, unsigned threads, size_t lds, size_t most,
                         hipStream_t s, const Args& args) {
   if (lds > 64 * 1024) {
     const int dev = current_device_index();
     if (!done[dev].load(std::memory_order_acquire)) {
       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)most);
       if (e != hipSuccess) return e;
       done[dev].store(true, std::memory_order_release);
     }

@@ -2,12 +2,12 @@
 // (w8.hip) or a gated block's two ternary ones (gated.hip), the weights streamed
 // once: what decoding takes, where the weights' bytes are the cost.
 //
-// W / wk blocks of 16 weight rows a workgroup; wk waves share a block along K
-// (contiguous shares of its tiles), and their int32 sums are joined in LDS.  The
-// token rows are staged in LDS, a segment of K that fits at a time, so a wave's
-// memory loads are the weights' alone: whole kilobytes, U tiles ahead.  A row of
-// LDS is 16 bytes over a multiple of 256, so that the 16 rows of an operand lie in
-// distinct banks.
+// A workgroup is 16 waves and takes 16 / wk blocks of 16 weight rows; wk waves share
+// a block along K (contiguous shares of its tiles), and their int32 sums are joined
+// in LDS.  The token rows are staged in LDS, a segment of K that fits at a time, so
+// a wave's memory loads are the weights' alone: whole kilobytes, U tiles ahead.  A
+// row of LDS is 16 bytes over a multiple of 256, so that the 16 rows of an operand
+// lie in distinct banks.
 #pragma once
 
 #include "codes_gemm.hpp"
@@ -26,6 +26,9 @@ struct RowsJob {
   int32_t seg;             // tiles of K staged at a time
 };
 
+constexpr int kRowsWaves = 16;
+constexpr int kRowsLds = 80000;  // two workgroups a CU
+
 // K of a tile, and matrices (gate and up).
 constexpr int rows_tile_k(bool ternary) { return ternary ? 256 : 64; }
 constexpr int rows_mats(bool ternary) { return ternary ? 2 : 1; }
@@ -35,9 +38,9 @@ inline int rows_ldx(int seg, bool ternary) { return (int)round_up(seg * rows_til
 
 // finish(token, first of four outputs, sums [matrices][4]) is called for what
 // exists of tokens and of groups of four outputs.
-template <int W, int U, bool TERNARY, typename Finish>
+template <int U, bool TERNARY, typename Finish>
 __device__ __forceinline__ void codes_rows_product(const RowsJob& J, int8_t* lds, const Finish& finish) {
-  constexpr int TK = rows_tile_k(TERNARY), MATS = rows_mats(TERNARY);
+  constexpr int W = kRowsWaves, TK = rows_tile_k(TERNARY), MATS = rows_mats(TERNARY);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int lr = lane & 15, lg = lane >> 4;
   const int blk = (int)blockIdx.x * (W / J.wk) + wave / J.wk;
@@ -138,9 +141,15 @@ __device__ __forceinline__ void codes_put4(uint16_t* row, int n, int cols, uint3
   }
 }
 
-// Waves per block and a workgroup, and the segments of K.
+// Waves of a block, and the segments of K.  Of ternary weights as many waves as
+// leave at most a workgroup a CU (gated 14336 x 4096 at 16 tokens: 224 workgroups
+// of four blocks 9.9 us, 448 of two 12.1, 896 of eight waves 15.2; at one token
+// 8.7, 10.3 and 9.1), which stage their tokens once.  8-bit weights have four times
+// the bytes a tile's tokens: eight waves a block, or 16 where that would leave CUs
+// without a workgroup (32768 x 4096 at 16 tokens: eight 29.1, four 32.9; 14336 x
+// 4096: eight 12.8, 16 16.3; 4096 x 4096: 16 7.2, eight 8.3).
 struct RowsPlan {
-  int waves, wk, seg;
+  int wk, seg;
   size_t lds;
 };
 
@@ -148,14 +157,24 @@ inline RowsPlan plan_rows(int64_t m, int64_t n, int64_t k, bool ternary) {
   const int tk = rows_tile_k(ternary), rows = (int)std::min<int64_t>(m, 16);
   const int64_t blocks = (n + 15) / 16, ktiles = (k + tk - 1) / tk;
   RowsPlan p = {};
-  p.wk = 8;
-  while (rows > 4 && p.wk > 1 && blocks * (p.wk / 2) >= 4096) p.wk /= 2;
-  p.waves = 8;
-  if (blocks <= 256 && ktiles * tk >= 4096) p.waves = p.wk = 16;
-  const int budget = p.waves == 16 ? 65000 : 62000;
-  p.seg = (int)std::min<int64_t>(ktiles, (budget / rows - 16) / 256 * 256 / tk);
-  p.lds = std::max<size_t>((size_t)rows * rows_ldx(p.seg, ternary), (size_t)p.waves * rows_mats(ternary) * 1024);
+  p.wk = kRowsWaves;
+  if (ternary) {
+    while (p.wk > 1 && blocks * p.wk > 256 * kRowsWaves) p.wk /= 2;
+  } else if (blocks > 256) {
+    p.wk = 8;
+  }
+  const int64_t most = std::min<int64_t>(ktiles, (kRowsLds / rows - 16) / 256 * 256 / tk);
+  const int64_t segs = (ktiles + most - 1) / most;
+  p.seg = (int)((ktiles + segs - 1) / segs);  // of about one size
+  p.lds = std::max<size_t>((size_t)rows * rows_ldx(p.seg, ternary), (size_t)kRowsWaves * rows_mats(ternary) * 1024);
   return p;
+}
+
+template <typename Args, typename Kernel>
+hipError_t launch_rows(const Args& a, const RowsPlan& p, Kernel kernel, std::atomic<bool>* done, hipStream_t s) {
+  const int per = kRowsWaves / p.wk;
+  const dim3 grid((unsigned)((a.j.blocks + per - 1) / per), (unsigned)((a.j.m + 15) / 16));
+  return codes_launch(kernel, done, grid, 64 * kRowsWaves, p.lds, kRowsLds, s, a);
 }
 
 }  // namespace bl

@@ -90,10 +90,10 @@ struct GatedRowsArgs {
   uint16_t* u;
 };
 
-template <int W, int U, bool SILU>
-__global__ __launch_bounds__(64 * W) void gated_rows_kernel(const GatedRowsArgs A) {
+template <bool SILU>
+__global__ __launch_bounds__(64 * kRowsWaves) void gated_rows_kernel(const GatedRowsArgs A) {
   extern __shared__ __align__(16) int8_t smem[];
-  codes_rows_product<W, U, true>(A.j, smem, [&](int m, int n, const v4i (&acc)[2]) {
+  codes_rows_product<1, true>(A.j, smem, [&](int m, int n, const v4i (&acc)[2]) {
     const float xs = *G(A.x_scale + m);
     const RowDiv dg = row_div_setup(xs * *G(A.gate_scale)), du = row_div_setup(xs * *G(A.up_scale));
     float g[4], u[4], a[4];
@@ -114,13 +114,8 @@ __global__ __launch_bounds__(64 * W) void gated_rows_kernel(const GatedRowsArgs 
 
 template <bool SILU>
 hipError_t launch_gated_rows(const GatedRowsArgs& a, const RowsPlan& p, hipStream_t s) {
-  const int per = p.waves / p.wk;
-  const dim3 grid((unsigned)((a.j.blocks + per - 1) / per), (unsigned)((a.j.m + 15) / 16));
-  if (p.waves == 16)
-    gated_rows_kernel<16, 1, SILU><<<grid, 1024, p.lds, s>>>(a);
-  else
-    gated_rows_kernel<8, 2, SILU><<<grid, 512, p.lds, s>>>(a);
-  return hipGetLastError();
+  static std::atomic<bool> done[kMaxDevices];
+  return launch_rows(a, p, &gated_rows_kernel<SILU>, done, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -253,7 +248,7 @@ template <typename T, bool SILU>
 hipError_t gated_gemm(const GatedGemmArgs& a, hipStream_t s) {
   static std::atomic<bool> done[kMaxDevices];
   const int64_t grid = round_up((int64_t)a.j.tiles_i * a.j.tiles_j * a.j.ksplit, 8);
-  return codes_launch(&gated_gemm_kernel<T, SILU>, done, (unsigned)grid, 64 * T::NW, T::kLds, s, a);
+  return codes_launch(&gated_gemm_kernel<T, SILU>, done, dim3((unsigned)grid), 64 * T::NW, T::kLds, T::kLds, s, a);
 }
 
 template <bool SILU>
@@ -319,7 +314,7 @@ hipError_t launch_gated_forward(const GatedArgs& b, char* ws, hipStream_t s) {
     a.g = b.g;
     a.u = b.u;
     if (b.k % 16) {
-      const hipError_t e = codes_rows(b.q, b.m, b.k, L.ldq, reinterpret_cast<int8_t*>(ws), s);
+      const hipError_t e = codes_pad(b.q, b.m, b.k, L.ldq, reinterpret_cast<int8_t*>(ws), s);
       if (e != hipSuccess) return e;
       J.q = reinterpret_cast<const int8_t*>(ws);
     }

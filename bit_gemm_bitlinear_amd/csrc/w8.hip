@@ -89,10 +89,9 @@ struct W8RowsArgs {
   uint16_t* y;
 };
 
-template <int W, int U>
-__global__ __launch_bounds__(64 * W) void w8_rows_kernel(const W8RowsArgs A) {
+__global__ __launch_bounds__(64 * kRowsWaves) void w8_rows_kernel(const W8RowsArgs A) {
   extern __shared__ __align__(16) int8_t smem[];
-  codes_rows_product<W, U, false>(A.j, smem, [&](int m, int n, const v4i (&acc)[1]) {
+  codes_rows_product<4, false>(A.j, smem, [&](int m, int n, const v4i (&acc)[1]) {
     const float xs = *G(A.x_scale + m);
     float v[4];
 #pragma unroll
@@ -228,7 +227,7 @@ template <typename T>
 hipError_t w8_gemm(const W8GemmArgs& a, hipStream_t s) {
   static std::atomic<bool> done[kMaxDevices];
   const int64_t grid = round_up((int64_t)a.j.tiles_i * a.j.tiles_j * a.j.ksplit, 8);
-  return codes_launch(&w8_gemm_kernel<T>, done, (unsigned)grid, 64 * T::NW, T::kLds, s, a);
+  return codes_launch(&w8_gemm_kernel<T>, done, dim3((unsigned)grid), 64 * T::NW, T::kLds, T::kLds, s, a);
 }
 
 struct W8Layout {
@@ -285,7 +284,7 @@ hipError_t launch_w8_forward(const W8Args& b, char* ws, hipStream_t s) {
     a.y = b.y;
     hipError_t e = hipSuccess;
     if (b.k % 16) {
-      e = codes_rows(b.q, b.m, b.k, L.ldq, reinterpret_cast<int8_t*>(ws), s);
+      e = codes_pad(b.q, b.m, b.k, L.ldq, reinterpret_cast<int8_t*>(ws), s);
       if (e != hipSuccess) return e;
       J.q = reinterpret_cast<const int8_t*>(ws);
     }
@@ -313,13 +312,8 @@ hipError_t launch_w8_forward(const W8Args& b, char* ws, hipStream_t s) {
   a.scale = b.scale;
   a.bias = b.bias;
   a.y = b.y;
-  const int per = p.waves / p.wk;
-  const dim3 grid((unsigned)((a.j.blocks + per - 1) / per), (unsigned)((b.m + 15) / 16));
-  if (p.waves == 16)
-    w8_rows_kernel<16, 2><<<grid, 1024, p.lds, s>>>(a);
-  else
-    w8_rows_kernel<8, 4><<<grid, 512, p.lds, s>>>(a);
-  return hipGetLastError();
+  static std::atomic<bool> done[kMaxDevices];
+  return launch_rows(a, p, &w8_rows_kernel, done, s);
 }
 
 }  // namespace bl
