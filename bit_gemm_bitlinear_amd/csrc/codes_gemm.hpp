@@ -40,12 +40,9 @@ struct CodesJob {
   int32_t slabs;           // ceil(k / 128)
   int32_t tiles_i, tiles_j;
   int32_t ksplit, kspw;  // parts of k, and slabs a part
+  int32_t past_cache;    // the outputs are more than the L2 caches hold, and go past them
   int32_t* part;         // ksplit > 1: int32 sums [ksplit][m][n] (gated: [ksplit][2][m][n])
 };
-
-constexpr int kCodesRow = 128;                           // bytes of a row of a slab
-constexpr int codes_b_row(bool ternary) { return ternary ? 32 : 128; }
-constexpr int codes_stage(int ti, int tj, bool ternary) { return ti * kCodesRow + tj * codes_b_row(ternary); }
 
 namespace codes_gemm {
 
@@ -96,21 +93,78 @@ __device__ __forceinline__ v4i expand16(uint32_t p) {
   return r;
 }
 
+// A wave's bf16 outputs of 32 rows on their way to memory.  A lane has runs of
+// four columns of one row; stored like that an instruction would touch 32 rows,
+// 16 bytes of each.  A pass through LDS, in a part of the wave's own (the ring is
+// done with), makes it whole rows: `cols` columns, 16 bytes a lane.
+template <int COLS>
+struct CodesRows {
+  static constexpr int kPitch = 2 * COLS + 16;  // 16 bytes off: rows start at distinct banks
+  static constexpr int kBytes = 32 * kPitch;
+  static constexpr int LPR = COLS / 8, RPI = 64 / LPR;  // lanes a row, rows an instruction
+
+  int8_t* mine;
+  __device__ __forceinline__ explicit CodesRows(int8_t* lds) : mine(lds) {}
+
+  // Columns c .. c + 3 (of the 32 rows' COLS) of row lr.
+  __device__ __forceinline__ void put(int lr, int c, uint32_t lo, uint32_t hi) const {
+    typedef int32_t v2i __attribute__((ext_vector_type(2)));
+    *reinterpret_cast<v2i*>(mine + lr * kPitch + 2 * c) = v2i{(int32_t)lo, (int32_t)hi};
+  }
+  // Rows m0 .. m0 + 31 at columns n0 ... of out [m][n]; what is past them is not stored.
+  __device__ __forceinline__ void store(uint16_t* out, int m0, int n0, int m, int n, bool past_cache) const {
+    const int lane = threadIdx.x & 63;
+    const int c = n0 + 8 * (lane % LPR);
+    const bool wide = (n & 7) == 0;  // output rows are 16-byte aligned
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < 32 / RPI; ++q) {
+      const int r = q * RPI + lane / LPR;
+      const v4i v = *reinterpret_cast<const v4i*>(mine + r * kPitch + 16 * (lane % LPR));
+      if (m0 + r >= m) continue;
+      uint16_t* row = out + (int64_t)(m0 + r) * n;
+      if (wide && c < n) {
+        if (COLS >= 64 && past_cache) {
+          // fenced: the compiler would make one store of the two branches', a plain one
+          asm volatile("" ::: "memory");
+          __builtin_nontemporal_store(v, G(reinterpret_cast<v4i*>(row + c)));
+          asm volatile("" ::: "memory");
+        } else {
+          *G(reinterpret_cast<v4i*>(row + c)) = v;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < n) *G(row + c + e) = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+};
+
 // One tile of TI tokens x TJ weight rows by WI x WJ waves.  TERNARY: the first
 // half of the TJ rows is the gate's, the second the up projection's of the same
 // TJ / 2 outputs, and so is each wave's share.
-template <int TI_, int TJ_, int WI_, int WJ_, int NST_, bool TERNARY>
+template <int TI_, int TJ_, int WI_, int WJ_, int NST_, bool TERNARY, int SL_ = 128>
 struct CodesTile {
+  static constexpr int SL = SL_;         // k of a slab, 128 or 64
+  static constexpr int CA = SL / 16;     // chunks of a row of activations or 8-bit weights
+  static constexpr int kRowB = TERNARY ? SL / 4 : SL;  // bytes of a row of weights
+  static constexpr int kSwzA = 16 / CA;  // rows in a row of banks
+  static __device__ __forceinline__ int swz(int r, int c) { return c ^ ((r / kSwzA) & (CA - 1)); }
   static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, NST = NST_, NW = WI * WJ;
   static constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;
-  static constexpr int kStage = codes_stage(TI, TJ, TERNARY);
+  static constexpr int kStage = TI * SL + TJ * kRowB;
   static constexpr int kLds = NST * kStage;
-  static constexpr int DA = TI / 8 / NW;  // loads of a slab, per wave
-  static constexpr int CB = TJ * codes_b_row(TERNARY) / 1024;  // of the weights, all waves
+  static constexpr int DA = TI * SL / 1024 / NW;  // loads of a slab, per wave
+  static constexpr int CB = TJ * kRowB / 1024;  // of the weights, all waves
   static constexpr int DB = CB < NW ? 1 : CB / NW;
   static constexpr int D = DA + DB;
+  static constexpr int kPerSimd = NW == 4 && FI * FJ > 8 ? 1 : 2;  // waves (registers)
   static constexpr int kCols = TERNARY ? TJ / 2 : TJ;  // outputs of a tile
-  static_assert(DA * 8 * NW == TI && (DB * NW == CB || NW % CB == 0), "whole loads");
+  using Rows = CodesRows<kCols / WJ>;                  // a wave's outputs
+  static_assert(NW * Rows::kBytes <= kLds, "they fit the ring");
+  static_assert(DA * 1024 * NW == TI * SL && (DB * NW == CB || NW % CB == 0), "whole loads");
   static_assert(FI * WI * 32 == TI && FJ * WJ * 32 == TJ && (!TERNARY || FJ % 2 == 0), "whole subtiles");
 
   // First row and (outputs') first column of the wave's share.
@@ -136,19 +190,20 @@ struct CodesTile {
     uint32_t ar[DA], ac[DA], br[DB], bc[DB];
 #pragma unroll
     for (int i = 0; i < DA; ++i) {
-      const int pos = (wv * DA + i) * 64 + lane, r = pos >> 3;
+      const int pos = (wv * DA + i) * 64 + lane, r = pos / CA;
       ar[i] = (uint32_t)min(r, J.m - 1 - i0) * (uint32_t)J.ldq;
-      ac[i] = 16 * ((pos & 7) ^ ((r >> 1) & 7));
+      ac[i] = 16 * swz(r, pos % CA);
     }
 #pragma unroll
     for (int i = 0; i < DB; ++i) {  // waves past the last piece load one again, so that all wait alike
       const int pos = ((wv % CB) * DB + i) * 64 + lane;
       if constexpr (TERNARY) {
-        const int r = pos >> 1, h = (pos & 1) ^ ((r >> 3) & 1), up = r >= TJ / 2, o = r - up * (TJ / 2);
+        const int r = SL == 128 ? pos >> 1 : pos, h = SL == 128 ? (pos & 1) ^ ((r >> 3) & 1) : 0;
+        const int up = r >= TJ / 2, o = r - up * (TJ / 2);
         br[i] = (uint32_t)min(o >> 4, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 2048) + 1024 * up + 16 * (o & 15);
         bc[i] = 256 * h;
       } else {
-        const int r = pos >> 3, c = (pos & 7) ^ ((r >> 1) & 7);
+        const int r = pos / CA, c = swz(r, pos % CA);
         br[i] = (uint32_t)min(r >> 4, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 1024) + 256 * (c & 3) + 16 * (r & 15);
         bc[i] = 1024 * (c >> 2);
       }
@@ -160,13 +215,16 @@ struct CodesTile {
     auto issue_one = [&](int d, int8_t* st) {
       if (d < DA) {
         // the row's last chunk for those past it
-        const uint32_t last = (uint32_t)(J.ldq - 16 - next * kCodesRow);
-        dma16(pa + (int64_t)next * kCodesRow + ar[d] + min(ac[d], last), st + (wv * DA + d) * 1024);
+        const uint32_t last = (uint32_t)(J.ldq - 16 - next * SL);
+        dma16(pa + (int64_t)next * SL + ar[d] + min(ac[d], last), st + (wv * DA + d) * 1024);
       } else {
         const int e = d - DA;
-        int8_t* dst = st + TI * kCodesRow + ((wv % CB) * DB + e) * 1024;
+        int8_t* dst = st + TI * SL + ((wv % CB) * DB + e) * 1024;
         if constexpr (TERNARY) {
-          dma16(pb + (int64_t)(next >> 1) * 2048 + 512 * (next & 1) + br[e] + bc[e], dst);
+          constexpr int PT = 256 / SL;  // slabs of a tile
+          dma16(pb + (int64_t)(next / PT) * 2048 + (4 * SL) * (next % PT) + br[e] + bc[e], dst);
+        } else if constexpr (SL == 64) {
+          dma16(pb + (int64_t)next * 1024 + br[e] + bc[e], dst);
         } else {
           // an odd last tile's half of the slab again
           const uint32_t last = (uint32_t)(J.ktiles - 1 - 2 * next) * 1024;
@@ -183,6 +241,7 @@ struct CodesTile {
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
+    constexpr int KS = SL / 32;
     // Fragments of step ks of a slab: 32 k, 16 a lane half (chunk 2 ks + lg of a
     // row; TERNARY: chunk 4 lg + ks, dword ks of the weights' chunk lg).
     v4i fa[2][FI], fb[2][FJ], cj[FJ];
@@ -190,22 +249,31 @@ struct CodesTile {
     auto load = [&](int ks, v4i (&a)[FI], v4i (&b)[FJ]) {
 #pragma unroll
       for (int i = 0; i < FI; ++i) {
-        const int r = wi0 + 32 * i + lr, c = TERNARY ? 4 * lg + ks : 2 * ks + lg;
-        a[i] = *reinterpret_cast<const v4i*>(sa + kCodesRow * r + 16 * (c ^ ((r >> 1) & 7)));
+        const int r = wi0 + 32 * i + lr, c = TERNARY ? KS * lg + ks : 2 * ks + lg;
+        a[i] = *reinterpret_cast<const v4i*>(sa + SL * r + 16 * swz(r, c));
       }
 #pragma unroll
       for (int j = 0; j < FJ; ++j) {
         const int r = brow(j) + lr;
-        const int8_t* sb = sa + TI * kCodesRow + codes_b_row(TERNARY) * r;
-        if constexpr (!TERNARY)
-          b[j] = *reinterpret_cast<const v4i*>(sb + 16 * ((2 * ks + lg) ^ ((r >> 1) & 7)));
-        else if (ks == 0)
-          b[j] = *reinterpret_cast<const v4i*>(sb + 16 * (lg ^ ((r >> 3) & 1)));
+        const int8_t* sb = sa + TI * SL + kRowB * r;
+        if constexpr (!TERNARY) {
+          b[j] = *reinterpret_cast<const v4i*>(sb + 16 * swz(r, 2 * ks + lg));
+        } else if (ks == 0) {
+          if constexpr (SL == 128) {
+            b[j] = *reinterpret_cast<const v4i*>(sb + 16 * (lg ^ ((r >> 3) & 1)));
+          } else {
+            typedef int32_t v2i __attribute__((ext_vector_type(2)));
+            const v2i w = *reinterpret_cast<const v2i*>(sb + 8 * lg);
+            b[j].x = w.x;
+            b[j].y = w.y;
+          }
+        }
       }
     };
-    // Products of step ks; with ISSUE, a load of the slab that goes to `st`
-    // between any two of them.
-    auto multiply = [&](auto issue, int ks, const v4i (&a)[FI], const v4i (&b)[FJ], int8_t* st) {
+    // Products of step ks.  `mid` runs behind the first of them, which waits for the
+    // step's fragments: what it reads from LDS then has the other products' time
+    // to arrive.  With ISSUE, a load of the slab that goes to `st` between any two.
+    auto multiply = [&](auto issue, int ks, const v4i (&a)[FI], const v4i (&b)[FJ], int8_t* st, const auto& mid) {
       constexpr bool ISSUE = decltype(issue)::value;
       constexpr int P = FI * FJ;
 #pragma unroll
@@ -218,6 +286,11 @@ struct CodesTile {
 #pragma unroll
         for (int i = 0; i < FI; ++i) {
           acc[i][j] = mfma_32x32x32_i8(w, a[i], acc[i][j]);
+          if (i + j == 0) {
+            __builtin_amdgcn_sched_barrier(0);
+            mid();
+            __builtin_amdgcn_sched_barrier(0);
+          }
           if constexpr (ISSUE) {
 #pragma unroll
             for (int d = 0; d < D; ++d)
@@ -229,9 +302,9 @@ struct CodesTile {
           }
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     };
 
-    constexpr int KS = 4;
 #pragma unroll
     for (int p = 0; p < NST; ++p)
       if (p < nsl) {
@@ -243,11 +316,10 @@ struct CodesTile {
     load(0, fa[0], fb[0]);
     int buf = 0;
     // 8-bit weights of an odd number of tiles: the last slab's second half is not there
-    const int half = !TERNARY && (J.ktiles & 1) && s0 + nsl == J.slabs ? nsl - 1 : -1;
-    // A slab: its first steps, then, when its last fragments are in registers
-    // and every wave is there, its buffer is free.  The next slab's first
-    // fragments are read ahead of the last products, and the buffer refilled
-    // between them.
+    const int half = !TERNARY && SL == 128 && (J.ktiles & 1) && s0 + nsl == J.slabs ? nsl - 1 : -1;
+    // A slab.  Behind the first product of its last step its fragments are all in
+    // registers: when every wave is there, its buffer is free.  The next slab's
+    // first fragments are then read, and the buffer refilled between the products.
     auto slab = [&](auto issue, int s) {
       constexpr bool ISSUE = decltype(issue)::value;
       if constexpr (TERNARY) {
@@ -256,21 +328,22 @@ struct CodesTile {
       }
 #pragma unroll
       for (int ks = 0; ks < KS - 1; ++ks) {
-        load(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
-        __builtin_amdgcn_sched_barrier(0);  // the reads go out ahead of this step's products
-        if (ISSUE || ks < KS / 2 || s != half) multiply(std::false_type{}, ks, fa[ks & 1], fb[ks & 1], nullptr);
+        auto ahead = [&]() { load(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]); };
+        if (ISSUE || ks < KS / 2 || s != half)
+          multiply(std::false_type{}, ks, fa[ks & 1], fb[ks & 1], nullptr, ahead);
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slab's LDS reads are done
       int8_t* st = smem + buf * kStage;
-      if (ISSUE || s + 1 < nsl) {
-        wait_vm<ISSUE ? (NST - 2) * D : 0>();
-        barrier();
-        buf = buf + 1 == NST ? 0 : buf + 1;
-        sa = smem + buf * kStage;
-        load(0, fa[0], fb[0]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if (ISSUE || s != half) multiply(issue, KS - 1, fa[(KS - 1) & 1], fb[(KS - 1) & 1], st);
+      auto turn = [&]() {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slab's LDS reads are done
+        if (ISSUE || s + 1 < nsl) {
+          wait_vm<ISSUE ? (NST - 2) * D : 0>();
+          barrier();
+          buf = buf + 1 == NST ? 0 : buf + 1;
+          sa = smem + buf * kStage;
+          load(0, fa[0], fb[0]);
+        }
+      };
+      if (ISSUE || s != half) multiply(issue, KS - 1, fa[(KS - 1) & 1], fb[(KS - 1) & 1], st, turn);
     };
     int s = 0;
     for (; s + NST < nsl; ++s) slab(std::true_type{}, s);
@@ -294,20 +367,6 @@ __device__ __forceinline__ bool codes_tile_of(int l, const CodesJob& J, int* ti,
   *ti = 4 * g + t % rows;
   *tj = t / rows;
   return true;
-}
-
-// 16 sums of a 32 x 32 subtile's row as bf16 pairs pk[8] (columns 8 a + 4 lg + 0..3
-// in pk[2 a], pk[2 a + 1]) to 8 consecutive columns twice: lanes of lg = 0 get
-// columns 0-7 in pk[0..3] and 16-23 in pk[4..7], those of lg = 1 8-15 and 24-31.
-__device__ __forceinline__ void codes_rows8(uint32_t (&pk)[8]) {
-#pragma unroll
-  for (int h = 0; h < 8; h += 4)
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const auto sw = __builtin_amdgcn_permlane32_swap(pk[h + t], pk[h + 2 + t], false, false);
-      pk[h + t] = sw[0];
-      pk[h + 2 + t] = sw[1];
-    }
 }
 
 // Up to eight bf16 outputs of one row from column n on.
@@ -380,7 +439,13 @@ inline hipError_t codes_pad(const int8_t* q, int64_t m, int64_t k, int32_t ldq, 
   return hipGetLastError();
 }
 
+// Outputs of more than the eight L2 caches' 32 MB: kept there they would push out the
+// operands, and be written back at the kernel's end (8-bit 2048 x 14336 x 4096: 141
+// -> 128 us).  Rows of a wave shorter than a cache line are stored plainly.
+inline int32_t codes_past_cache(int64_t m, int64_t n) { return 2 * m * n > (int64_t(32) << 20) ? 1 : 0; }
+
 inline void set_plan(CodesJob& J, const CodesPlan& p, int32_t* part) {
+  J.past_cache = codes_past_cache(J.m, J.n);
   J.slabs = p.slabs;
   J.tiles_i = p.tiles_i;
   J.tiles_j = p.tiles_j;

@@ -1,5 +1,5 @@
 // Host-side planning of the products of int8 activations with 8-bit and with a
-// gated block's ternary weights, past 16 tokens: which tile, and in how many parts
+// gated block's ternary weights: which kernel, which tile, and in how many parts
 // the sum is split.  From the shapes alone, so that the workspace queries agree
 // with the calls.
 //
@@ -12,45 +12,103 @@
 
 namespace bl {
 
+constexpr int kCodesCus = 256;  // MI355X
+
+// ---- weights streamed once for 16 token rows (codes_rows.hpp) ----
+
+constexpr int kRowsWaves = 16;
+constexpr int kRowsLds = 80000;  // two workgroups a CU
+
+// K of a tile, and matrices (gate and up).
+constexpr int rows_tile_k(bool ternary) { return ternary ? 256 : 64; }
+constexpr int rows_mats(bool ternary) { return ternary ? 2 : 1; }
+
+// LDS of a token row of a segment.
+constexpr int rows_ldx(int seg, bool ternary) { return (seg * rows_tile_k(ternary) + 255) / 256 * 256 + 16; }
+
+// Waves of a block, and the segments of K.  Of ternary weights as many waves as
+// leave at most a workgroup a CU (gated 14336 x 4096 at 16 tokens: 224 workgroups
+// of four blocks 9.9 us, 448 of two 12.1, 896 of eight waves 15.2; at one token
+// 8.7, 10.3 and 9.1), which stage their tokens once.  8-bit weights have four times
+// the bytes a tile's tokens: eight waves a block, or 16 where that would leave CUs
+// without a workgroup (32768 x 4096 at 16 tokens: eight 29.1, four 32.9; 14336 x
+// 4096: eight 12.8, 16 16.3; 4096 x 4096: 16 7.2, eight 8.3).
+struct RowsPlan {
+  int wk, seg;
+  int64_t lds;
+};
+
+inline RowsPlan plan_rows(int64_t m, int64_t n, int64_t k, bool ternary) {
+  const int tk = rows_tile_k(ternary), rows = (int)std::min<int64_t>(m, 16);
+  const int64_t blocks = (n + 15) / 16, ktiles = (k + tk - 1) / tk;
+  RowsPlan p = {};
+  p.wk = kRowsWaves;
+  if (ternary) {
+    while (p.wk > 1 && blocks * p.wk > kCodesCus * kRowsWaves) p.wk /= 2;
+  } else if (blocks > kCodesCus) {
+    p.wk = 8;
+  }
+  const int64_t most = std::min<int64_t>(ktiles, (kRowsLds / rows - 16) / 256 * 256 / tk);
+  const int64_t segs = (ktiles + most - 1) / most;
+  p.seg = (int)((ktiles + segs - 1) / segs);  // of about one size
+  p.lds = std::max<int64_t>((int64_t)rows * rows_ldx(p.seg, ternary), (int64_t)kRowsWaves * rows_mats(ternary) * 1024);
+  return p;
+}
+
+// ---- tiles on the matrix cores (codes_gemm.hpp) ----
+
 struct CodesPlan {
-  int cfg;
+  int cfg;  // tile, or -1: codes_rows.hpp, any number of tokens, 16 at a time
   int slabs, tiles_i, tiles_j, ksplit, kspw;
 };
 
-// Tile sizes (tokens x outputs), the workgroups a CU holds of them, and, measured
-// on an MI355X: the time of a slab of a workgroup by itself on its CU and with the
-// CU full, and the time to start a tile and write its outputs (us).
+// Tile sizes (tokens x outputs), k of a slab, the workgroups a CU holds, and,
+// measured on an MI355X (us): the time of a slab where few CUs have a workgroup,
+// where each has one, and where each has all it holds; that to start a tile and
+// write its outputs.
 struct CodesConfig {
-  int ti, tj, per_cu;
-  float alone, full, put;
+  int ti, tj, slab, per_cu;
+  float few, one, full, put;
 };
-constexpr CodesConfig kW8Configs[4] = {{32, 128, 2, 0.45f, 0.48f, 2.0f},
-                                       {64, 128, 2, 0.50f, 0.70f, 2.0f},
-                                       {128, 128, 2, 0.75f, 1.25f, 3.0f},
-                                       {256, 256, 1, 1.50f, 2.00f, 4.0f}};
-constexpr CodesConfig kGatedConfigs[4] = {{32, 128, 2, 0.30f, 0.40f, 2.0f},
-                                          {64, 64, 2, 0.30f, 0.40f, 2.0f},
-                                          {128, 128, 2, 0.90f, 1.75f, 4.0f},
-                                          {256, 128, 1, 1.10f, 1.75f, 4.0f}};
-constexpr int kCodesCus = 256;  // MI355X
+constexpr CodesConfig kW8Configs[3] = {{64, 64, 64, 2, 0.156f, 0.165f, 0.31f, 1.0f},
+                                       {128, 128, 64, 2, 0.28f, 0.32f, 0.64f, 2.5f},
+                                       {256, 256, 64, 1, 0.62f, 0.85f, 0.85f, 5.0f}};
+constexpr CodesConfig kGatedConfigs[3] = {{32, 128, 128, 2, 0.31f, 0.35f, 0.60f, 1.0f},
+                                          {64, 128, 128, 2, 0.39f, 0.48f, 0.82f, 1.8f},
+                                          {128, 128, 128, 2, 0.67f, 0.85f, 1.50f, 2.5f}};
+constexpr float kCodesStartUs = 3.5f;   // a launch
+constexpr float kCodesFinishUs = 3.0f;  // one more, that adds the parts
+constexpr float kCodesBytesPerUs = 6e6f;
 
-// The tile and the parts with the smallest estimated time.
-inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t slabs, bool gated) {
+// The kernel, tile and parts with the smallest estimated time (m > 16).  Measured
+// against single choices: 8-bit 17 x 4096 x 4096 rows 7.3 us, tiles 11.1; 64 x 14336
+// x 4096 rows 36, tiles of 64 x 64 15.2, of 256 x 256 48; 2048 x 14336 x 4096 of 64 x
+// 64 289, of 128 x 128 154, of 256 x 256 121; 300 x 4096 x 14336 in two parts 45, one
+// 69, four 52.
+inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
   CodesPlan best = {};
-  float least = 0.0f;
-  for (int cfg = 0; cfg < 4; ++cfg) {
+  best.cfg = -1;
+  const RowsPlan r = plan_rows(16, n, k, gated);
+  const int64_t rtk = rows_tile_k(gated), per = kRowsWaves / r.wk;
+  const int64_t rwgs = ((n + 15) / 16 + per - 1) / per * ((m + 15) / 16), tiles = ((k + rtk - 1) / rtk + r.wk - 1) / r.wk;
+  float least = kCodesStartUs + (float)((rwgs + 2 * kCodesCus - 1) / (2 * kCodesCus)) *
+                                    (gated ? 1.6f + 2.1f * (float)tiles : 1.0f + 1.1f * (float)tiles);
+  for (int cfg = 0; cfg < 3; ++cfg) {
     const CodesConfig& C = gated ? kGatedConfigs[cfg] : kW8Configs[cfg];
-    const int64_t ti = (m + C.ti - 1) / C.ti, tj = (n + C.tj - 1) / C.tj, tiles = ti * tj;
-    for (int want = 1; want <= 16; ++want) {
-      if (want > 1 && (slabs < 4 * want || tiles * want > 4 * kCodesCus)) break;
-      const int64_t kspw = (slabs + want - 1) / want, parts = (slabs + kspw - 1) / kspw;
-      const int64_t wgs = tiles * parts, room = kCodesCus * C.per_cu;
-      const int64_t rounds = (wgs + room - 1) / room;
-      const bool full = wgs > kCodesCus;
-      float us = (float)rounds * ((float)kspw * (full ? C.full : C.alone) + C.put);
-      // one more launch, the sums written and read back
-      if (parts > 1) us += 4.0f + 8.0f * (float)parts * (float)m * (float)n * (gated ? 2.0f : 1.0f) / 5e6f;
-      if (best.slabs && us >= least) continue;
+    const int64_t ti = (m + C.ti - 1) / C.ti, tj = (n + C.tj - 1) / C.tj, slabs = (k + C.slab - 1) / C.slab;
+    const int64_t room = kCodesCus * C.per_cu;
+    // the time of a round of up to `room` tiles
+    auto round = [&](int64_t wgs, int64_t kspw) {
+      const float slab = wgs > kCodesCus ? C.full : C.few + (C.one - C.few) * (float)wgs / kCodesCus;
+      return wgs ? (float)kspw * slab + C.put : 0.0f;
+    };
+    for (int64_t want = 1; want <= 16; ++want) {
+      if (want > 1 && (slabs * C.slab < 512 * want || ti * tj * want > 4 * kCodesCus)) break;
+      const int64_t kspw = (slabs + want - 1) / want, parts = (slabs + kspw - 1) / kspw, wgs = ti * tj * parts;
+      float us = kCodesStartUs + (float)(wgs / room) * round(room, kspw) + round(wgs % room, kspw);
+      if (parts > 1)
+        us += kCodesFinishUs + 8.0f * (float)parts * (float)m * (float)n * (gated ? 2.0f : 1.0f) / kCodesBytesPerUs;
+      if (us >= least) continue;
       least = us;
       best = CodesPlan{cfg, (int)slabs, (int)ti, (int)tj, (int)parts, (int)kspw};
     }

@@ -26,16 +26,6 @@ struct RowsJob {
   int32_t seg;             // tiles of K staged at a time
 };
 
-constexpr int kRowsWaves = 16;
-constexpr int kRowsLds = 80000;  // two workgroups a CU
-
-// K of a tile, and matrices (gate and up).
-constexpr int rows_tile_k(bool ternary) { return ternary ? 256 : 64; }
-constexpr int rows_mats(bool ternary) { return ternary ? 2 : 1; }
-
-// LDS of `rows` token rows of a segment.
-inline int rows_ldx(int seg, bool ternary) { return (int)round_up(seg * rows_tile_k(ternary), 256) + 16; }
-
 // finish(token, first of four outputs, sums [matrices][4]) is called for what
 // exists of tokens and of groups of four outputs.
 template <int U, bool TERNARY, typename Finish>
@@ -46,7 +36,7 @@ __device__ __forceinline__ void codes_rows_product(const RowsJob& J, int8_t* lds
   const int blk = (int)blockIdx.x * (W / J.wk) + wave / J.wk;
   const int part = wave % J.wk;
   const int m0 = (int)blockIdx.y * 16, rows = min(16, J.m - m0);
-  const int ldx = ((J.seg * TK + 255) & ~255) + 16;
+  const int ldx = rows_ldx(J.seg, TERNARY);
   // blocks and token rows past the end read the last one: their sums are not stored
   const uint8_t* wp = J.w + (int64_t)min(blk, J.blocks - 1) * J.ktiles * (1024 * MATS) + 16 * lane;
   const int8_t* xl = lds + min(lr, rows - 1) * ldx + (TERNARY ? 64 : 16) * lg;
@@ -141,40 +131,11 @@ __device__ __forceinline__ void codes_put4(uint16_t* row, int n, int cols, uint3
   }
 }
 
-// Waves of a block, and the segments of K.  Of ternary weights as many waves as
-// leave at most a workgroup a CU (gated 14336 x 4096 at 16 tokens: 224 workgroups
-// of four blocks 9.9 us, 448 of two 12.1, 896 of eight waves 15.2; at one token
-// 8.7, 10.3 and 9.1), which stage their tokens once.  8-bit weights have four times
-// the bytes a tile's tokens: eight waves a block, or 16 where that would leave CUs
-// without a workgroup (32768 x 4096 at 16 tokens: eight 29.1, four 32.9; 14336 x
-// 4096: eight 12.8, 16 16.3; 4096 x 4096: 16 7.2, eight 8.3).
-struct RowsPlan {
-  int wk, seg;
-  size_t lds;
-};
-
-inline RowsPlan plan_rows(int64_t m, int64_t n, int64_t k, bool ternary) {
-  const int tk = rows_tile_k(ternary), rows = (int)std::min<int64_t>(m, 16);
-  const int64_t blocks = (n + 15) / 16, ktiles = (k + tk - 1) / tk;
-  RowsPlan p = {};
-  p.wk = kRowsWaves;
-  if (ternary) {
-    while (p.wk > 1 && blocks * p.wk > 256 * kRowsWaves) p.wk /= 2;
-  } else if (blocks > 256) {
-    p.wk = 8;
-  }
-  const int64_t most = std::min<int64_t>(ktiles, (kRowsLds / rows - 16) / 256 * 256 / tk);
-  const int64_t segs = (ktiles + most - 1) / most;
-  p.seg = (int)((ktiles + segs - 1) / segs);  // of about one size
-  p.lds = std::max<size_t>((size_t)rows * rows_ldx(p.seg, ternary), (size_t)kRowsWaves * rows_mats(ternary) * 1024);
-  return p;
-}
-
 template <typename Args, typename Kernel>
 hipError_t launch_rows(const Args& a, const RowsPlan& p, Kernel kernel, std::atomic<bool>* done, hipStream_t s) {
   const int per = kRowsWaves / p.wk;
   const dim3 grid((unsigned)((a.j.blocks + per - 1) / per), (unsigned)((a.j.m + 15) / 16));
-  return codes_launch(kernel, done, grid, 64 * kRowsWaves, p.lds, kRowsLds, s, a);
+  return codes_launch(kernel, done, grid, 64 * kRowsWaves, (size_t)p.lds, kRowsLds, s, a);
 }
 
 }  // namespace bl

@@ -133,7 +133,7 @@ struct GatedGemmArgs {
 };
 
 template <typename T, bool SILU>
-__global__ __launch_bounds__(64 * T::NW, 2) void gated_gemm_kernel(const GatedGemmArgs A) {
+__global__ __launch_bounds__(64 * T::NW, T::kPerSimd) void gated_gemm_kernel(const GatedGemmArgs A) {
   extern __shared__ __align__(16) int8_t smem[];
   const CodesJob& J = A.j;
   int ti, tj, kp;
@@ -156,48 +156,41 @@ __global__ __launch_bounds__(64 * T::NW, 2) void gated_gemm_kernel(const GatedGe
     }
     return;
   }
-  const bool wide = (J.n & 7) == 0;  // output rows are 16-byte aligned
+  codes_gemm::barrier();
+  typename T::Rows rows(smem + T::wave() * T::Rows::kBytes);
   const float gs = load_f32_vmem(A.gate_scale), us = load_f32_vmem(A.up_scale);
 #pragma unroll
   for (int i = 0; i < T::FI; ++i) {
-    const int m = m0 + 32 * i;
-    const float xs = *G(A.x_scale + min(m, J.m - 1));
+    const float xs = *G(A.x_scale + min(m0 + 32 * i, J.m - 1));
     const RowDiv dg = row_div_setup(xs * gs), du = row_div_setup(xs * us);
-    const int64_t at = (int64_t)m * J.n;
+    auto put = [&](const auto& value) {
 #pragma unroll
-    for (int j = 0; j < FO; ++j) {
-      uint32_t pa[8], pg[8], pu[8];
+      for (int j = 0; j < FO; ++j)
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        float g[2], u[2], a[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          g[e] = row_div((float)acc[i][j][2 * h + e] * 0.015625f, dg);
-          u[e] = row_div((float)acc[i][j + FO][2 * h + e] * 0.015625f, du);
-          a[e] = gate_value<SILU>(g[e], u[e]);
-        }
-        pa[h] = pack_bf16x2(a[0], a[1]);
-        if (A.g) {
-          pg[h] = pack_bf16x2(g[0], g[1]);
-          pu[h] = pack_bf16x2(u[0], u[1]);
-        }
-      }
-      codes_rows8(pa);
-      if (A.g) {
-        codes_rows8(pg);
-        codes_rows8(pu);
-      }
-      if (m >= J.m) continue;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int n = n0 + 32 * j + 16 * h + 8 * lg;
-        codes_put8(A.a + at, n, J.n, wide, pa + 4 * h);
-        if (A.g) {
-          codes_put8(A.g + at, n, J.n, wide, pg + 4 * h);
-          codes_put8(A.u + at, n, J.n, wide, pu + 4 * h);
-        }
-      }
-    }
+        for (int a = 0; a < 4; ++a)
+          rows.put(lr, 32 * j + 8 * a + 4 * lg, pack_bf16x2(value(j, 4 * a), value(j, 4 * a + 1)),
+                   pack_bf16x2(value(j, 4 * a + 2), value(j, 4 * a + 3)));
+    };
+    // g and u of subtile j's sum r
+    auto outputs = [&](auto fastc) {
+      auto quotient = [&](int32_t sum, const RowDiv& d) {
+        const float v = (float)sum * 0.015625f;
+        return decltype(fastc)::value ? row_div_fast(v, d.d, d.y) : v / d.d;
+      };
+      auto g = [&](int j, int r) { return quotient(acc[i][j][r], dg); };
+      auto u = [&](int j, int r) { return quotient(acc[i][j + FO][r], du); };
+      put([&](int j, int r) { return gate_value<SILU>(g(j, r), u(j, r)); });
+      rows.store(A.a, m0 - lr + 32 * i, n0, J.m, J.n, J.past_cache);
+      if (!A.g) return;
+      put(g);
+      rows.store(A.g, m0 - lr + 32 * i, n0, J.m, J.n, J.past_cache);
+      put(u);
+      rows.store(A.u, m0 - lr + 32 * i, n0, J.m, J.n, J.past_cache);
+    };
+    if (__all(dg.fast && du.fast))  // the rows go out together
+      outputs(std::true_type{});
+    else
+      outputs(std::false_type{});
   }
 }
 
@@ -239,9 +232,8 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(const GatedGemmArgs A
   }
 }
 
-using GatedTile256 = CodesTile<256, 256, 2, 4, 3, true>;
 using GatedTile128 = CodesTile<128, 256, 2, 2, 3, true>;
-using GatedTile64 = CodesTile<64, 128, 2, 2, 6, true>;
+using GatedTile64 = CodesTile<64, 256, 1, 4, 4, true>;
 using GatedTile32 = CodesTile<32, 256, 1, 4, 6, true>;
 
 template <typename T, bool SILU>
@@ -253,8 +245,7 @@ hipError_t gated_gemm(const GatedGemmArgs& a, hipStream_t s) {
 
 template <bool SILU>
 hipError_t launch_gated_gemm(const GatedGemmArgs& a, int cfg, hipStream_t s) {
-  const hipError_t e = cfg == 3   ? gated_gemm<GatedTile256, SILU>(a, s)
-                       : cfg == 2 ? gated_gemm<GatedTile128, SILU>(a, s)
+  const hipError_t e = cfg == 2   ? gated_gemm<GatedTile128, SILU>(a, s)
                        : cfg == 1 ? gated_gemm<GatedTile64, SILU>(a, s)
                                   : gated_gemm<GatedTile32, SILU>(a, s);
   if (e != hipSuccess || a.j.ksplit == 1) return e;
@@ -271,8 +262,9 @@ struct GatedLayout {
 
 GatedLayout gated_layout(int64_t m, int64_t n, int64_t k) {
   GatedLayout L = {};
-  if (m <= 16) return L;
-  L.plan = plan_codes(m, n, (k + 127) / 128, true);
+  L.plan.cfg = -1;
+  if (m > 16) L.plan = plan_codes(m, n, k, true);
+  if (L.plan.cfg < 0) return L;
   L.ldq = (int32_t)round_up(k, 16);
   if (k % 16) L.total = align256((size_t)m * L.ldq);
   L.part = L.total;
@@ -294,8 +286,8 @@ hipError_t launch_gated_weights(const uint8_t* gate, bool gate_tiled, const uint
 size_t gated_forward_bytes(int64_t m, int64_t n, int64_t k) { return gated_layout(m, n, k).total; }
 
 hipError_t launch_gated_forward(const GatedArgs& b, char* ws, hipStream_t s) {
-  if (b.m > 16) {
-    const GatedLayout L = gated_layout(b.m, b.n, b.k);
+  const GatedLayout L = gated_layout(b.m, b.n, b.k);
+  if (L.plan.cfg >= 0) {
     GatedGemmArgs a = {};
     CodesJob& J = a.j;
     J.q = b.q;

@@ -122,7 +122,7 @@ struct W8GemmArgs {
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 template <typename T>
-__global__ __launch_bounds__(64 * T::NW, 2) void w8_gemm_kernel(const W8GemmArgs A) {
+__global__ __launch_bounds__(64 * T::NW, T::kPerSimd) void w8_gemm_kernel(const W8GemmArgs A) {
   extern __shared__ __align__(16) int8_t smem[];
   const CodesJob& J = A.j;
   int ti, tj, kp;
@@ -142,48 +142,52 @@ __global__ __launch_bounds__(64 * T::NW, 2) void w8_gemm_kernel(const W8GemmArgs
     }
     return;
   }
-  const bool wide = (J.n & 7) == 0;  // output rows are 16-byte aligned
-  float xs[T::FI], y[T::FI];
+  codes_gemm::barrier();
+  typename T::Rows rows(smem + T::wave() * T::Rows::kBytes);
+  // scales and bias of the lane's columns
+  float s[T::FJ][16];
+  uint32_t bias[T::FJ][8];
+  bool fast = true;
 #pragma unroll
-  for (int i = 0; i < T::FI; ++i) {
-    xs[i] = *G(A.x_scale + min(m0 + 32 * i, J.m - 1));
-    y[i] = 1.0f / xs[i];
-  }
+  for (int j = 0; j < T::FJ; ++j)
 #pragma unroll
-  for (int j = 0; j < T::FJ; ++j) {
-    float s[16];  // scales of the lane's columns
-    bool fast = true;
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < 4; ++a) {
+      const int n = n0 + 32 * j + 8 * a + 4 * lg;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[4 * a + e] = *G(A.scale + min(n0 + 32 * j + 8 * a + 4 * lg + e, J.n - 1));
-        fast = fast && w8_fast_scale(s[4 * a + e]);
+        s[j][4 * a + e] = *G(A.scale + min(n + e, J.n - 1));
+        fast = fast && w8_fast_scale(s[j][4 * a + e]);
       }
+      if (A.bias)
 #pragma unroll
-    for (int i = 0; i < T::FI; ++i) {
-      const int m = m0 + 32 * i;
-      const bool f = fast && w8_fast_row(xs[i]);
-      uint32_t pk[8];
-#pragma unroll
-      for (int h = 0; h < 8; ++h)
-        pk[h] = pack_bf16x2(w8_value(acc[i][j][2 * h], s[2 * h], xs[i], y[i], f),
-                            w8_value(acc[i][j][2 * h + 1], s[2 * h + 1], xs[i], y[i], f));
-      codes_rows8(pk);
-      if (m >= J.m) continue;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int n = n0 + 32 * j + 16 * h + 8 * lg;
-        if (A.bias) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t b0 = *G(A.bias + min(n + 2 * e, J.n - 1)), b1 = *G(A.bias + min(n + 2 * e + 1, J.n - 1));
-            pk[4 * h + e] = add_bf16x2(pk[4 * h + e], b0 | (b1 << 16));
-          }
-        }
-        codes_put8(A.y + (int64_t)m * J.n, n, J.n, wide, pk + 4 * h);
-      }
+        for (int e = 0; e < 2; ++e)
+          bias[j][2 * a + e] = (uint32_t)*G(A.bias + min(n + 2 * e, J.n - 1)) |
+                               ((uint32_t)*G(A.bias + min(n + 2 * e + 1, J.n - 1)) << 16);
     }
+#pragma unroll
+  for (int i = 0; i < T::FI; ++i) {
+    const float xs = *G(A.x_scale + min(m0 + 32 * i, J.m - 1)), y = 1.0f / xs;
+    auto values = [&](auto fastc) {
+#pragma unroll
+      for (int j = 0; j < T::FJ; ++j)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          uint32_t w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 4 * a + 2 * e;
+            w[e] = pack_bf16x2(w8_value(acc[i][j][r], s[j][r], xs, y, decltype(fastc)::value),
+                               w8_value(acc[i][j][r + 1], s[j][r + 1], xs, y, decltype(fastc)::value));
+            if (A.bias) w[e] = add_bf16x2(w[e], bias[j][2 * a + e]);
+          }
+          rows.put(lr, 32 * j + 8 * a + 4 * lg, w[0], w[1]);
+        }
+    };
+    if (__all(fast && w8_fast_row(xs)))
+      values(std::true_type{});
+    else
+      values(std::false_type{});
+    rows.store(A.y, m0 - lr + 32 * i, n0, J.m, J.n, J.past_cache);
   }
 }
 
@@ -218,10 +222,9 @@ __global__ __launch_bounds__(256) void w8_finish_kernel(const W8GemmArgs A, int6
   codes_put8(A.y + m * J.n, n, J.n, (J.n & 7) == 0, w);
 }
 
-using W8Tile256 = CodesTile<256, 256, 2, 4, 2, false>;
-using W8Tile128 = CodesTile<128, 128, 2, 2, 2, false>;
-using W8Tile64 = CodesTile<64, 128, 2, 2, 3, false>;
-using W8Tile32 = CodesTile<32, 128, 1, 4, 4, false>;
+using W8Tile256 = CodesTile<256, 256, 2, 4, 4, false, 64>;
+using W8Tile128 = CodesTile<128, 128, 2, 2, 5, false, 64>;
+using W8Tile64 = CodesTile<64, 64, 2, 2, 8, false, 64>;
 
 template <typename T>
 hipError_t w8_gemm(const W8GemmArgs& a, hipStream_t s) {
@@ -238,8 +241,9 @@ struct W8Layout {
 
 W8Layout w8_layout(int64_t m, int64_t n, int64_t k) {
   W8Layout L = {};
-  if (m <= 16) return L;
-  L.plan = plan_codes(m, n, (k + 127) / 128, false);
+  L.plan.cfg = -1;
+  if (m > 16) L.plan = plan_codes(m, n, k, false);
+  if (L.plan.cfg < 0) return L;
   L.ldq = (int32_t)round_up(k, 16);
   if (k % 16) L.total = align256((size_t)m * L.ldq);
   L.part = L.total;
@@ -265,8 +269,8 @@ hipError_t launch_w8_unpack(const int8_t* codes, const float* scale, int64_t n, 
 size_t w8_forward_bytes(int64_t m, int64_t n, int64_t k) { return w8_layout(m, n, k).total; }
 
 hipError_t launch_w8_forward(const W8Args& b, char* ws, hipStream_t s) {
-  if (b.m > 16) {
-    const W8Layout L = w8_layout(b.m, b.n, b.k);
+  const W8Layout L = w8_layout(b.m, b.n, b.k);
+  if (L.plan.cfg >= 0) {
     W8GemmArgs a = {};
     CodesJob& J = a.j;
     J.q = b.q;
@@ -288,10 +292,9 @@ hipError_t launch_w8_forward(const W8Args& b, char* ws, hipStream_t s) {
       if (e != hipSuccess) return e;
       J.q = reinterpret_cast<const int8_t*>(ws);
     }
-    e = L.plan.cfg == 3   ? w8_gemm<W8Tile256>(a, s)
-        : L.plan.cfg == 2 ? w8_gemm<W8Tile128>(a, s)
-        : L.plan.cfg == 1 ? w8_gemm<W8Tile64>(a, s)
-                          : w8_gemm<W8Tile32>(a, s);
+    e = L.plan.cfg == 2   ? w8_gemm<W8Tile256>(a, s)
+        : L.plan.cfg == 1 ? w8_gemm<W8Tile128>(a, s)
+                          : w8_gemm<W8Tile64>(a, s);
     if (e != hipSuccess || J.ksplit == 1) return e;
     const int64_t total = b.m * ((b.n + 7) / 8);
     w8_finish_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, total);
