@@ -285,6 +285,35 @@ __device__ __forceinline__ void prepare_weights(const PrepArgs& A, const uint8_t
 // bitlinear_gated_backward states them.  Of relu2 every product is exact in
 // fp32 (three significands of eight bits); of silu they are made in fp64: a
 // last bit of fp32 at a border of bf16 would be a whole step of the operand.
+
+// exp(-x) for 0 <= x, to 2^-40 of itself: 2^k times the Taylor sum of the rest, of at
+// most ln(2) / 2 (what the sum leaves out: 0.3466^11 / 11!).  Past 745 it is 0.
+__device__ __forceinline__ double exp_minus(double x) {
+  x = fmin(x, 800.0);
+  const double k = rint(x * -1.4426950408889634);
+  double r = fma(k, -0.6931471805599453, -x);
+  r = fma(k, -2.3190468138462996e-17, r);  // ln(2) beyond its first 53 bits
+  double p = 1.0 / 3628800.0;
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, (int)k);
+}
+
+// 1 / d for 1 <= d <= 2: the hardware's reciprocal (some 2^-22) and one step of
+// Newton's, which squares its error.
+__device__ __forceinline__ double reciprocal(double d) {
+  const double y = __builtin_amdgcn_rcp(d);
+  return fma(y, fma(-d, y, 1.0), y);
+}
+
 template <bool SILU>
 __device__ __forceinline__ void gate_grads(float da, float g, float u, float* dg, float* du) {
   if constexpr (!SILU) {
@@ -292,9 +321,9 @@ __device__ __forceinline__ void gate_grads(float da, float g, float u, float* dg
     *dg = 2.0f * ((da * u) * r);
     *du = (da * r) * r;
   } else {
-    const double x = g, e = exp(-fabs(x)), p = 1.0 / (1.0 + e);
+    const double x = g, e = exp_minus(fabs(x)), p = reciprocal(1.0 + e);
     const double s = x >= 0.0 ? p : e * p, t = x >= 0.0 ? e * p : p;  // sigmoid(g), sigmoid(-g)
-    *dg = (float)(((double)da * u) * (s * (1.0 + x * t)));
+    *dg = (float)(((double)da * u) * (s * fma(x, t, 1.0)));
     *du = (float)((double)da * (x * s));
   }
 }
