@@ -328,50 +328,104 @@ __device__ __forceinline__ void gate_grads(float da, float g, float u, float* dg
   }
 }
 
-// As prepare_dy, dg and du made of the tokens' da, g and u on the way.
-template <bool SILU>
+// Eight rows of C columns (a dword two) of x [m][cols] from (m0, n) on; what lies
+// outside is zeros.
+template <int C>
+__device__ __forceinline__ void load_rows(const uint16_t* __restrict__ x, int64_t m, int64_t cols, int64_t m0,
+                                          int64_t n, uint32_t (&r)[8][C / 2]) {
+  typedef uint32_t vec __attribute__((ext_vector_type(C / 2 > 1 ? C / 2 : 2), aligned(2)));
+  typedef uint32_t one __attribute__((aligned(2)));
+  const int mv = (int)min((int64_t)8, m - m0);    // rows that exist (may be <= 0)
+  const int nv = (int)min((int64_t)C, cols - n);  // columns
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // missing rows read the last one
+    const uint16_t* p = x + min(m0 + i, m - 1) * cols + n;
+    if (nv >= C) {
+      if constexpr (C == 2) {
+        r[i][0] = *G(reinterpret_cast<const one*>(p));
+      } else {
+        const vec v = *G(reinterpret_cast<const vec*>(p));
+#pragma unroll
+        for (int e = 0; e < C / 2; ++e) r[i][e] = v[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < C / 2; ++e) {
+        r[i][e] = 2 * e < nv ? (uint32_t)*G(p + 2 * e) : 0u;
+        if (2 * e + 1 < nv) r[i][e] |= (uint32_t)*G(p + 2 * e + 1) << 16;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i >= mv)
+#pragma unroll
+      for (int e = 0; e < C / 2; ++e) r[i][e] = 0u;
+}
+
+// As prepare_dy, dg and du made of the tokens' da, g and u on the way; C columns a
+// thread, 32 C a workgroup.
+template <bool SILU, int C>
 __device__ __forceinline__ void prepare_gated(const PrepArgs& A, int wg) {
-  const int cols = (int)((A.n + 255) >> 8);
-  const int64_t ms = wg / cols, n0 = (int64_t)(wg - (int)ms * cols) * 256;
+  const int cols = (int)((A.n + 32 * C - 1) / (32 * C));
+  const int64_t ms = wg / cols, n0 = (int64_t)(wg - (int)ms * cols) * (32 * C);
   const int mi = threadIdx.x & 7, ni = threadIdx.x >> 3;
-  const int64_t m0 = ms * 64 + 8 * mi, n = n0 + 8 * ni;
+  const int64_t m0 = ms * 64 + 8 * mi, n = n0 + C * ni;
   const int mv = (int)min((int64_t)8, A.m - m0);  // rows of the eight that exist (may be <= 0)
-  v4i rg[8], ru[8];
+  uint32_t rg[8][C / 2], ru[8][C / 2];
   {
-    v4i rd[8];
-    load_dy8(A.dy, A.m, A.n, m0, n, rd);
-    load_dy8(A.g, A.m, A.n, m0, n, rg);
-    load_dy8(A.u, A.m, A.n, m0, n, ru);
+    uint32_t rd[8][C / 2];
+    load_rows<C>(A.dy, A.m, A.n, m0, n, rd);
+    load_rows<C>(A.g, A.m, A.n, m0, n, rg);
+    load_rows<C>(A.u, A.m, A.n, m0, n, ru);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t d = (uint32_t)rd[i][e], g = (uint32_t)rg[i][e], u = (uint32_t)ru[i][e];
+      for (int e = 0; e < C / 2; ++e) {
+        const uint32_t d = rd[i][e], g = rg[i][e], u = ru[i][e];
         float g0, g1, u0, u1;
         gate_grads<SILU>(__uint_as_float(d << 16), __uint_as_float(g << 16), __uint_as_float(u << 16), &g0, &u0);
         gate_grads<SILU>(__uint_as_float(d & 0xFFFF0000u), __uint_as_float(g & 0xFFFF0000u),
                          __uint_as_float(u & 0xFFFF0000u), &g1, &u1);
-        rg[i][e] = (int32_t)pack_bf16x2(g0, g1);
-        ru[i][e] = (int32_t)pack_bf16x2(u0, u1);
+        rg[i][e] = pack_bf16x2(g0, g1);
+        ru[i][e] = pack_bf16x2(u0, u1);
       }
   }
+  typedef uint32_t vec __attribute__((ext_vector_type(C / 2 > 1 ? C / 2 : 2)));
+  auto row = [](const uint32_t(&r)[C / 2], uint16_t* d) {
+    if constexpr (C == 2) {
+      *G(reinterpret_cast<uint32_t*>(d)) = r[0];
+    } else {
+      vec v;
+#pragma unroll
+      for (int e = 0; e < C / 2; ++e) v[e] = r[e];
+      *G(reinterpret_cast<vec*>(d)) = v;
+    }
+  };
   if (A.dys && n < ((A.n + 63) & ~(int64_t)63)) {
     const int64_t ns = (A.n + 63) >> 6;
     uint16_t* d = A.dys + ((n >> 6) * A.m + m0) * 64 + (n & 63);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < mv) {
-        *G(reinterpret_cast<v4i*>(d + 64 * i)) = rg[i];
-        *G(reinterpret_cast<v4i*>(d + ns * A.m * 64 + 64 * i)) = ru[i];
+        row(rg[i], d + 64 * i);
+        row(ru[i], d + ns * A.m * 64 + 64 * i);
       }
   }
   if (A.dyt) {
+    auto column = [](const uint32_t(&r)[8][C / 2], int j) {
+      v4i o;
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        o[p] = (int32_t)__builtin_amdgcn_perm(r[2 * p + 1][j >> 1], r[2 * p][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+      return o;
+    };
     uint16_t* d = A.dyt + (ms * 2 * A.n + n) * 64 + 8 * mi;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < C; ++j)
       if (n + j < A.n) {
-        *G(reinterpret_cast<v4i*>(d + 64 * j)) = column8(rg, j);
-        *G(reinterpret_cast<v4i*>(d + (A.n + j) * 64)) = column8(ru, j);
+        *G(reinterpret_cast<v4i*>(d + 64 * j)) = column(rg, j);
+        *G(reinterpret_cast<v4i*>(d + (A.n + j) * 64)) = column(ru, j);
       }
   }
 }
@@ -387,7 +441,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(const PrepArgs A) {
     prepare_dy(A, wg);
 }
 
-template <bool SILU>
+template <bool SILU, int C>
 __global__ __launch_bounds__(256) void prepare_gated_kernel(const PrepArgs A) {
   const int wg = blockIdx.x;
   if (wg >= A.begin_up)
@@ -397,7 +451,7 @@ __global__ __launch_bounds__(256) void prepare_gated_kernel(const PrepArgs A) {
   else if (wg >= A.begin[1])
     prepare_xhat(A, wg - A.begin[1]);
   else
-    prepare_gated<SILU>(A, wg);
+    prepare_gated<SILU, C>(A, wg);
 }
 
 // ---------------------------------------------------------------------------
@@ -728,6 +782,138 @@ __device__ __forceinline__ void gemm_tile(const GemmJob& J, int ti, int tj, int 
   }
 }
 
+// A tile of 64 x 64 computed by each of four waves over every fourth slab, from a
+// ring of the wave's own: no wave waits for another until their sums are joined, in
+// order.  A tile by itself takes a quarter of the steps one after the other, and an
+// operand read from LDS serves four products instead of two (slabs of a gated
+// block's small products, a tile by itself: 0.36 us each as above).
+constexpr int kDeepWaves = 1, kDeepWavesC = 2;  // slabs of a wave's ring
+constexpr int kWavesPitch = 4 * 64 + 16;        // bytes of a row of 64 sums
+constexpr size_t kLdsWaves = std::max({4 * kDeepWaves * stage_bytes(64, 64, false),
+                                       4 * kDeepWavesC * stage_bytes(64, 64, true), 4 * 64 * kWavesPitch});
+
+template <bool CODES>
+__device__ __forceinline__ void gemm_tile_waves(const GemmJob& J, int ti, int tj, int kp, int8_t* smem) {
+  constexpr int T = 64, NW = 4, NST = CODES ? kDeepWavesC : kDeepWaves, KS = kSlab / 16;
+  constexpr int kStage = stage_bytes(T, T, CODES);
+  constexpr int DA = T / 8, DB = CODES ? 1 : T / 8, D = DA + DB;
+  static_assert(NST * D < 64, "vmcnt range");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int lr = lane & 31, lg = lane >> 5;
+  const int i0 = ti * T, j0 = tj * T;
+  const int s0 = kp * J.kspw, s1 = min(J.slabs, s0 + J.kspw);
+  const int first = s0 + wave, nsl = first < s1 ? (s1 - first + NW - 1) / NW : 0;  // this wave's slabs
+  uint32_t oa[DA], ob[DB];
+#pragma unroll
+  for (int i = 0; i < DA; ++i) {
+    const int pos = i * 64 + lane, r = pos >> 3;
+    oa[i] = (uint32_t)min(r, J.ra - 1 - i0) * (uint32_t)J.a_row + 16 * ((pos & 7) ^ ((r >> 1) & 7));
+  }
+#pragma unroll
+  for (int i = 0; i < DB; ++i) {
+    const int pos = i * 64 + lane, r = CODES ? pos : pos >> 3;
+    ob[i] = (uint32_t)min(j0 + r, J.rb - 1) * (CODES ? kCodes : kRow) + (CODES ? 0 : 16 * ((pos & 7) ^ ((r >> 1) & 7)));
+  }
+  const int64_t step_b = (int64_t)J.rb * (CODES ? kCodes : kRow);
+  const uint8_t *pa = J.a + first * J.a_slab + i0 * J.a_row, *pb = J.b + first * step_b;
+  int8_t* ring = smem + wave * NST * kStage;
+  auto issue = [&](int8_t* st) {
+#pragma unroll
+    for (int d = 0; d < DA; ++d) dma16(pa + oa[d], st + d * 1024);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) dma16(pb + ob[d], st + T * kRow + d * 1024);
+    pa += NW * J.a_slab;
+    pb += NW * step_b;
+  };
+  v16f acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  const Expand expand;
+#pragma unroll
+  for (int p = 0; p < NST; ++p)
+    if (p < nsl) issue(ring + p * kStage);
+  int buf = 0;
+  bool gate = CODES && first < J.split;  // the sum so far is the gate's
+  auto to_up = [&]() {                   // (see gemm_tile)
+    if (!CODES || !gate) return;
+    gate = false;
+    const float f = load_f32_vmem(J.scale) / load_f32_vmem(J.scale_gate);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] *= f;
+  };
+  for (int s = 0; s < nsl; ++s) {
+    if (first + NW * s >= J.split) to_up();
+    const int8_t* sa = ring + buf * kStage;
+    wait_slabs<D, NST - 1>(min(nsl - 1 - s, NST - 1));
+    asm volatile("" ::: "memory");  // the reads stay behind the wait
+    v4i fa[KS][2], fb[KS][2], cj[2];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 32 * i + lr, c = 16 * ((2 * ks + lg) ^ ((r >> 1) & 7));
+        fa[ks][i] = *reinterpret_cast<const v4i*>(sa + kRow * r + c);
+        if constexpr (!CODES) fb[ks][i] = *reinterpret_cast<const v4i*>(sa + T * kRow + kRow * r + c);
+      }
+    if constexpr (CODES) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) cj[j] = *reinterpret_cast<const v4i*>(sa + T * kRow + kCodes * (32 * j + lr));
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slab is in registers
+    if (s + NST < nsl) issue(ring + buf * kStage);
+    buf = buf + 1 == NST ? 0 : buf + 1;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v4i w;
+        if constexpr (CODES)
+          w = expand((uint32_t)cj[j][ks] << (8 - 8 * lg));  // the lane half's eight c
+        else
+          w = fb[ks][j];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i][j] = mfma_32x32x16(w, fa[ks][i], acc[i][j]);
+      }
+  }
+  to_up();
+  // Sums in LDS as rows of 64 (16 bytes off: rows start at distinct banks), one
+  // image a wave; then whole rows of their sum, four columns a lane.
+  constexpr int kPitch = kWavesPitch;
+  barrier();
+  int8_t* mine = smem + wave * T * kPitch;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<v4f*>(mine + (32 * i + lr) * kPitch + 4 * (32 * j + 8 * e + 4 * lg)) =
+            v4f{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+  const float sc = !J.cf ? load_f32_vmem(J.scale) : 1.0f;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = 16 * wave + 4 * q + (lane >> 4), col = 4 * (lane & 15);
+    const int8_t* at = smem + row * kPitch + 4 * col;
+    v4f v = *reinterpret_cast<const v4f*>(at);
+#pragma unroll
+    for (int w = 1; w < NW; ++w) v += *reinterpret_cast<const v4f*>(at + w * T * kPitch);
+    const int r = i0 + row, c = j0 + col;
+    if (r >= J.ra || c >= J.rb) continue;
+    const int64_t o = (int64_t)r * J.rb + c;
+    if (J.ksplit > 1)
+      *G(reinterpret_cast<v4f*>(J.part + (int64_t)kp * J.ra * J.rb + o)) = v;
+    else
+      put4<true>(J, r, o, v, sc);
+  }
+}
+
 // Workgroups go to the 8 XCDs round-robin and each has its own L2, so each XCD
 // takes one contiguous share of a job's tiles, walked in groups of up to four
 // tile rows so that neighbours in time share operands both ways.
@@ -764,7 +950,7 @@ constexpr int ring_bytes(int t, int deep, int deepc) {
 }
 constexpr size_t kLdsSmall = std::max(ring_bytes(64, kDeep64, kDeep64c), ring_bytes(128, kDeep128, kDeep128c));
 constexpr size_t kLdsBig = ring_bytes(256, kDeep256, kDeep256c);
-static_assert(2 * kLdsSmall <= 160 * 1024 && kLdsBig <= 160 * 1024, "LDS of a CU");
+static_assert(kLdsWaves <= kLdsSmall && 2 * kLdsSmall <= 160 * 1024 && kLdsBig <= 160 * 1024, "LDS of a CU");
 
 template <bool BIG, bool GATED>
 __global__ __launch_bounds__(BIG ? 512 : 256, 2) void gemm_kernel(const GemmArgs A) {
@@ -792,6 +978,11 @@ __global__ __launch_bounds__(BIG ? 512 : 256, 2) void gemm_kernel(const GemmArgs
       gemm_tile<128, 128, 2, 2, kDeep128c, true, GATED>(J, ti, tj, kp, smem);
     else
       gemm_tile<128, 128, 2, 2, kDeep128, false, GATED>(J, ti, tj, kp, smem);
+  } else if constexpr (GATED) {
+    if (J.codes)
+      gemm_tile_waves<true>(J, ti, tj, kp, smem);
+    else
+      gemm_tile_waves<false>(J, ti, tj, kp, smem);
   } else {
     if (J.codes)
       gemm_tile<64, 64, 2, 2, kDeep64c, true, GATED>(J, ti, tj, kp, smem);
@@ -1262,6 +1453,10 @@ size_t gated_backward_bytes(int64_t m, int64_t n, int64_t k, bool dx, bool dw) {
   return layout(m, n, k, dx, dw, true).total;
 }
 
+// Columns that a thread takes of dg and du: eight (whole pieces of memory both
+// ways), or two where eight would leave CUs without a workgroup.
+static int gated_columns(int64_t ms, int64_t n) { return ms * ((n + 255) / 256) >= 256 ? 8 : 2; }
+
 // Two launches (three where a product's sum is split): operands, products.
 hipError_t launch_gated_backward(const GatedBackwardArgs& b, char* ws, size_t ws_bytes, hipStream_t s) {
   const bool dx = b.dx != nullptr, dw = b.dw_gate != nullptr;
@@ -1287,17 +1482,25 @@ hipError_t launch_gated_backward(const GatedBackwardArgs& b, char* ws, size_t ws
   pa.packed_up = b.up;
   pa.tiled_up = b.up_tiled ? 1 : 0;
   pa.ut = reinterpret_cast<uint8_t*>(ws + L.ut);
-  int64_t wgs = ms * ((b.n + 255) / 256);
+  const int columns = gated_columns(ms, b.n);
+  int64_t wgs = ms * ((b.n + 32 * columns - 1) / (32 * columns));
   pa.begin[1] = (int32_t)wgs;
   if (dw) wgs += ms * ((b.k + 255) / 256);
   pa.begin[2] = (int32_t)wgs;
   if (dx) wgs += ns * ((b.k + 1023) / 1024);
   pa.begin_up = (int32_t)wgs;
   if (dx) wgs += ns * ((b.k + 1023) / 1024);
+  auto prepare = [&](auto silu) {
+    constexpr bool S = decltype(silu)::value;
+    if (columns == 8)
+      prepare_gated_kernel<S, 8><<<(unsigned)wgs, 256, 0, s>>>(pa);
+    else
+      prepare_gated_kernel<S, 2><<<(unsigned)wgs, 256, 0, s>>>(pa);
+  };
   if (b.silu)
-    prepare_gated_kernel<true><<<(unsigned)wgs, 256, 0, s>>>(pa);
+    prepare(std::true_type{});
   else
-    prepare_gated_kernel<false><<<(unsigned)wgs, 256, 0, s>>>(pa);
+    prepare(std::false_type{});
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
