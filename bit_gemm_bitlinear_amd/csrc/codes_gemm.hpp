@@ -397,18 +397,22 @@ __device__ __forceinline__ void codes_put_part(int32_t* row, int n0, int cols, c
   }
 }
 
-// Adds eight columns' sums of the parts, in order (`left`: columns that exist).
+// Adds eight columns' sums of the parts, in order (`left`: columns that exist);
+// four parts' loads at a time.
 __device__ __forceinline__ void codes_add_parts(const int32_t* src, int64_t slice, int ksplit, int left, bool wide,
                                                 int32_t (&v)[8]) {
   if (wide && left >= 8) {
-    for (int p = 0; p < ksplit; ++p) {
-      const v4i lo = *G(reinterpret_cast<const v4i*>(src + p * slice));
-      const v4i hi = *G(reinterpret_cast<const v4i*>(src + p * slice + 4));
+    for (int p = 0; p < ksplit; p += 4) {
+      v4i t[4][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] += lo[e];
-        v[4 + e] += hi[e];
-      }
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          t[u][h] = p + u < ksplit ? *G(reinterpret_cast<const v4i*>(src + (p + u) * slice + 4 * h)) : v4i{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += t[u][e >> 2][e & 3];
     }
   } else {
     for (int p = 0; p < ksplit; ++p)
@@ -422,20 +426,20 @@ __device__ __forceinline__ void codes_add_parts(const int32_t* src, int64_t slic
 // (K rounded up to 16, the rest zeros): 16 bytes a thread.
 static __global__ __launch_bounds__(256) void codes_pad_kernel(const int8_t* __restrict__ q, int64_t total,
                                                                 int32_t k, int32_t ldq, int8_t* __restrict__ out) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= total) return;
   const int cpr = ldq >> 4;
-  const int64_t m = id / cpr;
-  const int c = 16 * (int)(id - m * cpr);
-  v4i v;
+  for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+    const int64_t m = id / cpr;
+    const int c = 16 * (int)(id - m * cpr);
+    v4i v;
 #pragma unroll
-  for (int d = 0; d < 4; ++d) v[d] = c + 4 * d < k ? *G(reinterpret_cast<const int32_t*>(q + m * k + c + 4 * d)) : 0;
-  *G(reinterpret_cast<v4i*>(out + 16 * id)) = v;
+    for (int d = 0; d < 4; ++d) v[d] = c + 4 * d < k ? *G(reinterpret_cast<const int32_t*>(q + m * k + c + 4 * d)) : 0;
+    *G(reinterpret_cast<v4i*>(out + 16 * id)) = v;
+  }
 }
 
 inline hipError_t codes_pad(const int8_t* q, int64_t m, int64_t k, int32_t ldq, int8_t* out, hipStream_t s) {
-  const int64_t total = m * (ldq >> 4);
-  codes_pad_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(q, total, (int32_t)k, ldq, out);
+  const int64_t total = m * (ldq >> 4), grid = (total + 255) / 256;
+  codes_pad_kernel<<<(unsigned)(grid < 65536 ? grid : 65536), 256, 0, s>>>(q, total, (int32_t)k, ldq, out);
   return hipGetLastError();
 }
 

@@ -1,13 +1,12 @@
 // extern "C" entry points declared in include/bitlinear_layer.h and
-// include/bitlinear_ffn.h: host-side argument validation and dispatch.  As in abi.hip, no entry point allocates,
-// frees or synchronizes, and every argument is checked before anything is
-// enqueued.
+// include/bitlinear_ffn.h: host-side argument validation and dispatch.  As in
+// abi.hip, no entry point allocates device memory, frees any or synchronizes, and
+// every argument is checked before anything is enqueued.
 #include "../../include/bitlinear_ffn.h"
 
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 #include <initializer_list>
 #include <new>
 #include <vector>
@@ -30,9 +29,10 @@ constexpr int64_t kMaxBwdTiles = int64_t(1) << 22;  // 128 x 128 tiles of dx or 
 constexpr int64_t kMaxBwdElems = int64_t(1) << 37;  // of dy or q
 constexpr int64_t kMaxW4N = int64_t(1) << 24;
 constexpr int64_t kMaxW4M = int64_t(1) << 19;
-// 8-bit and gated weights: int32 sums of 128 * 127 (or 127 * 64) a step, and the
-// same grids.
+// 8-bit and gated weights: int32 sums of 128 * 127 (or 128 * 64) a step, the same
+// grids, and tiles of 128 x 128 outputs in a grid of 2^32 threads.
 constexpr int64_t kMaxSumK = int64_t(1) << 17;
+constexpr int64_t kMaxSumOut = int64_t(1) << 37;
 constexpr int32_t kMaxGrads = 1 << 20;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -119,7 +119,7 @@ int64_t w4_scales(int64_t n, int64_t k, int64_t group) { return (n + 15) / 16 * 
 bl_status check_sum_shape(int64_t m, int64_t n, int64_t k) {
   const bl_status st = check_shape(m, n, k);
   if (st != BL_OK) return st;
-  return k > kMaxSumK || n > kMaxW4N || m > kMaxW4M ? BL_ESHAPE : BL_OK;
+  return k > kMaxSumK || n > kMaxW4N || m > kMaxW4M || m * n > kMaxSumOut ? BL_ESHAPE : BL_OK;
 }
 
 int64_t w8_codes(int64_t n, int64_t k) { return (n + 15) / 16 * ((k + 63) / 64) * 1024; }

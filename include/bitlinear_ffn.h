@@ -17,9 +17,10 @@
  *             gradients clipped to it
  *
  * Shapes: as in bitlinear.h (M, N, K >= 1; K % 4 == 0; K <= 2^22; N <= 2^30;
- * M <= 2^24; products below 2^40) unless a function says otherwise.  `stream`
- * belongs to the device that is current in the call.  Inputs must be finite, as
- * there; a value that is not spoils the outputs whose formula reads it, and no
+ * M <= 2^24; products below 2^40) unless a function says otherwise; the forward
+ * products here take M up to 2^19, N up to 2^24, K up to 2^17 and M * N up to 2^37.
+ * `stream` belongs to the device that is current in the call.  Inputs must be
+ * finite, as there; a value that is not spoils the outputs whose formula reads it, and no
  * others.  Two launches that overlap in time must not share a workspace.
  */
 #ifndef BITLINEAR_FFN_H
@@ -37,11 +38,10 @@ extern "C" {
 #define BL_ACT_RELU2 1 /* max(g, 0)^2 */
 #define BL_ACT_SILU 2  /* g / (1 + exp(-g)) */
 
-/* Storage of the gate's and the up projection's ternary weights [N][K] each
- * (K up to 2^17, N up to 2^24), N padded to whole blocks of 16 rows and K to
- * whole tiles of 256 with zeros: bytes [ceil(N/16)][ceil(K/256)][2][4][16][16],
- * the gate's and the up projection's tile of 16 rows x 256 k in turn, one
- * kilobyte each.  Chunk [g][r] of a tile holds the 64 weights k = 64 g .. 64 g +
+/* Storage of the gate's and the up projection's ternary weights [N][K] each, N
+ * padded to whole blocks of 16 rows and K to whole tiles of 256 with zeros: bytes
+ * [ceil(N/16)][ceil(K/256)][2][4][16][16], the gate's and the up projection's tile
+ * of 16 rows x 256 k in turn, one kilobyte each.  Chunk [g][r] of a tile holds the 64 weights k = 64 g .. 64 g +
  * 63 of row r: weight 16 s + 4 d + j of them in byte 4 s + j at bits 6 - 2 d, as
  * two-bit two's complement (0, 1, -1). */
 size_t bitlinear_gated_weights_bytes(int64_t n, int64_t k);
@@ -64,7 +64,8 @@ size_t bitlinear_gated_forward_workspace_bytes(int64_t m, int64_t n, int64_t k);
  * and the product in fp32.  keep_g, keep_u: bf16(g) and bf16(u) [M][N], what
  * the BitLinear projections alone would give and the gradients read; both or
  * neither (NULL).  Outputs and workspace must not overlap an input or each
- * other.  M up to 2^19. */
+ * other.  One kernel; one more where K % 16 != 0 (the activations' rows are then
+ * aligned first) and where few tiles' sums are split over K. */
 bl_status bitlinear_gated_forward(int64_t m, int64_t n, int64_t k, const int8_t *q,
                                   const float *x_scale, const uint8_t *codes,
                                   const float *gate_scale, const float *up_scale,
@@ -102,8 +103,7 @@ bl_status bitlinear_gated_backward(
 /* --- 8-bit weights with a scale per output channel ------------------------ */
 
 /* Storage.  Weight [n][k] stands for scale[n] * v with v in -127..127.  N is
- * padded to whole blocks of 16 rows and K to whole tiles of 64, with zeros (K
- * up to 2^17, N up to 2^24):
+ * padded to whole blocks of 16 rows and K to whole tiles of 64, with zeros:
  *   codes: int8 [ceil(N/16)][ceil(K/64)][4][16][16], [n/16][k/64][(k%64)/16]
  *          [n%16][k%16].
  *   scale: fp32 [N]. */
@@ -128,7 +128,7 @@ size_t bitlinear_w8_forward_workspace_bytes(int64_t m, int64_t n, int64_t k);
  * int32 sums, one fp32 product and one division.  q, x_scale: int8 codes [M][K]
  * and scales [M] of the activations.  bias: [N] bf16, added to the rounded output
  * (rounded again), or NULL.  The output and the workspace must not overlap an
- * input or each other.  M up to 2^19. */
+ * input or each other.  One kernel; more as bitlinear_gated_forward. */
 bl_status bitlinear_w8_forward(int64_t m, int64_t n, int64_t k, const int8_t *q,
                                const float *x_scale, const int8_t *codes,
                                const float *scale, const uint16_t *bias, uint16_t *y,

@@ -51,7 +51,7 @@ def activation(act, g):
 def projection(q, x_scale, u, w_scale):
     """fp32(acc / (x_scale * w_scale)): an exact sum, one fp32 product, one
     division."""
-    acc = q.astype(np.int64) @ u.astype(np.int64).T
+    acc = q.astype(np.float64) @ u.astype(np.float64).T  # integers under 2^53: exact in any order
     d = (x_scale.astype(np.float32)[:, None] * np.float32(w_scale)).astype(np.float32)
     return (acc.astype(np.float32) / d).astype(np.float32)
 
@@ -105,7 +105,7 @@ def w8_pack(v):
 
 def w8_forward(q, x_scale, v, s):
     """y as bf16 bits: exact sums, one fp32 product and one division, rounded."""
-    acc = (q.astype(np.int64) @ v.astype(np.int64).T).astype(np.float32)
+    acc = (q.astype(np.float64) @ v.astype(np.float64).T).astype(np.float32)  # exact, as in projection()
     y = (acc * s.astype(np.float32)).astype(np.float32) / x_scale.astype(np.float32)[:, None]
     return f32_to_bf16(y.astype(np.float32))
 

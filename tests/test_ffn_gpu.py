@@ -96,7 +96,7 @@ def guarded(shape, dtype):
 SHAPES = [(1, 16, 256), (1, 1, 4), (2, 17, 260), (5, 40, 2084), (16, 33, 512), (17, 100, 1028), (31, 259, 252),
           (64, 130, 640), (77, 1003, 2084), (129, 300, 1280), (257, 515, 388), (300, 64, 4096), (1, 6912, 2560),
           (4, 4096, 1024), (513, 1024, 128), (16, 40, 6016),
-          (9, 70, 9500), (3, 4200, 64)]
+          (9, 70, 9500), (3, 4200, 64), (17, 33, 128), (17, 33, 8192), (33, 8200, 8192), (100, 8200, 516), (257, 8200, 8192)]
 
 
 def gated_inputs(bl, seed, m, n, k, tiled=False):
@@ -189,7 +189,8 @@ def test_gated_one_bad_row(bl):
 
 
 BACK = [(1, 1, 4), (1, 16, 64), (3, 5, 8), (64, 64, 64), (65, 67, 68), (40, 1000, 260), (301, 1001, 1284), (130, 520, 640),
-        (700, 200, 520), (520, 2048, 516)]
+        (700, 200, 520), (520, 2048, 516), (17, 515, 128), (100, 2050, 2080), (130, 33, 8192), (513, 515, 8192),
+        (1025, 33, 128), (2048, 33, 2080), (2048, 2050, 128), (1030, 260, 2052)]
 
 
 def backward_inputs(bl, seed, m, n, k):
@@ -331,7 +332,8 @@ def test_gated_backward_against_differences(bl, act):
 
 W8_SHAPES = [(1, 1, 4), (1, 16, 64), (1, 4096, 1024), (2, 17, 68), (5, 40, 2084), (9, 1003, 2084), (16, 33, 512),
              (17, 100, 1028), (33, 64, 4096), (64, 130, 640), (77, 515, 388), (129, 300, 1280), (257, 259, 252),
-             (300, 600, 2048), (600, 1030, 512), (3, 200, 16384), (16, 100, 14336), (12, 33, 9500), (2, 4200, 64)]
+             (300, 600, 2048), (600, 1030, 512), (3, 200, 16384), (16, 100, 14336), (12, 33, 9500), (2, 4200, 64),
+             (17, 33, 128), (17, 33, 4096), (100, 4100, 8192), (130, 8200, 8192), (200, 8200, 260), (1025, 8200, 128)]
 
 
 @pytest.mark.parametrize("bias", [False, True])

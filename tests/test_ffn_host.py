@@ -49,7 +49,7 @@ def test_exports(bl):
 
 
 BAD = [(0, 8, 64), (2, 0, 64), (2, 8, 0), (2, 8, 66), (2, 8, 2 ** 17 + 4), (2, 2 ** 24 + 1, 64), (2 ** 19 + 1, 8, 64),
-       (-1, 8, 64)]
+       (-1, 8, 64), (2 ** 19, 2 ** 18 + 1, 64)]
 
 
 # ---------------------------------------------------------------- gated
@@ -307,3 +307,100 @@ def test_relu2_gradients_are_exact_in_fp32():
     dg, du = np.float32(2) * ((da * u) * r), (da * r) * r
     f = np.float64
     assert np.array_equal(dg.astype(f), 2 * da.astype(f) * u * r) and np.array_equal(du.astype(f), da.astype(f) * r * r)
+
+
+# ---------------------------------------------------------------- plans
+
+PLAN_SRC = r"""
+#include "codes_plan.hpp"
+#include "backward_plan.hpp"
+#include <cstdio>
+#include <cstdlib>
+
+int main(int argc, char** argv) {
+  for (int i = 1; i + 2 < argc; i += 3) {
+    const long long m = atoll(argv[i]), n = atoll(argv[i + 1]), k = atoll(argv[i + 2]);
+    for (int gated = 0; gated < 2; ++gated) {
+      const bl::CodesPlan p = m > 16 ? bl::plan_codes(m, n, k, gated) : bl::CodesPlan{-1};
+      const bl::CodesConfig& C = (gated ? bl::kGatedConfigs : bl::kW8Configs)[p.cfg < 0 ? 0 : p.cfg];
+      const bl::RowsPlan r = bl::plan_rows(m, n, k, gated);
+      printf("%d %d %d %d %d %d %d %d %d %d %d %lld\n", p.cfg, p.slabs, p.tiles_i, p.tiles_j, p.ksplit, p.kspw, C.ti, C.tj,
+             C.slab, r.wk, r.seg, (long long)r.lds);
+    }
+    for (int want = 3; want >= 1; --want) {
+      const bool dx = want != 1, dw = want != 2;
+      const bl::BackwardPlan p = bl::plan_backward(m, n, k, dx, dw, true);
+      printf("%d %d %d %d %d %d %d\n", p.direct, dx ? p.cfg[0] : -1, p.ksplit[0], p.kspw[0], dw ? p.cfg[1] : -1, p.ksplit[1],
+             p.kspw[1]);
+    }
+  }
+  return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plans(tmp_path_factory):
+    """shapes -> per shape (forward plans of w8 and gated, gradient plans)."""
+    tmp = tmp_path_factory.mktemp("plan")
+    src, exe = tmp / "plan.cpp", tmp / "plan"
+    src.write_text(PLAN_SRC)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I", os.path.join(ROOT, "bit_gemm_bitlinear_amd", "csrc"), str(src), "-o",
+                    str(exe)], check=True)
+
+    def run(shapes):
+        out = subprocess.run([str(exe), *(str(v) for s in shapes for v in s)], capture_output=True, text=True,
+                             check=True).stdout.splitlines()
+        rows = [tuple(map(int, line.split())) for line in out]
+        assert len(rows) == 5 * len(shapes)
+        return [(rows[5 * i:5 * i + 2], rows[5 * i + 2:5 * i + 5]) for i in range(len(shapes))]
+
+    return run
+
+
+def test_plans_cover_the_products(plans):
+    rng = np.random.default_rng(7)
+    shapes = [(1, 1, 4), (16, 2 ** 24, 64), (2 ** 19, 2 ** 18, 4), (2 ** 19, 16, 2 ** 17), (17, 2 ** 24, 2 ** 14), (100, 100, 2 ** 17)]
+    shapes += [tuple(int(2 ** (b * rng.random())) * f for b, f in ((12, 1), (14, 1), (14, 4))) for _ in range(400)]
+    for (m, n, k), (forward, _) in zip(shapes, plans(shapes)):
+        for gated, (cfg, slabs, ti, tj, parts, per, rows, cols, slab, wk, seg, lds) in enumerate(forward):
+            tile, mats = (256, 2) if gated else (64, 1)
+            # rows kernel: the staged tokens and the sums fit, every tile has a wave
+            blocks, ktiles = -(-n // 16), -(-k // tile)
+            assert wk in (1, 2, 4, 8, 16) and 1 <= seg <= ktiles and lds <= 80000 and lds >= 16 * mats * 1024
+            assert lds >= min(m, 16) * (-(-seg * tile // 256) * 256 + 16)
+            assert -(-blocks // (16 // wk)) * 1024 < 2 ** 32 and (cfg >= 0 or -(-m // 16) <= 65535)
+            if cfg < 0:
+                continue
+            assert m > 16 and slabs == -(-k // slab) and ti == -(-m // rows) and tj == -(-n // cols)
+            assert 1 <= parts <= 16 and (parts - 1) * per < slabs <= parts * per  # no part is empty
+            assert (ti * tj * parts + 7) * (512 if rows == 256 else 256) < 2 ** 32
+
+
+def test_gradient_plans_cover_the_products(plans):
+    rng = np.random.default_rng(8)
+    shapes = [(1, 1, 4), (2048, 6912, 2560), (4096, 14336, 4096)]
+    shapes += [tuple(int(2 ** (b * rng.random())) * f for b, f in ((12, 1), (13, 1), (12, 4))) for _ in range(300)]
+    for (m, n, k), (_, gradients) in zip(shapes, plans(shapes)):
+        for direct, c0, p0, s0, c1, p1, s1 in gradients:
+            assert not direct and (c0 == 2) == (c1 == 2) or c0 < 0 or c1 < 0
+            for c, parts, per, slabs in ((c0, p0, s0, 2 * -(-n // 64)), (c1, p1, s1, -(-m // 64))):
+                if c >= 0:
+                    assert (parts - 1) * per < slabs <= parts * per
+
+
+def test_gpu_shapes_take_every_plan(plans):
+    """The GPU tests' shapes by plan: every kernel and tile, whole and in parts."""
+    from test_ffn_gpu import BACK, SHAPES, W8_SHAPES
+
+    for gated, shapes in enumerate((W8_SHAPES, SHAPES)):
+        seen = {(p[gated][0], p[gated][4] > 1) for s, (p, _) in zip(shapes, plans(shapes)) if s[0] > 16}
+        want = {(-1, False), (0, False), (0, True), (1, False), (1, True), (2, False)}
+        assert want <= seen, (gated, want - seen)
+    tiles, parts = set(), set()
+    for _, gradients in plans(BACK):
+        _, c0, p0, _, c1, p1, _ = gradients[0]
+        tiles |= {("dx", c0), ("dw", c1)}
+        parts |= {("dx", p0 > 1), ("dw", p1 > 1)}
+    assert tiles == {(w, c) for w in ("dx", "dw") for c in range(3)}
+    assert parts == {(w, c) for w in ("dx", "dw") for c in (False, True)}
