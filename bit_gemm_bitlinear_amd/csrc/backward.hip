@@ -281,11 +281,6 @@ __device__ __forceinline__ void prepare_weights(const PrepArgs& A, const uint8_t
           v4i{(int32_t)w[j], (int32_t)w[j + 1], (int32_t)w[j + 2], (int32_t)w[j + 3]};
 }
 
-// dg and du of a gated block's elements, from da and the kept g and u, as
-// bitlinear_gated_backward states them.  Of relu2 every product is exact in
-// fp32 (three significands of eight bits); of silu they are made in fp64: a
-// last bit of fp32 at a border of bf16 would be a whole step of the operand.
-
 // exp(-x) for 0 <= x, to 2^-40 of itself: 2^k times the Taylor sum of the rest, of at
 // most ln(2) / 2 (what the sum leaves out: 0.3466^11 / 11!).  Past 745 it is 0.
 __device__ __forceinline__ double exp_minus(double x) {
@@ -314,12 +309,17 @@ __device__ __forceinline__ double reciprocal(double d) {
   return fma(y, fma(-d, y, 1.0), y);
 }
 
+// dg and du of a gated block's elements, from da and the kept g and u, as
+// bitlinear_gated_backward states them.  The products are made in fp64: of relu2
+// (three significands of eight bits) they are exact there and no intermediate
+// leaves the range; of silu a last bit of fp32 at a border of bf16 would be a
+// whole step of the operand.
 template <bool SILU>
 __device__ __forceinline__ void gate_grads(float da, float g, float u, float* dg, float* du) {
   if constexpr (!SILU) {
-    const float r = fmaxf(g, 0.0f);
-    *dg = 2.0f * ((da * u) * r);
-    *du = (da * r) * r;
+    const double r = g < 0.0f ? 0.0f : g;  // NaN stays NaN
+    *dg = (float)(((double)da * u) * (2.0 * r));
+    *du = (float)(((double)da * r) * r);
   } else {
     const double x = g, e = exp_minus(fabs(x)), p = reciprocal(1.0 + e);
     const double s = x >= 0.0 ? p : e * p, t = x >= 0.0 ? e * p : p;  // sigmoid(g), sigmoid(-g)

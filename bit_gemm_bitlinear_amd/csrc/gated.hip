@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __res
 template <bool SILU>
 __device__ __forceinline__ float gate_value(float g, float u) {
   if constexpr (!SILU) {
-    const float r = fmaxf(g, 0.0f);
+    const float r = g < 0.0f ? 0.0f : g;  // NaN stays NaN
     return (r * u) * r;
   } else {
     const float e = __builtin_amdgcn_exp2f(fabsf(g) * -1.44269504f);

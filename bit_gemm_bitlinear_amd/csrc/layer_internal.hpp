@@ -1,5 +1,6 @@
-// Internal interface of the operators of bitlinear_layer.h and bitlinear_ffn.h, between their entry
-// points (layer_abi.hip; abi.hip for the forward on codes) and the kernels.
+// Internal interface of the operators of bitlinear_layer.h and bitlinear_ffn.h,
+// between their entry points (layer_abi.hip; abi.hip for the forward on codes) and
+// the kernels.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -20,8 +20,8 @@
  * M <= 2^24; products below 2^40) unless a function says otherwise; the forward
  * products here take M up to 2^19, N up to 2^24, K up to 2^17 and M * N up to 2^37.
  * `stream` belongs to the device that is current in the call.  Inputs must be
- * finite, as there; a value that is not spoils the outputs whose formula reads it, and no
- * others.  Two launches that overlap in time must not share a workspace.
+ * finite, as there; a value that is not spoils the outputs whose formula reads
+ * it, and no others.  Two launches that overlap in time must not share a workspace.
  */
 #ifndef BITLINEAR_FFN_H
 #define BITLINEAR_FFN_H
@@ -41,9 +41,9 @@ extern "C" {
 /* Storage of the gate's and the up projection's ternary weights [N][K] each, N
  * padded to whole blocks of 16 rows and K to whole tiles of 256 with zeros: bytes
  * [ceil(N/16)][ceil(K/256)][2][4][16][16], the gate's and the up projection's tile
- * of 16 rows x 256 k in turn, one kilobyte each.  Chunk [g][r] of a tile holds the 64 weights k = 64 g .. 64 g +
- * 63 of row r: weight 16 s + 4 d + j of them in byte 4 s + j at bits 6 - 2 d, as
- * two-bit two's complement (0, 1, -1). */
+ * of 16 rows x 256 k in turn, one kilobyte each.  Chunk [g][r] of a tile holds the
+ * 64 weights k = 64 g .. 64 g + 63 of row r: weight 16 s + 4 d + j of them in byte
+ * 4 s + j at bits 6 - 2 d, as two-bit two's complement (0, 1, -1). */
 size_t bitlinear_gated_weights_bytes(int64_t n, int64_t k);
 
 /* Lays packed weights (bitlinear_pack_weights; codes 0..2) out in that storage.
@@ -81,7 +81,7 @@ size_t bitlinear_gated_backward_workspace_bytes(int64_t m, int64_t n, int64_t k,
 /* Gradients of the block, from da [M][N] bf16, that of a, and the kept g and u
  * [M][N] bf16.  Those of g and u are bf16 values:
  *   dg = bf16(fp32(da * u * act'(g))),  du = bf16(fp32(da * act(g)))
- * (products exact, or in fp64, before the rounding to fp32.)  Either part is
+ * (products in fp64 before the rounding to fp32; of relu2 they are exact.)  Either part is
  * left out where its outputs are NULL (its inputs are then not read and may be
  * NULL):
  *   dx = bf16((dg . Ug) / gate_scale + (du . Uu) / up_scale) [M][K]
@@ -91,7 +91,9 @@ size_t bitlinear_gated_backward_workspace_bytes(int64_t m, int64_t n, int64_t k,
  *   dw_gate = dg^T . xhat,  dw_up = du^T . xhat              [N][K] fp32 each
  *     xhat = bf16(q / x_scale).  Both or neither.  accumulate: 0, or 1 to add to
  *     what they hold.
- * Sums are fp32.  Two kernels, or three where a product's sum is split. */
+ * Sums are fp32; dx's gate part is multiplied by up_scale / gate_scale (a normal
+ * fp32 value) on the way, and the whole divided by up_scale at the end.  Two
+ * kernels, or three where a product's sum is split. */
 bl_status bitlinear_gated_backward(
     int64_t m, int64_t n, int64_t k, int32_t activation, const uint16_t *da,
     const uint16_t *g, const uint16_t *u, const uint8_t *gate, int32_t gate_layout,
@@ -162,7 +164,7 @@ bl_status bitlinear_grad_norm(int32_t count, const bl_gradient *grads, float *no
 /* The same norm, and out = g * c rounded to its type, with
  * c = fp32(min(1, max_norm / (norm + 1e-6))), made of the fp64 norm.  A NaN among
  * the gradients makes c and every output NaN, an infinity makes c 0.  max_norm:
- * 0 or more, or infinite (nothing is clipped).  With c = 1, gradients in place
+ * 0 or more, or infinite (a finite norm is not clipped).  With c = 1, gradients in place
  * are left alone.  Outputs must not overlap a gradient (but their own, exactly),
  * an output or the norm. */
 bl_status bitlinear_clip_gradients(int32_t count, const bl_gradient *grads, float max_norm,

@@ -188,6 +188,20 @@ def test_gated_one_bad_row(bl):
         assert torch.equal(bad[keep], good[keep]) and not bool(torch.isfinite(bad[1]).any())
 
 
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+@pytest.mark.parametrize("m,n,k", [(3, 64, 512), (40, 64, 512), (20, 48, 8192), (300, 200, 260)])
+def test_gated_nan_row(bl, m, n, k, act):
+    """A projection that is not a number does not become one by its activation."""
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu = gated_inputs(bl, 15, m, n, k)
+    w = bl.gated_weights(tg, dsg, tu, dsu)
+    good = bl.forward_gated(dev(q), dev(xs), w, act, keep=True)
+    xs[1] = np.nan
+    bad = bl.forward_gated(dev(q), dev(xs), w, act, keep=True)
+    others = [i for i in range(m) if i != 1]
+    for b, g in zip(bad, good):
+        assert bool(torch.isnan(b[1]).all()) and torch.equal(b[others], g[others])
+
+
 BACK = [(1, 1, 4), (1, 16, 64), (3, 5, 8), (64, 64, 64), (65, 67, 68), (40, 1000, 260), (301, 1001, 1284), (130, 520, 640),
         (700, 200, 520), (520, 2048, 516), (17, 515, 128), (100, 2050, 2080), (130, 33, 8192), (513, 515, 8192),
         (1025, 33, 128), (2048, 33, 2080), (2048, 2050, 128), (1030, 260, 2052)]
@@ -275,6 +289,46 @@ def test_gate_gradients_bit_for_bit(bl, act):
         same = (got == want) | (np.abs(want) < TINY)  # below the normal range the matrix cores may flush
         assert np.all(same), (got[~same], want[~same])
         assert not np.any(f64(out[1])[:, 1:])
+
+
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+def test_gate_gradients_over_the_whole_range(bl, act):
+    """As above, for magnitudes whose partial products leave fp32's range where
+    the gradients do not."""
+    n = 20000
+    rng = np.random.default_rng(25)
+    da, g, u = (bf16(np.ldexp(rng.uniform(1, 2, n) * rng.choice([-1, 1], n), rng.integers(-120, 120, n)))
+                for _ in range(3))
+    with np.errstate(over="ignore"):
+        dg, du = ref.gate_gradients(*(t.astype(np.float64) for t in (da, g, u)), act)
+    ok = [(np.abs(t) > TINY) & (np.abs(t) < 2.0 ** 127) for t in (dg, du)]
+    part = np.abs(da.astype(np.float64) * u)
+    assert min(t.sum() for t in ok) > 1000
+    # (silu's derivative is of middle size or leaves the range itself)
+    assert act == "silu" or (ok[0] & ((part < TINY) | (part > 2.0 ** 128))).sum() > 100
+    q = np.zeros((1, 4), np.int8)
+    q[0, 0] = 127
+    out = bl.GatedBackwardCall(*(to_dev(oracle.f32_to_bf16(t[None])) for t in (da, g, u)), act, dev(q),
+                               dev(np.array([127], np.float32)))()
+    for got, want, o in ((out[1], dg, ok[0]), (out[2], du, ok[1])):
+        assert np.array_equal(f64(got)[o, 0], want[o])
+
+
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+@pytest.mark.parametrize("m,n,k", [(40, 70, 260), (300, 520, 516)])
+def test_gated_backward_nan(bl, m, n, k, act):
+    """One gate value that is not a number spoils its token's dx and its output's
+    weight gradients, whole, and nothing else."""
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu, da, g, u = backward_inputs(bl, 26, m, n, k)
+    da[1, 5] = 0.5
+    args = [to_dev(oracle.f32_to_bf16(t)) for t in (da, g, u)]
+    kw = dict(q=dev(q), x_scale=dev(xs), gate=tg, gate_scale=dsg, up=tu, up_scale=dsu)
+    good = bl.GatedBackwardCall(*args, act, **kw)()
+    args[1][1, 5] = float("nan")
+    bad = bl.GatedBackwardCall(*args, act, **kw)()
+    for b, w, at in ((bad[0], good[0], 1), (bad[1], good[1], 5), (bad[2], good[2], 5)):
+        others = [i for i in range(len(w)) if i != at]
+        assert bool(torch.isnan(b[at]).all()) and torch.equal(b[others], w[others])
 
 
 def test_gated_backward_tiled_weights(bl):
