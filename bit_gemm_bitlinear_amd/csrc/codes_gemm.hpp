@@ -2,13 +2,15 @@
 // 8-bit weights (w8.hip) or the two ternary weights of a gated block (gated.hip)
 // on the int8 matrix cores: C[i][j] = sum_k q[i][k] * w[j][k], exact in int32.
 //
-// K goes in slabs of 128.  Both operands go from global memory straight into a
-// ring of buffers in LDS:
-//   activations     rows of 128 bytes; chunk c (16 bytes) of row r at chunk
-//                   c ^ ((r / 2) & 7), so that the 16 rows that LDS serves
-//                   together lie in distinct banks
-//   8-bit weights   the same, gathered from the storage's kilobytes (a wave's
-//                   load takes eight pieces of 128 bytes)
+// K goes in slabs of 128 (a gated block, whose weights are then 32 bytes a row) or
+// of 64 (8-bit weights: of a 256 x 256 tile that is 32 KB, four of which fit LDS).
+// Both operands go from global memory straight into a ring of buffers in LDS:
+//   activations     rows of a slab's bytes; chunk c (16 bytes) of row r at chunk
+//                   c ^ ((r / 2) & 7), or c ^ ((r / 4) & 3) of a slab of 64, so
+//                   that the 16 rows that LDS serves together lie in distinct
+//                   banks
+//   8-bit weights   the same, gathered from the storage's kilobytes (a lane's
+//                   load takes 16 bytes of one)
 //   ternary weights 32 bytes a row; chunk h (64 weights) of row r at chunk
 //                   h ^ ((r / 8) & 1).  Expanded in registers (expand16)
 // The weights are the matrix core's first operand, so that a lane's sums belong
@@ -37,7 +39,7 @@ struct CodesJob {
   int32_t m, n, k;
   const uint8_t* w;
   int32_t ktiles, blocks;  // of the weights' storage
-  int32_t slabs;           // ceil(k / 128)
+  int32_t slabs;           // ceil(k / the tile's slab)
   int32_t tiles_i, tiles_j;
   int32_t ksplit, kspw;  // parts of k, and slabs a part
   int32_t past_cache;    // the outputs are more than the L2 caches hold, and go past them
@@ -145,10 +147,10 @@ struct CodesRows {
 // One tile of TI tokens x TJ weight rows by WI x WJ waves.  TERNARY: the first
 // half of the TJ rows is the gate's, the second the up projection's of the same
 // TJ / 2 outputs, and so is each wave's share.
-template <int TI_, int TJ_, int WI_, int WJ_, int NST_, bool TERNARY, int SL_ = 128>
+template <int TI_, int TJ_, int WI_, int WJ_, int NST_, bool TERNARY>
 struct CodesTile {
-  static constexpr int SL = SL_;         // k of a slab, 128 or 64
-  static constexpr int CA = SL / 16;     // chunks of a row of activations or 8-bit weights
+  static constexpr int SL = TERNARY ? 128 : 64;        // k of a slab
+  static constexpr int CA = SL / 16;                   // chunks of a row of activations or 8-bit weights
   static constexpr int kRowB = TERNARY ? SL / 4 : SL;  // bytes of a row of weights
   static constexpr int kSwzA = 16 / CA;  // rows in a row of banks
   static __device__ __forceinline__ int swz(int r, int c) { return c ^ ((r / kSwzA) & (CA - 1)); }
@@ -160,7 +162,6 @@ struct CodesTile {
   static constexpr int CB = TJ * kRowB / 1024;  // of the weights, all waves
   static constexpr int DB = CB < NW ? 1 : CB / NW;
   static constexpr int D = DA + DB;
-  static constexpr int kPerSimd = NW == 4 && FI * FJ > 8 ? 1 : 2;  // waves (registers)
   static constexpr int kCols = TERNARY ? TJ / 2 : TJ;  // outputs of a tile
   using Rows = CodesRows<kCols / WJ>;                  // a wave's outputs
   static_assert(NW * Rows::kBytes <= kLds, "they fit the ring");
@@ -198,14 +199,14 @@ struct CodesTile {
     for (int i = 0; i < DB; ++i) {  // waves past the last piece load one again, so that all wait alike
       const int pos = ((wv % CB) * DB + i) * 64 + lane;
       if constexpr (TERNARY) {
-        const int r = SL == 128 ? pos >> 1 : pos, h = SL == 128 ? (pos & 1) ^ ((r >> 3) & 1) : 0;
+        const int r = pos >> 1, h = (pos & 1) ^ ((r >> 3) & 1);
         const int up = r >= TJ / 2, o = r - up * (TJ / 2);
         br[i] = (uint32_t)min(o >> 4, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 2048) + 1024 * up + 16 * (o & 15);
         bc[i] = 256 * h;
       } else {
         const int r = pos / CA, c = swz(r, pos % CA);
-        br[i] = (uint32_t)min(r >> 4, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 1024) + 256 * (c & 3) + 16 * (r & 15);
-        bc[i] = 1024 * (c >> 2);
+        br[i] = (uint32_t)min(r >> 4, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 1024);
+        bc[i] = 256 * c + 16 * (r & 15);
       }
     }
     const int8_t* pa = J.q + (int64_t)i0 * J.ldq;
@@ -221,14 +222,9 @@ struct CodesTile {
         const int e = d - DA;
         int8_t* dst = st + TI * SL + ((wv % CB) * DB + e) * 1024;
         if constexpr (TERNARY) {
-          constexpr int PT = 256 / SL;  // slabs of a tile
-          dma16(pb + (int64_t)(next / PT) * 2048 + (4 * SL) * (next % PT) + br[e] + bc[e], dst);
-        } else if constexpr (SL == 64) {
-          dma16(pb + (int64_t)next * 1024 + br[e] + bc[e], dst);
+          dma16(pb + (int64_t)(next >> 1) * 2048 + 512 * (next & 1) + br[e] + bc[e], dst);  // two slabs a tile
         } else {
-          // an odd last tile's half of the slab again
-          const uint32_t last = (uint32_t)(J.ktiles - 1 - 2 * next) * 1024;
-          dma16(pb + (int64_t)next * 2048 + br[e] + min(bc[e], last), dst);
+          dma16(pb + (int64_t)next * 1024 + br[e] + bc[e], dst);
         }
       }
       if (d == D - 1) ++next;
@@ -259,14 +255,7 @@ struct CodesTile {
         if constexpr (!TERNARY) {
           b[j] = *reinterpret_cast<const v4i*>(sb + 16 * swz(r, 2 * ks + lg));
         } else if (ks == 0) {
-          if constexpr (SL == 128) {
-            b[j] = *reinterpret_cast<const v4i*>(sb + 16 * (lg ^ ((r >> 3) & 1)));
-          } else {
-            typedef int32_t v2i __attribute__((ext_vector_type(2)));
-            const v2i w = *reinterpret_cast<const v2i*>(sb + 8 * lg);
-            b[j].x = w.x;
-            b[j].y = w.y;
-          }
+          b[j] = *reinterpret_cast<const v4i*>(sb + 16 * (lg ^ ((r >> 3) & 1)));
         }
       }
     };
@@ -315,8 +304,6 @@ struct CodesTile {
     barrier();
     load(0, fa[0], fb[0]);
     int buf = 0;
-    // 8-bit weights of an odd number of tiles: the last slab's second half is not there
-    const int half = !TERNARY && SL == 128 && (J.ktiles & 1) && s0 + nsl == J.slabs ? nsl - 1 : -1;
     // A slab.  Behind the first product of its last step its fragments are all in
     // registers: when every wave is there, its buffer is free.  The next slab's
     // first fragments are then read, and the buffer refilled between the products.
@@ -329,8 +316,7 @@ struct CodesTile {
 #pragma unroll
       for (int ks = 0; ks < KS - 1; ++ks) {
         auto ahead = [&]() { load(ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]); };
-        if (ISSUE || ks < KS / 2 || s != half)
-          multiply(std::false_type{}, ks, fa[ks & 1], fb[ks & 1], nullptr, ahead);
+        multiply(std::false_type{}, ks, fa[ks & 1], fb[ks & 1], nullptr, ahead);
       }
       int8_t* st = smem + buf * kStage;
       auto turn = [&]() {
@@ -343,7 +329,7 @@ struct CodesTile {
           load(0, fa[0], fb[0]);
         }
       };
-      if (ISSUE || s != half) multiply(issue, KS - 1, fa[(KS - 1) & 1], fb[(KS - 1) & 1], st, turn);
+      multiply(issue, KS - 1, fa[(KS - 1) & 1], fb[(KS - 1) & 1], st, turn);
     };
     int s = 0;
     for (; s + NST < nsl; ++s) slab(std::true_type{}, s);

@@ -133,7 +133,7 @@ struct GatedGemmArgs {
 };
 
 template <typename T, bool SILU>
-__global__ __launch_bounds__(64 * T::NW, T::kPerSimd) void gated_gemm_kernel(const GatedGemmArgs A) {
+__global__ __launch_bounds__(64 * T::NW, 2) void gated_gemm_kernel(const GatedGemmArgs A) {
   extern __shared__ __align__(16) int8_t smem[];
   const CodesJob& J = A.j;
   int ti, tj, kp;

@@ -122,7 +122,7 @@ struct W8GemmArgs {
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 template <typename T>
-__global__ __launch_bounds__(64 * T::NW, T::kPerSimd) void w8_gemm_kernel(const W8GemmArgs A) {
+__global__ __launch_bounds__(64 * T::NW, 2) void w8_gemm_kernel(const W8GemmArgs A) {
   extern __shared__ __align__(16) int8_t smem[];
   const CodesJob& J = A.j;
   int ti, tj, kp;
@@ -222,9 +222,9 @@ __global__ __launch_bounds__(256) void w8_finish_kernel(const W8GemmArgs A, int6
   codes_put8(A.y + m * J.n, n, J.n, (J.n & 7) == 0, w);
 }
 
-using W8Tile256 = CodesTile<256, 256, 2, 4, 4, false, 64>;
-using W8Tile128 = CodesTile<128, 128, 2, 2, 5, false, 64>;
-using W8Tile64 = CodesTile<64, 64, 2, 2, 8, false, 64>;
+using W8Tile256 = CodesTile<256, 256, 2, 4, 4, false>;
+using W8Tile128 = CodesTile<128, 128, 2, 2, 5, false>;
+using W8Tile64 = CodesTile<64, 64, 2, 2, 8, false>;
 
 template <typename T>
 hipError_t w8_gemm(const W8GemmArgs& a, hipStream_t s) {

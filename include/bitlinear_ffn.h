@@ -142,7 +142,7 @@ bl_status bitlinear_w8_forward(int64_t m, int64_t n, int64_t k, const int8_t *q,
 #define BL_GRAD_F32 2
 
 /* One gradient: any number of elements (0 too), contiguous, its pointers aligned
- * to its elements (16-byte aligned ones are faster). */
+ * to its elements (faster where they are the same modulo 16 bytes). */
 typedef struct {
   const void *g;
   void *out;     /* clipped, may be g itself; bitlinear_grad_norm ignores it */

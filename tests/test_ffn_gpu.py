@@ -509,6 +509,32 @@ def test_clip_alignment_and_order(bl):
         bl.clip_grads([t, t], 1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("alike", [True, False])
+def test_clip_views_of_one_buffer(bl, dtype, alike):
+    """Gradients next to each other in one buffer, from any element on, and
+    clipped ones that lie as they do or otherwise: every length around the
+    kernels' pieces and chunks."""
+    lens = list(range(1, 20)) + [2047, 2048, 2049, 2050, 2055, 4096, 4099, 70001, 65536, 1]
+    total = sum(lens)
+    torch.manual_seed(44)
+    for at in (0, 1, 3, 7):
+        src = torch.randn(total + 24, device=DEV).to(dtype)
+        dst = torch.full_like(src, 3.0)
+        grads = src[at:at + total].split(lens)
+        shift = at if alike else at + 1
+        outs = dst[shift:shift + total].split(lens)
+        vals = [g.float().cpu().numpy() for g in grads]
+        norm, got = bl.clip_grads(grads, 0.7, outs=outs)
+        check_clip(norm, got, vals, 0.7)
+        assert bool((dst[:shift] == 3).all()) and bool((dst[shift + total:] == 3).all())
+        assert torch.equal(bl.grad_norm(grads), norm)
+        kept = src.clone()
+        norm, got = bl.clip_grads(grads, 0.7)
+        check_clip(norm, got, vals, 0.7)
+        assert torch.equal(src[:at], kept[:at]) and torch.equal(src[at + total:], kept[at + total:])
+
+
 def test_clip_extremes(bl):
     """Magnitudes whose squares leave fp32, values that are not finite, zeros."""
     big = torch.full((1000,), 2e38, device=DEV)
