@@ -188,7 +188,7 @@ struct CodesTile {
     const int blk0 = tj * (kCols / 16);
 
     // Per lane the offsets of a load's row and of its chunk in the slab.
-    uint32_t ar[DA], ac[DA], br[DB], bc[DB];
+    uint32_t ar[DA], ac[DA], br[DB];
 #pragma unroll
     for (int i = 0; i < DA; ++i) {
       const int pos = (wv * DA + i) * 64 + lane, r = pos / CA;
@@ -199,14 +199,11 @@ struct CodesTile {
     for (int i = 0; i < DB; ++i) {  // waves past the last piece load one again, so that all wait alike
       const int pos = ((wv % CB) * DB + i) * 64 + lane;
       if constexpr (TERNARY) {
-        const int r = pos >> 1, h = (pos & 1) ^ ((r >> 3) & 1);
-        const int up = r >= TJ / 2, o = r - up * (TJ / 2);
-        br[i] = (uint32_t)min(o >> 4, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 2048) + 1024 * up + 16 * (o & 15);
-        bc[i] = 256 * h;
+        const int b = pos >> 5, up = b >= TJ / 32;  // 512 bytes a block of 16 rows
+        br[i] = (uint32_t)min(b - up * (TJ / 32), J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 2048) + 1024 * up +
+                16 * (pos & 31);
       } else {
-        const int r = pos / CA, c = swz(r, pos % CA);
-        br[i] = (uint32_t)min(r >> 4, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 1024);
-        bc[i] = 256 * c + 16 * (r & 15);
+        br[i] = (uint32_t)min(pos >> 6, J.blocks - 1 - blk0) * ((uint32_t)J.ktiles * 1024) + 16 * (pos & 63);
       }
     }
     const int8_t* pa = J.q + (int64_t)i0 * J.ldq;
@@ -222,9 +219,9 @@ struct CodesTile {
         const int e = d - DA;
         int8_t* dst = st + TI * SL + ((wv % CB) * DB + e) * 1024;
         if constexpr (TERNARY) {
-          dma16(pb + (int64_t)(next >> 1) * 2048 + 512 * (next & 1) + br[e] + bc[e], dst);  // two slabs a tile
+          dma16(pb + (int64_t)(next >> 1) * 2048 + 512 * (next & 1) + br[e], dst);  // two slabs a tile
         } else {
-          dma16(pb + (int64_t)next * 1024 + br[e] + bc[e], dst);
+          dma16(pb + (int64_t)next * 1024 + br[e], dst);
         }
       }
       if (d == D - 1) ++next;
@@ -251,12 +248,11 @@ struct CodesTile {
 #pragma unroll
       for (int j = 0; j < FJ; ++j) {
         const int r = brow(j) + lr;
-        const int8_t* sb = sa + TI * SL + kRowB * r;
-        if constexpr (!TERNARY) {
-          b[j] = *reinterpret_cast<const v4i*>(sb + 16 * swz(r, 2 * ks + lg));
-        } else if (ks == 0) {
-          b[j] = *reinterpret_cast<const v4i*>(sb + 16 * (lg ^ ((r >> 3) & 1)));
-        }
+        const int8_t* sb = sa + TI * SL + 16 * kRowB * (r >> 4) + 16 * (r & 15);
+        if constexpr (!TERNARY)
+          b[j] = *reinterpret_cast<const v4i*>(sb + 256 * (2 * ks + lg));
+        else if (ks == 0)
+          b[j] = *reinterpret_cast<const v4i*>(sb + 256 * lg);
       }
     };
     // Products of step ks.  `mid` runs behind the first of them, which waits for the
