@@ -43,7 +43,8 @@ struct CodesJob {
   int32_t tiles_i, tiles_j;
   int32_t ksplit, kspw;  // parts of k, and slabs a part
   int32_t past_cache;    // the outputs are more than the L2 caches hold, and go past them
-  int32_t* part;         // ksplit > 1: int32 sums [ksplit][m][n] (gated: [ksplit][2][m][n])
+  int32_t* part;         // ksplit > 1: int32 sums [ksplit][m][ldp] (gated: [ksplit][2][m][ldp])
+  int32_t ldp;           // part_pitch(n)
 };
 
 namespace codes_gemm {
@@ -362,45 +363,31 @@ __device__ __forceinline__ void codes_put8(uint16_t* row, int n, int cols, bool 
   }
 }
 
-// int32 sums of a part (32 x 32 subtile: one row a lane).
-__device__ __forceinline__ void codes_put_part(int32_t* row, int n0, int cols, const v16i& acc) {
+// int32 sums of a part (32 x 32 subtile: one row a lane).  Rows of parts are of
+// whole eights of columns, `ldp`; the ones past N are sums of the last blocks again.
+__device__ __forceinline__ void codes_put_part(int32_t* row, int n0, int ldp, const v16i& acc) {
   const int lg = (threadIdx.x >> 5) & 1;
-  const bool wide = (cols & 3) == 0;
 #pragma unroll
   for (int a = 0; a < 4; ++a) {
     const int n = n0 + 8 * a + 4 * lg;
-    if (wide && n + 4 <= cols) {
+    if (n < ldp)
       *G(reinterpret_cast<v4i*>(row + n)) = v4i{acc[4 * a], acc[4 * a + 1], acc[4 * a + 2], acc[4 * a + 3]};
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < cols) *G(row + n + e) = acc[4 * a + e];
-    }
   }
 }
 
-// Adds eight columns' sums of the parts, in order (`left`: columns that exist);
-// four parts' loads at a time.
-__device__ __forceinline__ void codes_add_parts(const int32_t* src, int64_t slice, int ksplit, int left, bool wide,
-                                                int32_t (&v)[8]) {
-  if (wide && left >= 8) {
-    for (int p = 0; p < ksplit; p += 4) {
-      v4i t[4][2];
+// Adds eight columns' sums of the parts, in order, four parts' loads at a time.
+__device__ __forceinline__ void codes_add_parts(const int32_t* src, int64_t slice, int ksplit, int32_t (&v)[8]) {
+  for (int p = 0; p < ksplit; p += 4) {
+    v4i t[4][2];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          t[u][h] = p + u < ksplit ? *G(reinterpret_cast<const v4i*>(src + (p + u) * slice + 4 * h)) : v4i{0, 0, 0, 0};
+      for (int h = 0; h < 2; ++h)
+        t[u][h] = p + u < ksplit ? *G(reinterpret_cast<const v4i*>(src + (p + u) * slice + 4 * h)) : v4i{0, 0, 0, 0};
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += t[u][e >> 2][e & 3];
-    }
-  } else {
-    for (int p = 0; p < ksplit; ++p)
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < left) v[e] += *G(src + p * slice + e);
+      for (int e = 0; e < 8; ++e) v[e] += t[u][e >> 2][e & 3];
   }
 }
 
@@ -430,6 +417,9 @@ inline hipError_t codes_pad(const int8_t* q, int64_t m, int64_t k, int32_t ldq, 
 // -> 128 us).  Rows of a wave shorter than a cache line are stored plainly.
 inline int32_t codes_past_cache(int64_t m, int64_t n) { return 2 * m * n > (int64_t(32) << 20) ? 1 : 0; }
 
+// Columns of a row of a part.
+inline int64_t part_pitch(int64_t n) { return round_up(n, 8); }
+
 inline void set_plan(CodesJob& J, const CodesPlan& p, int32_t* part) {
   J.past_cache = codes_past_cache(J.m, J.n);
   J.slabs = p.slabs;
@@ -438,6 +428,7 @@ inline void set_plan(CodesJob& J, const CodesPlan& p, int32_t* part) {
   J.ksplit = p.ksplit;
   J.kspw = p.kspw;
   J.part = part;
+  J.ldp = (int32_t)part_pitch(J.n);
 }
 
 // Launches a kernel with `lds` bytes of dynamic LDS, of at most `most`: an attribute

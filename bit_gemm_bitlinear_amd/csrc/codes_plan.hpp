@@ -64,27 +64,31 @@ struct CodesPlan {
 
 // Tile sizes (tokens x outputs), k of a slab, the workgroups a CU holds, and,
 // measured on an MI355X (us): the time of a slab where few CUs have a workgroup,
-// where each has one, and where each has all it holds; that to start a tile and
-// write its outputs.
+// where each has one, where the first ones have two and where all have; that to
+// start a tile and write its outputs.
 struct CodesConfig {
   int ti, tj, slab, per_cu;
-  float few, one, full, put;
+  float few, one, two, full, put;
 };
-constexpr CodesConfig kW8Configs[3] = {{64, 64, 64, 2, 0.156f, 0.165f, 0.31f, 1.0f},
-                                       {128, 128, 64, 2, 0.28f, 0.32f, 0.64f, 2.5f},
-                                       {256, 256, 64, 1, 0.62f, 0.85f, 0.85f, 5.0f}};
-constexpr CodesConfig kGatedConfigs[3] = {{32, 128, 128, 2, 0.31f, 0.35f, 0.60f, 1.0f},
-                                          {64, 128, 128, 2, 0.39f, 0.48f, 0.82f, 1.8f},
-                                          {128, 128, 128, 2, 0.67f, 0.85f, 1.50f, 2.5f}};
+constexpr CodesConfig kW8Configs[] = {{64, 64, 64, 2, 0.16f, 0.17f, 0.19f, 0.22f, 1.0f},
+                                      {128, 128, 64, 2, 0.22f, 0.28f, 0.50f, 0.68f, 2.9f},
+                                      {128, 256, 64, 1, 0.32f, 0.52f, 0.0f, 0.0f, 3.0f},
+                                      {256, 256, 64, 1, 0.62f, 0.88f, 0.0f, 0.0f, 5.0f}};
+constexpr CodesConfig kGatedConfigs[] = {{32, 128, 128, 2, 0.32f, 0.35f, 0.46f, 0.55f, 1.0f},
+                                         {64, 128, 128, 2, 0.41f, 0.47f, 0.68f, 0.86f, 1.8f},
+                                         {128, 128, 128, 2, 0.71f, 0.87f, 1.24f, 1.55f, 2.5f}};
 constexpr float kCodesStartUs = 3.5f;   // a launch
 constexpr float kCodesFinishUs = 3.0f;  // one more, that adds the parts
+constexpr float kCodesPadUs = 3.0f;     // one before, that aligns the activations' rows
 constexpr float kCodesBytesPerUs = 6e6f;
 
 // The kernel, tile and parts with the smallest estimated time (m > 16).  Measured
-// against single choices: 8-bit 17 x 4096 x 4096 rows 7.3 us, tiles 11.1; 64 x 14336
-// x 4096 rows 36, tiles of 64 x 64 15.2, of 256 x 256 48; 2048 x 14336 x 4096 of 64 x
-// 64 289, of 128 x 128 154, of 256 x 256 121; 300 x 4096 x 14336 in two parts 45, one
-// 69, four 52.
+// against single choices (us, 8-bit): 17 x 4096 x 4096 rows 7.5, tiles 11; 64 x 14336
+// x 4096 rows 36, tiles of 64 x 64 16, of 128 x 128 19, of 256 x 256 in four parts 25;
+// 2048 x 4096 x 4096 of 128 x 128 45, of 128 x 256 39, of 256 x 256 54; 2048 x 14336 x
+// 4096 139, 138 and 120; 300 x 4096 x 14336 of 128 x 256 in four parts 38, of 128 x
+// 128 in two 40, of 256 x 256 in six 48.  Over 70 shapes of all sizes the choice is 4%
+// off the best one on average.
 inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
   CodesPlan best = {};
   best.cfg = -1;
@@ -93,19 +97,20 @@ inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
   const int64_t rwgs = ((n + 15) / 16 + per - 1) / per * ((m + 15) / 16), tiles = ((k + rtk - 1) / rtk + r.wk - 1) / r.wk;
   float least = kCodesStartUs + (float)((rwgs + 2 * kCodesCus - 1) / (2 * kCodesCus)) *
                                     (gated ? 1.6f + 2.1f * (float)tiles : 1.0f + 1.1f * (float)tiles);
-  for (int cfg = 0; cfg < 3; ++cfg) {
+  for (int cfg = 0; cfg < (gated ? 3 : 4); ++cfg) {
     const CodesConfig& C = gated ? kGatedConfigs[cfg] : kW8Configs[cfg];
     const int64_t ti = (m + C.ti - 1) / C.ti, tj = (n + C.tj - 1) / C.tj, slabs = (k + C.slab - 1) / C.slab;
     const int64_t room = kCodesCus * C.per_cu;
     // the time of a round of up to `room` tiles
     auto round = [&](int64_t wgs, int64_t kspw) {
-      const float slab = wgs > kCodesCus ? C.full : C.few + (C.one - C.few) * (float)wgs / kCodesCus;
+      const float share = (float)(wgs > kCodesCus ? wgs - kCodesCus : wgs) / kCodesCus;
+      const float slab = wgs > kCodesCus ? C.two + (C.full - C.two) * share : C.few + (C.one - C.few) * share;
       return wgs ? (float)kspw * slab + C.put : 0.0f;
     };
     for (int64_t want = 1; want <= 16; ++want) {
       if (want > 1 && (slabs * C.slab < 512 * want || ti * tj * want > 4 * kCodesCus)) break;
       const int64_t kspw = (slabs + want - 1) / want, parts = (slabs + kspw - 1) / kspw, wgs = ti * tj * parts;
-      float us = kCodesStartUs + (float)(wgs / room) * round(room, kspw) + round(wgs % room, kspw);
+      float us = kCodesStartUs + (k % 16 ? kCodesPadUs : 0.0f) + (float)(wgs / room) * round(room, kspw) + round(wgs % room, kspw);
       if (parts > 1)
         us += kCodesFinishUs + 8.0f * (float)parts * (float)m * (float)n * (gated ? 2.0f : 1.0f) / kCodesBytesPerUs;
       if (us >= least) continue;

@@ -150,8 +150,8 @@ __global__ __launch_bounds__(64 * T::NW, 2) void gated_gemm_kernel(const GatedGe
       if (m >= J.m) continue;
 #pragma unroll
       for (int j = 0; j < T::FJ; ++j) {
-        int32_t* row = J.part + ((int64_t)(2 * kp + (j >= FO)) * J.m + m) * J.n;
-        codes_put_part(row, n0 + 32 * (j % FO), J.n, acc[i][j]);
+        int32_t* row = J.part + ((int64_t)(2 * kp + (j >= FO)) * J.m + m) * J.ldp;
+        codes_put_part(row, n0 + 32 * (j % FO), J.ldp, acc[i][j]);
       }
     }
     return;
@@ -203,11 +203,11 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(const GatedGemmArgs A
   const int cpr = (J.n + 7) >> 3;
   const int64_t m = id / cpr;
   const int n = 8 * (int)(id - m * cpr);
-  const int64_t slice = (int64_t)J.m * J.n;
-  const int32_t* src = J.part + m * J.n + n;
+  const int64_t slice = (int64_t)J.m * J.ldp;
+  const int32_t* src = J.part + m * J.ldp + n;
   int32_t vg[8] = {0, 0, 0, 0, 0, 0, 0, 0}, vu[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  codes_add_parts(src, 2 * slice, J.ksplit, J.n - n, (J.n & 3) == 0, vg);
-  codes_add_parts(src + slice, 2 * slice, J.ksplit, J.n - n, (J.n & 3) == 0, vu);
+  codes_add_parts(src, 2 * slice, J.ksplit, vg);
+  codes_add_parts(src + slice, 2 * slice, J.ksplit, vu);
   const float xs = *G(A.x_scale + m);
   const RowDiv dg = row_div_setup(xs * *G(A.gate_scale)), du = row_div_setup(xs * *G(A.up_scale));
   uint32_t pa[4], pg[4], pu[4];
@@ -268,7 +268,7 @@ GatedLayout gated_layout(int64_t m, int64_t n, int64_t k) {
   L.ldq = (int32_t)round_up(k, 16);
   if (k % 16) L.total = align256((size_t)m * L.ldq);
   L.part = L.total;
-  if (L.plan.ksplit > 1) L.total = align256(L.total + 8 * (size_t)L.plan.ksplit * m * n);
+  if (L.plan.ksplit > 1) L.total = align256(L.total + 8 * (size_t)L.plan.ksplit * m * part_pitch(n));
   return L;
 }
 

@@ -136,9 +136,9 @@ __global__ __launch_bounds__(64 * T::NW, 2) void w8_gemm_kernel(const W8GemmArgs
     for (int i = 0; i < T::FI; ++i) {
       const int m = m0 + 32 * i;
       if (m >= J.m) continue;
-      int32_t* row = J.part + ((int64_t)kp * J.m + m) * J.n;
+      int32_t* row = J.part + ((int64_t)kp * J.m + m) * J.ldp;
 #pragma unroll
-      for (int j = 0; j < T::FJ; ++j) codes_put_part(row, n0 + 32 * j, J.n, acc[i][j]);
+      for (int j = 0; j < T::FJ; ++j) codes_put_part(row, n0 + 32 * j, J.ldp, acc[i][j]);
     }
     return;
   }
@@ -199,10 +199,8 @@ __global__ __launch_bounds__(256) void w8_finish_kernel(const W8GemmArgs A, int6
   const int cpr = (J.n + 7) >> 3;
   const int64_t m = id / cpr;
   const int n = 8 * (int)(id - m * cpr);
-  const int64_t slice = (int64_t)J.m * J.n;
-  const int32_t* src = J.part + m * J.n + n;
   int32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  codes_add_parts(src, slice, J.ksplit, J.n - n, (J.n & 3) == 0, v);
+  codes_add_parts(J.part + m * J.ldp + n, (int64_t)J.m * J.ldp, J.ksplit, v);
   const float xs = *G(A.x_scale + m), y = 1.0f / xs;
   float t[8];
 #pragma unroll
@@ -223,6 +221,7 @@ __global__ __launch_bounds__(256) void w8_finish_kernel(const W8GemmArgs A, int6
 }
 
 using W8Tile256 = CodesTile<256, 256, 2, 4, 4, false>;
+using W8TileWide = CodesTile<128, 256, 2, 4, 5, false>;
 using W8Tile128 = CodesTile<128, 128, 2, 2, 5, false>;
 using W8Tile64 = CodesTile<64, 64, 2, 2, 8, false>;
 
@@ -247,7 +246,7 @@ W8Layout w8_layout(int64_t m, int64_t n, int64_t k) {
   L.ldq = (int32_t)round_up(k, 16);
   if (k % 16) L.total = align256((size_t)m * L.ldq);
   L.part = L.total;
-  if (L.plan.ksplit > 1) L.total = align256(L.total + 4 * (size_t)L.plan.ksplit * m * n);
+  if (L.plan.ksplit > 1) L.total = align256(L.total + 4 * (size_t)L.plan.ksplit * m * part_pitch(n));
   return L;
 }
 
@@ -292,7 +291,8 @@ hipError_t launch_w8_forward(const W8Args& b, char* ws, hipStream_t s) {
       if (e != hipSuccess) return e;
       J.q = reinterpret_cast<const int8_t*>(ws);
     }
-    e = L.plan.cfg == 2   ? w8_gemm<W8Tile256>(a, s)
+    e = L.plan.cfg == 3   ? w8_gemm<W8Tile256>(a, s)
+        : L.plan.cfg == 2 ? w8_gemm<W8TileWide>(a, s)
         : L.plan.cfg == 1 ? w8_gemm<W8Tile128>(a, s)
                           : w8_gemm<W8Tile64>(a, s);
     if (e != hipSuccess || J.ksplit == 1) return e;

@@ -374,7 +374,7 @@ def test_plans_cover_the_products(plans):
                 continue
             assert m > 16 and slabs == -(-k // slab) and ti == -(-m // rows) and tj == -(-n // cols)
             assert 1 <= parts <= 16 and (parts - 1) * per < slabs <= parts * per  # no part is empty
-            assert (ti * tj * parts + 7) * (512 if rows == 256 else 256) < 2 ** 32
+            assert (ti * tj * parts + 7) * (512 if not gated and cols == 256 else 256) < 2 ** 32
 
 
 def test_gradient_plans_cover_the_products(plans):
@@ -396,6 +396,7 @@ def test_gpu_shapes_take_every_plan(plans):
     for gated, shapes in enumerate((W8_SHAPES, SHAPES)):
         seen = {(p[gated][0], p[gated][4] > 1) for s, (p, _) in zip(shapes, plans(shapes)) if s[0] > 16}
         want = {(-1, False), (0, False), (0, True), (1, False), (1, True), (2, False)}
+        want |= {(2, True)} if gated else {(2, True), (3, False), (3, True)}
         assert want <= seen, (gated, want - seen)
     tiles, parts = set(), set()
     for _, gradients in plans(BACK):
