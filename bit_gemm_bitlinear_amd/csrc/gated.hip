@@ -8,7 +8,10 @@
 // wavefront.  A weight is its two-bit two's complement, so that a shift and a mask
 // make four int8 values 64 u of a dword, in the activations' own order: no sum of
 // codes to subtract, no activations to reorder.  The sums come out 64 times too
-// large, exactly; the factor leaves in the epilogue.
+// large, exactly; the factor leaves in the epilogue.  Both sums of an output meet in
+// one lane, so act(g) * u costs no pass of its own (2048 x 6912 x 2560 with g and u
+// kept: 71 us, 2.04 POPS; the plain projections, activation and product as launches
+// of their own 118 without keeping them).
 #include "../../include/bitlinear_ffn.h"
 #include "codes_gemm.hpp"
 #include "codes_plan.hpp"

@@ -6,6 +6,9 @@
 // Storage (bitlinear_ffn.h): 16 rows x 64 k are one contiguous kilobyte, 16
 // bytes (consecutive k of one row) a lane of a wavefront: an operand of the
 // 16x16x64 int8 matrix-core op.  Sums are exact in int32.
+//
+// Up to 16 tokens the weights' bytes are the cost (codes_rows.hpp), past that tiles
+// on the matrix cores (codes_gemm.hpp); codes_plan.hpp chooses, with the figures.
 #include "../../include/bitlinear_ffn.h"
 #include "codes_gemm.hpp"
 #include "codes_plan.hpp"

@@ -267,7 +267,8 @@ def norm_gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     optional bf16 or fp32 weight [K], then act(gate) * up of its output: the
     BitLinears w_gate and w_up (latent fp32 [N, K] each) and the activation
     function, "relu2" or "silu".  Returns (h, a): h as norm_linear's, a bf16
-    [..., N]; differentiable throughout, without a token empty, as there."""
+    [..., N]; differentiable throughout, without a token empty, as there.  Up to
+    2^19 tokens, K up to 2^17."""
     bl._activation(activation)
     if residual is not None and residual.shape != x.shape:
         raise ValueError(f"residual must have shape {tuple(x.shape)}, got {tuple(residual.shape)}")
