@@ -765,6 +765,151 @@ def test_side_stream(bl):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("act", ["relu2", "silu"])
+def test_feed_forward_step_in_a_graph(bl, tr, act):
+    """The module's forward and backward pass and the clipping of its gradients,
+    captured once, against eager steps between the replays."""
+    torch.manual_seed(63)
+    m, k, n = 70, 256, 392
+    ffn = tr.FeedForward(k, n, act, device=DEV)
+    params = list(ffn.parameters())
+    x = torch.randn(m, k, device=DEV).to(torch.bfloat16).requires_grad_()
+    r = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+    dy = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+
+    def step():
+        h, y = ffn(x, r)
+        grads = torch.autograd.grad((y, h), (x, *params), (dy, r))
+        norm, _ = bl.clip_grads(list(grads[1:]), 0.5)
+        return (y.detach(), norm, *grads)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        with torch.no_grad():
+            x.copy_(torch.randn(m, k, device=DEV))
+            dy.copy_(torch.randn(m, k, device=DEV))
+            for p in params:
+                p.mul_(0.9)
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b), i
+
+
+def test_same_tensor_twice(bl, tr):
+    """One weight as gate and up, one tensor as x and residual, g as u."""
+    torch.manual_seed(64)
+    m, n, k = 37, 130, 264
+    x = torch.randn(m, k, device=DEV).to(torch.bfloat16).requires_grad_()
+    w = (0.05 * torch.randn(n, k, device=DEV)).requires_grad_()
+    w1, w2 = (w.detach().clone().requires_grad_() for _ in range(2))
+    x1, x2 = (x.detach().clone().requires_grad_() for _ in range(2))
+    da = torch.randn(m, n, device=DEV).to(torch.bfloat16)
+    _, a = tr.norm_gated(x, w, w, residual=x, activation="silu")
+    _, b = tr.norm_gated(x1, w1, w2, residual=x2, activation="silu")
+    assert torch.equal(a, b)
+    a.backward(da)
+    b.backward(da)
+    assert torch.equal(w.grad, w1.grad + w2.grad) and torch.equal(x.grad, x1.grad + x2.grad)
+    (p, s), q, xs = bl.pack_weights(w.detach()), *bl.act_quant(x.detach())
+    out = bl.forward_gated(q, xs, bl.gated_weights(p, s, p, s), "relu2", keep=True)
+    assert torch.equal(out.g, out.u) and torch.equal(out.g, bl.forward_quantized(q, xs, p, s))
+    one = bl.GatedBackwardCall(da, out.g, out.g, "relu2", q, xs, p, s, p, s)()
+    two = bl.GatedBackwardCall(da, out.g, out.u, "relu2", q, xs, p, s, p, s)()
+    assert all(torch.equal(i, j) for i, j in zip(one, two))
+
+
+def test_calls_from_threads(bl):
+    """Host threads with streams, shapes and workspaces of their own."""
+    import threading
+
+    def calls(i):
+        q, xs, ug, sg, uu, su, tg, dsg, tu, dsu, da, g, u = backward_inputs(bl, 70 + i, 20 + 90 * i, 200 + 8 * i, 1024)
+        dda, dg, du = (to_dev(oracle.f32_to_bf16(t)) for t in (da, g, u))
+        dq, dxs = dev(q), dev(xs)
+        w8 = bl.pack_weights_w8(torch.from_numpy(ug.astype(np.float32)).to(DEV))
+        back = bl.GatedBackwardCall(dda, dg, du, "silu", dq, dxs, tg, dsg, tu, dsu)
+        outs = [torch.empty_like(t) for t in back._out[1:]]
+        return (bl.GatedCall(dq, dxs, bl.gated_weights(tg, dsg, tu, dsu), "silu"), bl.W8Call(dq, dxs, w8), back,
+                bl.ClipGradsCall(list(back._out[1:]), 1e-3, outs=outs))
+
+    def run(cs):
+        for c in cs:
+            c()
+        return [cs[0].out.a, cs[1].out, *cs[2]._out, cs[3].norm, *cs[3].outs]
+
+    sets = [calls(i) for i in range(4)]
+    want = [[t.clone() for t in run(cs)] for cs in sets]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    got = run(sets[i])
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    bad.append(i)
+        except Exception as e:  # reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+
+
+@pytest.mark.parametrize("m,n,k", [(2 ** 21, 1, 4), (1, 2 ** 20, 4), (3, 5, 2 ** 22), (40, 2 ** 20, 4)])
+def test_gated_backward_largest_sizes(bl, m, n, k):
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu, da, g, u = backward_inputs(bl, 72, m, n, k)
+    xhat = oracle.bf16_to_f32(layer.restore_activations(q, xs))
+    want = ref.gated_backward(*(t.astype(np.float64) for t in (da, g, u)), "relu2", ug, sg, uu, su, xhat)
+    args = [to_dev(oracle.f32_to_bf16(t)) for t in (da, g, u)]
+    check_backward(bl.GatedBackwardCall(*args, "relu2", dev(q), dev(xs), tg, dsg, tu, dsu)(), want, m, n)
+
+
+# The limits: tokens, outputs, width.
+LIMITS = [(2 ** 19, 17, 4), (2 ** 19, 1, 20), (1, 2 ** 24, 4), (17, 2 ** 24, 4), (2, 19, 2 ** 17), (40, 19, 2 ** 17),
+          (300, 19, 2 ** 17 - 4)]
+
+
+@pytest.mark.parametrize("m,n,k", LIMITS)
+def test_largest_sizes(bl, m, n, k):
+    rng = np.random.default_rng(71)
+    q, xs = dev(rng.integers(-128, 128, (m, k)).astype(np.int8)), torch.rand(m, device=DEV) + 0.5
+    ends = torch.tensor(sorted({0, m // 2, m - 1}), device=DEV)
+    cols = torch.tensor(sorted({0, n // 2, n - 1}), device=DEV)
+    w = torch.randn(n, k, device=DEV)
+    w8 = bl.pack_weights_w8(w)
+    v = torch.round(bl.unpack_weights_w8(w8)[cols].double() / w8.scale[cols].double()[:, None])
+    acc = (q[ends].double()[:, None, :] * v[None]).sum(-1).float()  # whole numbers under 2^53, rounded once
+    y = bl.forward_w8(q, xs, w8)
+    assert torch.equal(y[ends][:, cols], (acc * w8.scale[cols] / xs[ends][:, None]).to(torch.bfloat16))
+    del y, w8
+    packed, scale = bl.pack_weights(w)
+    del w
+    out = bl.forward_gated(q, xs, bl.gated_weights(packed, scale, packed, scale), "relu2", keep=True)
+    u = torch.round(bl.unpack_weights(packed)[cols].double())
+    acc = (q[ends].double()[:, None, :] * u[None]).sum(-1).float()
+    g = acc / (xs[ends][:, None] * scale)
+    assert torch.equal(out.g[ends][:, cols], g.to(torch.bfloat16)) and torch.equal(out.g, out.u)
+    a, want = out.a[ends][:, cols].double(), g.double().relu() ** 2 * g.double()
+    assert bool(((a - want).abs() <= want.abs() * (BF * (1 + 3 * U) + 3 * U) + TINY).all())
+
+
 def test_large_offsets(bl):
     """Outputs and weights of more than 2^31 elements, and gradients too."""
     m, n, k = 70000, 32768, 64
