@@ -77,26 +77,32 @@ constexpr CodesConfig kW8Configs[] = {{64, 64, 64, 2, 0.16f, 0.17f, 0.19f, 0.22f
 constexpr CodesConfig kGatedConfigs[] = {{32, 128, 128, 2, 0.32f, 0.35f, 0.46f, 0.55f, 1.0f},
                                          {64, 128, 128, 2, 0.41f, 0.47f, 0.68f, 0.86f, 1.8f},
                                          {128, 128, 128, 2, 0.71f, 0.87f, 1.24f, 1.55f, 2.5f}};
-constexpr float kCodesStartUs = 3.5f;   // a launch
-constexpr float kCodesFinishUs = 3.0f;  // one more, that adds the parts
-constexpr float kCodesPadUs = 3.0f;     // one before, that aligns the activations' rows
-constexpr float kCodesBytesPerUs = 6e6f;
+constexpr float kCodesStartUs = 3.5f;     // a launch
+constexpr float kCodesFinishUs = 3.0f;    // one more, that adds the parts
+constexpr float kCodesPadUs = 3.0f;       // one before, that aligns the activations' rows
+constexpr float kCodesStageUs = 3e-4f;    // a column of 16 tokens staged four bytes at a time
+constexpr float kCodesBytesPerUs = 6e6f;  // of parts
+constexpr float kCodesReadPerUs = 5e6f;   // of weights
 
 // The kernel, tile and parts with the smallest estimated time (m > 16).  Measured
 // against single choices (us, 8-bit): 17 x 4096 x 4096 rows 7.5, tiles 11; 64 x 14336
 // x 4096 rows 36, tiles of 64 x 64 16, of 128 x 128 19, of 256 x 256 in four parts 25;
 // 2048 x 4096 x 4096 of 128 x 128 45, of 128 x 256 39, of 256 x 256 54; 2048 x 14336 x
 // 4096 139, 138 and 120; 300 x 4096 x 14336 of 128 x 256 in four parts 38, of 128 x
-// 128 in two 40, of 256 x 256 in six 48.  Over 70 shapes of all sizes the choice is 4%
-// off the best one on average.
+// 128 in two 40, of 256 x 256 in six 48.  Over 210 shapes of all sizes the choice is
+// 1% off the best one on average, 36% at most.
 inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
   CodesPlan best = {};
   best.cfg = -1;
   const RowsPlan r = plan_rows(16, n, k, gated);
-  const int64_t rtk = rows_tile_k(gated), per = kRowsWaves / r.wk;
-  const int64_t rwgs = ((n + 15) / 16 + per - 1) / per * ((m + 15) / 16), tiles = ((k + rtk - 1) / rtk + r.wk - 1) / r.wk;
+  const int64_t rtk = rows_tile_k(gated), per = kRowsWaves / r.wk, ktiles = (k + rtk - 1) / rtk;
+  const int64_t rwgs = ((n + 15) / 16 + per - 1) / per * ((m + 15) / 16);
+  const float tiles = ktiles < r.wk ? (float)ktiles / (float)r.wk : (float)((ktiles + r.wk - 1) / r.wk);  // a wave's
+  const float load = std::min(1.0f, (float)rwgs / (2 * kCodesCus));
   float least = kCodesStartUs + (float)((rwgs + 2 * kCodesCus - 1) / (2 * kCodesCus)) *
-                                    (gated ? 1.6f + 2.1f * (float)tiles : 1.0f + 1.1f * (float)tiles);
+                                    ((gated ? 1.6f + 2.1f * tiles : 1.0f + (0.6f + 0.5f * load) * tiles) +
+                                     (k % 16 ? kCodesStageUs * (float)k : 0.0f));
+  const float reading = (float)n * (float)k * (gated ? 0.5f : 1.0f) / kCodesReadPerUs;  // the weights
   for (int cfg = 0; cfg < (gated ? 3 : 4); ++cfg) {
     const CodesConfig& C = gated ? kGatedConfigs[cfg] : kW8Configs[cfg];
     const int64_t ti = (m + C.ti - 1) / C.ti, tj = (n + C.tj - 1) / C.tj, slabs = (k + C.slab - 1) / C.slab;
@@ -110,7 +116,8 @@ inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
     for (int64_t want = 1; want <= 16; ++want) {
       if (want > 1 && (slabs * C.slab < 512 * want || ti * tj * want > 4 * kCodesCus)) break;
       const int64_t kspw = (slabs + want - 1) / want, parts = (slabs + kspw - 1) / kspw, wgs = ti * tj * parts;
-      float us = kCodesStartUs + (k % 16 ? kCodesPadUs : 0.0f) + (float)(wgs / room) * round(room, kspw) + round(wgs % room, kspw);
+      float us = kCodesStartUs + (k % 16 ? kCodesPadUs : 0.0f) +
+                 std::max((float)(wgs / room) * round(room, kspw) + round(wgs % room, kspw), reading);
       if (parts > 1)
         us += kCodesFinishUs + 8.0f * (float)parts * (float)m * (float)n * (gated ? 2.0f : 1.0f) / kCodesBytesPerUs;
       if (us >= least) continue;

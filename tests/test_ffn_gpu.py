@@ -389,7 +389,8 @@ W8_SHAPES = [(1, 1, 4), (1, 16, 64), (1, 4096, 1024), (2, 17, 68), (5, 40, 2084)
              (17, 100, 1028), (33, 64, 4096), (64, 130, 640), (77, 515, 388), (129, 300, 1280), (257, 259, 252),
              (300, 600, 2048), (600, 1030, 512), (3, 200, 16384), (16, 100, 14336), (12, 33, 9500), (2, 4200, 64),
              (17, 33, 128), (17, 33, 4096), (100, 4100, 8192), (130, 8200, 8192), (200, 8200, 260), (1025, 8200, 128),
-             (72, 5851, 5360), (520, 4100, 516), (1030, 4101, 260), (76, 11238, 10264), (138, 11219, 13852)]
+             (72, 5851, 5360), (520, 4100, 516), (1030, 4101, 260), (76, 11238, 10264), (138, 11219, 13852),
+             (157, 6253, 10824)]
 
 
 @pytest.mark.parametrize("bias", [False, True])
