@@ -882,6 +882,55 @@ def test_gated_backward_largest_sizes(bl, m, n, k):
     check_backward(bl.GatedBackwardCall(*args, "relu2", dev(q), dev(xs), tg, dsg, tu, dsu)(), want, m, n)
 
 
+def test_refusals(bl):
+    """What does not fit is refused before anything runs, and leaves outputs as
+    they were."""
+    m, n, k = 40, 48, 512
+    q, xs, ug, sg, uu, su, tg, dsg, tu, dsu, da, g, u = backward_inputs(bl, 73, m, n, k)
+    dq, dxs = dev(q), dev(xs)
+    dda, dg, du = (to_dev(oracle.f32_to_bf16(t)) for t in (da, g, u))
+    w, w8 = bl.gated_weights(tg, dsg, tu, dsu), bl.pack_weights_w8(torch.randn(n, k, device=DEV))
+    out = torch.full((m, n), 3.0, dtype=torch.bfloat16, device=DEV)
+    bad = (ValueError, TypeError, bl.BitLinearError)
+    for call in (lambda: bl.forward_w8(dq[:, :256].contiguous(), dxs, w8, out=out),  # another width
+                 lambda: bl.forward_w8(dq[:, ::2], dxs, w8, out=out),
+                 lambda: bl.forward_w8(dq, dxs[:-1], w8, out=out),
+                 lambda: bl.forward_w8(dq, dxs.double(), w8, out=out),
+                 lambda: bl.forward_w8(dq, dxs, w8, out=out[:-1]),
+                 lambda: bl.forward_w8(dq, dxs, w8, out=out, bias=torch.zeros(n, device=DEV)),
+                 lambda: bl.forward_w8(dq, dxs, w8._replace(n=n + 16), out=out),
+                 lambda: bl.forward_w8(dq, dxs, w8._replace(codes=w8.codes.cpu()), out=out),
+                 lambda: bl.forward_w8(dq.cpu(), dxs, w8, out=out),
+                 lambda: bl.forward_w8(dq, dxs, w8, out=out, bias=out.view(-1)[:n]),  # overlaps
+                 lambda: bl.GatedCall(dq, dxs, w, "gelu", out=bl.Gated(out, None, None))(),
+                 lambda: bl.GatedCall(dq, dxs, w, "silu", keep=True, out=bl.Gated(out, None, None))(),
+                 lambda: bl.GatedCall(dq, dxs, w, "silu", out=bl.Gated(out, out, out))(),
+                 lambda: bl.GatedCall(dq, dxs, w._replace(k=k - 256), "silu", out=bl.Gated(out, None, None))(),
+                 lambda: bl.gated_weights(tg, dsg, tu[:32], dsu),
+                 lambda: bl.gated_weights(tg, dsg, tu, dsu.double()),
+                 lambda: bl.GatedBackwardCall(dda, dg, du, "silu"),
+                 lambda: bl.GatedBackwardCall(dda, dg, du[:-1], "silu", dq, dxs),
+                 lambda: bl.GatedBackwardCall(dda, dg, du, "silu", dq, dxs, tg, dsg),
+                 lambda: bl.GatedBackwardCall(dda, dg, du, "silu", dq, dxs, accumulate=True),
+                 lambda: bl.GatedBackwardCall(dda, dg, du, "silu", gate=tg, gate_scale=dsg, up=tu, up_scale=dsu,
+                                              dx=dda.view(-1)[:0].view(0, k)),
+                 lambda: bl.clip_grads([], 1.0),
+                 lambda: bl.clip_grads([out, out[1:]], 1.0),
+                 lambda: bl.clip_grads([out], 1.0, outs=[out.view(-1)[1:].view(-1)]),
+                 lambda: bl.clip_grads([out, torch.zeros(4)], 1.0),
+                 lambda: bl.clip_grads([out[:, ::2]], 1.0),
+                 lambda: bl.clip_grads([out], -1.0)):
+        with pytest.raises(bad):
+            call()
+    for make in (lambda ws: bl.GatedBackwardCall(dda, dg, du, "silu", dq, dxs, workspace=ws),
+                 lambda ws: bl.GradNormCall([out], workspace=ws)):
+        need = make(None).workspace.numel()
+        assert need > 0
+        with pytest.raises(bad):
+            make(torch.empty(need - 256, dtype=torch.uint8, device=DEV))()
+    assert bool((out == 3).all())
+
+
 # The limits: tokens, outputs, width.
 LIMITS = [(2 ** 19, 17, 4), (2 ** 19, 1, 20), (1, 2 ** 24, 4), (17, 2 ** 24, 4), (2, 19, 2 ** 17), (40, 19, 2 ** 17),
           (300, 19, 2 ** 17 - 4)]
