@@ -205,7 +205,8 @@ def test_gated_nan_row(bl, m, n, k, act):
 
 BACK = [(1, 1, 4), (1, 16, 64), (3, 5, 8), (64, 64, 64), (65, 67, 68), (40, 1000, 260), (301, 1001, 1284), (130, 520, 640),
         (700, 200, 520), (520, 2048, 516), (17, 515, 128), (100, 2050, 2080), (130, 33, 8192), (513, 515, 8192),
-        (1025, 33, 128), (2048, 33, 2080), (2048, 2050, 128), (1030, 260, 2052)]
+        (1025, 33, 128), (2048, 33, 2080), (2048, 2050, 128), (1030, 260, 2052),
+        (1350, 36, 4), (1115, 2867, 80), (141, 2788, 5420), (73, 2434, 1036)]
 
 
 def backward_inputs(bl, seed, m, n, k):

@@ -398,10 +398,8 @@ def test_gpu_shapes_take_every_plan(plans):
         want = {(-1, False), (0, False), (0, True), (1, False), (1, True), (2, False)}
         want |= {(2, True)} if gated else {(2, True), (3, False), (3, True)}
         assert want <= seen, (gated, want - seen)
-    tiles, parts = set(), set()
+    tiles = set()
     for _, gradients in plans(BACK):
         _, c0, p0, _, c1, p1, _ = gradients[0]
-        tiles |= {("dx", c0), ("dw", c1)}
-        parts |= {("dx", p0 > 1), ("dw", p1 > 1)}
-    assert tiles == {(w, c) for w in ("dx", "dw") for c in range(3)}
-    assert parts == {(w, c) for w in ("dx", "dw") for c in (False, True)}
+        tiles |= {("dx", c0, p0 > 1), ("dw", c1, p1 > 1)}
+    assert tiles >= {(w, c, p) for w in ("dx", "dw") for c in range(3) for p in (False, True)} - {("dw", 2, True)}
