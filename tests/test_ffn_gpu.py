@@ -831,6 +831,28 @@ def test_same_tensor_twice(bl, tr):
     assert all(torch.equal(i, j) for i, j in zip(one, two))
 
 
+def test_broadcast_and_strided_inputs(bl, tr):
+    """norm_gated of inputs that are not contiguous rows, against contiguous ones:
+    a broadcast input's gradient is the sum over its copies."""
+    torch.manual_seed(65)
+    m, n, k = 24, 72, 256
+    wg, wu = ((0.05 * torch.randn(n, k, device=DEV)).requires_grad_() for _ in range(2))
+    da = torch.randn(n, m, device=DEV).to(torch.bfloat16).t()  # columns first
+    one = torch.randn(1, k, device=DEV).to(torch.bfloat16).requires_grad_()
+    wide = torch.randn(m, 2 * k, device=DEV).to(torch.bfloat16).requires_grad_()
+    turned = torch.randn(k, m, device=DEV).to(torch.bfloat16).requires_grad_()
+    for leaf, view in ((one, lambda t: t.expand(m, k)), (wide, lambda t: t[:, 1:2 * k:2]), (turned, lambda t: t.t())):
+        for act in ("relu2", "silu"):
+            rows = view(leaf).detach().contiguous().requires_grad_()
+            got, want = tr.norm_gated(view(leaf), wg, wu, activation=act)[1], tr.norm_gated(rows, wg, wu, activation=act)[1]
+            assert torch.equal(got, want)
+            got = torch.autograd.grad(got, (leaf, wg, wu), da)
+            want = torch.autograd.grad(want, (rows, wg, wu), da.contiguous())
+            assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+            full = torch.autograd.grad(view(leaf), leaf, want[0])[0]  # what torch makes of the same rows
+            assert torch.equal(got[0], full)
+
+
 def test_calls_from_threads(bl):
     """Host threads with streams, shapes and workspaces of their own."""
     import threading
