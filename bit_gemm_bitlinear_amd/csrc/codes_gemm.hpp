@@ -42,8 +42,8 @@ namespace bl {
 typedef int32_t v16i __attribute__((ext_vector_type(16)));
 
 struct CodesJob {
-  const int8_t* q;  // rows of ldq bytes, 16-byte aligned
-  int32_t ldq;      // ldq % 16 == 0
+  const int8_t* q;  // rows of ldq bytes
+  int32_t ldq;      // a multiple of 16, or of 4 (tiles that load WORDS)
   int32_t m, n, k;
   const uint8_t* w;
   int32_t ktiles, blocks;  // of the weights' storage
@@ -83,6 +83,11 @@ __device__ __forceinline__ void wait_slabs(int ahead) {
 __device__ __forceinline__ void dma16(const void* src, int8_t* lds_dst) {
   __builtin_amdgcn_global_load_lds((const BL_GLOBAL void*)src,
                                    (__attribute__((address_space(3))) void*)lds_dst, 16, 0, 0);
+}
+
+__device__ __forceinline__ void dma4(const void* src, int8_t* lds_dst) {
+  __builtin_amdgcn_global_load_lds((const BL_GLOBAL void*)src,
+                                   (__attribute__((address_space(3))) void*)lds_dst, 4, 0, 0);
 }
 
 __device__ __forceinline__ void barrier() {
@@ -155,8 +160,9 @@ struct CodesRows {
 
 // One tile of TI tokens x TJ weight rows by WI x WJ waves.  TERNARY: the first
 // half of the TJ rows is the gate's, the second the up projection's of the same
-// TJ / 2 outputs, and so is each wave's share.
-template <int TI_, int TJ_, int WI_, int WJ_, int NST_, bool TERNARY>
+// TJ / 2 outputs, and so is each wave's share.  WORDS: activations are loaded four
+// bytes a lane, from rows of any multiple of that, in place of 16.
+template <int TI_, int TJ_, int WI_, int WJ_, int NST_, bool TERNARY, bool WORDS = false>
 struct CodesTile {
   static constexpr int SL = TERNARY ? 128 : 64;        // k of a slab
   static constexpr int CA = SL / 16;                   // chunks of a row of activations or 8-bit weights
@@ -167,14 +173,15 @@ struct CodesTile {
   static constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;
   static constexpr int kStage = TI * SL + TJ * kRowB;
   static constexpr int kLds = NST * kStage;
-  static constexpr int DA = TI * SL / 1024 / NW;  // loads of a slab, per wave
+  static constexpr int kLoadA = WORDS ? 256 : 1024;  // bytes of a load of activations
+  static constexpr int DA = TI * SL / kLoadA / NW;   // loads of a slab, per wave
   static constexpr int CB = TJ * kRowB / 1024;  // of the weights, all waves
   static constexpr int DB = CB < NW ? 1 : CB / NW;
   static constexpr int D = DA + DB;
   static constexpr int kCols = TERNARY ? TJ / 2 : TJ;  // outputs of a tile
   using Rows = CodesRows<kCols / WJ>;                  // a wave's outputs
   static_assert(NW * Rows::kBytes <= kLds, "they fit the ring");
-  static_assert(DA * 1024 * NW == TI * SL && (DB * NW == CB || NW % CB == 0), "whole loads");
+  static_assert(DA * kLoadA * NW == TI * SL && (NST - 1) * D < 64 && (DB * NW == CB || NW % CB == 0), "whole loads");
   static_assert(FI * WI * 32 == TI && FJ * WJ * 32 == TJ && (!TERNARY || FJ % 2 == 0), "whole subtiles");
 
   // First row and (outputs') first column of the wave's share.
@@ -197,9 +204,14 @@ struct CodesTile {
     const int blk0 = tj * (kCols / 16);
 
     // Per lane the offsets of a load's row and of its chunk in the slab.
-    uint32_t ar[DA], ac[DA], br[DB];
+    uint32_t ar[WORDS ? 1 : DA], ac[WORDS ? 1 : DA], br[DB];
+    const uint32_t row_end = (uint32_t)(J.m - 1 - i0) * (uint32_t)J.ldq;
+    if constexpr (WORDS) {  // of load 0 of wave 0, without the swizzle, which is one of the load
+      ar[0] = (uint32_t)(lane / (SL / 4)) * (uint32_t)J.ldq;
+      ac[0] = 4 * (lane % (SL / 4));
+    }
 #pragma unroll
-    for (int i = 0; i < DA; ++i) {
+    for (int i = 0; i < (WORDS ? 0 : DA); ++i) {
       const int pos = (wv * DA + i) * 64 + lane, r = pos / CA;
       ar[i] = (uint32_t)min(r, J.m - 1 - i0) * (uint32_t)J.ldq;
       ac[i] = 16 * swz(r, pos % CA);
@@ -220,7 +232,12 @@ struct CodesTile {
     int next = s0;  // the slab that is loaded next
     // Load d (of D) of the next slab into the buffer st.
     auto issue_one = [&](int d, int8_t* st) {
-      if (d < DA) {
+      if (WORDS && d < DA) {
+        const int l = wv * DA + d;
+        const uint32_t row = min(ar[0] + (uint32_t)(l * (256 / SL)) * (uint32_t)J.ldq, row_end);
+        const uint32_t last = (uint32_t)(J.ldq - 4 - next * SL);  // the row's last word for those past it
+        dma4(pa + (int64_t)next * SL + row + min(ac[0] ^ (uint32_t)(16 * (l & (CA - 1))), last), st + l * 256);
+      } else if (d < DA) {
         // the row's last chunk for those past it
         const uint32_t last = (uint32_t)(J.ldq - 16 - next * SL);
         dma16(pa + (int64_t)next * SL + ar[d] + min(ac[d], last), st + (wv * DA + d) * 1024);

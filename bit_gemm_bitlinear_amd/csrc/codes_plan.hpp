@@ -60,6 +60,7 @@ inline RowsPlan plan_rows(int64_t m, int64_t n, int64_t k, bool ternary) {
 struct CodesPlan {
   int cfg;  // tile, or -1: codes_rows.hpp, any number of tokens, 16 at a time
   int slabs, tiles_i, tiles_j, ksplit, kspw;
+  bool pad;  // the activations' rows are aligned to 16 bytes first
 };
 
 // Tile sizes (tokens x outputs), k of a slab, the workgroups a CU holds, and,
@@ -80,6 +81,12 @@ constexpr CodesConfig kGatedConfigs[] = {{32, 128, 128, 2, 0.32f, 0.35f, 0.46f, 
 constexpr float kCodesStartUs = 3.5f;     // a launch
 constexpr float kCodesFinishUs = 3.0f;    // one more, that adds the parts
 constexpr float kCodesPadUs = 3.0f;       // one before, that aligns the activations' rows
+// Rows that are no multiple of 16 bytes: the two smaller tiles load them in words, as
+// they are, the larger ones, whose loads count for more, from an aligned copy (words
+// against the copy, us: 8-bit 64 x 64 401 x 5316 x 356 14.0 and 15.6, 128 x 256 300 x
+// 14336 x 4100 41 and 36, 256 x 256 2048 x 14336 x 4100 139 and 128; gated 1348 x 227 x
+// 268 6.1 and 8.0, 300 x 6912 x 2564 24.4 and 23.7).
+constexpr int kCodesWordTiles = 2;
 constexpr float kCodesStageUs = 3e-4f;    // a column of 16 tokens staged four bytes at a time
 constexpr float kCodesBytesPerUs = 6e6f;  // of parts
 constexpr float kCodesReadPerUs = 5e6f;   // of weights
@@ -100,9 +107,11 @@ inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
   const float tiles = ktiles < r.wk ? (float)ktiles / (float)r.wk : (float)((ktiles + r.wk - 1) / r.wk);  // a wave's
   const float load = std::min(1.0f, (float)rwgs / (2 * kCodesCus));
   float least = kCodesStartUs + (float)((rwgs + 2 * kCodesCus - 1) / (2 * kCodesCus)) *
-                                    ((gated ? 1.6f + 2.1f * tiles : 1.0f + (0.6f + 0.5f * load) * tiles) +
+                                    ((gated ? 1.6f + (1.2f + 0.9f * load) * tiles : 1.0f + (0.6f + 0.5f * load) * tiles) +
                                      (k % 16 ? kCodesStageUs * (float)k : 0.0f));
-  const float reading = (float)n * (float)k * (gated ? 0.5f : 1.0f) / kCodesReadPerUs;  // the weights
+  // reading the weights (more slowly where CUs have two of the smallest tiles: 45 x 9299
+  // x 9620 in two parts of those 39 us, of 128 x 128 in three 29)
+  const float reading = (float)n * (float)k * (gated ? 0.5f : 1.0f) / kCodesReadPerUs;
   for (int cfg = 0; cfg < (gated ? 3 : 4); ++cfg) {
     const CodesConfig& C = gated ? kGatedConfigs[cfg] : kW8Configs[cfg];
     const int64_t ti = (m + C.ti - 1) / C.ti, tj = (n + C.tj - 1) / C.tj, slabs = (k + C.slab - 1) / C.slab;
@@ -116,13 +125,15 @@ inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
     for (int64_t want = 1; want <= 16; ++want) {
       if (want > 1 && (slabs * C.slab < 512 * want || ti * tj * want > 4 * kCodesCus)) break;
       const int64_t kspw = (slabs + want - 1) / want, parts = (slabs + kspw - 1) / kspw, wgs = ti * tj * parts;
-      float us = kCodesStartUs + (k % 16 ? kCodesPadUs : 0.0f) +
-                 std::max((float)(wgs / room) * round(room, kspw) + round(wgs % room, kspw), reading);
+      const bool pad = k % 16 != 0 && cfg >= kCodesWordTiles;
+      float us = kCodesStartUs + (pad ? kCodesPadUs : 0.0f) +
+                 std::max((float)(wgs / room) * round(room, kspw) + round(wgs % room, kspw),
+                          cfg == 0 && wgs > kCodesCus ? 1.3f * reading : reading);
       if (parts > 1)
         us += kCodesFinishUs + 8.0f * (float)parts * (float)m * (float)n * (gated ? 2.0f : 1.0f) / kCodesBytesPerUs;
       if (us >= least) continue;
       least = us;
-      best = CodesPlan{cfg, (int)slabs, (int)ti, (int)tj, (int)parts, (int)kspw};
+      best = CodesPlan{cfg, (int)slabs, (int)ti, (int)tj, (int)parts, (int)kspw, pad};
     }
   }
   return best;

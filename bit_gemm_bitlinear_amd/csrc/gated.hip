@@ -236,8 +236,10 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(const GatedGemmArgs A
 }
 
 using GatedTile128 = CodesTile<128, 256, 2, 2, 3, true>;
-using GatedTile64 = CodesTile<64, 256, 1, 4, 4, true>;
-using GatedTile32 = CodesTile<32, 256, 1, 4, 6, true>;
+template <bool WORDS>
+using GatedTile64 = CodesTile<64, 256, 1, 4, 4, true, WORDS>;
+template <bool WORDS>
+using GatedTile32 = CodesTile<32, 256, 1, 4, 6, true, WORDS>;
 
 template <typename T, bool SILU>
 hipError_t gated_gemm(const GatedGemmArgs& a, hipStream_t s) {
@@ -248,9 +250,11 @@ hipError_t gated_gemm(const GatedGemmArgs& a, hipStream_t s) {
 
 template <bool SILU>
 hipError_t launch_gated_gemm(const GatedGemmArgs& a, int cfg, hipStream_t s) {
-  const hipError_t e = cfg == 2   ? gated_gemm<GatedTile128, SILU>(a, s)
-                       : cfg == 1 ? gated_gemm<GatedTile64, SILU>(a, s)
-                                  : gated_gemm<GatedTile32, SILU>(a, s);
+  const bool words = a.j.ldq % 16 != 0;
+  const hipError_t e =
+      cfg == 2   ? gated_gemm<GatedTile128, SILU>(a, s)
+      : cfg == 1 ? (words ? gated_gemm<GatedTile64<true>, SILU>(a, s) : gated_gemm<GatedTile64<false>, SILU>(a, s))
+                 : (words ? gated_gemm<GatedTile32<true>, SILU>(a, s) : gated_gemm<GatedTile32<false>, SILU>(a, s));
   if (e != hipSuccess || a.j.ksplit == 1) return e;
   const int64_t total = (int64_t)a.j.m * ((a.j.n + 7) / 8);
   gated_finish_kernel<SILU><<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, total);
@@ -268,8 +272,8 @@ GatedLayout gated_layout(int64_t m, int64_t n, int64_t k) {
   L.plan.cfg = -1;
   if (m > 16) L.plan = plan_codes(m, n, k, true);
   if (L.plan.cfg < 0) return L;
-  L.ldq = (int32_t)round_up(k, 16);
-  if (k % 16) L.total = align256((size_t)m * L.ldq);
+  L.ldq = (int32_t)(L.plan.pad ? round_up(k, 16) : k);
+  if (L.plan.pad) L.total = align256((size_t)m * L.ldq);
   L.part = L.total;
   if (L.plan.ksplit > 1) L.total = align256(L.total + 8 * (size_t)L.plan.ksplit * m * part_pitch(n));
   return L;
@@ -308,7 +312,7 @@ hipError_t launch_gated_forward(const GatedArgs& b, char* ws, hipStream_t s) {
     a.a = b.a;
     a.g = b.g;
     a.u = b.u;
-    if (b.k % 16) {
+    if (L.plan.pad) {
       const hipError_t e = codes_pad(b.q, b.m, b.k, L.ldq, reinterpret_cast<int8_t*>(ws), s);
       if (e != hipSuccess) return e;
       J.q = reinterpret_cast<const int8_t*>(ws);

@@ -233,8 +233,10 @@ __global__ __launch_bounds__(256) void w8_finish_kernel(const W8GemmArgs A, int6
 
 using W8Tile256 = CodesTile<256, 256, 2, 4, 4, false>;
 using W8TileWide = CodesTile<128, 256, 2, 4, 5, false>;
-using W8Tile128 = CodesTile<128, 128, 2, 2, 5, false>;
-using W8Tile64 = CodesTile<64, 64, 2, 2, 8, false>;
+template <bool WORDS>
+using W8Tile128 = CodesTile<128, 128, 2, 2, 5, false, WORDS>;
+template <bool WORDS>
+using W8Tile64 = CodesTile<64, 64, 2, 2, 8, false, WORDS>;
 
 template <typename T>
 hipError_t w8_gemm(const W8GemmArgs& a, hipStream_t s) {
@@ -254,8 +256,8 @@ W8Layout w8_layout(int64_t m, int64_t n, int64_t k) {
   L.plan.cfg = -1;
   if (m > 16) L.plan = plan_codes(m, n, k, false);
   if (L.plan.cfg < 0) return L;
-  L.ldq = (int32_t)round_up(k, 16);
-  if (k % 16) L.total = align256((size_t)m * L.ldq);
+  L.ldq = (int32_t)(L.plan.pad ? round_up(k, 16) : k);
+  if (L.plan.pad) L.total = align256((size_t)m * L.ldq);
   L.part = L.total;
   if (L.plan.ksplit > 1) L.total = align256(L.total + 4 * (size_t)L.plan.ksplit * m * part_pitch(n));
   return L;
@@ -296,15 +298,16 @@ hipError_t launch_w8_forward(const W8Args& b, char* ws, hipStream_t s) {
     a.bias = b.bias;
     a.y = b.y;
     hipError_t e = hipSuccess;
-    if (b.k % 16) {
+    if (L.plan.pad) {
       e = codes_pad(b.q, b.m, b.k, L.ldq, reinterpret_cast<int8_t*>(ws), s);
       if (e != hipSuccess) return e;
       J.q = reinterpret_cast<const int8_t*>(ws);
     }
+    const bool words = L.ldq % 16 != 0;
     e = L.plan.cfg == 3   ? w8_gemm<W8Tile256>(a, s)
         : L.plan.cfg == 2 ? w8_gemm<W8TileWide>(a, s)
-        : L.plan.cfg == 1 ? w8_gemm<W8Tile128>(a, s)
-                          : w8_gemm<W8Tile64>(a, s);
+        : L.plan.cfg == 1 ? (words ? w8_gemm<W8Tile128<true>>(a, s) : w8_gemm<W8Tile128<false>>(a, s))
+                          : (words ? w8_gemm<W8Tile64<true>>(a, s) : w8_gemm<W8Tile64<false>>(a, s));
     if (e != hipSuccess || J.ksplit == 1) return e;
     const int64_t total = b.m * ((b.n + 7) / 8);
     w8_finish_kernel<<<(unsigned)((total + 255) / 256), 256, 0, s>>>(a, total);

@@ -97,7 +97,8 @@ SHAPES = [(1, 16, 256), (1, 1, 4), (2, 17, 260), (5, 40, 2084), (16, 33, 512), (
           (64, 130, 640), (77, 1003, 2084), (129, 300, 1280), (257, 515, 388), (300, 64, 4096), (1, 6912, 2560),
           (4, 4096, 1024), (513, 1024, 128), (16, 40, 6016),
           (9, 70, 9500), (3, 4200, 64), (17, 33, 128), (17, 33, 8192), (33, 8200, 8192), (100, 8200, 516), (257, 8200, 8192),
-          (4104, 1001, 260), (1637, 1191, 13232)]
+          (4104, 1001, 260), (1637, 1191, 13232), (19, 33, 4180), (2347, 782, 4), (1705, 33, 12604), (1956, 2155, 16),
+          (1474, 14156, 4), (4284, 387, 12628), (21, 35, 12400), (27, 30, 5020), (3103, 35, 6768)]
 
 
 def gated_inputs(bl, seed, m, n, k, tiled=False):
@@ -391,7 +392,8 @@ W8_SHAPES = [(1, 1, 4), (1, 16, 64), (1, 4096, 1024), (2, 17, 68), (5, 40, 2084)
              (300, 600, 2048), (600, 1030, 512), (3, 200, 16384), (16, 100, 14336), (12, 33, 9500), (2, 4200, 64),
              (17, 33, 128), (17, 33, 4096), (100, 4100, 8192), (130, 8200, 8192), (200, 8200, 260), (1025, 8200, 128),
              (72, 5851, 5360), (520, 4100, 516), (1030, 4101, 260), (76, 11238, 10264), (138, 11219, 13852),
-             (157, 6253, 10824)]
+             (157, 6253, 10824), (20, 37, 5172), (269, 13215, 16), (66, 2499, 16300), (260, 13997, 16), (309, 14354, 1928),
+             (153, 5841, 7648), (141, 5525, 15108), (3236, 12715, 4)]
 
 
 @pytest.mark.parametrize("bias", [False, True])

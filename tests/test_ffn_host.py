@@ -394,9 +394,9 @@ def test_gpu_shapes_take_every_plan(plans):
     from test_ffn_gpu import BACK, SHAPES, W8_SHAPES
 
     for gated, shapes in enumerate((W8_SHAPES, SHAPES)):
-        seen = {(p[gated][0], p[gated][4] > 1) for s, (p, _) in zip(shapes, plans(shapes)) if s[0] > 16}
-        want = {(-1, False), (0, False), (0, True), (1, False), (1, True), (2, False)}
-        want |= {(2, True)} if gated else {(2, True), (3, False), (3, True)}
+        seen = {(p[gated][0], p[gated][4] > 1, s[2] % 16 > 0) for s, (p, _) in zip(shapes, plans(shapes)) if s[0] > 16}
+        want = {(c, p, odd) for c in range(3 if gated else 4) for p in (False, True) for odd in (False, True)}
+        want = want - {(3, True, False)} | {(-1, False, False), (-1, False, True)}
         assert want <= seen, (gated, want - seen)
     tiles = set()
     for _, gradients in plans(BACK):
