@@ -96,8 +96,8 @@ constexpr float kCodesReadPerUs = 5e6f;   // of weights
 // x 4096 rows 36, tiles of 64 x 64 16, of 128 x 128 19, of 256 x 256 in four parts 25;
 // 2048 x 4096 x 4096 of 128 x 128 45, of 128 x 256 39, of 256 x 256 54; 2048 x 14336 x
 // 4096 139, 138 and 120; 300 x 4096 x 14336 of 128 x 256 in four parts 38, of 128 x
-// 128 in two 40, of 256 x 256 in six 48.  Over 210 shapes of all sizes the choice is
-// 1% off the best one on average, 36% at most.
+// 128 in two 40, of 256 x 256 in six 48.  Over 240 shapes of all sizes the choice is
+// 1% off the best one on average, a quarter at most.
 inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
   CodesPlan best = {};
   best.cfg = -1;
