@@ -205,7 +205,7 @@ struct CodesTile {
 
     // Per lane the offsets of a load's row and of its chunk in the slab.
     uint32_t ar[WORDS ? 1 : DA], ac[WORDS ? 1 : DA], br[DB];
-    const uint32_t row_end = (uint32_t)(J.m - 1 - i0) * (uint32_t)J.ldq;
+    const uint32_t row_end = tile_last_row(TI, J.m - i0, J.ldq);
     if constexpr (WORDS) {  // of load 0 of wave 0, without the swizzle, which is one of the load
       ar[0] = (uint32_t)(lane / (SL / 4)) * (uint32_t)J.ldq;
       ac[0] = 4 * (lane % (SL / 4));

@@ -91,6 +91,13 @@ constexpr float kCodesStageUs = 3e-4f;    // a column of 16 tokens staged four b
 constexpr float kCodesBytesPerUs = 6e6f;  // of parts
 constexpr float kCodesReadPerUs = 5e6f;   // of weights
 
+// Where the last row that a tile of `ti` tokens has begins, from its first one: rows of
+// ldq bytes, of which `left` are left of the product.  The tile's own rows are under 2^25
+// bytes, those that are left may be past 2^32.
+constexpr uint32_t tile_last_row(int32_t ti, int32_t left, int32_t ldq) {
+  return (uint32_t)((left < ti ? left : ti) - 1) * (uint32_t)ldq;
+}
+
 // The kernel, tile and parts with the smallest estimated time (m > 16).  Measured
 // against single choices (us, 8-bit): 17 x 4096 x 4096 rows 7.5, tiles 11; 64 x 14336
 // x 4096 rows 36, tiles of 64 x 64 16, of 128 x 128 19, of 256 x 256 in four parts 25;

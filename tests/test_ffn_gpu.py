@@ -1015,3 +1015,24 @@ def test_large_offsets(bl):
     q = torch.full((1, k), 2, device=DEV, dtype=torch.int8)
     y = bl.forward_w8(q, torch.ones(1, device=DEV), w8)
     assert float(y[0, -1]) == 10 and float(y[0, 0]) == 14 and int(torch.count_nonzero(y)) == 2
+
+
+def test_odd_width_past_four_gigabytes_of_codes(bl):
+    """Tiles that load activations in words, of a product whose codes are more than
+    2^32 bytes: every row against the same rows in calls of their own."""
+    m, n, k = 65552, 64, 65540
+    gen = torch.Generator(device=DEV).manual_seed(75)
+    q = torch.empty((m, k), dtype=torch.int8, device=DEV)
+    for i in range(0, m, 8192):
+        q[i:i + 8192] = torch.randint(-128, 128, q[i:i + 8192].shape, generator=gen, device=DEV, dtype=torch.int8)
+    xs = torch.rand(m, generator=gen, device=DEV) + 0.5
+    w = torch.randn(n, k, generator=gen, device=DEV)
+    w8 = bl.pack_weights_w8(w)
+    packed, scale = bl.pack_weights(w)
+    gw = bl.gated_weights(packed, scale, packed.flip(0).contiguous(), scale)
+    y, a = bl.forward_w8(q, xs, w8), bl.forward_gated(q, xs, gw, "relu2", keep=True)
+    for i in list(range(0, 512, 128)) + [m // 2, m - 128]:  # the first rows are the farthest from the end
+        part, ps = q[i:i + 128].clone(), xs[i:i + 128].clone()
+        assert torch.equal(y[i:i + 128], bl.forward_w8(part, ps, w8)), i
+        small = bl.forward_gated(part, ps, gw, "relu2", keep=True)
+        assert all(torch.equal(b[i:i + 128], c) for b, c in zip(a, small)), i

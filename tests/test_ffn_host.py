@@ -403,3 +403,54 @@ def test_gpu_shapes_take_every_plan(plans):
         _, c0, p0, _, c1, p1, _ = gradients[0]
         tiles |= {("dx", c0, p0 > 1), ("dw", c1, p1 > 1)}
     assert tiles >= {(w, c, p) for w in ("dx", "dw") for c in range(3) for p in (False, True)} - {("dw", 2, True)}
+
+
+WORD_ROWS_SRC = r"""
+#include "codes_plan.hpp"
+#include <cstdio>
+#include <cstdlib>
+
+// Per shape and product the tile that loads words, and how many of its rows begin elsewhere
+// than the product's row (or the last one, for those past it).
+int main(int argc, char** argv) {
+  for (int i = 1; i + 2 < argc; i += 3) {
+    const long long m = atoll(argv[i]), n = atoll(argv[i + 1]), k = atoll(argv[i + 2]);
+    for (int gated = 0; gated < 2; ++gated) {
+      const bl::CodesPlan p = bl::plan_codes(m, n, k, gated);
+      if (p.cfg < 0 || p.cfg >= bl::kCodesWordTiles || k % 16 == 0) {
+        printf("-1 0\n");
+        continue;
+      }
+      const int ti = (gated ? bl::kGatedConfigs : bl::kW8Configs)[p.cfg].ti;
+      long long wrong = 0;
+      for (long long i0 = 0; i0 < m; i0 += ti) {
+        const uint32_t end = bl::tile_last_row(ti, (int32_t)(m - i0), (int32_t)k);
+        for (int r = 0; r < ti; ++r)
+          wrong += std::min((uint32_t)r * (uint32_t)k, end) != std::min<long long>(r, m - 1 - i0) * k;
+      }
+      printf("%d %lld\n", p.cfg, wrong);
+    }
+  }
+  return 0;
+}
+"""
+
+# Odd widths and more than 2^32 bytes of codes: (tokens, outputs, width).
+WORD_ROWS = [(65552, 64, 65540), (65600, 64, 65540), (131072, 64, 32772), (524288, 16, 131068), (76411, 61, 64684)]
+
+
+def test_rows_of_tiles_that_load_words(tmp_path):
+    """Where each row of a tile begins, with more than 2^32 bytes of codes after it."""
+    src, exe = tmp_path / "rows.cpp", tmp_path / "rows"
+    src.write_text(WORD_ROWS_SRC)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I", os.path.join(ROOT, "bit_gemm_bitlinear_amd", "csrc"), str(src), "-o",
+                    str(exe)], check=True)
+    shapes = WORD_ROWS + [(33, 40, 20), (300, 19, 2 ** 17 - 4), (1705, 33, 12604), (401, 5316, 356)]
+    out = subprocess.run([str(exe), *(str(v) for s in shapes for v in s)], capture_output=True, text=True,
+                         check=True).stdout.splitlines()
+    rows = [tuple(map(int, line.split())) for line in out]
+    assert len(rows) == 2 * len(shapes)
+    # the GPU test's shape takes such a tile in both products
+    assert rows[0][0] in (0, 1) and rows[1][0] in (0, 1)
+    for i, shape in enumerate(shapes):
+        assert rows[2 * i][1] == 0 and rows[2 * i + 1][1] == 0, (shape, rows[2 * i:2 * i + 2])
