@@ -66,9 +66,12 @@ __global__ __launch_bounds__(256) void gated_weights_kernel(const uint8_t* __res
   }
 }
 
-// act(g) * u.  exp(-|g|) is at most 1, so nothing overflows that the result
-// does not; exp2 and the reciprocal are the hardware's, a few steps of fp32 off
-// where the result keeps eight bits (and 0 for exp(-|g|) under 2^-126).
+// act(g) * u.  exp(-|g|) is at most 1 and so is a sigmoid, and act(g) is made before
+// it meets u: no step overflows that the result does not (g * u first made NaN of a large
+// negative g and a large u, where the result is 0).  exp2 and the reciprocal are the
+// hardware's.  exp2's argument is a rounded product, so the error grows with |g|: up to
+// (14 + 2 |g|) * 2^-24 of the result (|g| = 80: 1e-5, where it keeps eight bits);
+// exp(-|g|) under 2^-126 is 0.
 template <bool SILU>
 __device__ __forceinline__ float gate_value(float g, float u) {
   if constexpr (!SILU) {
@@ -76,7 +79,7 @@ __device__ __forceinline__ float gate_value(float g, float u) {
     return (r * u) * r;
   } else {
     const float e = __builtin_amdgcn_exp2f(fabsf(g) * -1.44269504f);
-    return g * u * ((g >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e));
+    return g * ((g >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e)) * u;
   }
 }
 

@@ -61,12 +61,12 @@ size_t bitlinear_gated_forward_workspace_bytes(int64_t m, int64_t n, int64_t k);
  *   g = acc_gate / (x_scale * gate_scale),  u = acc_up / (x_scale * up_scale)
  *   a = bf16(act(g) * u)                                      [M][N] bf16
  * acc: exact int32 sums; g and u: one correctly rounded fp32 division each; act
- * and the product in fp32.  keep_g, keep_u: bf16(g) and bf16(u) [M][N], what
- * the BitLinear projections alone would give and the gradients read; both or
- * neither (NULL).  Outputs and workspace must not overlap an input or each
- * other.  One kernel; one more where K % 16 != 0 and the tokens are many (the
- * activations' rows are then aligned first), and one where few tiles' sums are split
- * over K. */
+ * and the product in fp32 (silu: act(g) first, and exp(-|g|) under 2^-126 is 0).
+ * keep_g, keep_u: bf16(g) and bf16(u) [M][N], what the BitLinear projections alone
+ * would give and the gradients read; both or neither (NULL).  Outputs and workspace
+ * must not overlap an input or each other.  One kernel; one more where K % 16 != 0
+ * and the tokens are many (the activations' rows are then aligned first), and one
+ * where few tiles' sums are split over K. */
 bl_status bitlinear_gated_forward(int64_t m, int64_t n, int64_t k, const int8_t *q,
                                   const float *x_scale, const uint8_t *codes,
                                   const float *gate_scale, const float *up_scale,

@@ -1036,3 +1036,32 @@ def test_odd_width_past_four_gigabytes_of_codes(bl):
         assert torch.equal(y[i:i + 128], bl.forward_w8(part, ps, w8)), i
         small = bl.forward_gated(part, ps, gw, "relu2", keep=True)
         assert all(torch.equal(b[i:i + 128], c) for b, c in zip(a, small)), i
+
+
+@pytest.mark.parametrize("gs,us", [(1e-17, 1e-17), (10, 1e-34), (20, 1e-34), (1e-30, 1e5)])
+@pytest.mark.parametrize("m,n,k", [(3, 64, 512), (40, 64, 512), (20, 48, 8192), (300, 200, 260)])
+def test_gated_silu_of_large_factors(bl, m, n, k, gs, us):
+    """Projections that are both large: no step leaves fp32's range where the result
+    does not.  Within |g| < 88 as check_gated has it; above, the sigmoid of g >= 0 is 1 to
+    2^-126, and the rest is two products and the rounding to bf16; below, the
+    result is |g u| exp(-88) at most, and exp(-88) is under TINY."""
+    q, xs, ug, _, uu, _, tg, _, tu, _ = gated_inputs(bl, 16, m, n, k)
+    xs[:] = 1.0
+    gs, us = np.float32(gs), np.float32(us)
+    r = bl.forward_gated(dev(q), dev(xs), bl.gated_weights(tg, dev(np.array([gs])), tu, dev(np.array([us]))), "silu",
+                         keep=True)
+    want, g, u = ref.gated_forward(q, xs, ug, gs, uu, us, "silu")
+    a, gu = f64(r.a), g.astype(np.float64) * u
+    assert np.isfinite(g).all() and np.isfinite(u).all()
+    assert us > 1 or np.abs(gu[g < 0]).max() > 3.5e38  # g * u alone leaves the range
+    assert not np.isnan(a).any()
+    fine = np.abs(want) < 3.3e38
+    assert np.isfinite(a[fine]).all()
+    over = np.abs(want) > 3.41e38  # past bf16's largest value and half a step
+    assert np.array_equal(a[over], np.sign(want[over]) * np.inf)
+    mid = fine & (np.abs(g) < 88)
+    check_gated(a[mid], g[mid], u[mid], want[mid], "silu")
+    high = fine & (g >= 88)
+    assert np.all(np.abs(a - gu)[high] <= np.abs(gu[high]) * (BF * (1 + 6 * U) + 6 * U) + TINY)
+    low = fine & (g <= -88)
+    assert np.all(np.abs(a[low]) <= np.abs(gu[low]) * TINY)
