@@ -29,28 +29,30 @@ __device__ __forceinline__ int64_t w8_offset(int64_t row, int64_t e, int64_t kti
 }
 
 // A workgroup a row: its largest magnitude, its scale, its codes.  Rows past N
-// and codes past K are zeros.  (14336 x 4096: 105 us; the second reading of a row
-// comes from a cache.)
+// and codes past K are zeros.  The magnitudes are compared as bits: a weight that is not
+// a number makes its row's scale, and so the row's outputs, not a number.  (14336 x 4096:
+// 105 us; the second reading of a row comes from a cache.)
 __global__ __launch_bounds__(256) void w8_pack_kernel(const float* __restrict__ w, int64_t n, int64_t k,
                                                       int64_t rows, int8_t* __restrict__ codes,
                                                       float* __restrict__ scale) {
-  __shared__ float red[4];
+  __shared__ uint32_t red[4];
   const int64_t ktiles = (k + 63) / 64;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const float* src = w + row * k;
-    float a = 0.0f;
+    uint32_t a = 0;
     if (row < n)
       for (int64_t e = 4 * threadIdx.x; e < k; e += 1024) {  // K % 4 == 0
         const v4f v = *G(reinterpret_cast<const v4f*>(src + e));
-        a = fmaxf(fmaxf(a, fmaxf(fabsf(v[0]), fabsf(v[1]))), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a = max(a, magnitude_bits(v[i]));
       }
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor(a, o));
+    for (int o = 32; o >= 1; o >>= 1) a = max(a, (uint32_t)__shfl_xor((int)a, o));
     __syncthreads();  // the last row's values are read
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = a;
     __syncthreads();
-    a = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    float s = a / 127.0f;
+    a = max(max(red[0], red[1]), max(red[2], red[3]));
+    float s = __uint_as_float(a) / 127.0f;
     if (s == 0.0f) s = 1.0f;
     if (row < n && threadIdx.x == 0) *G(scale + row) = s;
     for (int64_t e = 4 * threadIdx.x; e < ktiles * 64; e += 1024) {

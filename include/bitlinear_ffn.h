@@ -114,7 +114,8 @@ size_t bitlinear_w8_codes_bytes(int64_t n, int64_t k);
 
 /* Quantize latent fp32 weights [N][K]: scale = max_k|w| / 127 (1 where that is
  * 0), v = clamp(round(w / scale), -127, 127), one correctly rounded fp32
- * division each.  One kernel. */
+ * division each.  A row with a NaN has the scale NaN, one with an infinity and no NaN
+ * an infinite one: none of its outputs is finite.  One kernel. */
 bl_status bitlinear_w8_pack(const float *w, int64_t n, int64_t k, int8_t *codes,
                             float *scale, void *stream);
 

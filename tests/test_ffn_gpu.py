@@ -1065,3 +1065,29 @@ def test_gated_silu_of_large_factors(bl, m, n, k, gs, us):
     assert np.all(np.abs(a - gu)[high] <= np.abs(gu[high]) * (BF * (1 + 6 * U) + 6 * U) + TINY)
     low = fine & (g <= -88)
     assert np.all(np.abs(a[low]) <= np.abs(gu[low]) * TINY)
+
+
+@pytest.mark.parametrize("m", [1, 9, 40, 300])
+@pytest.mark.parametrize("k", [64, 68, 4096])
+def test_w8_weights_that_are_not_finite(bl, m, k):
+    """A weight that is not a number, or infinite, spoils its row's scale and all of that
+    output's values, and no others."""
+    torch.manual_seed(76)
+    n = 70
+    q, xs = (dev(t) for t in codes(np.random.default_rng(76), m, k))
+    w = 0.02 * torch.randn(n, k, device=DEV)
+    good = bl.pack_weights_w8(w)
+    y = bl.forward_w8(q, xs, good)
+    nan, inf = float("nan"), float("inf")
+    for values, kind in (((nan,), torch.isnan), ((inf,), torch.isinf), ((-inf, 1.0), torch.isinf), ((inf, nan), torch.isnan),
+                         ((-nan, -inf), torch.isnan)):
+        for at in (0, k - len(values), min(k - 4, 63)):
+            bad = w.clone()
+            bad[33, at:at + len(values)] = torch.tensor(values, device=DEV)
+            p = bl.pack_weights_w8(bad)
+            others = [i for i in range(n) if i != 33]
+            assert bool(kind(p.scale[33])) and torch.equal(p.scale[others], good.scale[others])
+            got = bl.forward_w8(q, xs, p)
+            assert not bool(torch.isfinite(got[:, 33]).any())
+            assert torch.equal(got[:, others], y[:, others])
+            assert torch.equal(bl.unpack_weights_w8(p)[others], bl.unpack_weights_w8(good)[others])
