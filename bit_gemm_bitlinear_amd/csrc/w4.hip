@@ -28,6 +28,8 @@ typedef int32_t v2i __attribute__((ext_vector_type(2)));
 
 // One wave per row and group: the group's largest magnitude, its scale, and
 // the bytes of the pairs (k, k + 4).  Rows past N and groups past K are zeros.
+// The magnitudes are compared as bits: a weight that is not a number makes its
+// group's scale, and so the row's outputs, not a number.
 __global__ __launch_bounds__(256) void w4_pack_kernel(const float* __restrict__ w, int64_t n,
                                                       int64_t k, int group, int64_t groups_pad,
                                                       int64_t total, uint8_t* __restrict__ codes,
@@ -39,12 +41,12 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const float* __restrict__ 
     const int64_t row = id / groups_pad, gi = id - row * groups_pad;
     const bool real = row < n && gi < groups;
     const float* src = w + row * k + gi * group;
-    float a = 0.0f;
+    uint32_t a = 0;
     if (real)
-      for (int e = lane; e < group; e += 64) a = fmaxf(a, fabsf(src[e]));
+      for (int e = lane; e < group; e += 64) a = max(a, magnitude_bits(src[e]));
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor(a, o));
-    uint16_t sb = real ? f32_to_bf16(a / 7.0f) : (uint16_t)0;
+    for (int o = 32; o >= 1; o >>= 1) a = max(a, (uint32_t)__shfl_xor((int)a, o));
+    uint16_t sb = real ? f32_to_bf16(__uint_as_float(a) / 7.0f) : (uint16_t)0;
     if (real && sb == 0) sb = 0x3F80;
     const float s = bf16_to_f32(sb);
     for (int p = lane; p < group / 2; p += 64) {

@@ -164,7 +164,8 @@ size_t bitlinear_w4_scales_bytes(int64_t n, int64_t k, int64_t group);
 
 /* Quantize latent fp32 weights [N][K]: scale = bf16(max|w| / 7) over the
  * group (1 where that is 0), v = clamp(round(w / scale), -8, 7), one
- * correctly rounded fp32 division each.  One kernel. */
+ * correctly rounded fp32 division each.  A group with a NaN has the scale NaN, one
+ * with an infinity and no NaN an infinite one.  One kernel. */
 bl_status bitlinear_w4_pack(const float *w, int64_t n, int64_t k, int64_t group,
                             uint8_t *codes, uint16_t *scales, void *stream);
 

@@ -827,3 +827,30 @@ def test_backward_far_tokens(bl):
     check_input(alone[0], want, mag, n)
     check_weight(dw, *weight_gradient(bl, dy, q, xs), last)
     assert bool(((db.double() - dy.double().sum(0)).abs() <= (last + 2) * U * dy.double().abs().sum(0)).all())
+
+
+@pytest.mark.parametrize("m", [1, 9])
+@pytest.mark.parametrize("k,group", [(64, 32), (256, 64), (512, 128), (2048, 1024)])
+def test_w4_weights_that_are_not_finite(bl, m, k, group):
+    """A weight that is not a number, or infinite, spoils its group's scale and all of
+    that output's values, and no others."""
+    torch.manual_seed(76)
+    n = 37
+    x = torch.randn(m, k, device=DEV).to(torch.bfloat16)
+    q, xs = bl.act_quant(x)
+    w = 0.02 * torch.randn(n, k, device=DEV)
+    good = bl.pack_weights_w4(w, group)
+    y, u = bl.forward_w4(q, xs, good), bl.unpack_weights_w4(good)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        for at in (0, group - 1, k - 1):
+            bad = w.clone()
+            bad[20, at] = value
+            p = bl.pack_weights_w4(bad, group)
+            others = [i for i in range(n) if i != 20]
+            scales = bl.unpack_weights_w4(p)
+            g = at // group * group
+            assert not bool(torch.isfinite(scales[20, g:g + group]).any())
+            rest = [i for i in range(k) if not g <= i < g + group]
+            assert torch.equal(scales[20, rest], u[20, rest]) and torch.equal(scales[others], u[others])
+            got = bl.forward_w4(q, xs, p)
+            assert not bool(torch.isfinite(got[:, 20]).any()) and torch.equal(got[:, others], y[:, others])
