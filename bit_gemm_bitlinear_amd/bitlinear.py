@@ -1146,11 +1146,12 @@ class GradNormCall:
     shapes on one device): fp32 [1], on the device."""
 
     def __init__(self, grads, workspace=None):
-        self._arr, self._dev = _gradients(list(grads), None)
+        grads = list(grads)  # once: what a generator made is held by this list alone
+        self._arr, self._dev = _gradients(grads, None)
         self.norm = _rows_f32(1, self._dev)
         need = int(_lib.bitlinear_grad_norm_workspace_bytes(len(self._arr), self._arr))
         self.workspace = _workspace(need, self._dev, workspace)
-        self._keep = list(grads)
+        self._keep = grads
         self._args = (len(self._arr), self._arr, _ptr(self.norm), _ptr(self.workspace), _nbytes(self.workspace))
 
     def __call__(self, stream=None) -> torch.Tensor:

@@ -8,6 +8,8 @@ arithmetic: U = 2^-24 is half a step of fp32, a result rounded to bf16 is off by
 whole step (2^-23) per term, as their rounding mode is not ours to choose.
 """
 
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -1091,3 +1093,32 @@ def test_w8_weights_that_are_not_finite(bl, m, k):
             assert not bool(torch.isfinite(got[:, 33]).any())
             assert torch.equal(got[:, others], y[:, others])
             assert torch.equal(bl.unpack_weights_w8(p)[others], bl.unpack_weights_w8(good)[others])
+
+
+def test_gradients_from_a_generator(bl):
+    """Prepared calls hold the tensors that a generator made for them."""
+    torch.manual_seed(77)
+    src = [torch.randn(5000 + i, device=DEV).to(torch.bfloat16) for i in range(20)]
+    total = float(torch.sqrt(sum(t.double().square().sum() for t in src)))
+    for make in (bl.GradNormCall, lambda it: bl.ClipGradsCall(it, 0.5)):
+        refs = []
+
+        def made():
+            for t in src:
+                g = t.float()
+                refs.append(weakref.ref(g))
+                yield g
+                del g
+
+        call = make(made())
+        assert len(refs) == 20 and all(r() is not None for r in refs)
+        other = [torch.full((5000 + i,), 1e9, device=DEV) for i in range(20)]  # on what would be free
+        norm = call()
+        norm = norm[0] if isinstance(norm, tuple) else norm
+        assert abs(float(norm) - total) <= 2 * U * total
+        del other
+    assert abs(float(bl.grad_norm(t.float() for t in src)) - total) <= 2 * U * total
+    norm, outs = bl.clip_grads((t.float() for t in src), 0.5)
+    assert abs(float(norm) - total) <= 2 * U * total
+    for o, t in zip(outs, src):
+        assert torch.allclose(o.double(), t.double() * (0.5 / (total + 1e-6)), rtol=4 * U, atol=0)
