@@ -1164,7 +1164,9 @@ class ClipGradsCall:
     each is multiplied by min(1, max_norm / (norm + 1e-6)), in place or into
     `outs`.  No gradient may be listed twice.  A call returns (norm, outs), norm
     fp32 [1] on the device: that before clipping.  Nothing waits for it: a norm
-    that is not finite is the caller's to look at."""
+    that is not finite is the caller's to look at.  Autograd is told of the tensors
+    that a call writes (not of a graph's replays), and so refuses to go back through
+    a graph that has saved them."""
 
     def __init__(self, grads, max_norm: float, outs=None, workspace=None):
         grads = list(grads)
@@ -1182,6 +1184,7 @@ class ClipGradsCall:
 
     def __call__(self, stream=None):
         _launch(_lib.bitlinear_clip_gradients, self._args, self._dev, stream)
+        torch.autograd.graph.increment_version(self.outs)
         return self.norm, self.outs
 
 

@@ -1122,3 +1122,35 @@ def test_gradients_from_a_generator(bl):
     assert abs(float(norm) - total) <= 2 * U * total
     for o, t in zip(outs, src):
         assert torch.allclose(o.double(), t.double() * (0.5 / (total + 1e-6)), rtol=4 * U, atol=0)
+
+
+def test_clipping_is_seen_by_autograd(bl, tr):
+    """Clipping in place a tensor that a graph has saved makes that graph's backward
+    pass an error, as torch's own in-place operations do."""
+    def saved(x):
+        g = torch.autograd.grad(x.square().sum(), x, create_graph=True)[0]
+        return g, g.square().sum()  # saves g
+
+    x = torch.randn(50, device=DEV, requires_grad=True)
+    for clip in (lambda g: bl.clip_grads([g], 0.1), lambda g: bl.clip_grads([g.detach()], 0.1),
+                 lambda g: bl.clip_grads([torch.zeros_like(g)], 0.1, outs=[g])):
+        g, loss = saved(x)
+        clip(g)
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+    p = torch.nn.Parameter(x.detach().clone())
+    g, loss = saved(p)
+    p.grad = g
+    tr.clip_grad_norm([p], 0.1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    # what is only read stays usable
+    g, loss = saved(x)
+    want = torch.autograd.grad(loss, x, retain_graph=True)[0]
+    bl.grad_norm([g])
+    bl.clip_grads([g], 0.1, outs=[torch.empty_like(g)])
+    assert torch.equal(torch.autograd.grad(loss, x)[0], want)
+    with torch.inference_mode():  # tensors without a version
+        g = torch.full((100,), 2.0, device=DEV)
+        norm, (o,) = bl.clip_grads([g], 10.0)
+    assert float(norm) == 20 and bool((o - 1).abs().max() < 1e-6)
