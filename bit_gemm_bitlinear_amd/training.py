@@ -292,12 +292,12 @@ def clip_grad_norm(parameters, max_norm: float) -> torch.Tensor:
     at most max_norm; returns the norm before, a 0-d fp32 tensor on the device.
     Two passes over the gradients, and nothing waits for them: where the norm is
     not finite, the gradients are spoiled as bitlinear.ClipGradsCall says, and the
-    caller's to look at.  A parameter listed twice counts once."""
-    if isinstance(parameters, torch.Tensor):
-        parameters = [parameters]
+    caller's to look at.  A parameter listed twice counts once; without a gradient
+    the norm is 0, on the first parameter's device."""
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = list({id(p): p.grad for p in parameters if p.grad is not None}.values())
     if not grads:
-        return torch.zeros(())
+        return torch.zeros((), device=parameters[0].device if parameters else None)
     return bl.clip_grads(grads, max_norm)[0].reshape(())
 
 

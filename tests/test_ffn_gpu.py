@@ -1154,3 +1154,14 @@ def test_clipping_is_seen_by_autograd(bl, tr):
         g = torch.full((100,), 2.0, device=DEV)
         norm, (o,) = bl.clip_grads([g], 10.0)
     assert float(norm) == 20 and bool((o - 1).abs().max() < 1e-6)
+
+
+def test_clip_grad_norm_without_a_gradient(tr):
+    """Zero on the parameters' device, from any iterable."""
+    ffn = tr.FeedForward(64, 128, device=DEV)
+    want = torch.zeros((), device=DEV)
+    for params in (ffn.parameters(), list(ffn.parameters()), ffn.gate, (p for p in ffn.parameters())):
+        norm = tr.clip_grad_norm(params, 1.0)
+        assert norm.device == want.device and norm.dtype == torch.float32 and norm.dim() == 0 and float(norm) == 0
+    torch.stack([norm, want])
+    assert float(tr.clip_grad_norm([], 1.0)) == 0
