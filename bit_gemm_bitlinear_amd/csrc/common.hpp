@@ -82,10 +82,6 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) {
   return __uint_as_float(bits16 << 16);
 }
 
-// |x| as bits: whole numbers in the order of the magnitudes, infinity above them and
-// NaN above that, so that a maximum of them keeps a NaN (fmaxf drops it).
-__device__ __forceinline__ uint32_t magnitude_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
 // fp32 -> bf16, round to nearest even: gfx950's v_cvt_pk_bf16_f32 (one
 // instruction; NaN stays NaN).
 __device__ __forceinline__ uint16_t f32_to_bf16(float f) {

@@ -17,6 +17,7 @@
 #include "common.hpp"
 #include "internal.hpp"
 #include "layer_internal.hpp"
+#include "magnitude.hpp"
 
 #include <algorithm>
 

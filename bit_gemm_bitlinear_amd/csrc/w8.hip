@@ -16,6 +16,7 @@
 #include "common.hpp"
 #include "internal.hpp"
 #include "layer_internal.hpp"
+#include "magnitude.hpp"
 
 namespace bl {
 
