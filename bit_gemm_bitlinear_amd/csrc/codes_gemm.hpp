@@ -22,8 +22,8 @@
 // sums are not stored.
 //
 // What bounds a tile: of 256 x 256 the matrix cores, busy 55% of the cycles that a
-// CU has work, at the clock that their power leaves (8-bit 2048 x 14336 x 4096: 116
-// us, 2.07 POPS; on zeros 103); smaller ones the cache lines that a CU's L1 has in
+// CU has work, at the clock that their power leaves (8-bit 2048 x 14336 x 4096: 117
+// us, 2.06 POPS; on zeros 103); smaller ones the cache lines that a CU's L1 has in
 // flight, some 70: about 24 bytes a cycle go to LDS whatever the tile, so a tile
 // that needs fewer bytes a product is faster until it leaves CUs without work
 // (codes_plan.hpp), and loads are whole lines where they can be (weights in the

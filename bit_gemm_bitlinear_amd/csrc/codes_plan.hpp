@@ -80,7 +80,10 @@ constexpr CodesConfig kGatedConfigs[] = {{32, 128, 128, 2, 0.32f, 0.35f, 0.46f, 
                                          {128, 128, 128, 2, 0.71f, 0.87f, 1.24f, 1.55f, 2.5f}};
 constexpr float kCodesStartUs = 3.5f;     // a launch
 constexpr float kCodesFinishUs = 3.0f;    // one more, that adds the parts
-constexpr float kCodesPadUs = 3.0f;       // one before, that aligns the activations' rows
+// One before, that aligns the activations' rows, whatever their bytes (2048 x 4100 codes
+// 6 us by itself, 4096 x 12604 20, 16384 x 8196 46, where products of 4096 outputs take
+// 41, 213 and 540).
+constexpr float kCodesPadUs = 3.0f;
 // Rows that are no multiple of 16 bytes: the two smaller tiles load them in words, as
 // they are, the larger ones, whose loads count for more, from an aligned copy (words
 // against the copy, us: 8-bit 64 x 64 401 x 5316 x 356 14.0 and 15.6, 128 x 256 300 x
@@ -99,12 +102,13 @@ constexpr uint32_t tile_last_row(int32_t ti, int32_t left, int32_t ldq) {
 }
 
 // The kernel, tile and parts with the smallest estimated time (m > 16).  Measured
-// against single choices (us, 8-bit): 17 x 4096 x 4096 rows 7.5, tiles 11; 64 x 14336
-// x 4096 rows 36, tiles of 64 x 64 16, of 128 x 128 19, of 256 x 256 in four parts 25;
-// 2048 x 4096 x 4096 of 128 x 128 45, of 128 x 256 39, of 256 x 256 54; 2048 x 14336 x
-// 4096 139, 138 and 120; 300 x 4096 x 14336 of 128 x 256 in four parts 38, of 128 x
-// 128 in two 40, of 256 x 256 in six 48.  Over 240 shapes of all sizes the choice is
-// 1% off the best one on average, a quarter at most.
+// against single choices (us, 8-bit): 17 x 4096 x 4096 rows 6.6, tiles 10; 64 x 14336
+// x 4096 rows 35, tiles of 64 x 64 14.6, of 128 x 128 18, of 256 x 256 in four parts 25;
+// 2048 x 4096 x 4096 of 128 x 128 43, of 128 x 256 39, of 256 x 256 55; 2048 x 14336 x
+// 4096 139, 137 and 122; 300 x 4096 x 14336 of 128 x 256 in five parts, which it takes,
+// 38.8, in four 38.1, of 128 x 128 in two 39, of 256 x 256 in seven 46.  Over 240 drawn
+// shapes of each product the choice is 1.6% off the best one on average, over 10% in 14,
+// a third at most (8-bit 2449 x 1647 x 9396, of 64 x 64: 98; of 128 x 256 74).
 inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
   CodesPlan best = {};
   best.cfg = -1;
@@ -116,8 +120,9 @@ inline CodesPlan plan_codes(int64_t m, int64_t n, int64_t k, bool gated) {
   float least = kCodesStartUs + (float)((rwgs + 2 * kCodesCus - 1) / (2 * kCodesCus)) *
                                     ((gated ? 1.6f + (1.2f + 0.9f * load) * tiles : 1.0f + (0.6f + 0.5f * load) * tiles) +
                                      (k % 16 ? kCodesStageUs * (float)k : 0.0f));
-  // reading the weights (more slowly where CUs have two of the smallest tiles: 45 x 9299
-  // x 9620 in two parts of those 39 us, of 128 x 128 in three 29)
+  // reading the weights (more slowly where CUs have two of the smallest tiles: 8-bit 45 x
+  // 9299 x 9620 in two parts of those 38 us, of 128 x 128 in three 27; the gated product's
+  // smallest tiles take the same factor, which changed none of its 240 choices)
   const float reading = (float)n * (float)k * (gated ? 0.5f : 1.0f) / kCodesReadPerUs;
   for (int cfg = 0; cfg < (gated ? 3 : 4); ++cfg) {
     const CodesConfig& C = gated ? kGatedConfigs[cfg] : kW8Configs[cfg];

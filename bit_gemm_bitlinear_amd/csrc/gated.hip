@@ -10,7 +10,7 @@
 // codes to subtract, no activations to reorder.  The sums come out 64 times too
 // large, exactly; the factor leaves in the epilogue.  Both sums of an output meet in
 // one lane, so act(g) * u costs no pass of its own (2048 x 6912 x 2560 with g and u
-// kept: 71 us, 2.04 POPS; the plain projections, activation and product as launches
+// kept: 72 us, 2.02 POPS; the plain projections, activation and product as launches
 // of their own 118 without keeping them).
 #include "../../include/bitlinear_ffn.h"
 #include "codes_gemm.hpp"
